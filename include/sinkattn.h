@@ -209,6 +209,149 @@ sinkattn_status sinkattn_grpo_loss(const sinkattn_grpo_problem* g, const float* 
                                    float* stats, float* dlogp, float* advantages,
                                    void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------- rollout
+ * The 4-bit paged key/value cache and what a rollout does with it.  One
+ * prompt's pages are shared by the rollouts of its GRPO group; every new
+ * token attends to the cache and is sampled with the log-probability that
+ * sinkattn_grpo_loss takes as logp_old.
+ *
+ * All state is on the device and every call is asynchronous, so a step can be
+ * captured into a CUDA graph and replayed while the sequences grow.
+ *
+ * Format.  pages is [num_pages][num_heads_kv][page_size / 16] blocks of 16
+ * tokens, 1152 bytes each.  With g = 0..7, t = 0..3, lane = 4 g + t:
+ *   [0, 512)      keys' codes: per lane 8 bytes of token g, then 8 of token
+ *                 g + 8, dims 16 t .. 16 t + 15
+ *   [512, 1024)   values' codes: per lane 4 bytes each of tokens 2t, 2t + 1,
+ *                 2t + 8, 2t + 9, dims 8 g .. 8 g + 7
+ *   [1024, 1088)  keys' scales: per lane of tokens g and g + 8, those dims
+ *   [1088, 1152)  values' scales: per (16 dims, t) of the four tokens
+ * A byte holds two e2m1 codes, the lower dim in the low nibble (0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 and a sign); a scale is e4m3 and serves 16 dims of a token.
+ * A value is code * scale * (the head's fp32 factor k_scale or v_scale, which
+ * is finite and positive).
+ *
+ * Pages.  Slot s holds seqlens[s] tokens in the pages page_table[s][0 ..
+ * ceil(seqlens[s] / page_size) - 1]; the other entries mean nothing.
+ * refcount[p] says how many slots hold page p; 0 is free.  Calls that need
+ * pages take the lowest-numbered free ones, request after request.  A new
+ * cache is page_table all -1, seqlens and refcount all 0.
+ *
+ * Entries of `slots` outside [0, num_slots) are idle: nothing is written for
+ * them, they read as an empty sequence.  A page number outside
+ * [0, num_pages), or a position beyond the table, is never accessed: tokens
+ * there are not written and read as NaN.  Limits: page_size 16, 32, 64, 128
+ * or 256; max_pages * page_size <= 2^30; 4096 entries per call; head_dim 64.
+ * All pointers of the cache are 16-byte aligned; int32 and fp32 lists
+ * elsewhere 4-byte aligned. */
+typedef struct {
+  void* pages;            /* uint8 [num_pages][num_heads_kv][page_size * 72] */
+  int32_t* page_table;    /* [num_slots][max_pages] */
+  int32_t* seqlens;       /* [num_slots] */
+  int32_t* refcount;      /* [num_pages] */
+  const float* k_scale;   /* [num_heads_kv] */
+  const float* v_scale;   /* [num_heads_kv] */
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t num_heads_kv;
+  int32_t num_slots;
+  int32_t max_pages;
+} sinkattn_kv4_cache;
+
+/* reserve: slot slots[i] grows by new_tokens[i] tokens and gets the pages
+ * they need; done[i] = 1.  Pages are given in the order of the requests; one
+ * that does not fit, and every later one that needs a page, gets none and
+ * done[i] = 0.  done[i] = 0 also for a slot out of range, a slot named
+ * earlier in the call, a negative count or a length beyond the table.  The
+ * last page of a slot is never shared (see fork), so a grown slot can be
+ * written at once. */
+sinkattn_status sinkattn_kv4_reserve(const sinkattn_kv4_cache* cache, const int32_t* slots, const int32_t* new_tokens,
+                                     int32_t n, int32_t* done, void* stream);
+
+/* fork: the empty slot dst[i] becomes a copy of src[i]: full pages are shared
+ * (refcount + 1), of a page that is not full the blocks that hold tokens are
+ * copied to a new page.  Several entries may name one source; all sources are
+ * read as they were before the call.  done[i] = 0, and nothing changes for
+ * the entry, where a slot is out of range, dst[i] is not empty or is named
+ * earlier in the call, or the pages run out (then every later entry that
+ * needs one gets none either). */
+sinkattn_status sinkattn_kv4_fork(const sinkattn_kv4_cache* cache, const int32_t* src, const int32_t* dst, int32_t n,
+                                  int32_t* done, void* stream);
+
+/* free: the slots give their pages back (refcount - 1) and are empty; their
+ * used table entries become -1.  Naming a slot again, or an empty one, does
+ * nothing. */
+sinkattn_status sinkattn_kv4_free(const sinkattn_kv4_cache* cache, const int32_t* slots, int32_t n, void* stream);
+
+/* compact: writes the live pages of `from` (refcount > 0), in the order of
+ * their numbers, to pages 0 .. live - 1 of `to`, with refcount, page_table
+ * (entries not in use -1) and seqlens to match; *count (device) = live.  If
+ * live > to->num_pages, `to` is left as it was and only count is written.
+ * `from` is not changed.  Both have the same page_size, num_heads_kv,
+ * num_slots and max_pages, and share no memory except, if the caller likes,
+ * the scales (`to` keeps its own, which must be equal). */
+size_t sinkattn_kv4_compact_workspace_size(const sinkattn_kv4_cache* from);
+sinkattn_status sinkattn_kv4_compact(const sinkattn_kv4_cache* from, const sinkattn_kv4_cache* to, int32_t* count,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* append: quantises k and v (bf16 [total, num_heads_kv, 64]) into the cache.
+ * Rows cu_new[b] .. cu_new[b + 1] - 1 are the last positions of slot
+ * slots[b], whose length already counts them (reserve first); cu_new is int32
+ * [num_seqs + 1] on the device, nondecreasing, or NULL for total / num_seqs
+ * rows each.  Rows behind the last offset are not read.  Per 16 dims with
+ * y = x / factor: scale = e4m3(min(max|y| / 6, 448)), code = e2m1(y / scale),
+ * both rounded to nearest even, codes saturating, 0 where the scale is 0.  16
+ * dims that hold a NaN or an infinity read back as NaN.  A slot may be named
+ * once per call. */
+sinkattn_status sinkattn_kv4_append(const sinkattn_kv4_cache* cache, const int32_t* slots, int32_t num_seqs,
+                                    const int32_t* cu_new, int32_t total, const void* k, const void* v, void* stream);
+
+/* read: the same rows back as bf16 (rounded once from the fp32 product), for
+ * instance the whole prefix for sinkattn_fwd.  A slot may be named more than
+ * once.  Rows before a sequence's begin are zero; rows behind the last offset
+ * are left as they were. */
+sinkattn_status sinkattn_kv4_read(const sinkattn_kv4_cache* cache, const int32_t* slots, int32_t num_seqs,
+                                  const int32_t* cu, int32_t total, void* k, void* v, void* stream);
+
+/* Decode forward over the cache: as sinkattn_decode_fwd (causal) with slots
+ * for sequences.  q and o bf16 [num_seqs * q_per_seq, num_heads_q, 64], lse
+ * fp32 [num_heads_q, num_seqs * q_per_seq]; row b * q_per_seq + i is position
+ * seqlens[slots[b]] - q_per_seq + i.  Rows at negative positions (an idle
+ * entry, a sequence shorter than q_per_seq) get o = 0, lse = -inf.  The
+ * lengths are read on the device.  (num_heads_q / num_heads_kv) * q_per_seq
+ * <= 128.  The workspace (sinkattn_kv4_decode_workspace_size bytes for
+ * num_rows = num_seqs * q_per_seq, 16-byte aligned, its size depends on the
+ * device's SM count) is zero-filled once; every call leaves it usable for
+ * later calls of any shape it is large enough for, not for calls that overlap
+ * on the GPU.  Results do not depend on the order in which the GPU runs the
+ * parts of the work. */
+size_t sinkattn_kv4_decode_workspace_size(int64_t num_rows, int32_t num_heads_q);
+sinkattn_status sinkattn_kv4_decode_fwd(const sinkattn_kv4_cache* cache, const int32_t* slots, int32_t num_seqs,
+                                        int32_t q_per_seq, int32_t num_heads_q, int64_t window, int64_t prefix,
+                                        float scale, const void* q, const float* sink, void* o, float* lse,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Token sampling from logits [rows][row_stride] (the first `vocab` of each
+ * row; dtype 0 fp32, 1 bf16, 2 fp16) and one random number u[r] in [0, 1) per
+ * row, with temperature, top_k, top_p and min_p per row (device, [rows]):
+ *   e_i = exp((x_i - max x) / temperature), order: larger x first, of equal
+ *   ones the lower index; top_k keeps the first top_k (<= 0 or >= vocab: all);
+ *   top_p the shortest run of those whose mass is at least top_p of theirs
+ *   (>= 1: all, <= 0: the first one); min_p those with e_i >= min(min_p, 1).
+ *   The token is the first index whose kept mass up to and including it
+ *   exceeds u times the kept mass.  temperature 0: the first in the order,
+ *   with e at temperature 1.
+ * tokens int32; logp = log(e / sum of all e), what sinkattn_grpo_loss takes
+ * as logp_old; logq = log(e / kept mass) (0 where one token is kept).  Logits
+ * of -inf are never chosen; a row of nothing else gives token -1 and -inf.  A
+ * row with a NaN or +inf logit, a NaN parameter, a negative or infinite
+ * temperature gives token -1 and NaN.  u outside [0, 1) is clamped.  vocab
+ * <= 2^18, row_stride >= vocab, any alignment of the rows. */
+sinkattn_status sinkattn_sample_tokens(const void* logits, int32_t dtype, int32_t rows, int32_t vocab,
+                                       int64_t row_stride, const float* u, const float* temperature,
+                                       const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
+                                       float* logp, float* logq, void* stream);
+
 /* Packed-sequence front end (multi-turn trajectories of different lengths,
  * SinkFlex-RL section 3).  seqlens: device int32 [num_seqs];
  * cu_seqlens_out: device int32 [num_seqs + 1] receives the exclusive prefix

@@ -27,3 +27,15 @@ from .api import (  # noqa: F401
     sinkattn_unpack,
     sinkattn_varlen_plan,
 )
+from .rollout import (  # noqa: F401
+    KV4Cache,
+    kv4_append,
+    kv4_compact,
+    kv4_decode_fwd,
+    kv4_decode_workspace,
+    kv4_fork,
+    kv4_free,
+    kv4_read,
+    kv4_reserve,
+    sample_tokens,
+)

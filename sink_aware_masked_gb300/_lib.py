@@ -51,8 +51,26 @@ class GrpoProblem(ctypes.Structure):
     ]
 
 
+class Kv4Cache(ctypes.Structure):
+    _fields_ = [
+        ("pages", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("seqlens", ctypes.c_void_p),
+        ("refcount", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_heads_kv", ctypes.c_int32),
+        ("num_slots", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+    ]
+
+
 _PP = ctypes.POINTER(Problem)
 _GP = ctypes.POINTER(GrpoProblem)
+_KP = ctypes.POINTER(Kv4Cache)
+_f32 = ctypes.c_float
 SIGNATURES = {
     "sinkattn_fwd_workspace_size": (_sz, [_PP]),
     "sinkattn_bwd_workspace_size": (_sz, [_PP]),
@@ -64,6 +82,18 @@ SIGNATURES = {
     "sinkattn_decode_fwd": (ctypes.c_int, [_PP, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "sinkattn_grpo_workspace_size": (_sz, [_GP]),
     "sinkattn_grpo_loss": (ctypes.c_int, [_GP, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sinkattn_kv4_reserve": (ctypes.c_int, [_KP, _vp, _vp, _i32, _vp, _vp]),
+    "sinkattn_kv4_fork": (ctypes.c_int, [_KP, _vp, _vp, _i32, _vp, _vp]),
+    "sinkattn_kv4_free": (ctypes.c_int, [_KP, _vp, _i32, _vp]),
+    "sinkattn_kv4_compact_workspace_size": (_sz, [_KP]),
+    "sinkattn_kv4_compact": (ctypes.c_int, [_KP, _KP, _vp, _vp, _sz, _vp]),
+    "sinkattn_kv4_append": (ctypes.c_int, [_KP, _vp, _i32, _vp, _i32, _vp, _vp, _vp]),
+    "sinkattn_kv4_read": (ctypes.c_int, [_KP, _vp, _i32, _vp, _i32, _vp, _vp, _vp]),
+    "sinkattn_kv4_decode_workspace_size": (_sz, [_i64, _i32]),
+    "sinkattn_kv4_decode_fwd": (ctypes.c_int, [_KP, _vp, _i32, _i32, _i32, _i64, _i64, _f32, _vp, _vp, _vp, _vp, _vp,
+                                               _sz, _vp]),
+    "sinkattn_sample_tokens": (ctypes.c_int, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                              _vp]),
     "sinkattn_varlen_plan": (ctypes.c_int, [_vp, _i32, _vp, _vp]),
     "sinkattn_pack": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp]),
     "sinkattn_unpack": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp]),

@@ -136,6 +136,64 @@ struct GrpoArgs {
 size_t grpo_workspace_bytes(int num_rollouts, int total_tokens);
 cudaError_t launch_grpo(const GrpoArgs& a, cudaStream_t s);
 
+// 4-bit paged key/value cache (kv4.cuh) after validation.
+struct Kv4Cache {
+  uint8_t* pages;
+  int32_t* page_table;  // [num_slots, max_pages]
+  int32_t* seqlens;     // [num_slots]
+  int32_t* refcount;    // [num_pages]
+  const float* k_scale; // [num_heads_kv]
+  const float* v_scale;
+  int num_pages, page_size, num_heads_kv, num_slots, max_pages;
+  int page_log2;    // page_size = 1 << page_log2
+  int blocks_log2;  // blocks of 16 tokens in a page, log2
+};
+constexpr int kKv4MaxRequests = 4096;  // entries of one reserve / fork / append / decode call
+
+cudaError_t launch_kv4_reserve(const Kv4Cache& c, const int32_t* slots, const int32_t* add, int n, int32_t* done,
+                               cudaStream_t s);
+cudaError_t launch_kv4_fork(const Kv4Cache& c, const int32_t* src, const int32_t* dst, int n, int32_t* done,
+                            cudaStream_t s);
+cudaError_t launch_kv4_free(const Kv4Cache& c, const int32_t* slots, int n, cudaStream_t s);
+size_t kv4_compact_workspace_bytes(int num_pages);
+cudaError_t launch_kv4_compact(const Kv4Cache& from, const Kv4Cache& to, int32_t* count, void* workspace,
+                               cudaStream_t s);
+// k and v [total, Hkv, 64] bf16 are written to the cache (append) or from it (read).
+cudaError_t launch_kv4_append(const Kv4Cache& c, const int32_t* slots, int n, const int32_t* cu, int total,
+                              const void* k, const void* v, cudaStream_t s);
+cudaError_t launch_kv4_read(const Kv4Cache& c, const int32_t* slots, int n, const int32_t* cu, int total, void* k,
+                            void* v, cudaStream_t s);
+
+struct Kv4DecodeArgs {
+  const int32_t* slots;  // [num_seqs]
+  const void* q;         // [num_seqs * n, Hq, 64]
+  const float* sink;
+  void* o;
+  float* lse;            // [Hq, num_seqs * n]
+  void* workspace;
+  int num_seqs, n, hq, window, prefix;
+  float scale;
+};
+size_t kv4_decode_workspace_bytes(long long rows, int hq);
+cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, cudaStream_t s);
+
+// Token sampling (sample.cu).
+struct SampleArgs {
+  const void* logits;  // [rows, stride], the first `vocab` of each row
+  int dtype;           // 0 fp32, 1 bf16, 2 fp16
+  int rows, vocab;
+  long long stride;    // elements
+  const float* u;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t* tokens;
+  float* logp;
+  float* logq;
+};
+cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
+
 // Optional events recorded around the main kernels (measurement hook).
 struct ProfileEvents {
   cudaEvent_t start = nullptr, stop = nullptr;

@@ -1,0 +1,280 @@
+"""The rollout side: a 4-bit paged key/value cache, attention over it, and token sampling.
+
+As in ``api``, this is argument marshalling only: every step runs in the CUDA
+kernels of libsinkattn.so (the formats and contracts are in
+include/sinkattn.h).  Calls are asynchronous on the current stream of the
+tensors' device and allocate nothing but outputs that are not passed in, so a
+step can be captured into a CUDA graph.
+
+One rollout step of B sequences::
+
+    done = kv4_reserve(cache, slots, ones)               # room for the new tokens
+    kv4_append(cache, slots, k, v)                       # k, v [B, Hkv, 64] bf16
+    o, lse = kv4_decode_fwd(cache, slots, q, sink, q_per_seq=1, workspace=ws)
+    ...
+    tokens, logp, logq = sample_tokens(logits, u, temperature=t, top_p=p)
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional
+
+import torch
+
+from . import _lib
+from .api import HEAD_DIM, WINDOW_INF, _check, _on_gpu, _ptr
+
+BLOCK_TOKENS = 16
+TOKEN_BYTES = 72  # per token and kv head: 2 x 32 bytes of codes, 2 x 4 scales
+
+_LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _call(name: str, dev: torch.device, *args) -> None:
+    """Call the library on ``dev``'s current stream (the last argument of every entry point)."""
+    fn = getattr(_lib.load(), name)
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _lib.check(name, st)
+
+
+class KV4Cache:
+    """Keys and values of up to ``num_slots`` sequences in 4 bits, in shared pages.
+
+    pages uint8 [num_pages, Hkv, page_size * 72], page_table int32
+    [num_slots, max_pages], seqlens int32 [num_slots], refcount int32
+    [num_pages], k_scale and v_scale float32 [Hkv] (finite, positive: a value
+    is code * e4m3 scale * its head's factor).  The cache keeps these tensors
+    and works on them in place; ``empty`` makes the tensors of a new one.
+    """
+
+    def __init__(self, pages, page_table, seqlens, refcount, k_scale, v_scale):
+        dev = pages.device if isinstance(pages, torch.Tensor) else None
+        _check("pages", pages, torch.uint8, (None, None, None), dev)
+        num_pages, heads, page_bytes = (int(x) for x in pages.shape)
+        if page_bytes % (BLOCK_TOKENS * TOKEN_BYTES) != 0:
+            raise ValueError(f"pages holds {page_bytes} bytes per page and head, expected a multiple of "
+                             f"{BLOCK_TOKENS * TOKEN_BYTES}")
+        _check("page_table", page_table, torch.int32, (None, None), dev)
+        _check("seqlens", seqlens, torch.int32, (page_table.shape[0],), dev)
+        _check("refcount", refcount, torch.int32, (num_pages,), dev)
+        _check("k_scale", k_scale, torch.float32, (heads,), dev)
+        _check("v_scale", v_scale, torch.float32, (heads,), dev)
+        _on_gpu("pages", pages)
+        self.pages, self.page_table, self.seqlens, self.refcount = pages, page_table, seqlens, refcount
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.device = pages.device
+        self.num_pages, self.num_heads_kv = num_pages, heads
+        self.page_size = page_bytes // TOKEN_BYTES
+        self.num_slots, self.max_pages = (int(x) for x in page_table.shape)
+        self._struct = _lib.Kv4Cache(
+            pages=_ptr(pages), page_table=_ptr(page_table), seqlens=_ptr(seqlens), refcount=_ptr(refcount),
+            k_scale=_ptr(k_scale), v_scale=_ptr(v_scale), num_pages=num_pages, page_size=self.page_size,
+            num_heads_kv=heads, num_slots=self.num_slots, max_pages=self.max_pages)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, num_pages: int, num_slots: int, max_pages: int, num_heads_kv: int, *, page_size: int = 64,
+              k_scale=None, v_scale=None, device="cuda") -> "KV4Cache":
+        """A cache whose slots are empty and whose pages are free (factors 1 unless given)."""
+        if page_size not in (16, 32, 64, 128, 256):
+            raise ValueError(f"page_size must be 16, 32, 64, 128 or 256, not {page_size}")
+        one = lambda s: torch.ones(num_heads_kv, dtype=torch.float32, device=device) if s is None else s  # noqa: E731
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.zeros((num_pages, num_heads_kv, page_size * TOKEN_BYTES), dtype=torch.uint8, device=device),
+                   torch.full((num_slots, max_pages), -1, **i32), torch.zeros(num_slots, **i32),
+                   torch.zeros(num_pages, **i32), one(k_scale), one(v_scale))
+
+
+def _list(name: str, t, n: Optional[int], dev) -> None:
+    _check(name, t, torch.int32, (n,), dev)
+
+
+def _done(cache: KV4Cache, n: int, done):
+    if done is None:
+        return torch.empty(n, dtype=torch.int32, device=cache.device)
+    _list("done", done, n, cache.device)
+    return done
+
+
+def kv4_reserve(cache: KV4Cache, slots, new_tokens, *, done=None):
+    """Slot slots[i] grows by new_tokens[i] tokens (int32 [n], on the device); returns done int32 [n].
+
+    A request that finds no room gets done = 0 and stays as it was, and so
+    does every later one that needs a page.
+    """
+    _list("slots", slots, None, cache.device)
+    n = slots.shape[0]
+    _list("new_tokens", new_tokens, n, cache.device)
+    done = _done(cache, n, done)
+    _call("sinkattn_kv4_reserve", cache.device, cache._ref, _ptr(slots), _ptr(new_tokens), n, _ptr(done))
+    return done
+
+
+def kv4_fork(cache: KV4Cache, src, dst, *, done=None):
+    """The empty slots dst[i] become copies of src[i], sharing its full pages; returns done int32 [n]."""
+    _list("src", src, None, cache.device)
+    n = src.shape[0]
+    _list("dst", dst, n, cache.device)
+    done = _done(cache, n, done)
+    _call("sinkattn_kv4_fork", cache.device, cache._ref, _ptr(src), _ptr(dst), n, _ptr(done))
+    return done
+
+
+def kv4_free(cache: KV4Cache, slots) -> None:
+    """Empties the slots; pages that no other slot holds become free."""
+    _list("slots", slots, None, cache.device)
+    _call("sinkattn_kv4_free", cache.device, cache._ref, _ptr(slots), slots.shape[0])
+
+
+def kv4_compact(cache: KV4Cache, to: KV4Cache, *, count=None, workspace=None):
+    """Moves the pages in use to the front of another cache's pool; returns their number, int32 [1].
+
+    ``to`` has the same page size, heads, slots and table width and memory of
+    its own; if it is too small it is left as it was (compare the count).
+    """
+    dev = cache.device
+    if to.device != dev:
+        raise ValueError(f"to is on {to.device}, expected {dev}")
+    if count is None:
+        count = torch.empty(1, dtype=torch.int32, device=dev)
+    _list("count", count, 1, dev)
+    if workspace is None:
+        size = int(_lib.load().sinkattn_kv4_compact_workspace_size(cache._ref))
+        workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
+    _check("workspace", workspace, torch.uint8, (None,), dev)
+    _call("sinkattn_kv4_compact", dev, cache._ref, to._ref, _ptr(count), _ptr(workspace), workspace.numel())
+    return count
+
+
+def kv4_append(cache: KV4Cache, slots, k, v, *, cu_new=None) -> None:
+    """Writes k and v (bf16 [T, Hkv, 64]) as the last positions of the slots, in 4 bits.
+
+    Slot slots[b] takes rows cu_new[b] .. cu_new[b + 1] - 1 (int32
+    [len(slots) + 1], on the device), or T / len(slots) rows each without
+    cu_new; its length counts them already (kv4_reserve).  No slot is named
+    twice in a call.
+    """
+    dev = cache.device
+    _list("slots", slots, None, dev)
+    _check("k", k, torch.bfloat16, (None, cache.num_heads_kv, HEAD_DIM), dev)
+    _check("v", v, torch.bfloat16, tuple(k.shape), dev)
+    n = slots.shape[0]
+    if cu_new is not None:
+        _list("cu_new", cu_new, n + 1, dev)
+    _call("sinkattn_kv4_append", dev, cache._ref, _ptr(slots), n, _ptr(cu_new), k.shape[0], _ptr(k), _ptr(v))
+
+
+def kv4_read(cache: KV4Cache, slots, total: int, *, cu=None, k=None, v=None):
+    """The last rows of the slots as bf16: returns (k, v) [total, Hkv, 64].
+
+    Slot slots[b] gives rows cu[b] .. cu[b + 1] - 1 (or total / len(slots)
+    each): with cu the offsets of whole lengths, the sequences as sinkattn_fwd
+    takes them.  Rows before a sequence's begin are zero; rows behind cu[-1]
+    are not written.
+    """
+    dev = cache.device
+    _list("slots", slots, None, dev)
+    n = slots.shape[0]
+    shape = (int(total), cache.num_heads_kv, HEAD_DIM)
+    if cu is not None:
+        _list("cu", cu, n + 1, dev)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
+    _check("k", k, torch.bfloat16, shape, dev)
+    _check("v", v, torch.bfloat16, shape, dev)
+    _call("sinkattn_kv4_read", dev, cache._ref, _ptr(slots), n, _ptr(cu), shape[0], _ptr(k), _ptr(v))
+    return k, v
+
+
+def kv4_decode_workspace(cache: KV4Cache, q) -> torch.Tensor:
+    """A zero-filled workspace for kv4_decode_fwd with queries shaped like q."""
+    size = int(_lib.load().sinkattn_kv4_decode_workspace_size(int(q.shape[0]), int(q.shape[1])))
+    if size == 0:
+        raise ValueError(f"kv4_decode_workspace: no workspace for queries of shape {list(q.shape)}")
+    return torch.zeros(size, dtype=torch.uint8, device=cache.device)
+
+
+def kv4_decode_fwd(cache: KV4Cache, slots, q, sink, *, q_per_seq: int, window: int = WINDOW_INF, prefix: int = 0,
+                   scale: Optional[float] = None, o=None, lse=None, workspace=None):
+    """Decode forward over the cache: returns (o, lse) for the last q_per_seq positions of each slot.
+
+    q, o [len(slots) * q_per_seq, Hq, 64] bf16, sink [Hq] fp32, lse [Hq, rows]
+    fp32; mask, sink and lse as in sinkattn_decode_fwd.  The new positions'
+    keys and values are in the cache already.  Rows of idle slots and rows
+    before a sequence's begin get o = 0 and lse = -inf.  A workspace
+    (kv4_decode_workspace) can be kept for calls that follow one another, of any
+    shape it is large enough for; without one a zero-filled one is made per
+    call.
+    """
+    dev = cache.device
+    if q is None or q.dim() != 3:
+        raise ValueError("q must be a 3-D tensor [rows, heads, head_dim]")
+    if q.shape[2] != HEAD_DIM:
+        raise ValueError(f"head_dim must be {HEAD_DIM} (q: {q.shape[2]})")
+    hq = q.shape[1]
+    if hq % cache.num_heads_kv != 0 or hq == 0:
+        raise ValueError(f"query heads ({hq}) must be a multiple of key/value heads ({cache.num_heads_kv})")
+    _list("slots", slots, None, dev)
+    n = slots.shape[0]
+    rows = n * int(q_per_seq)
+    _check("q", q, torch.bfloat16, (rows, hq, HEAD_DIM), dev)
+    _check("sink", sink, torch.float32, (hq,), dev)
+    o = torch.empty_like(q) if o is None else o
+    lse = torch.empty((hq, rows), dtype=torch.float32, device=dev) if lse is None else lse
+    _check("o", o, torch.bfloat16, tuple(q.shape), dev)
+    _check("lse", lse, torch.float32, (hq, rows), dev)
+    if workspace is None:
+        workspace = kv4_decode_workspace(cache, q)
+    _check("workspace", workspace, torch.uint8, (None,), dev)
+    _call("sinkattn_kv4_decode_fwd", dev, cache._ref, _ptr(slots), n, int(q_per_seq), hq, int(window), int(prefix),
+          1.0 / math.sqrt(HEAD_DIM) if scale is None else float(scale), _ptr(q), _ptr(sink), _ptr(o), _ptr(lse),
+          _ptr(workspace), workspace.numel())
+    return o, lse
+
+
+def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, logp=None,
+                  logq=None):
+    """Samples one token per row: returns (tokens int32 [B], logp fp32 [B], logq fp32 [B]).
+
+    logits [B, V] fp32, bf16 or fp16, rows contiguous (any row stride); u fp32
+    [B] random numbers in [0, 1); temperature, top_p, min_p fp32 [B] and top_k
+    int32 [B] (default 1, off, off and off).  logp is the token's
+    log-probability at the temperature over the whole vocabulary (grpo_loss's
+    logp_old), logq the one among the kept tokens.  temperature 0 takes the
+    largest logit (the lowest index of equal ones).  A row without an allowed
+    token gives -1 and -inf, an invalid row -1 and NaN.
+    """
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D tensor [rows, vocab]")
+    if logits.dtype not in _LOGIT_TYPES:
+        raise TypeError(f"logits has dtype {logits.dtype}, expected float32, bfloat16 or float16")
+    B, V = (int(x) for x in logits.shape)
+    if (V > 1 and logits.stride(1) != 1) or (B > 1 and logits.stride(0) < V):
+        raise ValueError("logits must have contiguous rows that do not overlap")
+    dev = logits.device
+    _check("u", u, torch.float32, (B,), dev)
+    f32 = lambda x: torch.full((B,), x, dtype=torch.float32, device=dev)  # noqa: E731
+    temperature = f32(1.0) if temperature is None else temperature
+    top_p = f32(1.0) if top_p is None else top_p
+    min_p = f32(0.0) if min_p is None else min_p
+    top_k = torch.zeros(B, dtype=torch.int32, device=dev) if top_k is None else top_k
+    _check("temperature", temperature, torch.float32, (B,), dev)
+    _check("top_k", top_k, torch.int32, (B,), dev)
+    _check("top_p", top_p, torch.float32, (B,), dev)
+    _check("min_p", min_p, torch.float32, (B,), dev)
+    tokens = torch.empty(B, dtype=torch.int32, device=dev) if tokens is None else tokens
+    logp = torch.empty(B, dtype=torch.float32, device=dev) if logp is None else logp
+    logq = torch.empty(B, dtype=torch.float32, device=dev) if logq is None else logq
+    _check("tokens", tokens, torch.int32, (B,), dev)
+    _check("logp", logp, torch.float32, (B,), dev)
+    _check("logq", logq, torch.float32, (B,), dev)
+    _on_gpu("logits", logits)
+    _call("sinkattn_sample_tokens", dev, _ptr(logits), _LOGIT_TYPES[logits.dtype], B, V,
+          logits.stride(0) if B > 1 else V, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+          _ptr(tokens), _ptr(logp), _ptr(logq))
+    return tokens, logp, logq

@@ -1,0 +1,174 @@
+"""Token sampling: CUDA path vs the float64 oracle (needs a GB300).
+
+A token is decided where u times the kept mass lies among the cumulated
+masses.  The kernel's exponentials are off by a few 2^-22 each (the exponent
+is rounded to 2^-24 of its value, up to about 20 where mass still counts, and
+the hardware exponential adds 2^-22), so a cumulated mass is off by well under
+TOL = 2^-18 of the whole: the token given must own a stretch of the cumulated
+mass that lies within TOL of u's place, and where no border is that near it is
+the oracle's.  The logarithms are held to the same bound (plus their own
+rounding, 2^-23 of their value).  A cut of top-p or min-p nearer than rounding
+to a border may fall on either side of one token; the cases' seeds have none
+that shows.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.rollout_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+TOL = 2.0 ** -18
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from sink_aware_masked_gb300 import build
+
+    build.build()
+
+
+def run(x, u, t, k, p, m):
+    import sink_aware_masked_gb300 as sa
+
+    f = lambda a: torch.tensor(np.asarray(a), dtype=torch.float32, device=DEV)  # noqa: E731
+    out = sa.sample_tokens(x, f(u), temperature=f(t), top_k=torch.tensor(np.asarray(k), dtype=torch.int32, device=DEV),
+                           top_p=f(p), min_p=f(m))
+    return [a.cpu().numpy() for a in out]
+
+
+def check(x, u, t, k, p, m):
+    """Every row against the oracle."""
+    got = run(x, u, t, k, p, m)
+    xs = x.double().cpu().numpy()
+    r32 = lambda a: np.asarray(a, dtype=np.float32).astype(np.float64)  # noqa: E731
+    u, t, p, m = r32(u), r32(t), r32(p), r32(m)
+    for r in range(x.shape[0]):
+        row = xs[r], u[r], t[r], int(k[r]), p[r], m[r]
+        token = int(got[0][r])
+        bad = ref.sample_invalid(*row)
+        if bad is not None:
+            assert token == -1 and all(np.array_equal(a[r], np.float32(bad), equal_nan=True) for a in got[1:])
+            continue
+        z, total, kept, cum, at = ref.kept_tokens(*row)
+        i = int(np.searchsorted(kept, token))
+        assert i < len(kept) and kept[i] == token, (r, token, "is not kept")
+        lo, hi = (cum[i - 1] if i else 0.0) / cum[-1], cum[i] / cum[-1]
+        assert lo - TOL <= at / cum[-1] <= hi + TOL, (r, token, lo, at / cum[-1], hi)
+        if len(kept) == 1 or np.abs(cum[:-1] - at).min() > TOL * cum[-1]:
+            assert token == ref.sample(*row)[0], r
+        for a, b in ((got[1][r], z[token] - np.log(total)), (got[2][r], z[token] - np.log(cum[-1]))):
+            assert abs(a - b) <= TOL + 2.0 ** -23 * abs(b), (r, a, b)
+
+
+SIZES = [(1, 1), (3, 2), (2, 7), (5, 33), (4, 500), (2, 4096), (3, 4099), (2, 8193), (2, 32768), (2, 50257), (1, 201088),
+         (1, 262144)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("rows,vocab", SIZES)
+def test_parity(rows, vocab, dtype):
+    rng = np.random.RandomState(vocab % 1000 + rows)
+    combos = [(1.0, 0, 1.0, 0.0), (0.7, 50, 1.0, 0.0), (1.3, 0, 0.9, 0.0), (1.0, 0, 1.0, 0.1), (0.9, 300, 0.8, 0.01),
+              (0.0, 0, 1.0, 0.0), (1.0, 1, 0.5, 0.0), (1.0, 5000, 0.999, 0.0), (1.0, 0, 0.05, 0.0), (2.0, 7, 0.0, 0.0)]
+    # a row stride that leaves rows at any alignment, and junk behind the row's end
+    pad = 5
+    x = torch.from_numpy(rng.randn(rows * len(combos), vocab + pad) * 3).to(dtype).to(DEV)
+    x[:, vocab:] = 1e4
+    t, k, p, m = (np.array([c[i] for c in combos] * rows) for i in range(4))
+    check(x[:, :vocab], rng.rand(rows * len(combos)), t, k, p, m)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_ties_go_to_the_lowest_index(dtype):
+    """Rows of few values: the cuts of top-k and top-p lie among equal logits, thousands of them."""
+    rng = np.random.RandomState(3)
+    V = 20011
+    x = torch.from_numpy(rng.randint(0, 3, (12, V)) * 0.5).to(dtype).to(DEV)
+    x[0] = 1.25   # all equal
+    x[1] = 0.0
+    x[1, ::2] = -0.0  # one value
+    k = [700, 12345, 0, 5, 20010, 0, 0, 9000, 1, 0, 3000, 0]
+    p = [1.0, 1.0, 0.123, 1.0, 1.0, 0.9, 0.5, 0.3, 1.0, 0.7, 0.99, 0.0]
+    check(x, rng.rand(12), np.ones(12), k, p, np.zeros(12))
+
+
+def test_masked_rows_and_what_is_not_valid():
+    x = torch.randn((14, 3000), device=DEV)
+    x[0] = float("-inf")                    # nothing allowed
+    x[1] = float("-inf")
+    x[1, 2777] = -50.0                      # one allowed
+    x[2, 5] = float("nan")
+    x[3, 2999] = float("inf")
+    x[4] = float("nan")
+    x[5, :2990] = float("-inf")             # ten allowed, top-k of 100
+    x[6, 1:] = torch.finfo(torch.float32).min
+    x[13, 3] = -float("nan")
+    t = [1.0] * 14
+    t[7], t[8], t[9] = -1.0, float("inf"), float("nan")
+    p = [1.0] * 14
+    p[10] = float("nan")
+    m = [0.0] * 14
+    m[11] = float("nan")
+    u = [0.5] * 14
+    u[12] = float("nan")
+    tok, logp, logq = run(x, u, t, [100] * 14, p, m)
+    assert tok[0] == -1 and np.isneginf(logp[0]) and np.isneginf(logq[0])
+    assert tok[1] == 2777 and abs(logp[1]) < 1e-6 and abs(logq[1]) < 1e-6
+    assert tok[5] >= 2990 and tok[6] == 0 and logp[6] == 0
+    for r in (2, 3, 4, 7, 8, 9, 10, 11, 12, 13):
+        assert tok[r] == -1 and np.isnan(logp[r]) and np.isnan(logq[r]), r
+    check(x, u, t, [100] * 14, p, m)
+
+
+def test_ends_of_u_and_of_the_parameters():
+    x = torch.tensor([[0.0, 1.0, 2.0, -1.0, float("-inf")]], device=DEV).repeat(8, 1)
+    tok, logp, logq = run(x, [0, 1 - 2.0 ** -24, -3, 7, 0.5, 0.5, 0.5, 0.5], [1, 1, 1, 1, 1e-30, 1e30, 1, 1],
+                          [0, 0, 0, 0, 0, 0, -5, 10 ** 9], [1] * 7 + [2], [0, 0, 0, 0, 0, 0, 1.0, 9.0])
+    assert tok.tolist() == [0, 3, 0, 3, 2, 2, 2, 2]
+    assert abs(logp[5] - np.log(0.25)) < 1e-6 and logp[4] == 0 and logq[6] == 0 and logq[7] == 0
+
+
+def test_rows_stand_alone_and_repeat_bit_by_bit():
+    rng = np.random.RandomState(5)
+    x = torch.from_numpy(rng.randn(300, 10007) * 3).float().to(DEV)
+    u, t, k, p, m = rng.rand(300), rng.uniform(0, 2, 300), rng.randint(0, 400, 300), rng.uniform(0.2, 1.2, 300), np.zeros(300)
+    a = run(x, u, t, k, p, m)
+    b = run(x, u, t, k, p, m)
+    assert all(np.array_equal(i, j) for i, j in zip(a, b))
+    for r in (0, 17, 299):
+        one = run(x[r:r + 1], u[r:r + 1], t[r:r + 1], k[r:r + 1], p[r:r + 1], m[r:r + 1])
+        assert all(i[0] == j[r] for i, j in zip(one, a))
+    check(x[:40], u[:40], t[:40], k[:40], p[:40], m[:40])
+
+
+def test_frequencies():
+    """Many u over one row: each token's share is its probability (the u are a grid, so within two grid steps)."""
+    probs = np.array([0.5, 0.25, 0.125, 0.125])
+    n = 4096
+    x = torch.from_numpy(np.log(probs)).float().to(DEV)[None].repeat(n, 1)
+    tok, _, _ = run(x, (np.arange(n) + 0.5) / n, np.ones(n), np.zeros(n), np.ones(n), np.zeros(n))
+    assert np.abs(np.bincount(tok, minlength=4) / n - probs).max() <= 2 / n
+
+
+def test_captured_and_replayed():
+    import sink_aware_masked_gb300 as sa
+
+    x, u = torch.zeros((4, 5000), device=DEV), torch.zeros(4, device=DEV)
+    kw = dict(temperature=torch.full((4,), 0.8, device=DEV), top_k=torch.full((4,), 40, dtype=torch.int32, device=DEV),
+              top_p=torch.full((4,), 0.9, device=DEV), min_p=torch.zeros(4, device=DEV))
+    outs = [torch.zeros(4, dtype=torch.int32, device=DEV), torch.zeros(4, device=DEV), torch.zeros(4, device=DEV)]
+    names = dict(zip(("tokens", "logp", "logq"), outs))
+    sa.sample_tokens(x, u, **kw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sa.sample_tokens(x, u, **kw, **names)
+    for seed in range(5):
+        torch.manual_seed(seed)
+        x.copy_(torch.randn(4, 5000) * 2)
+        u.copy_(torch.rand(4))
+        graph.replay()
+        want = sa.sample_tokens(x, u, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
