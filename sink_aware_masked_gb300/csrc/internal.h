@@ -67,6 +67,10 @@ constexpr int kPreTokens = 8;
 // workspace sizes they imply are the same with or without a GPU.
 int device_sms();
 
+// Device address of the library's status word on the current device (looked
+// up once per device), or nullptr.
+int* device_status_word();
+
 inline int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
 
 // One backward work item: key tile `kt` of sequence `b`, query chunk `chunk`
@@ -175,7 +179,7 @@ struct Kv4DecodeArgs {
   float scale;
 };
 size_t kv4_decode_workspace_bytes(long long rows, int hq);
-cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, cudaStream_t s);
+cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, int* status, cudaStream_t s);
 
 // Token sampling (sample.cu).
 struct SampleArgs {

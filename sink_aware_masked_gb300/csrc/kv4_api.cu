@@ -22,6 +22,8 @@ sinkattn_status check_cache(const sinkattn_kv4_cache* c, sa::Kv4Cache& out) {
     return SINKATTN_ERR_UNSUPPORTED;
   if (c->num_heads_kv > sa::kMaxHeadsQ) return SINKATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(c->max_pages) * c->page_size > (1LL << 30)) return SINKATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(c->num_pages) * c->num_heads_kv * (c->page_size / 16) > 0xffffffffLL)
+    return SINKATTN_ERR_UNSUPPORTED;  // blocks are numbered in 32 bits (2^32 of them are 4.9 TB)
   if (!c->pages || !c->page_table || !c->seqlens || !c->refcount || !c->k_scale || !c->v_scale)
     return SINKATTN_ERR_INVALID_ARG;
   if (!aligned16(c->pages) || !aligned16(c->page_table) || !aligned16(c->seqlens) || !aligned16(c->refcount) ||
@@ -174,7 +176,9 @@ sinkattn_status sinkattn_kv4_decode_fwd(const sinkattn_kv4_cache* cache, const i
   const int w = window < 0 || window >= (1LL << 30) ? -1 : static_cast<int>(window);
   const int p = static_cast<int>(std::min<int64_t>(prefix, 1LL << 30));
   const sa::Kv4DecodeArgs a{slots, q, sink, o, lse, workspace, num_seqs, q_per_seq, num_heads_q, w, p, scale};
-  return from_cuda(sa::launch_kv4_decode(c, a, static_cast<cudaStream_t>(stream)));
+  int* status = sa::device_status_word();
+  if (status == nullptr) return SINKATTN_ERR_CUDA;
+  return from_cuda(sa::launch_kv4_decode(c, a, status, static_cast<cudaStream_t>(stream)));
 }
 
 sinkattn_status sinkattn_sample_tokens(const void* logits, int32_t dtype, int32_t rows, int32_t vocab,

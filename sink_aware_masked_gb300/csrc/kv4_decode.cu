@@ -16,30 +16,39 @@
 // by a power of two per row (its 8 bits fit); P is rounded to f16 (2^-11);
 // S, O and the statistics are fp32.
 //
-// The softmax keeps a reference exponent m per row that need not be the
+// The softmax keeps a reference score m per row that need not be the
 // maximum: it moves (and O and l are rescaled) only when a score exceeds it
-// by 2^8, which keeps P below f16's range and leaves one compare and one vote
+// by a factor of 2^8, which keeps P below f16's range and leaves one compare and one vote
 // per block in the ordinary case.
 //
 // Work: the visible blocks of all (sequence, kv head, row group) pairs in one
-// line, cut into equal shares, one per CTA; a share's blocks of one pair are
-// taken by the CTA's warps in turn and merged in shared memory.  A pair cut
-// between CTAs leaves partial results in the workspace, and the last CTA of
-// the pair to arrive merges them in CTA order.
+// line, cut into equal shares, one per worker.  A worker is a CTA, whose warps
+// take a pair's blocks in turn and merge in shared memory; or, where there are
+// many pairs with few blocks each, a single warp, which takes whole pairs and
+// merges nothing.  A pair cut between CTAs leaves partial results in the
+// workspace, and the last CTA of the pair to arrive merges them in order.
 #include "kv4.cuh"
+#include "tc.cuh"
 
+#ifndef KV4_W1
+#define KV4_W1 4
+#define KV4_C1 3
+#define KV4_T 4
+#define KV4_ST 2
+#endif
 namespace sa {
 namespace {
 
 using namespace kv4;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kRowPad = 68;       // floats per row in shared memory
 constexpr float kSlack = 8.f;     // log2 units a score may exceed its row's reference
-// Partial rows that the CTAs of one SM can leave: two pairs cut per CTA, and
-// CTAs x rows per SM is 2 x 8, 1 x 16 or 1 x 32 by variant.
+// Partial rows that the CTAs of one SM can leave, two pairs cut each: at most
+// 4 CTAs of 8 rows, 2 of 16 or 1 of 32.
 constexpr int kPartRowsPerSm = 64;
+
+// Blocks of the longest pair up to which warps work alone, each on whole pairs.
+constexpr int kAloneBlocks = 48;
 
 struct DecK {
   Kv4Cache c;
@@ -48,8 +57,9 @@ struct DecK {
   const float* sink;
   __nv_bfloat16* o;
   float* lse;
-  float* part;    // [2 * grid][rows][64 + 2]
+  float* part;    // [2 * workers][rows][64 + 2]
   int* counters;  // [pairs]
+  int* status;    // the library's status word (bounded waits)
   int num_seqs, n, hq, group, rows, row_groups, window, prefix;
   float scale;
 };
@@ -59,6 +69,14 @@ SA_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with nothing to add to.
+SA_DEV void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // 8x8 f16 transpose across the warp.
@@ -86,13 +104,13 @@ struct Span {
   SA_DEV int block(int i) const { return i < pre ? i : i - pre + lo; }
 };
 
-SA_DEV Span visible_span(const DecK& p, int b) {
+SA_DEV Span visible_span(const DecK& p, int len) {
   Span s;
-  s.len = slot_len(p.c, p.slots[b]);
-  s.end = (s.len >> 4) + ((s.len & 15) != 0);
-  const int first = max(s.len - p.n, 0);  // the earliest of the positions
+  s.len = len;
+  s.end = (len >> 4) + ((len & 15) != 0);
+  const int first = max(len - p.n, 0);  // the earliest of the positions
   s.lo = p.window < 0 ? 0 : max(first - p.window, 0) >> 4;
-  const int pre = min(p.prefix, s.len);
+  const int pre = min(p.prefix, len);
   s.pre = min((pre >> 4) + ((pre & 15) != 0), s.lo);
   return s;
 }
@@ -102,17 +120,18 @@ struct Tile {  // one block's bytes as this lane needs them
   uint32_t ks, vs;
 };
 
-SA_DEV void load_tile(const Kv4Cache& c, int page, int head, int blk, Tile& t) {
-  const uint8_t* b = block_ptr(c, max(page, 0), head, blk);
+// A warp's ring in shared memory: a turn is four blocks.
+constexpr int kTurnBlocks = KV4_T;
+constexpr int kTurnBytes = kTurnBlocks * kBlockBytes;
+constexpr int kStages = KV4_ST;
+constexpr int kBatchTurns = 32 / kTurnBlocks;
+
+SA_DEV void read_tile(const uint8_t* stage, Tile& t) {
   const int lane = threadIdx.x & 31;
-  t.k = __ldg(reinterpret_cast<const uint4*>(b) + lane);
-  t.v = __ldg(reinterpret_cast<const uint4*>(b + kVCodes) + lane);
-  t.ks = __ldg(reinterpret_cast<const uint16_t*>(b + kKScales) + lane);
-  t.vs = __ldg(reinterpret_cast<const uint32_t*>(b + kVScales) + 4 * (lane >> 3) + (lane & 3));
-  if (page < 0) {  // a missing page reads as NaN
-    t.ks = kNaNScale * 0x0101u;
-    t.vs = kNaNScale * 0x01010101u;
-  }
+  t.k = *reinterpret_cast<const uint4*>(stage + 16 * lane);
+  t.v = *reinterpret_cast<const uint4*>(stage + kVCodes + 16 * lane);
+  t.ks = *reinterpret_cast<const uint16_t*>(stage + kKScales + 2 * lane);
+  t.vs = *reinterpret_cast<const uint32_t*>(stage + kVScales + 4 * (4 * (lane >> 3) + (lane & 3)));
 }
 
 // What a warp keeps of its rows.  Row 8 nt + 2 t + e of the tile is lane t's
@@ -122,8 +141,8 @@ template <int NT>
 struct Rows {
   float o[NT][4][4];     // O^T: [dim pair 8 g + 2 i, + 1][row e]: c0 c1 dim 8g+2i, c2 c3 dim 8g+2i+1
   float sum[NT][2];
-  float ref[NT][2];      // reference exponent, 0 while the row has seen no key
-  float limit[NT][2];    // ref + kSlack, -inf while the row has seen no key
+  float ref[NT][2];      // reference score (before the coefficient), 0 while the row has seen no key
+  float limit[NT][2];    // score beyond which ref moves, -inf while the row has seen no key
 };
 
 template <int NT>
@@ -143,67 +162,80 @@ SA_DEV void rows_clear(Rows<NT>& r) {
   }
 }
 
+template <int U>
 struct MaskArgs {
-  int key0;  // position of the block's first key
+  int key0[U];      // positions of the blocks' first keys; kVoid for a block that is not there
+  bool missing[U];  // its page is not in the pool: it reads as NaN
   int window, prefix;
+  SA_DEV bool sees(int at, int key) const {
+    return key <= at && (window < 0 || key >= at - window || key < prefix);
+  }
 };
+constexpr int kVoid = 0x7fffff00;  // beyond every position
 
-// One block of 16 keys.  kMasked: some (row, key) of it is not visible.
+// U blocks of 16 keys.  kMasked: some (row, key) of them is not visible, or a page is missing.
 // pos[nt][e]: the rows' positions (-1 for rows that are not there).
-template <int NT, bool kMasked>
-SA_DEV void block_step(Rows<NT>& r, const Tile& tile, const uint32_t (&qf)[NT][4][2], const float (&coef)[NT][2],
-                       const int (&pos)[NT][2], const MaskArgs& mk) {
-  const int g = lane_g(), t = lane_t();
-  float s[NT][4];
+template <int NT, int U, bool kMasked>
+SA_DEV void block_step(Rows<NT>& r, const Tile (&tile)[U], const uint32_t (&qf)[NT][4][2], const float (&coef)[NT][2],
+                       const int (&pos)[NT][2], const MaskArgs<U>& mk) {
+  const int g = lane_g();
+  // scores before their row's coefficient: s[u][nt][e] key g of block u, s[u][nt][2 + e] key g + 8, row e
+  float s[U][NT][4];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-  {
-    const uint32_t two = e4m3x2(tile.ks);
+  for (int u = 0; u < U; ++u) {
+    uint32_t ks = tile[u].ks;
+    if (kMasked && mk.missing[u]) ks = kNaNScale * 0x0101u;
+    const uint32_t two = e4m3x2(ks);
     const uint32_t sa = __byte_perm(two, 0, 0x1010), sb = __byte_perm(two, 0, 0x3232);
     uint32_t x[4], y[4], z[4], w[4];
-    e2m1x8(tile.k.x, x);
-    e2m1x8(tile.k.z, z);
-    e2m1x8(tile.k.y, y);
-    e2m1x8(tile.k.w, w);
+    e2m1x8(tile[u].k.x, x);
+    e2m1x8(tile[u].k.z, z);
+    e2m1x8(tile[u].k.y, y);
+    e2m1x8(tile[u].k.w, w);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t a0 = hmul2(x[j], sa), a1 = hmul2(z[j], sb), a2 = hmul2(y[j], sa), a3 = hmul2(w[j], sb);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], a0, a1, a2, a3, qf[nt][j][0], qf[nt][j][1]);
+      for (int nt = 0; nt < NT; ++nt) {
+        if (j == 0)
+          mma_f16_first(s[u][nt], a0, a1, a2, a3, qf[nt][j][0], qf[nt][j][1]);
+        else
+          mma_f16(s[u][nt], a0, a1, a2, a3, qf[nt][j][0], qf[nt][j][1]);
+      }
     }
   }
-  // scores in log2 units: s[nt][e] key g, s[nt][2 + e] key g + 8, row e
   bool move = false;
+  float top[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      s[nt][e] *= coef[nt][e];
-      s[nt][2 + e] *= coef[nt][e];
-      if (kMasked) {
-        const int at = pos[nt][e], lo = mk.window < 0 ? 0 : at - mk.window;
-        const int k0 = mk.key0 + g, k1 = k0 + 8;
-        if (!(k0 <= at && (k0 >= lo || k0 < mk.prefix))) s[nt][e] = -INFINITY;
-        if (!(k1 <= at && (k1 >= lo || k1 < mk.prefix))) s[nt][2 + e] = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (kMasked) {
+          if (!mk.sees(pos[nt][e], mk.key0[u] + g)) s[u][nt][e] = -INFINITY;
+          if (!mk.sees(pos[nt][e], mk.key0[u] + g + 8)) s[u][nt][2 + e] = -INFINITY;
+        }
       }
-      move |= fmaxf(s[nt][e], s[nt][2 + e]) > r.limit[nt][e];
+      top[nt][e] = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+      for (int u = 1; u < U; ++u) top[nt][e] = fmaxf(top[nt][e], fmaxf(s[u][nt][e], s[u][nt][2 + e]));
+      move |= top[nt][e] > r.limit[nt][e];
     }
   if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float m = fmaxf(s[nt][e], s[nt][2 + e]);
+        float m = top[nt][e];
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        // rows that have seen nothing hold zeros: their factor may be anything finite
         if (m > r.limit[nt][e]) {
-          const float f = r.limit[nt][e] == -INFINITY ? 0.f : ex2(r.ref[nt][e] - m);
+          // a row that has seen nothing holds zeros (or a NaN, which stays)
+          const float f = r.limit[nt][e] == -INFINITY ? 0.f : ex2((r.ref[nt][e] - m) * coef[nt][e]);
           r.ref[nt][e] = m;
-          r.limit[nt][e] = m + kSlack;
+          r.limit[nt][e] = m + __fdividef(kSlack, coef[nt][e]);
           r.sum[nt][e] *= f;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -213,95 +245,331 @@ SA_DEV void block_step(Rows<NT>& r, const Tile& tile, const uint32_t (&qf)[NT][4
         }
       }
   }
-  uint32_t pf[NT][2];
+  uint32_t pf[U][NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      s[nt][e] = ex2(s[nt][e] - r.ref[nt][e]);
-      s[nt][2 + e] = ex2(s[nt][2 + e] - r.ref[nt][e]);
-      r.sum[nt][e] += s[nt][e] + s[nt][2 + e];
-    }
-    pf[nt][0] = transpose8(pack_f16(s[nt][0], s[nt][1]));
-    pf[nt][1] = transpose8(pack_f16(s[nt][2], s[nt][3]));
-  }
-  uint32_t vs = tile.vs;
-  if (kMasked) {
-    // What a masked key holds must not reach a row that does not see it, and
-    // 0 * NaN would: NaN scales are taken out of the product, and the rows
-    // that do see such a key get a NaN in the dims it stands for.
-    const bool nan = any_nan_scale(vs);
-    if (__any_sync(0xffffffffu, nan)) {
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-      for (int key = 0; key < 16; ++key) {
-        const int i = (key & 1) + 2 * (key >> 3);
-        const uint32_t byte = __shfl_sync(0xffffffffu, vs, 4 * g + ((key & 7) >> 1)) >> (8 * i) & 0x7fu;
-        if (byte != kNaNScale) continue;
-        const int kp = mk.key0 + key;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int at = pos[nt][e];
-            if (kp <= at && (mk.window < 0 || kp >= at - mk.window || kp < mk.prefix)) {
-#pragma unroll
-              for (int d = 0; d < 4; ++d) r.o[nt][d][e] = r.o[nt][d][2 + e] = __int_as_float(0x7fffffff);
-            }
-          }
+      for (int e = 0; e < 2; ++e) {
+        // subtracted first: the largest of huge scores has to give exactly 2^0
+        s[u][nt][e] = ex2((s[u][nt][e] - r.ref[nt][e]) * coef[nt][e]);
+        s[u][nt][2 + e] = ex2((s[u][nt][2 + e] - r.ref[nt][e]) * coef[nt][e]);
+        r.sum[nt][e] += s[u][nt][e] + s[u][nt][2 + e];
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if ((vs >> (8 * i) & 0x7fu) == kNaNScale) vs &= ~(0xffu << (8 * i));
+      pf[u][nt][0] = transpose8(pack_f16(s[u][nt][0], s[u][nt][1]));
+      pf[u][nt][1] = transpose8(pack_f16(s[u][nt][2], s[u][nt][3]));
     }
   }
-  const uint32_t s01 = e4m3x2(vs), s23 = e4m3x2(vs >> 16);
-  uint32_t e01, o01, e23, o23, a[4], b[4], c[4], d[4];
-  pair_tokens(tile.v.x, tile.v.y, e01, o01);
-  pair_tokens(tile.v.z, tile.v.w, e23, o23);
-  e2m1x8(e01, a);
-  e2m1x8(o01, b);
-  e2m1x8(e23, c);
-  e2m1x8(o23, d);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a0 = hmul2(a[i], s01), a1 = hmul2(b[i], s01), a2 = hmul2(c[i], s23), a3 = hmul2(d[i], s23);
+  for (int u = 0; u < U; ++u) {
+    uint32_t vs = tile[u].vs;
+    if (kMasked) {
+      // What a masked key holds must not reach a row that does not see it, and
+      // 0 * NaN would: NaN scales are taken out of the product, and the rows
+      // that do see such a key get a NaN in the dims it stands for.
+      if (mk.missing[u]) vs = kNaNScale * 0x01010101u;
+      if (__any_sync(0xffffffffu, any_nan_scale(vs))) {
+#pragma unroll 1
+        for (int key = 0; key < 16; ++key) {
+          const int i = (key & 1) + 2 * (key >> 3);
+          const uint32_t byte = __shfl_sync(0xffffffffu, vs, 4 * g + ((key & 7) >> 1)) >> (8 * i) & 0x7fu;
+          if (byte != kNaNScale) continue;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) mma_f16(r.o[nt][i], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (mk.sees(pos[nt][e], mk.key0[u] + key)) {
+#pragma unroll
+                for (int d = 0; d < 4; ++d) r.o[nt][d][e] = r.o[nt][d][2 + e] = __int_as_float(0x7fffffff);
+              }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((vs >> (8 * i) & 0x7fu) == kNaNScale) vs &= ~(0xffu << (8 * i));
+      }
+    }
+    const uint32_t s01 = e4m3x2(vs), s23 = e4m3x2(vs >> 16);
+    uint32_t e01, o01, e23, o23, a[4], b[4], c[4], d[4];
+    pair_tokens(tile[u].v.x, tile[u].v.y, e01, o01);
+    pair_tokens(tile[u].v.z, tile[u].v.w, e23, o23);
+    e2m1x8(e01, a);
+    e2m1x8(o01, b);
+    e2m1x8(e23, c);
+    e2m1x8(o23, d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a0 = hmul2(a[i], s01), a1 = hmul2(b[i], s01), a2 = hmul2(c[i], s23), a3 = hmul2(d[i], s23);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_f16(r.o[nt][i], a0, a1, a2, a3, pf[u][nt][0], pf[u][nt][1]);
+    }
   }
 }
 
-// Writes one finished row pair of dims: o = alpha * acc / sum, lse.
-SA_DEV void finish_row(const DecK& p, int b, int head, int row, int d0, int nd, const float* acc, float sum, float ref,
-                       float factor) {
+// What a warp will do next: 32 of its blocks, one per lane.
+struct Batch {
+  const uint8_t* src;  // the lane's block
+  int key0;            // position of its first key
+  // bit per block, the same in all lanes; missing: its page is not in the pool; next: it follows the one before it
+  // in memory
+  uint32_t valid, masked, missing, next;
+};
+
+// The part of a pair that a worker takes: blocks [blk0, blk1) of `blocks`.
+struct Segment {
+  long long x;  // its place in the line that is shared out
+  int b, in_seq, blk0, blk1, blocks, slot, head, row0;
+  Span span;
+};
+
+// A warp's way through its blocks of a segment (turns part, part + parts,
+// ..., each the part of four aligned blocks that the segment has): page numbers are loaded two batches ahead; the blocks come through
+// the ring by bulk copies, one lane per block, two turns in flight.
+class Stream {
+ public:
+  SA_DEV Stream(const DecK& p, const uint8_t* ring, uint32_t bars, const tc::Abort& abort, int part, int parts)
+      : p_(p), ring_(ring), bars_(bars), abort_(abort), part_(part), parts_(parts) {}
+
+  // Starts a segment's first copies; none of an earlier one is in flight.
+  SA_DEV void begin(const Segment& s) {
+    seg_ = s;
+    const int all = (s.blk1 - 1) / kTurnBlocks - s.blk0 / kTurnBlocks + 1;
+    turns_ = s.span.len > 0 && all > part_ && !dead_ ? (all - part_ + parts_ - 1) / parts_ : 0;
+    if (turns_ == 0) return;
+    const int page0 = load_page(0);
+    page_ = turns_ > kBatchTurns ? load_page(32) : -1;
+    cur_ = to_batch(page0, 0);
+    __syncwarp();  // every lane is done with the ring
+    const int now = min(turns_, kStages);
+#pragma unroll
+    for (int d = 0; d < kStages; ++d)
+      if (d < now) fetch(cur_, d, used_ + d);
+  }
+
+  // Calls step(the turn's bytes, its batch, its first bit) for every turn.
+  template <class F>
+  SA_DEV void run(F step) {
+#pragma unroll 1
+    for (int turn = 0; turn < turns_; ++turn) {
+      const int in_batch = turn % kBatchTurns, stage = used_ % kStages;
+      if (in_batch == kBatchTurns / 2 && turns_ > turn + kBatchTurns / 2)
+        next_ = to_batch(page_, (turn + kBatchTurns / 2) * kTurnBlocks);
+      if (!tc::mbar_wait_warp(bars_ + 8 * stage, used_ / kStages & 1, abort_)) {
+        // Out of time, which the status word says: nothing more is started,
+        // and what is in flight has as long again to land.
+        dead_ = true;
+        const long long t0 = clock64();
+        for (int use = used_, last = used_ + min(kStages, turns_ - turn); use < last;)
+          if (tc::mbar_try_wait(bars_ + 8 * (use % kStages), use / kStages & 1) ||
+              clock64() - t0 > tc::kTimeoutCycles)
+            ++use;
+        break;
+      }
+      step(ring_ + stage * kTurnBytes, cur_, in_batch * kTurnBlocks);
+      __syncwarp();  // every lane is done with the stage
+      if (turn + kStages < turns_)
+        fetch(in_batch + kStages < kBatchTurns ? cur_ : next_, (in_batch + kStages) % kBatchTurns, used_ + kStages);
+      ++used_;
+      if (in_batch == kBatchTurns - 1) {
+        cur_ = next_;
+        if (turns_ > turn + 1 + kBatchTurns) page_ = load_page((turn + 1 + kBatchTurns) * kTurnBlocks);
+      }
+    }
+  }
+
+ private:
+  SA_DEV int place(int j0) const {  // the lane's block j0 + lane, as a number in the pair
+    const int j = j0 + (threadIdx.x & 31);
+    return (seg_.blk0 & ~(kTurnBlocks - 1)) + kTurnBlocks * part_ + parts_ * (j & ~(kTurnBlocks - 1)) +
+           (j & (kTurnBlocks - 1));
+  }
+  SA_DEV int load_page(int j0) const {
+    const int i = place(j0);
+    return i >= seg_.blk0 && i < seg_.blk1 ? page_of(p_.c, seg_.slot, seg_.span.block(i)) : -1;
+  }
+  SA_DEV Batch to_batch(int page, int j0) const {
+    Batch b;
+    b.src = p_.c.pages;
+    b.key0 = kVoid;
+    bool masked = true;
+    const int i = place(j0);
+    const bool valid = i >= seg_.blk0 && i < seg_.blk1, missing = valid && page < 0;
+    if (valid) {
+      const int blk = seg_.span.block(i);
+      if (!missing) b.src = block_ptr(p_.c, page, seg_.head, blk);
+      b.key0 = blk * kBlockTokens;
+      const int key1 = b.key0 + kBlockTokens - 1, len = seg_.span.len;
+      // seen by all rows: the earliest position causally, the last one's window
+      masked = missing || key1 > len - p_.n ||
+               !(p_.window < 0 || b.key0 >= len - 1 - p_.window || key1 < p_.prefix);
+    }
+    b.valid = __ballot_sync(0xffffffffu, valid);
+    b.masked = __ballot_sync(0xffffffffu, masked);
+    b.missing = __ballot_sync(0xffffffffu, missing);
+    const uint64_t at = reinterpret_cast<uint64_t>(b.src), before = __shfl_up_sync(0xffffffffu, at, 1);
+    b.next = __ballot_sync(0xffffffffu, before + kBlockBytes == at);
+    return b;
+  }
+  // Starts the copies of a batch's turn, the warp's use-th.
+  SA_DEV void fetch(const Batch& b, int in_batch, int use) {
+    const int lane = threadIdx.x & 31, stage = use % kStages;
+    constexpr uint32_t kAll = (1u << kTurnBlocks) - 1;
+    const int bit0 = in_batch * kTurnBlocks;
+    const uint32_t there = (b.valid & ~b.missing) >> bit0 & kAll;
+    const uint32_t bar = bars_ + 8 * stage, to = smem_u32(ring_) + stage * kTurnBytes;
+    if (there == kAll && (b.next >> bit0 & kAll & ~1u) == (kAll & ~1u)) {  // the ordinary case: one run in one page
+      if (lane == bit0) {
+        tc::mbar_expect_tx(bar, kTurnBytes);
+        tc::bulk_load(to, b.src, kTurnBytes, bar);
+      }
+      return;
+    }
+    if (lane == 0) tc::mbar_expect_tx(bar, __popc(there) * kBlockBytes);
+    __syncwarp();
+    const int mine = lane & (kTurnBlocks - 1);
+    if (lane / kTurnBlocks == in_batch && (there >> mine & 1u))
+      tc::bulk_load(to + mine * kBlockBytes, b.src, kBlockBytes, bar);
+  }
+
+  const DecK& p_;
+  const uint8_t* ring_;
+  uint32_t bars_;
+  tc::Abort abort_;
+  int part_, parts_, used_ = 0, turns_ = 0, page_ = -1;
+  bool dead_ = false;
+  Segment seg_;
+  Batch cur_, next_;
+};
+
+// A row's running softmax over some of its keys: kD of the accumulator's
+// dims.  ref is -inf where none of the keys was seen.
+template <int kD>
+struct Piece {
+  float acc[kD], sum, ref;
+};
+
+// Writes dims d0 .. d0 + kD - 1 of a finished row: o = alpha * acc / sum, and lse.
+template <int kD>
+SA_DEV void finish_row(const DecK& p, int b, int head, int row, int d0, const Piece<kD>& f, float sink, float factor) {
   const int i = row / p.group, h = head * p.group + row % p.group;
   const int64_t at = static_cast<int64_t>(b) * p.n + i;
-  const float lse = sum == 0.f ? -INFINITY : (ref + lg2(sum)) * kLn2;
-  const float w = sum == 0.f ? 0.f : factor / (sum * (1.f + __expf(p.sink[h] - lse)));
+  const float lse = f.sum == 0.f ? -INFINITY : (f.ref + lg2(f.sum)) * kLn2;
+  const float w = __fdividef(factor, f.sum * (1.f + __expf(sink - lse)));
   __nv_bfloat16* o = p.o + (at * p.hq + h) * kHeadDim + d0;
-  for (int e = 0; e < nd; e += 2)
-    *reinterpret_cast<uint32_t*>(o + e) = sum == 0.f ? 0u : pack_bf16(acc[e] * w, acc[e + 1] * w);
+  uint32_t v[kD / 2];
+#pragma unroll
+  for (int e = 0; e < kD / 2; ++e) v[e] = f.sum == 0.f ? 0u : pack_bf16(f.acc[2 * e] * w, f.acc[2 * e + 1] * w);
+  if constexpr (kD == 2) *reinterpret_cast<uint32_t*>(o) = v[0];
+  if constexpr (kD == 4) *reinterpret_cast<uint2*>(o) = make_uint2(v[0], v[1]);
+  if constexpr (kD == 8) *reinterpret_cast<uint4*>(o) = make_uint4(v[0], v[1], v[2], v[3]);
   if (d0 == 0) p.lse[static_cast<int64_t>(h) * p.num_seqs * p.n + at] = lse;
 }
 
-template <int NT, int kDepth>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(const DecK p) {
+// Partial results in the workspace: kRows x 64 accumulators, then (ref, sum) per row.
+template <int kRows, int kD>
+SA_DEV void put_piece(float* part, int row, int d0, const Piece<kD>& f) {
+#pragma unroll
+  for (int d = 0; d < kD; d += 2)
+    __stcg(reinterpret_cast<float2*>(part + row * kHeadDim + d0 + d), make_float2(f.acc[d], f.acc[d + 1]));
+  if (d0 == 0) __stcg(reinterpret_cast<float2*>(part + kRows * kHeadDim + 2 * row), make_float2(f.ref, f.sum));
+}
+
+// The pieces of workers c0 .. c1, in order.
+template <int kRows, int kD, class F>
+SA_DEV Piece<kD> merge_pieces(F part_of, int c0, int c1, int row, int d0) {
+  Piece<kD> all;
+  all.sum = 0.f;
+  all.ref = -INFINITY;
+#pragma unroll
+  for (int d = 0; d < kD; ++d) all.acc[d] = 0.f;
+  for (int c = c0; c <= c1; ++c) all.ref = fmaxf(all.ref, __ldcg(part_of(c) + kRows * kHeadDim + 2 * row));
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float* from = part_of(c);
+    const float2 st = __ldcg(reinterpret_cast<const float2*>(from + kRows * kHeadDim + 2 * row));
+    // a piece that saw nothing holds zeros, or a NaN that must come through
+    const float f = st.x == -INFINITY ? (st.y == 0.f ? 0.f : 1.f) : ex2(st.x - all.ref);
+    all.sum += f * st.y;
+#pragma unroll
+    for (int d = 0; d < kD; d += 2) {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(from + row * kHeadDim + d0 + d));
+      all.acc[d] += f * v.x;
+      all.acc[d + 1] += f * v.y;
+    }
+  }
+  return all;
+}
+
+// The line of all blocks cut into equal shares: worker c takes [start(c), start(c + 1)).
+struct Shares {
+  long long work, each;
+  int workers, more;  // the first `more` workers take one block more than `each`
+  float per_block;
+  SA_DEV Shares(long long w, int n) : work(w), workers(n) {
+    if (w < (1LL << 32)) {  // the cheaper division
+      each = static_cast<uint32_t>(w) / static_cast<uint32_t>(n);
+    } else {
+      each = w / n;
+    }
+    more = static_cast<int>(w - each * n);
+    per_block = __fdividef(static_cast<float>(n), static_cast<float>(w));
+  }
+  SA_DEV long long start(int c) const { return c * each + min(c, more); }
+  SA_DEV int owner(long long x) const {  // the share that holds block x: an estimate, off by one at most, put right
+    int c = min(max(static_cast<int>(static_cast<float>(x) * per_block), 0), workers - 1);
+    while (start(c) > x) --c;
+    while (start(c + 1) <= x) ++c;
+    return c;
+  }
+};
+
+struct SeqInfo {  // a sequence of the call, in shared memory
+  long long upto;  // blocks of the sequences before it
+  int len, slot;
+};
+
+struct Cut {  // a pair that other workers have parts of
+  long long pair, p0;  // its number and its place in the line
+  int c0, c1, b, head, row0;
+};
+
+template <int NT, int kWarps, int kPerSm>
+__global__ void __launch_bounds__(kWarps * 32, kPerSm) kv4_decode_kernel(const DecK p) {
+  constexpr int kThreads = kWarps * 32;
   constexpr int kRows = 8 * NT;
+  constexpr int kAloneRows = NT <= 2 ? 2 * NT : 1;  // rows a lane finishes when its warp works alone
   constexpr int kPartFloats = kRows * (kHeadDim + 2);
-  constexpr int kDims = kRows * kHeadDim / kThreads;  // output dims per thread when merging: 2, 4 or 8
+  constexpr int kDims = kRows * kHeadDim / kThreads;  // dims per thread when a CTA merges: 2, 4 or 8
   extern __shared__ __align__(16) uint8_t smem[];
-  // merge area [warps][rows][kRowPad], statistics [warps][rows][2], then the running block counts [num_seqs + 1]
-  float* acc_sh = reinterpret_cast<float*>(smem);
+  // the warps' rings, merge area [warps][rows][kRowPad], statistics [warps][rows][2], then the sequences
+  float* acc_sh = reinterpret_cast<float*>(smem + kWarps * kStages * kTurnBytes);
   float* stat_sh = acc_sh + kWarps * kRows * kRowPad;
-  long long* upto = reinterpret_cast<long long*>(stat_sh + kWarps * kRows * 2);
+  SeqInfo* seqs = reinterpret_cast<SeqInfo*>(stat_sh + kWarps * kRows * 2);
   __shared__ long long warp_sum[kWarps];
-  __shared__ int last_sh;
+  __shared__ __align__(8) uint64_t bars[kWarps * kStages];
+  __shared__ Cut cuts[2];
+  __shared__ int last_sh[2], abort_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane_g(), t = lane_t();
 
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(smem_u32(&bars[warp * kStages + i]), 1);
+    tc::fence_mbar_init();
+    if (warp == 0) abort_flag = 0;
+  }
   // blocks per sequence (an empty one counts as one: its rows are written too) and their running total
-  long long carry = 0;
+  long long blocks_all = 0;
+  int longest = 0;
   for (int base = 0; base < p.num_seqs; base += kThreads) {
     const int b = base + tid;
-    long long x = b < p.num_seqs ? max(visible_span(p, b).count(), 1) : 0;
+    long long x = 0;
+    SeqInfo info;
+    if (b < p.num_seqs) {
+      info.slot = p.slots[b];
+      info.len = slot_len(p.c, info.slot);
+      x = max(visible_span(p, info.len).count(), 1);
+    }
+    const long long own = x;
+    longest = max(longest, static_cast<int>(min(x, 1LL << 30)));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -309,64 +577,116 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
     }
     if (lane == 31) warp_sum[warp] = x;
     __syncthreads();
-    long long before = carry, all = 0;
+    long long before = blocks_all;
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) before += warp_sum[w];
-      all += warp_sum[w];
+      blocks_all += warp_sum[w];
     }
-    if (b < p.num_seqs) upto[b + 1] = before + x;
-    carry += all;
+    if (b < p.num_seqs) {
+      info.upto = before + x - own;
+      seqs[b] = info;
+    }
     __syncthreads();
   }
-  if (tid == 0) upto[0] = 0;
-  __syncthreads();
 
+  const bool few = __syncthreads_and(longest <= kAloneBlocks) != 0;
   const int per_seq = p.c.num_heads_kv * p.row_groups;  // pairs per sequence
-  const long long work = carry * per_seq, pairs = static_cast<long long>(p.num_seqs) * per_seq;
-  // at least a block for every warp of a CTA, unless that leaves pairs without a CTA of their own
-  const long long want = max((work + kWarps - 1) / kWarps, pairs);
-  const long long ctas = min(static_cast<long long>(gridDim.x), want);
-  const long long cta = blockIdx.x;
-  if (cta >= ctas) return;
-  long long x = cta * work / ctas;
-  const long long x_end = (cta + 1) * work / ctas;
+  const long long work = blocks_all * per_seq, pairs = static_cast<long long>(p.num_seqs) * per_seq;
+  // many pairs, all of them short
+  const bool alone = NT <= 2 && few && pairs >= gridDim.x;
+  // a turn at least for every warp, unless that leaves pairs without a worker of their own
+  const long long want = alone ? pairs : max((work + kTurnBlocks * kWarps - 1) / (kTurnBlocks * kWarps), pairs);
+  const int most = static_cast<int>(gridDim.x) * (alone ? kWarps : 1);
+  // the line that is shared out: all blocks, or all pairs
+  const Shares shares(alone ? pairs : work, static_cast<int>(min(static_cast<long long>(most), want)));
+  const int worker = alone ? warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) : blockIdx.x;
+  if (worker >= shares.workers) return;  // a whole CTA, or a warp of one that never meets the others again
+  const long long x_end = shares.start(worker + 1);
 
-  while (x < x_end) {
-    int b;
-    {  // the sequence that holds x
-      int lo = 0, hi = p.num_seqs - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (upto[mid] * per_seq <= x)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      b = lo;
+  // The segment at x, the first of the rest of pair in_seq of sequence b.
+  const auto segment_at = [&](long long x, int b, int in_seq, int blk0) {
+    Segment s;
+    const SeqInfo info = seqs[b];
+    s.x = x;
+    s.b = b;
+    s.in_seq = in_seq;
+    s.blk0 = blk0;
+    s.slot = info.slot;
+    s.span = visible_span(p, info.len);
+    s.blocks = max(s.span.count(), 1);
+    s.blk1 = alone ? s.blocks : static_cast<int>(min(static_cast<long long>(s.blocks), blk0 + (x_end - x)));
+    s.head = p.row_groups == 1 ? in_seq : in_seq / p.row_groups;
+    s.row0 = (in_seq - s.head * p.row_groups) * kRows;
+    return s;
+  };
+  Segment seg;
+  {  // the pair that holds the share's first block
+    const long long x = shares.start(worker);
+    int lo = 0, hi = p.num_seqs - 1;
+    while (!alone && lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (seqs[mid].upto * per_seq <= x)
+        lo = mid;
+      else
+        hi = mid - 1;
     }
-    const Span span = visible_span(p, b);
-    const int blocks = max(span.count(), 1);
-    const long long off = x - upto[b] * per_seq;
-    const int in_seq = static_cast<int>(off / blocks), blk0 = static_cast<int>(off % blocks);
-    const int blk1 = static_cast<int>(min(static_cast<long long>(blocks), blk0 + (x_end - x)));
-    const int head = in_seq / p.row_groups, row0 = in_seq % p.row_groups * kRows;
-    const int slot = p.slots[b];
+    if (alone) {
+      lo = static_cast<int>(x / per_seq);
+      seg = segment_at(x, lo, static_cast<int>(x - static_cast<long long>(lo) * per_seq), 0);
+    } else {
+      const long long off = x - seqs[lo].upto * per_seq;
+      const int blocks = max(visible_span(p, seqs[lo].len).count(), 1);
+      int in_seq = min(static_cast<int>(__fdividef(static_cast<float>(off), static_cast<float>(blocks))), per_seq - 1);
+      while (static_cast<long long>(in_seq) * blocks > off) --in_seq;
+      while (static_cast<long long>(in_seq + 1) * blocks <= off) ++in_seq;
+      seg = segment_at(x, lo, in_seq, static_cast<int>(off - static_cast<long long>(in_seq) * blocks));
+    }
+  }
 
-    // query rows: lane (g, t) holds row g's dims 16 t .. 16 t + 15 as B fragments
+  // What a segment needs besides its blocks, loaded ahead: query rows (lane
+  // (g, t): row g's dims 16 t .. 16 t + 15), factors, and the sinks of the
+  // rows that this thread will finish.
+  uint32_t qw[NT][8];
+  float k_factor, v_factor, sink[kAloneRows];
+  const int merge_row = tid / (kThreads / kRows), merge_dim = tid % (kThreads / kRows) * kDims;
+  const auto load_ahead = [&](const Segment& s) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = s.row0 + 8 * nt + g;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) qw[nt][i] = 0;
+      if (row < p.rows) {
+        const int64_t at = static_cast<int64_t>(s.b) * p.n + row / p.group;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + (at * p.hq + s.head * p.group + row % p.group) * kHeadDim + 16 * t);
+        const uint4 u = __ldg(src), v = __ldg(src + 1);
+        qw[nt][0] = u.x, qw[nt][1] = u.y, qw[nt][2] = u.z, qw[nt][3] = u.w;
+        qw[nt][4] = v.x, qw[nt][5] = v.y, qw[nt][6] = v.z, qw[nt][7] = v.w;
+      }
+    }
+    k_factor = __ldg(p.c.k_scale + s.head);
+    v_factor = __ldg(p.c.v_scale + s.head);
+    const auto sink_of = [&](int row) { return row < p.rows ? __ldg(p.sink + s.head * p.group + row % p.group) : 0.f; };
+    if (NT <= 2 && alone) {
+#pragma unroll
+      for (int i = 0; i < kAloneRows; ++i) sink[i] = sink_of(s.row0 + 8 * (i >> 1) + 2 * t + (i & 1));
+    } else {
+      sink[0] = sink_of(s.row0 + merge_row);
+    }
+  };
+
+  Stream stream(p, smem + warp * kStages * kTurnBytes, smem_u32(&bars[warp * kStages]), tc::Abort{&abort_flag, p.status},
+                alone ? 0 : warp, alone ? 1 : kWarps);
+  int n_cuts = 0;
+  load_ahead(seg);
+  stream.begin(seg);
+  while (true) {
     uint32_t qf[NT][4][2];
     float coef[NT][2];
     int pos[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + 8 * nt + g;
-      uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (row < p.rows) {
-        const int64_t at = static_cast<int64_t>(b) * p.n + row / p.group;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (at * p.hq + head * p.group + row % p.group) * kHeadDim + 16 * t);
-        const uint4 u = __ldg(src), v = __ldg(src + 1);
-        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w, w[4] = v.x, w[5] = v.y, w[6] = v.z, w[7] = v.w;
-      }
+      const uint32_t(&w)[8] = qw[nt];
       uint32_t top = 0;  // the row's largest exponent field
 #pragma unroll
       for (int i = 0; i < 8; ++i) top = max(top, max(w[i] >> 7 & 0xffu, w[i] >> 23 & 0xffu));
@@ -381,54 +701,76 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
         qf[nt][i][0] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
         qf[nt][i][1] = pack_f16(__uint_as_float(w[4 + i] << 16) * up, __uint_as_float(w[4 + i] & 0xffff0000u) * up);
       }
-      const float mine = down * (p.scale * kLog2e * p.c.k_scale[head]);
+      const float mine = down * (p.scale * kLog2e * k_factor);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         coef[nt][r] = __shfl_sync(0xffffffffu, mine, 4 * (2 * t + r));
-        const int rr = row0 + 8 * nt + 2 * t + r;
-        pos[nt][r] = rr < p.rows ? span.len - p.n + rr / p.group : -1;
+        const int rr = seg.row0 + 8 * nt + 2 * t + r;
+        pos[nt][r] = rr < p.rows ? seg.span.len - p.n + rr / p.group : -1;
       }
     }
+    const float v_scale = v_factor;
+    float row_sink[kAloneRows];
+#pragma unroll
+    for (int i = 0; i < kAloneRows; ++i) row_sink[i] = sink[i];
 
     Rows<NT> r;
     rows_clear(r);
-    if (span.len > 0) {
-      const int first = span.len - p.n;  // every block wholly at or before `first` is seen by all rows causally
-      const int last_lo = p.window < 0 ? 0 : span.len - 1 - p.window;
-      Tile tile[kDepth];
-      int page[kDepth];
+    stream.run([&](const uint8_t* at, const Batch& batch, int bit0) {
+#pragma unroll 1
+      for (int u0 = 0; u0 < kTurnBlocks; u0 += 2) {
+        const int bit = bit0 + u0;
+        if ((batch.valid >> bit & 3u) == 0) continue;
+        Tile tile[2];
+        read_tile(at + u0 * kBlockBytes, tile[0]);
+        read_tile(at + (u0 + 1) * kBlockBytes, tile[1]);
+        MaskArgs<2> mk;
+        mk.window = p.window;
+        mk.prefix = p.prefix;
+        if ((batch.masked >> bit & 3u) == 0) {
+          block_step<NT, 2, false>(r, tile, qf, coef, pos, mk);
+        } else {
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        const int i = blk0 + warp + d * kWarps;
-        page[d] = i < blk1 ? page_of(p.c, slot, span.block(i)) : -1;
-      }
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d) {
-        const int i = blk0 + warp + d * kWarps;
-        if (i < blk1) load_tile(p.c, page[d], head, span.block(i), tile[d]);
-        const int ahead = i + kDepth * kWarps;
-        page[d] = ahead < blk1 ? page_of(p.c, slot, span.block(ahead)) : -1;
-      }
-      for (int i0 = blk0 + warp; i0 < blk1; i0 += kDepth * kWarps) {
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-          const int i = i0 + d * kWarps;
-          if (i >= blk1) break;
-          const int key0 = span.block(i) * kBlockTokens, key1 = key0 + kBlockTokens - 1;
-          const MaskArgs mk{key0, p.window, p.prefix};
-          if (key1 <= first && (key0 >= last_lo || key1 < p.prefix))
-            block_step<NT, false>(r, tile[d], qf, coef, pos, mk);
-          else
-            block_step<NT, true>(r, tile[d], qf, coef, pos, mk);
-          const int ahead = i + kDepth * kWarps;
-          if (ahead < blk1) load_tile(p.c, page[d], head, span.block(ahead), tile[d]);
-          const int further = ahead + kDepth * kWarps;
-          page[d] = further < blk1 ? page_of(p.c, slot, span.block(further)) : -1;
+          for (int u = 0; u < 2; ++u) {
+            mk.key0[u] = __shfl_sync(0xffffffffu, batch.key0, bit + u);
+            mk.missing[u] = batch.missing >> (bit + u) & 1u;
+          }
+          block_step<NT, 2, true>(r, tile, qf, coef, pos, mk);
         }
       }
+    });
+
+    // the next segment is on its way while this one is finished
+    const Segment done = seg;
+    const long long x_next = done.x + (alone ? 1 : done.blk1 - done.blk0);
+    const bool more = x_next < x_end;
+    if (more) {
+      const bool same = done.in_seq + 1 < per_seq;
+      seg = segment_at(x_next, same ? done.b : done.b + 1, same ? done.in_seq + 1 : 0, 0);
+      load_ahead(seg);
+      stream.begin(seg);
     }
 
-    // the warps' results into shared memory
+    // A pair that is cut is published when the worker is through, with one
+    // fence and no copies in flight for it to wait for.
+    const bool whole = done.blk0 == 0 && done.blk1 == done.blocks;
+    const long long p0 = done.x - done.blk0;
+    float* mine = p.part + (2 * static_cast<int64_t>(worker) + (done.blk0 == 0 && done.x > shares.start(worker))) * kPartFloats;
+    if (!whole) {
+      if (tid == 0) {
+        Cut c;
+        c.pair = static_cast<long long>(done.b) * per_seq + done.in_seq;
+        c.p0 = p0;
+        c.c0 = shares.owner(p0);
+        c.c1 = shares.owner(p0 + done.blocks - 1);
+        c.b = done.b;
+        c.head = done.head;
+        c.row0 = done.row0;
+        cuts[n_cuts] = c;
+      }
+      ++n_cuts;
+    }
+
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -436,94 +778,107 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_decode_kernel(c
         float sum = r.sum[nt][e];
         sum += __shfl_xor_sync(0xffffffffu, sum, 4);
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int row = 8 * nt + 2 * t + e;
-        float4* to = reinterpret_cast<float4*>(acc_sh + (warp * kRows + row) * kRowPad + 8 * g);
-        to[0] = make_float4(r.o[nt][0][e], r.o[nt][0][2 + e], r.o[nt][1][e], r.o[nt][1][2 + e]);
-        to[1] = make_float4(r.o[nt][2][e], r.o[nt][2][2 + e], r.o[nt][3][e], r.o[nt][3][2 + e]);
-        if (g == 0) {
-          stat_sh[(warp * kRows + row) * 2] = r.limit[nt][e] == -INFINITY ? -INFINITY : r.ref[nt][e];
-          stat_sh[(warp * kRows + row) * 2 + 1] = sum;
-        }
+        r.sum[nt][e] = sum + __shfl_xor_sync(0xffffffffu, sum, 16);
+        r.ref[nt][e] = r.limit[nt][e] == -INFINITY ? -INFINITY : r.ref[nt][e] * coef[nt][e];  // log2 units from here
       }
-    __syncthreads();
-
-    // thread: one row, kDims of its dims
-    const int row = tid / (kThreads / kRows), d0 = tid % (kThreads / kRows) * kDims;
-    float acc[kDims], sum = 0.f, ref = -INFINITY;
+    const auto piece_of = [&](int nt, int e) {
+      Piece<8> f;
 #pragma unroll
-    for (int d = 0; d < kDims; ++d) acc[d] = 0.f;
-    for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, stat_sh[(w * kRows + row) * 2]);
-    for (int w = 0; w < kWarps; ++w) {
-      const float m = stat_sh[(w * kRows + row) * 2];
-      if (m == -INFINITY) {  // nothing of it was seen; what it holds is zero, or NaN where a score was
-        sum += stat_sh[(w * kRows + row) * 2 + 1];
-        continue;
-      }
-      const float f = ex2(m - ref);
-      sum += f * stat_sh[(w * kRows + row) * 2 + 1];
+      for (int i = 0; i < 4; ++i) f.acc[2 * i] = r.o[nt][i][e], f.acc[2 * i + 1] = r.o[nt][i][2 + e];
+      f.sum = r.sum[nt][e];
+      f.ref = r.ref[nt][e];
+      return f;
+    };
+    if (NT <= 2 && alone) {
+      const auto each_row = [&](auto f) {
 #pragma unroll
-      for (int d = 0; d < kDims; ++d) acc[d] += f * acc_sh[(w * kRows + row) * kRowPad + d0 + d];
-    }
-
-    const float factor = p.c.v_scale[head];
-    const bool there = row0 + row < p.rows;
-    if (blk0 == 0 && blk1 == blocks) {
-      if (there) finish_row(p, b, head, row0 + row, d0, kDims, acc, sum, ref, factor);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (done.row0 + 8 * nt + 2 * t + e < p.rows) f(nt, e, 8 * nt + 2 * t + e);
+      };
+      each_row([&](int nt, int e, int row) {
+        finish_row<8>(p, done.b, done.head, done.row0 + row, 8 * g, piece_of(nt, e), row_sink[(2 * nt + e) % kAloneRows],
+                      v_scale);
+      });
     } else {
-      const long long pair = static_cast<long long>(b) * per_seq + in_seq;
-      const long long p0 = x - blk0, p1 = p0 + blocks;  // the pair's place in the line
-      const long long c0 = ((p0 + 1) * ctas - 1) / work, c1 = (p1 * ctas - 1) / work;
-      const auto slot_of = [&](long long c) { return p.part + (2 * c + (p0 > c * work / ctas ? 1 : 0)) * kPartFloats; };
-      float* mine = slot_of(cta);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const Piece<8> f = piece_of(nt, e);
+          const int at = warp * kRows + 8 * nt + 2 * t + e;
+          float4* to = reinterpret_cast<float4*>(acc_sh + at * kRowPad + 8 * g);
+          to[0] = make_float4(f.acc[0], f.acc[1], f.acc[2], f.acc[3]);
+          to[1] = make_float4(f.acc[4], f.acc[5], f.acc[6], f.acc[7]);
+          if (g == 0) *reinterpret_cast<float2*>(stat_sh + 2 * at) = make_float2(f.ref, f.sum);
+        }
+      __syncthreads();
+      // thread: one row, kDims of its dims
+      Piece<kDims> f;
+      f.sum = 0.f;
+      f.ref = -INFINITY;
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) f.acc[d] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) f.ref = fmaxf(f.ref, stat_sh[(w * kRows + merge_row) * 2]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 st = *reinterpret_cast<const float2*>(stat_sh + (w * kRows + merge_row) * 2);
+        const float m = st.x == -INFINITY ? (st.y == 0.f ? 0.f : 1.f) : ex2(st.x - f.ref);
+        f.sum += m * st.y;
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) f.acc[d] += m * acc_sh[(w * kRows + merge_row) * kRowPad + merge_dim + d];
+      }
+      const bool there = done.row0 + merge_row < p.rows;
       if (there) {
-#pragma unroll
-        for (int d = 0; d < kDims; ++d) __stcg(mine + row * kHeadDim + d0 + d, acc[d]);
-        if (d0 == 0) {
-          __stcg(mine + kRows * kHeadDim + 2 * row, ref);
-          __stcg(mine + kRows * kHeadDim + 2 * row + 1, sum);
-        }
+        if (whole)
+          finish_row<kDims>(p, done.b, done.head, done.row0 + merge_row, merge_dim, f, row_sink[0], v_scale);
+        else
+          put_piece<kRows, kDims>(mine, merge_row, merge_dim, f);
       }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) last_sh = atomicAdd(p.counters + pair, 1) == static_cast<int>(c1 - c0);
-      __syncthreads();
-      if (last_sh) {
-        __threadfence();
-        if (tid == 0) p.counters[pair] = 0;
-        if (there) {
-          float all[kDims], total = 0.f, top = -INFINITY;
-#pragma unroll
-          for (int d = 0; d < kDims; ++d) all[d] = 0.f;
-          for (long long c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(slot_of(c) + kRows * kHeadDim + 2 * row));
-          for (long long c = c0; c <= c1; ++c) {
-            const float* from = slot_of(c);
-            const float m = __ldcg(from + kRows * kHeadDim + 2 * row), l = __ldcg(from + kRows * kHeadDim + 2 * row + 1);
-            const float f = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - top);
-            total += f * l;
-#pragma unroll
-            for (int d = 0; d < kDims; ++d) all[d] += f * __ldcg(from + row * kHeadDim + d0 + d);
-          }
-          finish_row(p, b, head, row0 + row, d0, kDims, all, total, top, factor);
-        }
-      }
+      if (more) __syncthreads();  // the merge area is free again
     }
-    __syncthreads();  // the merge area is free again
-    x += blk1 - blk0;
+    if (!more) break;
+  }
+
+  if (n_cuts == 0) return;
+  const auto arrive = [&](const Cut& c) {  // by one thread, after a barrier: is this worker the pair's last?
+    __threadfence();  // the worker's piece, ordered before by the barrier, is there for whoever sees the count
+    const bool last = atomicAdd(p.counters + c.pair, 1) == c.c1 - c.c0;
+    __threadfence();
+    if (last) p.counters[c.pair] = 0;
+    return last;
+  };
+  // a worker's first pair left its piece in the first of its two places, a later one in the second
+  const auto part_of = [&](const Cut& c) {
+    return [&p, &shares, p0 = c.p0](int w) {
+      return p.part + (2 * static_cast<int64_t>(w) + (p0 > shares.start(w) ? 1 : 0)) * kPartFloats;
+    };
+  };
+  const auto sink_at = [&](const Cut& c, int row) { return __ldg(p.sink + c.head * p.group + row % p.group); };
+  __syncthreads();
+  if (tid < n_cuts) last_sh[tid] = arrive(cuts[tid]);
+  __syncthreads();
+  for (int i = 0; i < n_cuts; ++i) {
+    if (!last_sh[i]) continue;
+    const Cut c = cuts[i];
+    if (c.row0 + merge_row < p.rows)
+      finish_row<kDims>(p, c.b, c.head, c.row0 + merge_row, merge_dim,
+                        merge_pieces<kRows, kDims>(part_of(c), c.c0, c.c1, merge_row, merge_dim),
+                        sink_at(c, c.row0 + merge_row), __ldg(p.c.v_scale + c.head));
   }
 }
 
-template <int NT, int kDepth>
+template <int NT, int kWarps, int kPerSm>
 cudaError_t launch_variant(const DecK& p, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(kWarps) * 8 * NT * (kRowPad + 2) * 4 + (p.num_seqs + 1) * 8;
-  const auto kernel = kv4_decode_kernel<NT, kDepth>;
-  if (smem > 48 * 1024) {  // more than a kernel has without asking
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
-  const int grid = device_sms() * (NT == 1 ? 2 : 1);
-  kernel<<<grid, kThreads, smem, s>>>(p);
+  const size_t smem = static_cast<size_t>(kWarps) * (kStages * kTurnBytes + 8 * NT * (kRowPad + 2) * 4) +
+                      p.num_seqs * sizeof(SeqInfo);
+  const auto kernel = kv4_decode_kernel<NT, kWarps, kPerSm>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kernel<<<device_sms() * kPerSm, kWarps * 32, smem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -532,14 +887,15 @@ cudaError_t launch_variant(const DecK& p, cudaStream_t s) {
 // Partial results first, in a place that depends on the GPU alone, then the
 // counters (zero between calls, at most one per query row and head): a
 // workspace zeroed once serves calls of any shape it is large enough for.
-static size_t part_bytes() { return static_cast<size_t>(device_sms()) * kPartRowsPerSm * (kHeadDim + 2) * 4; }
-
-size_t kv4_decode_workspace_bytes(long long rows, int hq) {
-  return (part_bytes() + 255) / 256 * 256 + static_cast<size_t>(rows) * hq * 4;
+static size_t part_bytes() {
+  return (static_cast<size_t>(device_sms()) * kPartRowsPerSm * (kHeadDim + 2) * 4 + 255) / 256 * 256;
 }
 
-cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, cudaStream_t s) {
+size_t kv4_decode_workspace_bytes(long long rows, int hq) { return part_bytes() + static_cast<size_t>(rows) * hq * 4; }
+
+cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, int* status, cudaStream_t s) {
   DecK p;
+  p.status = status;
   p.c = c;
   p.slots = a.slots;
   p.q = static_cast<const __nv_bfloat16*>(a.q);
@@ -547,7 +903,7 @@ cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, cudaStr
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
   p.part = static_cast<float*>(a.workspace);
-  p.counters = reinterpret_cast<int*>(static_cast<uint8_t*>(a.workspace) + (part_bytes() + 255) / 256 * 256);
+  p.counters = reinterpret_cast<int*>(static_cast<uint8_t*>(a.workspace) + part_bytes());
   p.num_seqs = a.num_seqs;
   p.n = a.n;
   p.hq = a.hq;
@@ -558,9 +914,9 @@ cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, cudaStr
   p.scale = a.scale;
   const int nt = p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : 4;
   p.row_groups = ceil_div(p.rows, 8 * nt);
-  if (nt == 1) return launch_variant<1, 4>(p, s);
-  if (nt == 2) return launch_variant<2, 3>(p, s);
-  return launch_variant<4, 2>(p, s);
+  if (nt == 1) return launch_variant<1, KV4_W1, KV4_C1>(p, s);
+  if (nt == 2) return launch_variant<2, 8, 1>(p, s);
+  return launch_variant<4, 8, 1>(p, s);
 }
 
 }  // namespace sa

@@ -141,6 +141,8 @@ sinkattn_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SINKATTN_OK
 
 }  // namespace
 
+int* sa::device_status_word() { return status_word(); }
+
 extern "C" {
 
 int32_t sinkattn_kernel_launches(const sinkattn_problem* prob, int32_t which) {
