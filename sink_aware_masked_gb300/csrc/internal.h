@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <vector>
 
 namespace sa {
@@ -66,6 +67,21 @@ constexpr int kPreTokens = 8;
 // (a GB300) when no device answers, so that host-side plans and the
 // workspace sizes they imply are the same with or without a GPU.
 int device_sms();
+
+// Asks once per device for a kernel's dynamic shared memory above 48 KB (one
+// static object per kernel; two threads that come first at once both ask).
+struct SmemOptIn {
+  std::atomic<bool> done[256] = {};
+  template <class K>
+  cudaError_t operator()(K kernel, size_t bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 256 && done[dev].load(std::memory_order_acquire))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess && dev < 256) done[dev].store(true, std::memory_order_release);
+    return e;
+  }
+};
 
 // Device address of the library's status word on the current device (looked
 // up once per device), or nullptr.

@@ -30,12 +30,6 @@
 #include "kv4.cuh"
 #include "tc.cuh"
 
-#ifndef KV4_W1
-#define KV4_W1 4
-#define KV4_C1 3
-#define KV4_T 4
-#define KV4_ST 2
-#endif
 namespace sa {
 namespace {
 
@@ -121,9 +115,9 @@ struct Tile {  // one block's bytes as this lane needs them
 };
 
 // A warp's ring in shared memory: a turn is four blocks.
-constexpr int kTurnBlocks = KV4_T;
+constexpr int kTurnBlocks = 4;
 constexpr int kTurnBytes = kTurnBlocks * kBlockBytes;
-constexpr int kStages = KV4_ST;
+constexpr int kStages = 2;
 constexpr int kBatchTurns = 32 / kTurnBlocks;
 
 SA_DEV void read_tile(const uint8_t* stage, Tile& t) {
@@ -717,25 +711,27 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) kv4_decode_kernel(const D
     Rows<NT> r;
     rows_clear(r);
     stream.run([&](const uint8_t* at, const Batch& batch, int bit0) {
+      constexpr int U = 2;  // blocks per step: two independent chains of products
+      constexpr uint32_t kAny = (1u << U) - 1;
 #pragma unroll 1
-      for (int u0 = 0; u0 < kTurnBlocks; u0 += 2) {
+      for (int u0 = 0; u0 < kTurnBlocks; u0 += U) {
         const int bit = bit0 + u0;
-        if ((batch.valid >> bit & 3u) == 0) continue;
-        Tile tile[2];
-        read_tile(at + u0 * kBlockBytes, tile[0]);
-        read_tile(at + (u0 + 1) * kBlockBytes, tile[1]);
-        MaskArgs<2> mk;
+        if ((batch.valid >> bit & kAny) == 0) continue;
+        Tile tile[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) read_tile(at + (u0 + u) * kBlockBytes, tile[u]);
+        MaskArgs<U> mk;
         mk.window = p.window;
         mk.prefix = p.prefix;
-        if ((batch.masked >> bit & 3u) == 0) {
-          block_step<NT, 2, false>(r, tile, qf, coef, pos, mk);
+        if ((batch.masked >> bit & kAny) == 0) {
+          block_step<NT, U, false>(r, tile, qf, coef, pos, mk);
         } else {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < U; ++u) {
             mk.key0[u] = __shfl_sync(0xffffffffu, batch.key0, bit + u);
             mk.missing[u] = batch.missing >> (bit + u) & 1u;
           }
-          block_step<NT, 2, true>(r, tile, qf, coef, pos, mk);
+          block_step<NT, U, true>(r, tile, qf, coef, pos, mk);
         }
       }
     });
@@ -872,13 +868,12 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) kv4_decode_kernel(const D
 
 template <int NT, int kWarps, int kPerSm>
 cudaError_t launch_variant(const DecK& p, cudaStream_t s) {
-  const size_t smem = static_cast<size_t>(kWarps) * (kStages * kTurnBytes + 8 * NT * (kRowPad + 2) * 4) +
-                      p.num_seqs * sizeof(SeqInfo);
+  constexpr size_t kFixed = static_cast<size_t>(kWarps) * (kStages * kTurnBytes + 8 * NT * (kRowPad + 2) * 4);
   const auto kernel = kv4_decode_kernel<NT, kWarps, kPerSm>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(kernel, kFixed + kKv4MaxRequests * sizeof(SeqInfo));
   if (e != cudaSuccess) return e;
-  kernel<<<device_sms() * kPerSm, kWarps * 32, smem, s>>>(p);
+  kernel<<<device_sms() * kPerSm, kWarps * 32, kFixed + p.num_seqs * sizeof(SeqInfo), s>>>(p);
   return cudaGetLastError();
 }
 
@@ -914,7 +909,7 @@ cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, int* st
   p.scale = a.scale;
   const int nt = p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : 4;
   p.row_groups = ceil_div(p.rows, 8 * nt);
-  if (nt == 1) return launch_variant<1, KV4_W1, KV4_C1>(p, s);
+  if (nt == 1) return launch_variant<1, 4, 3>(p, s);
   if (nt == 2) return launch_variant<2, 8, 1>(p, s);
   return launch_variant<4, 8, 1>(p, s);
 }

@@ -28,18 +28,46 @@ from .api import HEAD_DIM, WINDOW_INF, _check, _on_gpu, _ptr
 BLOCK_TOKENS = 16
 TOKEN_BYTES = 72  # per token and kv head: 2 x 32 bytes of codes, 2 x 4 scales
 
+_SCALE = 1.0 / math.sqrt(HEAD_DIM)
 _LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+# The current device and a device's current stream as plain integers: a small
+# step's time is its calls' time on the host, and torch.cuda.current_stream()
+# makes a Stream object on the way.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_functions = {}
 
 
 def _call(name: str, dev: torch.device, *args) -> None:
     """Call the library on ``dev``'s current stream (the last argument of every entry point)."""
-    fn = getattr(_lib.load(), name)
-    if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_lib.load(), name)
+    index = dev.index
+    if index == _current_device():
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _lib.check(name, st)
+            st = fn(*args, _raw_stream(index))
+    if st != 0:
+        _lib.check(name, st)
+
+
+def _tensor(name: str, t, dtype: torch.dtype, shape, dev) -> int:
+    """Checks a tensor as ``api._check`` does, which words the refusal, and returns its address."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _check(name, t, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _vector(name: str, t, dtype: torch.dtype, dev) -> int:
+    """The length of a 1-D tensor that is checked like any other."""
+    if not (isinstance(t, torch.Tensor) and t.dim() == 1):
+        _check(name, t, dtype, (None,), dev)
+    return t.shape[0]
 
 
 class KV4Cache:
@@ -90,45 +118,35 @@ class KV4Cache:
                    torch.zeros(num_pages, **i32), one(k_scale), one(v_scale))
 
 
-def _list(name: str, t, n: Optional[int], dev) -> None:
-    _check(name, t, torch.int32, (n,), dev)
-
-
-def _done(cache: KV4Cache, n: int, done):
-    if done is None:
-        return torch.empty(n, dtype=torch.int32, device=cache.device)
-    _list("done", done, n, cache.device)
-    return done
-
-
 def kv4_reserve(cache: KV4Cache, slots, new_tokens, *, done=None):
     """Slot slots[i] grows by new_tokens[i] tokens (int32 [n], on the device); returns done int32 [n].
 
     A request that finds no room gets done = 0 and stays as it was, and so
     does every later one that needs a page.
     """
-    _list("slots", slots, None, cache.device)
-    n = slots.shape[0]
-    _list("new_tokens", new_tokens, n, cache.device)
-    done = _done(cache, n, done)
-    _call("sinkattn_kv4_reserve", cache.device, cache._ref, _ptr(slots), _ptr(new_tokens), n, _ptr(done))
+    dev, i32 = cache.device, torch.int32
+    n = _vector("slots", slots, i32, dev)
+    sp, np_ = _tensor("slots", slots, i32, (n,), dev), _tensor("new_tokens", new_tokens, i32, (n,), dev)
+    done = torch.empty_like(slots) if done is None else done
+    _call("sinkattn_kv4_reserve", dev, cache._ref, sp, np_, n, _tensor("done", done, i32, (n,), dev))
     return done
 
 
 def kv4_fork(cache: KV4Cache, src, dst, *, done=None):
     """The empty slots dst[i] become copies of src[i], sharing its full pages; returns done int32 [n]."""
-    _list("src", src, None, cache.device)
-    n = src.shape[0]
-    _list("dst", dst, n, cache.device)
-    done = _done(cache, n, done)
-    _call("sinkattn_kv4_fork", cache.device, cache._ref, _ptr(src), _ptr(dst), n, _ptr(done))
+    dev, i32 = cache.device, torch.int32
+    n = _vector("src", src, i32, dev)
+    sp, dp = _tensor("src", src, i32, (n,), dev), _tensor("dst", dst, i32, (n,), dev)
+    done = torch.empty_like(src) if done is None else done
+    _call("sinkattn_kv4_fork", dev, cache._ref, sp, dp, n, _tensor("done", done, i32, (n,), dev))
     return done
 
 
 def kv4_free(cache: KV4Cache, slots) -> None:
     """Empties the slots; pages that no other slot holds become free."""
-    _list("slots", slots, None, cache.device)
-    _call("sinkattn_kv4_free", cache.device, cache._ref, _ptr(slots), slots.shape[0])
+    dev = cache.device
+    n = _vector("slots", slots, torch.int32, dev)
+    _call("sinkattn_kv4_free", dev, cache._ref, _tensor("slots", slots, torch.int32, (n,), dev), n)
 
 
 def kv4_compact(cache: KV4Cache, to: KV4Cache, *, count=None, workspace=None):
@@ -142,12 +160,13 @@ def kv4_compact(cache: KV4Cache, to: KV4Cache, *, count=None, workspace=None):
         raise ValueError(f"to is on {to.device}, expected {dev}")
     if count is None:
         count = torch.empty(1, dtype=torch.int32, device=dev)
-    _list("count", count, 1, dev)
+    cp = _tensor("count", count, torch.int32, (1,), dev)
     if workspace is None:
         size = int(_lib.load().sinkattn_kv4_compact_workspace_size(cache._ref))
         workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=dev)
-    _check("workspace", workspace, torch.uint8, (None,), dev)
-    _call("sinkattn_kv4_compact", dev, cache._ref, to._ref, _ptr(count), _ptr(workspace), workspace.numel())
+    wn = _vector("workspace", workspace, torch.uint8, dev)
+    _call("sinkattn_kv4_compact", dev, cache._ref, to._ref, cp, _tensor("workspace", workspace, torch.uint8, (wn,), dev),
+          wn)
     return count
 
 
@@ -159,14 +178,15 @@ def kv4_append(cache: KV4Cache, slots, k, v, *, cu_new=None) -> None:
     cu_new; its length counts them already (kv4_reserve).  No slot is named
     twice in a call.
     """
-    dev = cache.device
-    _list("slots", slots, None, dev)
-    _check("k", k, torch.bfloat16, (None, cache.num_heads_kv, HEAD_DIM), dev)
-    _check("v", v, torch.bfloat16, tuple(k.shape), dev)
-    n = slots.shape[0]
-    if cu_new is not None:
-        _list("cu_new", cu_new, n + 1, dev)
-    _call("sinkattn_kv4_append", dev, cache._ref, _ptr(slots), n, _ptr(cu_new), k.shape[0], _ptr(k), _ptr(v))
+    dev, bf16 = cache.device, torch.bfloat16
+    n = _vector("slots", slots, torch.int32, dev)
+    sp = _tensor("slots", slots, torch.int32, (n,), dev)
+    if not (isinstance(k, torch.Tensor) and k.dim() == 3):
+        _check("k", k, bf16, (None, cache.num_heads_kv, HEAD_DIM), dev)
+    shape = (k.shape[0], cache.num_heads_kv, HEAD_DIM)
+    kp, vp = _tensor("k", k, bf16, shape, dev), _tensor("v", v, bf16, shape, dev)
+    cp = None if cu_new is None else _tensor("cu_new", cu_new, torch.int32, (n + 1,), dev)
+    _call("sinkattn_kv4_append", dev, cache._ref, sp, n, cp, shape[0], kp, vp)
 
 
 def kv4_read(cache: KV4Cache, slots, total: int, *, cu=None, k=None, v=None):
@@ -177,17 +197,15 @@ def kv4_read(cache: KV4Cache, slots, total: int, *, cu=None, k=None, v=None):
     takes them.  Rows before a sequence's begin are zero; rows behind cu[-1]
     are not written.
     """
-    dev = cache.device
-    _list("slots", slots, None, dev)
-    n = slots.shape[0]
+    dev, bf16 = cache.device, torch.bfloat16
+    n = _vector("slots", slots, torch.int32, dev)
+    sp = _tensor("slots", slots, torch.int32, (n,), dev)
     shape = (int(total), cache.num_heads_kv, HEAD_DIM)
-    if cu is not None:
-        _list("cu", cu, n + 1, dev)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v is None else v
-    _check("k", k, torch.bfloat16, shape, dev)
-    _check("v", v, torch.bfloat16, shape, dev)
-    _call("sinkattn_kv4_read", dev, cache._ref, _ptr(slots), n, _ptr(cu), shape[0], _ptr(k), _ptr(v))
+    cp = None if cu is None else _tensor("cu", cu, torch.int32, (n + 1,), dev)
+    k = torch.empty(shape, dtype=bf16, device=dev) if k is None else k
+    v = torch.empty_like(k) if v is None else v
+    _call("sinkattn_kv4_read", dev, cache._ref, sp, n, cp, shape[0], _tensor("k", k, bf16, shape, dev),
+          _tensor("v", v, bf16, shape, dev))
     return k, v
 
 
@@ -212,28 +230,26 @@ def kv4_decode_fwd(cache: KV4Cache, slots, q, sink, *, q_per_seq: int, window: i
     call.
     """
     dev = cache.device
-    if q is None or q.dim() != 3:
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a 3-D tensor [rows, heads, head_dim]")
-    if q.shape[2] != HEAD_DIM:
-        raise ValueError(f"head_dim must be {HEAD_DIM} (q: {q.shape[2]})")
-    hq = q.shape[1]
+    _, hq, d = q.shape
+    if d != HEAD_DIM:
+        raise ValueError(f"head_dim must be {HEAD_DIM} (q: {d})")
     if hq % cache.num_heads_kv != 0 or hq == 0:
         raise ValueError(f"query heads ({hq}) must be a multiple of key/value heads ({cache.num_heads_kv})")
-    _list("slots", slots, None, dev)
-    n = slots.shape[0]
+    n = _vector("slots", slots, torch.int32, dev)
+    sp = _tensor("slots", slots, torch.int32, (n,), dev)
     rows = n * int(q_per_seq)
-    _check("q", q, torch.bfloat16, (rows, hq, HEAD_DIM), dev)
-    _check("sink", sink, torch.float32, (hq,), dev)
+    shape = (rows, hq, HEAD_DIM)
+    qp, kp = _tensor("q", q, torch.bfloat16, shape, dev), _tensor("sink", sink, torch.float32, (hq,), dev)
     o = torch.empty_like(q) if o is None else o
     lse = torch.empty((hq, rows), dtype=torch.float32, device=dev) if lse is None else lse
-    _check("o", o, torch.bfloat16, tuple(q.shape), dev)
-    _check("lse", lse, torch.float32, (hq, rows), dev)
     if workspace is None:
         workspace = kv4_decode_workspace(cache, q)
-    _check("workspace", workspace, torch.uint8, (None,), dev)
-    _call("sinkattn_kv4_decode_fwd", dev, cache._ref, _ptr(slots), n, int(q_per_seq), hq, int(window), int(prefix),
-          1.0 / math.sqrt(HEAD_DIM) if scale is None else float(scale), _ptr(q), _ptr(sink), _ptr(o), _ptr(lse),
-          _ptr(workspace), workspace.numel())
+    wn = _vector("workspace", workspace, torch.uint8, dev)
+    _call("sinkattn_kv4_decode_fwd", dev, cache._ref, sp, n, int(q_per_seq), hq, int(window), int(prefix),
+          _SCALE if scale is None else float(scale), qp, kp, _tensor("o", o, torch.bfloat16, shape, dev),
+          _tensor("lse", lse, torch.float32, (hq, rows), dev), _tensor("workspace", workspace, torch.uint8, (wn,), dev), wn)
     return o, lse
 
 
@@ -251,30 +267,27 @@ def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=
     """
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a 2-D tensor [rows, vocab]")
-    if logits.dtype not in _LOGIT_TYPES:
+    kind = _LOGIT_TYPES.get(logits.dtype)
+    if kind is None:
         raise TypeError(f"logits has dtype {logits.dtype}, expected float32, bfloat16 or float16")
-    B, V = (int(x) for x in logits.shape)
+    B, V = logits.shape
     if (V > 1 and logits.stride(1) != 1) or (B > 1 and logits.stride(0) < V):
         raise ValueError("logits must have contiguous rows that do not overlap")
     dev = logits.device
-    _check("u", u, torch.float32, (B,), dev)
-    f32 = lambda x: torch.full((B,), x, dtype=torch.float32, device=dev)  # noqa: E731
-    temperature = f32(1.0) if temperature is None else temperature
-    top_p = f32(1.0) if top_p is None else top_p
-    min_p = f32(0.0) if min_p is None else min_p
-    top_k = torch.zeros(B, dtype=torch.int32, device=dev) if top_k is None else top_k
-    _check("temperature", temperature, torch.float32, (B,), dev)
-    _check("top_k", top_k, torch.int32, (B,), dev)
-    _check("top_p", top_p, torch.float32, (B,), dev)
-    _check("min_p", min_p, torch.float32, (B,), dev)
-    tokens = torch.empty(B, dtype=torch.int32, device=dev) if tokens is None else tokens
-    logp = torch.empty(B, dtype=torch.float32, device=dev) if logp is None else logp
-    logq = torch.empty(B, dtype=torch.float32, device=dev) if logq is None else logq
-    _check("tokens", tokens, torch.int32, (B,), dev)
-    _check("logp", logp, torch.float32, (B,), dev)
-    _check("logq", logq, torch.float32, (B,), dev)
+    f32, i32, one = torch.float32, torch.int32, (B,)
+    up = _tensor("u", u, f32, one, dev)
+    temperature = torch.ones_like(u) if temperature is None else temperature
+    top_k = torch.zeros(B, dtype=i32, device=dev) if top_k is None else top_k
+    top_p = torch.ones_like(u) if top_p is None else top_p
+    min_p = torch.zeros_like(u) if min_p is None else min_p
+    tp, kp = _tensor("temperature", temperature, f32, one, dev), _tensor("top_k", top_k, i32, one, dev)
+    pp, mp = _tensor("top_p", top_p, f32, one, dev), _tensor("min_p", min_p, f32, one, dev)
+    tokens = torch.empty_like(top_k) if tokens is None else tokens
+    logp = torch.empty_like(u) if logp is None else logp
+    logq = torch.empty_like(u) if logq is None else logq
+    to, lp, lq = (_tensor("tokens", tokens, i32, one, dev), _tensor("logp", logp, f32, one, dev),
+                  _tensor("logq", logq, f32, one, dev))
     _on_gpu("logits", logits)
-    _call("sinkattn_sample_tokens", dev, _ptr(logits), _LOGIT_TYPES[logits.dtype], B, V,
-          logits.stride(0) if B > 1 else V, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
-          _ptr(tokens), _ptr(logp), _ptr(logq))
+    _call("sinkattn_sample_tokens", dev, logits.data_ptr(), kind, B, V, logits.stride(0) if B > 1 else V, up, tp, kp, pp,
+          mp, to, lp, lq)
     return tokens, logp, logq
