@@ -9,18 +9,28 @@
 //   token = the first index, in index order, whose kept mass up to and
 //   including it exceeds u times the kept mass
 //
-// A cluster of CTAs takes one row: every CTA keeps its slice of the logits in
-// shared memory, so HBM is read once, and what follows is passes over shared
-// memory with a few numbers exchanged between the CTAs.
+// A row belongs to a CTA, or to a cluster of CTAs where there are few rows.
+// Pass 1 reads it from HBM and leaves the maximum, Z and every thread's own
+// maximum; later passes find it in L2.
 //
-// Selection without sorting: a histogram (count and mass) of the candidates
-// over equal steps of x finds the step in which the cut lies; its members, if
-// few, are ranked by one CTA, else they are split again by their exact key
-// (x's bits and the index, so all keys differ) until they are few.
+//   Nothing to select: the token lies in the chunk whose mass, known from
+//   pass 1, holds u Z; that chunk alone is read again.
+//   top-k or min-p: the threads' maxima (or min-p itself) bound the kept
+//   logits from below.  Pass 2 collects the few that reach the bound, and one
+//   CTA sorts them; what is kept is a run at their front.
+//   Otherwise (top-p alone, top-k in the thousands, long lists): a histogram
+//   (count and mass) over equal steps of x finds the step in which a cut
+//   lies; its members, if few, are ranked by one CTA, else they are split
+//   again by their exact key (x's bits and the index, so all keys differ)
+//   until they are few.  A last pass sums what is kept.
 //
-// Masses are 43-bit fixed point, e / Z * 2^43: integer sums are the same in
-// every order, so histogram atomics leave the result reproducible, and 2^18
-// of them lose at most 2^-25 of the whole.
+// Arithmetic.  e is fp32 (the difference before the scale: a large logit must
+// not lose what tells it from its neighbours).  Partial sums of a thread are
+// fp32, everything above is 64-bit fixed point: the slice sums of Z in units
+// of 2^-40, masses under selection in units of Z 2^-43.  Integer sums are the
+// same in every order, so histogram atomics leave the result reproducible,
+// and 2^18 roundings lose at most 2^-22 (Z) or 2^-25 of the whole.  FP64 is
+// not used: its rate on this GPU would cost more than all the rest.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -32,6 +42,12 @@
 namespace sa {
 namespace {
 
+#ifndef SMP_PER
+#define SMP_PER 2
+#define SMP_MAX 8
+#define SMP_SLICE 16384
+#endif
+
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
@@ -39,9 +55,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kIndexBits = 18;            // vocabularies up to 2^18
 constexpr int kBins = 1024;
-constexpr int kList = 4096;               // candidates a CTA keeps a list of
-constexpr int kGather = kThreads;         // members the last step ranks, one per thread
-constexpr double kMassOne = 8796093022208.0;  // 2^43
+constexpr int kGather = kThreads;         // members that the last step of a search ranks, one per thread
+constexpr int kList = 2048;               // candidates that are sorted at once
+constexpr int kChunks = 16;               // runs of a slice whose masses are kept apart
+constexpr int kUnroll = 4;                // vectors a thread has in flight
+constexpr float kMassOne = 8796093022208.f;   // 2^43
+constexpr float kSumOne = 1099511627776.f;    // 2^40
 constexpr int kLowBits = 13;
 
 typedef unsigned long long u64;
@@ -50,21 +69,33 @@ struct Pick {  // what a histogram step found
   int bin;
   u64 members;     // candidates in the bin
   u64 count, mass; // of all bins before it
+  u64 target;
+};
+
+struct Histogram {
+  uint32_t count[kBins], mass_hi[kBins], mass_lo[kBins];  // this CTA's
+  uint32_t all_count[kBins];                              // CTA 0: the row's
+  u64 all_mass[kBins];
+  u64 key[kGather], key_mass[kGather], sorted[kGather], sorted_mass[kGather];
+};
+
+struct Sorted {
+  u64 key[kList];
+  u64 bin[kThreads];  // masses by index
 };
 
 struct Shared {
   u64 exchange[2][kMaxCluster];
-  double warp_d[kWarps];
   u64 warp_u[kWarps], warp_v[kWarps];
-  float warp_f[kWarps];
-  u64 lo, hi, cut, cut_mass;
+  float chunk_max[kChunks][kWarps], chunk_sum[kChunks][kWarps];
+  u64 chunk_mass[kChunks][kWarps];
+  u64 cut, cut_mass;
   Pick pick;
-  int list_n, gathered, found;
-  uint32_t count[kBins], mass_hi[kBins], mass_lo[kBins];  // this CTA's histogram
-  uint32_t all_count[kBins];                              // CTA 0: the row's
-  u64 all_mass[kBins];
-  u64 key[kGather], key_mass[kGather], sorted[kGather], sorted_mass[kGather];
-  uint16_t list[kList];
+  int gathered, found, last;
+  union {
+    Histogram h;
+    Sorted s;
+  };
 };
 
 template <int kType>
@@ -112,6 +143,9 @@ SA_DEV uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);
   return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
+SA_DEV float key_value(uint32_t key) {
+  return __uint_as_float((key >> 31) ? key ^ 0x80000000u : ~key);
+}
 SA_DEV u64 full_key(float x, int index) {
   return static_cast<u64>(order_key(x)) << kIndexBits | ((1u << kIndexBits) - 1 - index);
 }
@@ -143,59 +177,49 @@ class Row {
   typedef Elem<kType> E;
   typedef typename E::T T;
 
-  SA_DEV Row(Shared& sh, T* raw) : sh_(sh), raw_(raw), cluster_(cg::this_cluster()) {
+  SA_DEV Row(Shared& sh) : sh_(sh), cluster_(cg::this_cluster()) {
     rank_ = cluster_.block_rank();
     ctas_ = cluster_.num_blocks();
   }
 
   SA_DEV void run(const SampleArgs& a, int row, int slice) {
     const int tid = threadIdx.x;
+    cluster_.barrier_arrive();
     vocab_ = a.vocab;
     first_ = min(static_cast<int>(rank_) * slice, a.vocab);
-    const int last = min(first_ + slice, a.vocab);
-    const T* x = static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.stride;
-    cluster_.barrier_arrive();
-    float mine = load(x, last);
-    const float thread_max = mine;
-    mine = warp_max(mine);
-    if ((tid & 31) == 0) sh_.warp_f[tid >> 5] = mine;
-    __syncthreads();
-    mine = sh_.warp_f[0];
-    for (int w = 1; w < kWarps; ++w) mine = fmaxf(mine, sh_.warp_f[w]);
-    max_ = -INFINITY;
-    cluster_.barrier_wait();  // every CTA of the cluster runs: its shared memory may be written
-    exchange(__float_as_uint(mine), [&](u64 v) { max_ = fmaxf(max_, __uint_as_float(static_cast<uint32_t>(v))); });
+    const T* x = static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.stride + first_;
+    shift_ = static_cast<int>((reinterpret_cast<uintptr_t>(x) / sizeof(T)) % E::kVec);
+    base_ = x - shift_;
+    end_ = shift_ + min(slice, a.vocab - first_);
+    vectors_ = end_ > shift_ ? (end_ + E::kVec - 1) / E::kVec : 0;
+    const int turns = (vectors_ + kThreads - 1) / kThreads;
+    chunk_turns_ = max((turns + kChunks - 1) / kChunks, 1);
+    chunk_turns_ = (chunk_turns_ + kUnroll - 1) / kUnroll * kUnroll;
 
     const float temperature = a.temperature[row], top_p = a.top_p[row], min_p = a.min_p[row], u = a.u[row];
     int k = a.top_k[row];
+    const bool valid = temperature >= 0.f && temperature < INFINITY && top_p == top_p && min_p == min_p && u == u;
     const bool greedy = temperature == 0.f;
-    const double inv_t = greedy ? 1.0 : 1.0 / static_cast<double>(temperature);
-    scale_ = static_cast<float>(fmin(1.4426950408889634 * inv_t, 1e38));
-    if (!(temperature >= 0.f && temperature < INFINITY) || top_p != top_p || min_p != min_p || u != u) {
+    temperature_ = greedy || !valid ? 1.f : temperature;
+    scale_ = fminf(__fdiv_rn(kLog2e, temperature_), 1e38f);
+    if (greedy || top_p <= 0.f) k = 1;
+    const bool by_count = k > 0 && k < vocab_, by_mass = top_p < 1.f, by_floor = min_p > 0.f;
+    const bool chunks = !by_count && !by_mass && !by_floor;
+
+    const float thread_max = pass1(chunks);
+    cluster_.barrier_wait();  // every CTA of the cluster runs: its shared memory may be written
+    if (!valid) {
       if (rank_ == 0 && tid == 0) put(a, row, -1, NAN, NAN);
       return;
     }
-    if (max_ == -INFINITY) {  // nothing is allowed, or all there is is NaN
-      const float v = any_nan() ? NAN : -INFINITY;
+    reduce_max_and_sum();
+    if (z_ == 0.f || max_ == INFINITY || z_ != z_) {
+      const float v = z_ == 0.f ? -INFINITY : NAN;  // nothing is allowed, or something is not a number
       if (rank_ == 0 && tid == 0) put(a, row, -1, v, v);
       return;
     }
-    // Z; a NaN among the logits makes it NaN, an infinite one too
-    float part = 0.f;
-    each_vector([&](const float* v, int) {
-#pragma unroll
-      for (int e = 0; e < E::kVec; ++e) part += mass(v[e]);
-    });
-    const double slice_z = block_sum_d(static_cast<double>(part));
-    z_ = 0.0;
-    exchange(__double_as_longlong(slice_z), [&](u64 v) { z_ += __longlong_as_double(static_cast<long long>(v)); });
-    if (max_ == INFINITY || z_ != z_) {
-      if (rank_ == 0 && tid == 0) put(a, row, -1, NAN, NAN);
-      return;
-    }
-    to_fixed_ = static_cast<float>(kMassOne / z_);
+    to_fixed_ = __fdiv_rn(kMassOne, z_);
 
-    if (greedy || top_p <= 0.f) k = 1;
     if (k == 1) {  // the largest, of equal ones the lowest index
       int at = vocab_;
       each_vector([&](const float* v, int base) {
@@ -206,32 +230,37 @@ class Row {
       at = block_min(at);
       int best = vocab_;
       exchange(static_cast<u64>(at), [&](u64 v) { best = min(best, static_cast<int>(v)); });
-      if (rank_ == 0 && tid == 0) put(a, row, best, static_cast<float>(-log(z_)), 0.f);
+      if (rank_ == 0 && tid == 0) put(a, row, best, -ln(z_), 0.f);
       return;
     }
-
+    // below 1, so that the kept mass exceeds the target
+    const float share = fminf(fmaxf(u, 0.f), 0.99999994f);
     cut_ = 0;
     min_mass_ = fminf(min_p, 1.f);
-    const bool by_count = k > 0 && k < vocab_, by_mass = top_p < 1.f;
-    if (by_count || by_mass) {
-      float floor = -INFINITY;
-      if (by_count) {
-        floor = count_floor(thread_max, k);
-      } else {
-        // what lies below (1 - p) Z / vocab holds less than (1 - p) Z together; 1 % to spare for rounding
-        const double least = (1.0 - static_cast<double>(top_p)) * 0.99 * z_ / vocab_;
-        floor = static_cast<float>(max_ + log(least) / inv_t * 1.0001);
-        floor -= fabsf(floor) * 2.4e-7f;
-      }
-      make_list(floor);
-      // steps for the first histogram: the candidates' range, or what holds all mass that counts
-      const float range = floor > -INFINITY ? max_ - floor : static_cast<float>(30.0 / inv_t);
-      per_step_ = range > 0.f ? fminf((kBins - 1) / range, 1e30f) : 0.f;
-      double kept = z_ * static_cast<double>(to_fixed_);
-      if (by_count) kept = static_cast<double>(search(true, static_cast<double>(k)));
-      if (by_mass) search(false, static_cast<double>(top_p) * kept);
+    if (chunks) {
+      sample_chunks(a, row, share);
+      return;
     }
-    sample(a, row, u, inv_t);
+    // what lies below floor is not kept, nor does its mass count for top-p
+    float floor = -INFINITY;
+    if (by_count) floor = count_floor(thread_max, k);
+    if (by_floor && !(by_count && by_mass)) floor = fmaxf(floor, mass_floor(min_mass_ * 0.999f));
+    if (floor > -INFINITY && sample_list(a, row, floor, by_count ? k : vocab_, by_mass ? top_p : 1.f, by_count, share))
+      return;
+    // what lies below (1 - p) Z / vocab holds less than (1 - p) Z together; 1 % to spare for rounding
+    if (!by_count && by_mass)
+      floor = fmaxf(floor, mass_floor((1.f - top_p) * 0.99f * z_ / vocab_));
+    floor_ = floor;
+    if (by_count || by_mass) {
+      // steps for the first histogram: the candidates' range, or what holds all mass that counts
+      const float range = floor > -INFINITY ? max_ - floor : 30.f * temperature_;
+      per_step_ = range > 0.f ? fminf((kBins - 1) / range, 1e30f) : 0.f;
+      u64 kept = 0;
+      if (by_count) kept = search(true, k, 0.f);
+      if (by_mass) search(false, by_count ? part_of(kept, top_p) : 0, top_p);
+    }
+    chunk_masses();
+    sample_chunks(a, row, share);
   }
 
  private:
@@ -240,88 +269,150 @@ class Row {
   SA_DEV void exchange(u64 v, F take) {
     u64* buf = sh_.exchange[parity_];
     parity_ ^= 1;  // the other half may still be read by a slower CTA
+    if (ctas_ == 1) {
+      take(v);
+      return;
+    }
     if (threadIdx.x < ctas_) cluster_.map_shared_rank(buf, threadIdx.x)[rank_] = v;
     cluster_.sync();
     for (unsigned r = 0; r < ctas_; ++r) take(buf[r]);
   }
+  SA_DEV void sync_all() {
+    if (ctas_ == 1)
+      __syncthreads();
+    else
+      cluster_.sync();
+  }
 
-  // Copies the slice into shared memory at the alignment it has in global
-  // memory, -inf around it, and returns the thread's largest logit.
-  SA_DEV float load(const T* x, int last) {
-    const int tid = threadIdx.x;
-    shift_ = static_cast<int>((reinterpret_cast<uintptr_t>(x + first_) / sizeof(T)) % E::kVec);
-    const int n = last - first_, end = shift_ + n;
-    vectors_ = n > 0 ? (end + E::kVec - 1) / E::kVec : 0;
-    float top = -INFINITY;
-    const T* base = x + first_ - shift_;
-    const auto keep = [&](int v, uint4 w) {
-      reinterpret_cast<uint4*>(raw_)[v] = w;
-      float f[E::kVec];
-      E::unpack(w, f);
+  // Vector v of the slice, aligned as in global memory, -inf outside the slice.
+  SA_DEV uint4 load(int v) const {
+    union {
+      uint4 q;
+      T t[E::kVec];
+    } w;
+    if (v * E::kVec >= shift_ && (v + 1) * E::kVec <= end_) return __ldg(reinterpret_cast<const uint4*>(base_) + v);
 #pragma unroll
-      for (int e = 0; e < E::kVec; ++e) top = fmaxf(top, f[e]);
-    };
-    const auto edge = [&](int v) {
-#pragma unroll
-      for (int e = 0; e < E::kVec; ++e) {
-        const int i = v * E::kVec + e;
-        const T w = i >= shift_ && i < end ? base[i] : E::lowest();
-        raw_[i] = w;
-        top = fmaxf(top, E::one(w));
-      }
-    };
-    const int v0 = shift_ > 0 ? 1 : 0, v1 = end / E::kVec;  // [v0, v1): whole vectors
-    constexpr int kUnroll = 4;
-    int v = v0 + tid;
-    for (; v + (kUnroll - 1) * kThreads < v1; v += kUnroll * kThreads) {
+    for (int e = 0; e < E::kVec; ++e) {
+      const int i = v * E::kVec + e;
+      w.t[e] = i >= shift_ && i < end_ ? base_[i] : E::lowest();
+    }
+    return w.q;
+  }
+  SA_DEV int index_of(int v) const { return first_ + v * E::kVec - shift_; }
+
+  // f(values, index of the first) for the slice's vectors in [turn0, turn1) x threads; padding is -inf.
+  template <class F>
+  SA_DEV void turns_of_vectors(int turn0, int turn1, F f) {
+    for (int t = turn0; t < turn1; t += kUnroll) {
       uint4 w[kUnroll];
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) w[i] = __ldcs(reinterpret_cast<const uint4*>(base) + v + i * kThreads);
+      for (int i = 0; i < kUnroll; ++i) {
+        const int v = (t + i) * kThreads + threadIdx.x;
+        if (v < vectors_) w[i] = load(v);
+      }
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) keep(v + i * kThreads, w[i]);
+      for (int i = 0; i < kUnroll; ++i) {
+        const int v = (t + i) * kThreads + threadIdx.x;
+        if (v < vectors_) {
+          float x[E::kVec];
+          E::unpack(w[i], x);
+          f(x, index_of(v));
+        }
+      }
     }
-    for (; v < v1; v += kThreads) keep(v, __ldcs(reinterpret_cast<const uint4*>(base) + v));
-    if (vectors_ > 0) {
-      if (tid == 0 && v0 == 1) edge(0);
-      if (tid == 32 && vectors_ - 1 >= v1 && (vectors_ > 1 || v0 == 0)) edge(vectors_ - 1);
+  }
+  template <class F>
+  SA_DEV void each_vector(F f) {
+    turns_of_vectors(0, (vectors_ + kThreads - 1) / kThreads, f);
+  }
+  SA_DEV int chunks() const {
+    return ((vectors_ + kThreads - 1) / kThreads + chunk_turns_ - 1) / chunk_turns_;
+  }
+
+  // Maximum and sum of one pass, the sum relative to the running maximum; per
+  // chunk and warp, or (chunks false) per warp as chunk 0.
+  SA_DEV float pass1(bool by_chunk) {
+    const int warp = threadIdx.x >> 5, turns = (vectors_ + kThreads - 1) / kThreads;
+    const int step = by_chunk ? chunk_turns_ : max(turns, 1);
+    float top = -3.402823466e38f;  // so that a difference with -inf is -inf
+    for (int c = 0; c * step < max(turns, 1); ++c) {
+      float sum = 0.f;
+      turns_of_vectors(c * step, min((c + 1) * step, turns), [&](const float* x, int) {
+        float m = x[0];
+#pragma unroll
+        for (int e = 1; e < E::kVec; ++e) m = fmaxf(m, x[e]);
+        if (m > top) {
+          sum *= ex2((top - m) * scale_);
+          top = m;
+        }
+#pragma unroll
+        for (int e = 0; e < E::kVec; ++e) sum += ex2((x[e] - top) * scale_);
+      });
+      const float warp_top = warp_max(top);
+      const float warp_total = warp_sum(sum * ex2((top - warp_top) * scale_));
+      if ((threadIdx.x & 31) == 0) sh_.chunk_max[c][warp] = warp_top, sh_.chunk_sum[c][warp] = warp_total;
     }
+    pass1_parts_ = (by_chunk ? chunks() : 1) * kWarps;
     __syncthreads();
     return top;
   }
 
-  // f(values, index of the first) for every vector; the indices of padding lie outside [first, last) but are -inf.
-  template <class F>
-  SA_DEV void each_vector(F f) {
-    for (int v = threadIdx.x; v < vectors_; v += kThreads) {
-      float x[E::kVec];
-      E::unpack(reinterpret_cast<const uint4*>(raw_)[v], x);
-      f(x, first_ + v * E::kVec - shift_);
+  // max_ and z_ (0: no logit above -inf, NaN: a NaN or +inf among them), and
+  // the chunks' sums in fixed point, relative to max_.  Every warp does it all.
+  SA_DEV void reduce_max_and_sum() {
+    const int lane = threadIdx.x & 31;
+    const float* maxima = &sh_.chunk_max[0][0];
+    const float* sums = &sh_.chunk_sum[0][0];
+    float top = -3.402823466e38f;
+    for (int i = lane; i < pass1_parts_; i += 32) top = fmaxf(top, maxima[i]);
+    max_ = -3.402823466e38f;
+    exchange(__float_as_uint(warp_max(top)),
+             [&](u64 v) { max_ = fmaxf(max_, __uint_as_float(static_cast<uint32_t>(v))); });
+    u64 sum = 0;
+    bool bad = false;
+    for (int i = lane; i < pass1_parts_; i += 32) {
+      const float s = sums[i] * ex2((maxima[i] - max_) * scale_);
+      bad |= s != s;
+      const u64 fixed = static_cast<u64>(s * kSumOne);
+      sum += fixed;
+      if (threadIdx.x < 32) (&sh_.chunk_mass[0][0])[i] = fixed;
     }
+    sum = warp_sum(sum);
+    u64 all = 0;
+    exchange(__any_sync(0xffffffffu, bad) ? ~0ull : sum, [&](u64 v) {
+      bad |= v == ~0ull;
+      all += v;
+    });
+    z_ = __any_sync(0xffffffffu, bad) ? NAN : static_cast<float>(all) * (1.f / kSumOne);
+    __syncthreads();
+  }
+
+  // ceil(mass * p)
+  static SA_DEV u64 part_of(u64 mass, float p) {
+    const u64 m = mass << 20, q = static_cast<u64>(fmaxf(p, 0.f) * 4294967296.f) << 12;  // mass < 2^44, p < 1
+    return __umul64hi(m, q) + (m * q != 0);
+  }
+  // The mass of everything, given that of the candidates: theirs alone where
+  // no more is left than rounding, so that equal masses are counted exactly.
+  SA_DEV u64 whole_mass(u64 candidates) const {
+    const u64 all = static_cast<u64>(z_ * to_fixed_);
+    return all > candidates + (candidates >> 20) ? all : candidates;
+  }
+
+  // floor(mass * u), below mass.
+  static SA_DEV u64 u_of(u64 mass, float u) {
+    return __umul64hi(mass << 4, static_cast<u64>(u * 4294967296.f) << 28);  // mass < 2^60, u < 1
+  }
+
+  static SA_DEV float ln(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y * kLn2;
   }
 
   SA_DEV float mass(float x) const { return ex2((x - max_) * scale_); }
   SA_DEV u64 fixed(float x) const { return static_cast<u64>(mass(x) * to_fixed_); }
 
-  SA_DEV bool any_nan() {  // in the whole row; every CTA of the cluster asks
-    int bad = 0;
-    each_vector([&](const float* v, int) {
-#pragma unroll
-      for (int e = 0; e < E::kVec; ++e) bad |= v[e] != v[e];
-    });
-    bad = __syncthreads_or(bad);
-    bool any = false;
-    exchange(static_cast<u64>(bad), [&](u64 v) { any |= v != 0; });
-    return any;
-  }
-
-  SA_DEV double block_sum_d(double x) {
-    x = warp_sum(x);
-    if ((threadIdx.x & 31) == 0) sh_.warp_d[threadIdx.x >> 5] = x;
-    __syncthreads();
-    double s = 0.0;
-    for (int w = 0; w < kWarps; ++w) s += sh_.warp_d[w];
-    return s;
-  }
   SA_DEV int block_min(int x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x = min(x, __shfl_xor_sync(0xffffffffu, x, o));
@@ -331,57 +422,176 @@ class Row {
     return x;
   }
 
-  // A value that at least k logits reach: in each CTA the k / ctas-th largest
-  // of the threads' maxima, and the least of those over the CTAs.
-  SA_DEV float count_floor(float thread_max, int k) {
-    const int quota = (k + ctas_ - 1) / ctas_;
-    if (quota > kThreads) return -INFINITY;
-    const uint32_t key = order_key(thread_max);
-    uint32_t lo = 0;
-#pragma unroll 1
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t mid = lo | 1u << bit;
-      if (__syncthreads_count(key >= mid) >= quota) lo = mid;
-    }
-    uint32_t least = 0xffffffffu;
-    exchange(lo, [&](u64 v) { least = min(least, static_cast<uint32_t>(v)); });
-    const uint32_t bits = (least >> 31) ? least ^ 0x80000000u : ~least;
-    const float f = __uint_as_float(bits);
-    return f == f ? f : -INFINITY;  // fewer threads than the quota hold anything: key 0
+  // The logit at which e is `least`, rounded down.
+  SA_DEV float mass_floor(float least) const {
+    const float f = max_ + ln(least) * temperature_ * (least < 1.f ? 1.0001f : 1.f);
+    return f - fabsf(f) * 2.4e-7f;
   }
 
-  // The slice's candidates (x >= floor); scan_all_ where they are too many for a list.
-  SA_DEV void make_list(float floor) {
-    floor_ = floor;
-    if (threadIdx.x == 0) sh_.list_n = 0;
-    __syncthreads();
-    each_vector([&](const float* x, int base) {
+  // A value that at least k logits reach: in each warp the k / warps-th
+  // largest of the lanes' maxima, and the least of those over the row's warps.
+  SA_DEV float count_floor(float thread_max, int k) {
+    const int warps = kWarps * ctas_, quota = (k + warps - 1) / warps;
+    if (quota > 32) return -INFINITY;
+    const uint32_t key = order_key(thread_max);
+    uint32_t lo = 0;
 #pragma unroll
-      for (int e = 0; e < E::kVec; ++e)
-        if (x[e] >= floor && x[e] > -INFINITY) {
-          const int at = atomicAdd(&sh_.list_n, 1);
-          if (at < kList) sh_.list[at] = static_cast<uint16_t>(base + e - first_);
-        }
-    });
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t mid = lo | 1u << bit;
+      if (__popc(__ballot_sync(0xffffffffu, key >= mid)) >= quota) lo = mid;
+    }
     __syncthreads();
-    list_n_ = sh_.list_n;
+    if ((threadIdx.x & 31) == 0) sh_.warp_u[threadIdx.x >> 5] = lo;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) lo = min(lo, static_cast<uint32_t>(sh_.warp_u[w]));
+    uint32_t least = 0xffffffffu;
+    exchange(lo, [&](u64 v) { least = min(least, static_cast<uint32_t>(v)); });
+    const float f = key_value(least);
+    return f > -3.402823466e38f ? f : -INFINITY;  // some warp has too few logits above -inf
+  }
+
+  // Collects the logits from floor on, sorts them and samples from their
+  // front.  False (for all CTAs alike) if they are too many.
+  SA_DEV bool sample_list(const SampleArgs& a, int row, float floor, int k, float top_p, bool by_count, float share) {
+    const int tid = threadIdx.x;
+    if (tid == 0) sh_.gathered = 0;
+    sync_all();
+    {
+      int* n = cluster_.map_shared_rank(&sh_.gathered, 0);
+      u64* keys = cluster_.map_shared_rank(sh_.s.key, 0);
+      each_vector([&](const float* x, int base) {
+        float m = x[0];
+#pragma unroll
+        for (int e = 1; e < E::kVec; ++e) m = fmaxf(m, x[e]);
+        if (m < floor) return;
+#pragma unroll
+        for (int e = 0; e < E::kVec; ++e)
+          if (x[e] >= floor) {
+            const int at = atomicAdd(n, 1);
+            if (at < kList) keys[at] = full_key(x[e], base + e);
+          }
+      });
+    }
+    sync_all();
+    int n = sh_.gathered;
+    if (ctas_ > 1) {
+      int all = 0;
+      exchange(rank_ == 0 ? static_cast<u64>(n) : 0, [&](u64 v) { all += static_cast<int>(v); });
+      n = all;
+    }
+    if (n > kList) return false;
+    if (rank_ != 0) return true;
+
+    int size = 32;
+    while (size < n) size *= 2;
+    for (int i = n + tid; i < size; i += kThreads) sh_.s.key[i] = 0;
+    __syncthreads();
+    sort_keys(size);
+    // masses of the first k, in order: kPer entries per thread
+    constexpr int kPer = kList / kThreads;
+    u64 upto[kPer], own = 0;
+    float e[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid * kPer + j;
+      e[j] = i < min(n, k) ? mass(key_value(static_cast<uint32_t>(sh_.s.key[i] >> kIndexBits))) : 0.f;
+      own += static_cast<u64>(e[j] * to_fixed_);
+      upto[j] = own;
+    }
+    const u64 before = block_scan(own, sh_.warp_u) - own;
+    u64 all = 0;
+    for (int w = 0; w < kWarps; ++w) all += sh_.warp_u[w];
+    // top-p counts against the first k, or, without top-k, against everything
+    const u64 target = top_p < 1.f ? part_of(by_count ? all : whole_mass(all), top_p) : ~0ull;
+    int kept = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = tid * kPer + j;
+      const u64 excluded = before + (j > 0 ? upto[j > 0 ? j - 1 : 0] : 0);
+      if (i < min(n, k) && e[j] >= min_mass_ && e[j] > 0.f && (i == 0 || excluded < target)) ++kept;
+    }
+    kept = block_sum_int(kept);  // they are the first ones
+    // the kept masses by index: first over runs of indices, then inside the run that holds the target
+    const int width = (vocab_ + kThreads - 1) / kThreads;
+    u64 target_in = 0, total = 0;
+    int lo = 0;
+    for (int level = 0; level < 2; ++level) {
+      sh_.s.bin[tid] = 0;
+      __syncthreads();
+      for (int i = tid; i < kept; i += kThreads) {
+        const u64 key = sh_.s.key[i];
+        const int index = (1 << kIndexBits) - 1 - static_cast<int>(key & ((1u << kIndexBits) - 1));
+        const u64 m = static_cast<u64>(mass(key_value(static_cast<uint32_t>(key >> kIndexBits))) * to_fixed_);
+        if (level == 0)
+          atomicAdd(&sh_.s.bin[index / width], m);
+        else if (index >= lo && index < lo + width)
+          sh_.s.bin[index - lo] = m;
+      }
+      if (tid == 0) sh_.found = kThreads;
+      __syncthreads();
+      const u64 in = sh_.s.bin[tid], run = block_scan(in, level == 0 ? sh_.warp_u : sh_.warp_v);
+      if (level == 0) {
+        for (int w = 0; w < kWarps; ++w) total += sh_.warp_u[w];
+        target_in = u_of(total, share);
+      }
+      if (run > target_in && run - in <= target_in) {
+        sh_.found = tid;
+        sh_.cut_mass = run - in;
+      }
+      __syncthreads();
+      if (level == 0) {
+        lo = sh_.found * width;
+        target_in -= sh_.cut_mass;
+        __syncthreads();
+      }
+    }
+    const int token = lo + sh_.found;
+    for (int i = tid; i < kept; i += kThreads)
+      if ((1 << kIndexBits) - 1 - static_cast<int>(sh_.s.key[i] & ((1u << kIndexBits) - 1)) == token)
+        put_token(a, row, token, key_value(static_cast<uint32_t>(sh_.s.key[i] >> kIndexBits)),
+                  kept == 1 ? 1.f : __fdiv_rn(static_cast<float>(total), to_fixed_));
+    return true;
+  }
+
+  // Descending bitonic sort of sh_.s.key[0 .. size), size a power of two.
+  SA_DEV void sort_keys(int size) {
+    for (int k = 2; k <= size; k *= 2)
+      for (int j = k / 2; j > 0; j /= 2) {
+        for (int i = threadIdx.x; i < size / 2; i += kThreads) {
+          const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
+          const u64 x = sh_.s.key[lo], y = sh_.s.key[hi];
+          if ((x < y) == ((lo & k) == 0)) sh_.s.key[lo] = y, sh_.s.key[hi] = x;
+        }
+        // pairs closer than 32 stay inside the 64 keys of one warp
+        if (j > 32)
+          __syncthreads();
+        else if (j == 1 && k >= 64)
+          __syncthreads();
+        else
+          __syncwarp();
+      }
+    __syncthreads();
+  }
+
+  SA_DEV int block_sum_int(int x) {
+    x = warp_sum(x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh_.warp_u[threadIdx.x >> 5] = x;
+    __syncthreads();
+    int s = 0;
+    for (int w = 0; w < kWarps; ++w) s += static_cast<int>(sh_.warp_u[w]);
+    __syncthreads();
+    return s;
   }
 
   // f(x, index) for the slice's candidates.
   template <class F>
   SA_DEV void each_candidate(F f) {
-    if (list_n_ <= kList) {
-      for (int i = threadIdx.x; i < list_n_; i += kThreads) {
-        const int at = sh_.list[i];
-        f(E::one(raw_[at + shift_]), first_ + at);
-      }
-    } else {
-      each_vector([&](const float* x, int base) {
+    each_vector([&](const float* x, int base) {
 #pragma unroll
-        for (int e = 0; e < E::kVec; ++e)
-          if (x[e] >= floor_ && x[e] > -INFINITY) f(x[e], base + e);
-      });
-    }
+      for (int e = 0; e < E::kVec; ++e)
+        if (x[e] >= floor_ && x[e] > -INFINITY) f(x[e], base + e);
+    });
   }
 
   SA_DEV int step_of(float x) const { return static_cast<int>(fminf((max_ - x) * per_step_, kBins - 1.f)); }
@@ -389,50 +599,55 @@ class Row {
   // Histogram of what bin_of gives a bin (>= 0), summed over the cluster; the
   // first bin at which count or mass reaches the target, starting from before.
   template <class F>
-  SA_DEV Pick histogram(bool by_count, double target, u64 count0, u64 mass0, F bin_of) {
+  SA_DEV Pick histogram(bool by_count, u64 target, float top_p, u64 count0, u64 mass0, F bin_of) {
     const int tid = threadIdx.x;
-    for (int i = tid; i < kBins; i += kThreads) sh_.count[i] = sh_.mass_hi[i] = sh_.mass_lo[i] = 0;
+    for (int i = tid; i < kBins; i += kThreads) sh_.h.count[i] = sh_.h.mass_hi[i] = sh_.h.mass_lo[i] = 0;
     __syncthreads();
     each_candidate([&](float x, int index) {
       const int bin = bin_of(x, index);
       if (bin < 0) return;
       const u64 m = fixed(x);
-      atomicAdd(&sh_.count[bin], 1u);
-      atomicAdd(&sh_.mass_hi[bin], static_cast<uint32_t>(m >> kLowBits));
-      atomicAdd(&sh_.mass_lo[bin], static_cast<uint32_t>(m & ((1u << kLowBits) - 1)));
+      atomicAdd(&sh_.h.count[bin], 1u);
+      atomicAdd(&sh_.h.mass_hi[bin], static_cast<uint32_t>(m >> kLowBits));
+      atomicAdd(&sh_.h.mass_lo[bin], static_cast<uint32_t>(m & ((1u << kLowBits) - 1)));
     });
-    cluster_.sync();
+    sync_all();
     const int share = kBins / ctas_;
     for (int i = rank_ * share + tid; i < static_cast<int>(rank_ + 1) * share; i += kThreads) {
       uint32_t n = 0;
       u64 m = 0;
       for (unsigned r = 0; r < ctas_; ++r) {
-        n += cluster_.map_shared_rank(sh_.count, r)[i];
-        m += (static_cast<u64>(cluster_.map_shared_rank(sh_.mass_hi, r)[i]) << kLowBits) +
-             cluster_.map_shared_rank(sh_.mass_lo, r)[i];
+        n += cluster_.map_shared_rank(sh_.h.count, r)[i];
+        m += (static_cast<u64>(cluster_.map_shared_rank(sh_.h.mass_hi, r)[i]) << kLowBits) +
+             cluster_.map_shared_rank(sh_.h.mass_lo, r)[i];
       }
-      cluster_.map_shared_rank(sh_.all_count, 0)[i] = n;
-      cluster_.map_shared_rank(sh_.all_mass, 0)[i] = m;
+      cluster_.map_shared_rank(sh_.h.all_count, 0)[i] = n;
+      cluster_.map_shared_rank(sh_.h.all_mass, 0)[i] = m;
     }
-    cluster_.sync();
+    sync_all();
     if (rank_ == 0) {
       constexpr int kPer = kBins / kThreads;
       u64 n = 0, m = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) n += sh_.all_count[tid * kPer + j], m += sh_.all_mass[tid * kPer + j];
+      for (int j = 0; j < kPer; ++j) n += sh_.h.all_count[tid * kPer + j], m += sh_.h.all_mass[tid * kPer + j];
       const u64 n_in = block_scan(n, sh_.warp_u), m_in = block_scan(m, sh_.warp_v);
       if (tid == 0) sh_.found = kBins;
       __syncthreads();
       u64 nb = count0 + n_in - n, mb = mass0 + m_in - m;
-      Pick p;
+      if (target == 0) {
+        u64 candidates = 0;
+        for (int w = 0; w < kWarps; ++w) candidates += sh_.warp_v[w];
+        target = part_of(whole_mass(candidates), top_p);
+      }
+      Pick p, lastp;
+      p.target = lastp.target = target;
       p.bin = kBins;
       int last = -1;  // the thread's last bin with members
-      Pick lastp;
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const int bin = tid * kPer + j;
-        const u64 c = sh_.all_count[bin], ms = sh_.all_mass[bin];
-        const bool reached = by_count ? static_cast<double>(nb + c) >= target : static_cast<double>(mb + ms) >= target;
+        const u64 c = sh_.h.all_count[bin], ms = sh_.h.all_mass[bin];
+        const bool reached = (by_count ? nb + c : mb + ms) >= target;
         if (c > 0) last = bin, lastp.bin = bin, lastp.members = c, lastp.count = nb, lastp.mass = mb;
         if (reached && c > 0 && p.bin == kBins) p.bin = bin, p.members = c, p.count = nb, p.mass = mb;
         nb += c;
@@ -448,14 +663,14 @@ class Row {
         if (last >= 0) atomicMax(&sh_.found, last);
         __syncthreads();
         if (last >= 0 && sh_.found == last) sh_.pick = lastp;
-        if (sh_.found < 0 && tid == 0) sh_.pick = Pick{-1, 0, count0, mass0};
+        if (sh_.found < 0 && tid == 0) sh_.pick = Pick{-1, 0, count0, mass0, target};
       } else if (p.bin == hit) {
         sh_.pick = p;
       }
       __syncthreads();
       if (tid > 0 && tid < ctas_) *cluster_.map_shared_rank(&sh_.pick, tid) = sh_.pick;
     }
-    cluster_.sync();
+    sync_all();
     return sh_.pick;
   }
 
@@ -470,10 +685,11 @@ class Row {
 
   // Moves cut_ to the key of the last candidate that is kept and returns the
   // mass of the kept ones.  Candidates below the present cut do not count.
-  SA_DEV u64 search(bool by_count, double target) {
+  // Target 0: top_p of the mass of everything.
+  SA_DEV u64 search(bool by_count, u64 target, float top_p) {
     const int tid = threadIdx.x;
     const u64 cut = cut_;
-    Pick p = histogram(by_count, target, 0, 0, [&](float x, int index) {
+    Pick p = histogram(by_count, target, top_p, 0, 0, [&](float x, int index) {
       return full_key(x, index) >= cut ? step_of(x) : -1;
     });
     const int step = p.bin;
@@ -504,7 +720,7 @@ class Row {
     while (p.members > kGather) {  // keys differ, so each turn leaves fewer
       int shift = 0;
       while (((hi - lo) >> shift) >= kBins) ++shift;
-      p = histogram(by_count, target, p.count, p.mass, [&](float x, int index) {
+      p = histogram(by_count, p.target, 0.f, p.count, p.mass, [&](float x, int index) {
         const u64 key = full_key(x, index);
         return key >= cut && key >= lo && key <= hi && step_of(x) == step ? static_cast<int>((hi - key) >> shift) : -1;
       });
@@ -515,11 +731,11 @@ class Row {
     }
     // the members to CTA 0, which ranks them
     if (tid == 0) sh_.gathered = 0;
-    cluster_.sync();
+    sync_all();
     {
       int* n = cluster_.map_shared_rank(&sh_.gathered, 0);
-      u64* keys = cluster_.map_shared_rank(sh_.key, 0);
-      u64* masses = cluster_.map_shared_rank(sh_.key_mass, 0);
+      u64* keys = cluster_.map_shared_rank(sh_.h.key, 0);
+      u64* masses = cluster_.map_shared_rank(sh_.h.key_mass, 0);
       each_candidate([&](float x, int index) {
         const u64 key = full_key(x, index);
         if (key >= cut && key >= lo && key <= hi && step_of(x) == step) {
@@ -528,25 +744,25 @@ class Row {
         }
       });
     }
-    cluster_.sync();
+    sync_all();
     if (rank_ == 0) {
       const int n = min(sh_.gathered, kGather);
       u64 key = 0;
       if (tid < n) {
-        key = sh_.key[tid];
+        key = sh_.h.key[tid];
         int r = 0;
-        for (int j = 0; j < n; ++j) r += sh_.key[j] > key;
-        sh_.sorted[r] = key;
-        sh_.sorted_mass[r] = sh_.key_mass[tid];
+        for (int j = 0; j < n; ++j) r += sh_.h.key[j] > key;
+        sh_.h.sorted[r] = key;
+        sh_.h.sorted_mass[r] = sh_.h.key_mass[tid];
       }
       if (tid == 0) sh_.found = n - 1;
       __syncthreads();
-      const u64 m = p.mass + block_scan(tid < n ? sh_.sorted_mass[tid] : 0, sh_.warp_u);
-      const bool reached = by_count ? static_cast<double>(p.count + tid + 1) >= target : static_cast<double>(m) >= target;
+      const u64 m = p.mass + block_scan(tid < n ? sh_.h.sorted_mass[tid] : 0, sh_.warp_u);
+      const bool reached = (by_count ? p.count + tid + 1 : m) >= p.target;
       if (tid < n && reached) atomicMin(&sh_.found, tid);
       __syncthreads();
       if (tid == max(sh_.found, 0)) {
-        sh_.cut = n > 0 ? sh_.sorted[tid] : cut;
+        sh_.cut = n > 0 ? sh_.h.sorted[tid] : cut;
         sh_.cut_mass = m;
       }
       __syncthreads();
@@ -555,82 +771,99 @@ class Row {
         *cluster_.map_shared_rank(&sh_.cut_mass, tid) = sh_.cut_mass;
       }
     }
-    cluster_.sync();
+    sync_all();
     cut_ = sh_.cut;
     return sh_.cut_mass;
   }
 
-  SA_DEV u64 kept_mass(float x, int index) const {
-    if (static_cast<u64>(order_key(x)) < (cut_ >> kIndexBits) || full_key(x, index) < cut_) return 0;
+  SA_DEV float kept_mass(float x, int index) const {
+    if (static_cast<u64>(order_key(x)) < (cut_ >> kIndexBits) || full_key(x, index) < cut_) return 0.f;
     const float e = mass(x);
-    return e >= min_mass_ ? static_cast<u64>(e * to_fixed_) : 0;
+    return e >= min_mass_ ? e : 0.f;
   }
 
-  // Index order: a CTA's slice, in it the warps' runs of vectors, in those the turns, lanes and elements.
-  SA_DEV void sample(const SampleArgs& a, int row, float u, double inv_t) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (vectors_ + kWarps - 1) / kWarps;
-    const int v0 = min(warp * per, vectors_), v1 = min(v0 + per, vectors_);
-    const auto vector_mass = [&](int v, u64* each) {
-      u64 s = 0;
-      float f[E::kVec];
-      E::unpack(reinterpret_cast<const uint4*>(raw_)[v], f);
+  // The kept mass of every chunk, by warp.
+  SA_DEV void chunk_masses() {
+    __syncthreads();
+    for (int c = 0; c < chunks(); ++c) {
+      float sum = 0.f;
+      turns_of_vectors(c * chunk_turns_, min((c + 1) * chunk_turns_, (vectors_ + kThreads - 1) / kThreads),
+                       [&](const float* x, int base) {
 #pragma unroll
-      for (int e = 0; e < E::kVec; ++e) {
-        const u64 m = kept_mass(f[e], first_ + v * E::kVec + e - shift_);
-        if (each != nullptr) each[e] = m;
-        s += m;
-      }
-      return s;
-    };
-    u64 mine = 0;
-    for (int v = v0 + lane; v < v1; v += 32) mine += vector_mass(v, nullptr);
-    mine = warp_sum(mine);
-    __syncthreads();
-    if (lane == 0) sh_.warp_u[warp] = mine;
-    __syncthreads();
-    u64 before = 0, slice = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sh_.warp_u[w];
-      slice += sh_.warp_u[w];
+                         for (int e = 0; e < E::kVec; ++e)
+                           if (x[e] >= floor_) sum += kept_mass(x[e], base + e);
+                       });
+      sum = warp_sum(sum);
+      if ((threadIdx.x & 31) == 0) sh_.chunk_mass[c][threadIdx.x >> 5] = static_cast<u64>(sum * kSumOne);
     }
-    u64 total = 0, earlier = 0;
+    __syncthreads();
+  }
+
+  // Index order: the CTAs' slices, in them chunks, turns, threads and elements.
+  SA_DEV void sample_chunks(const SampleArgs& a, int row, float share) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    // a lane's chunk (kChunks <= 32), and the slice, in every warp alike
+    u64 mine = 0;
+    if (lane < chunks())
+      for (int w = 0; w < kWarps; ++w) mine += sh_.chunk_mass[lane][w];
+    const u64 chunk_upto = warp_scan(mine);
+    const u64 slice = __shfl_sync(0xffffffffu, chunk_upto, 31);
+    u64 total = 0, before = 0;
     unsigned r = 0;
     exchange(slice, [&](u64 v) {
-      if (r++ < rank_) earlier += v;
+      if (r++ < rank_) before += v;
       total += v;
     });
-    // below 1, so that the sum over all exceeds the target
-    const double target = static_cast<double>(fminf(fmaxf(u, 0.f), 0.99999994f)) * static_cast<double>(total);
-    before += earlier;
-    if (!(static_cast<double>(before) <= target && static_cast<double>(before + mine) > target)) return;
-    for (int v = v0; v < v1; v += 32) {
-      u64 each[E::kVec];
-      const u64 m = v + lane < v1 ? vector_mass(v + lane, each) : 0;
-      const u64 upto = before + warp_scan(m);
-      const unsigned hit = __ballot_sync(0xffffffffu, static_cast<double>(upto) > target);
-      if (hit == 0) {
-        before = __shfl_sync(0xffffffffu, upto, 31);
-        continue;
-      }
-      if (lane == __ffs(hit) - 1) {
-        u64 run = upto - m;
+    const u64 target = u_of(total, share);
+    if (!(before <= target && before + slice > target)) return;  // exactly one CTA holds the target
+    const unsigned beyond = __ballot_sync(0xffffffffu, before + chunk_upto > target);
+    const int chunk = __ffs(beyond) - 1;
+    before += __shfl_sync(0xffffffffu, chunk_upto - mine, chunk);
+    if (tid == 0) sh_.found = sh_.last = -1;
+    __syncthreads();
+    const int turns = (vectors_ + kThreads - 1) / kThreads;
+    for (int t = chunk * chunk_turns_; t < min((chunk + 1) * chunk_turns_, turns); ++t) {
+      const int v = t * kThreads + tid;
+      u64 e[E::kVec], own = 0;
+      int last = -1;
+      if (v < vectors_) {
+        float x[E::kVec];
+        E::unpack(load(v), x);
 #pragma unroll
-        for (int e = 0; e < E::kVec; ++e) {
-          run += each[e];
-          if (static_cast<double>(run) > target) {
-            const int at = (v + lane) * E::kVec + e;
-            const double d = (static_cast<double>(E::one(raw_[at])) - static_cast<double>(max_)) * inv_t;
-            const double kept = static_cast<double>(total) / static_cast<double>(to_fixed_);
-            put(a, row, first_ + at - shift_, static_cast<float>(d - log(z_)), static_cast<float>(d - log(kept)));
-            break;
+        for (int i = 0; i < E::kVec; ++i) {
+          e[i] = x[i] >= floor_ ? static_cast<u64>(kept_mass(x[i], index_of(v) + i) * kSumOne) : 0;
+          own += e[i];
+          if (e[i] > 0) last = i;
+        }
+      }
+      const u64 upto = before + block_scan(own, sh_.warp_u);
+      if (last >= 0) {
+        atomicMax(&sh_.last, v * E::kVec + last);
+        if (upto > target && upto - own <= target) {
+          u64 run = upto - own;
+          bool hit = false;
+#pragma unroll
+          for (int i = 0; i < E::kVec; ++i) {
+            run += e[i];
+            if (!hit && run > target) sh_.found = v * E::kVec + i, hit = true;
           }
         }
       }
-      return;
+      __syncthreads();
+      if (sh_.found >= 0) break;
+      for (int w = 0; w < kWarps; ++w) before += sh_.warp_u[w];
+      __syncthreads();
     }
+    // the chunk's sum was rounded elsewhere: where the walk falls short of the target, the last kept one
+    const int at = sh_.found >= 0 ? sh_.found : sh_.last;
+    if (tid == 0 && at >= 0)
+      put_token(a, row, first_ + at - shift_, E::one(base_[at]), static_cast<float>(total) * (1.f / kSumOne));
   }
 
+  SA_DEV void put_token(const SampleArgs& a, int row, int token, float x, float kept) const {
+    const float d = __fdiv_rn(x - max_, temperature_);
+    put(a, row, token, d - ln(z_), d - ln(kept));
+  }
   static SA_DEV void put(const SampleArgs& a, int row, int token, float logp, float logq) {
     a.tokens[row] = token;
     a.logp[row] = logp;
@@ -638,39 +871,38 @@ class Row {
   }
 
   Shared& sh_;
-  T* raw_;
   cg::cluster_group cluster_;
+  const T* base_;
   unsigned rank_, ctas_;
   int parity_ = 0;
-  int vocab_, first_, shift_, vectors_, list_n_;
-  float max_, scale_, to_fixed_, min_mass_, floor_, per_step_;
-  double z_;
+  int vocab_, first_, shift_, end_, vectors_, chunk_turns_, pass1_parts_;
+  float temperature_, scale_, max_, z_, to_fixed_, min_mass_, floor_ = -INFINITY, per_step_;
   u64 cut_;
 };
 
 template <int kType>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a, int slice) {
+__global__ void __launch_bounds__(kThreads, SMP_PER) sample_kernel(const SampleArgs a, int slice) {
   extern __shared__ __align__(16) uint8_t smem[];
-  Shared& sh = *reinterpret_cast<Shared*>(smem);
-  Row<kType> row(sh, reinterpret_cast<typename Elem<kType>::T*>(smem + (sizeof(Shared) + 15) / 16 * 16));
+  Row<kType> row(*reinterpret_cast<Shared*>(smem));
   row.run(a, blockIdx.x / cg::this_cluster().num_blocks(), slice);
 }
 
 template <int kType>
 cudaError_t launch_type(const SampleArgs& a, cudaStream_t s) {
+  // CTAs per row go by the vocabulary alone, so that a row's result does not
+  // depend on the batch around it.
   int ctas = 1;
-  while (ctas < kMaxCluster && ceil_div(a.vocab, ctas) > 4096) ctas *= 2;
+  while (ctas < SMP_MAX && ceil_div(a.vocab, ctas) > SMP_SLICE) ctas *= 2;
   const int vec = Elem<kType>::kVec;
   const int slice = ceil_div(ceil_div(a.vocab, ctas), vec) * vec;
-  const size_t smem =
-      (sizeof(Shared) + 15) / 16 * 16 + (static_cast<size_t>(slice) + 2 * vec) * sizeof(typename Elem<kType>::T);
   const auto kernel = sample_kernel<kType>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(kernel, sizeof(Shared));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = sizeof(Shared);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -172,3 +172,14 @@ def test_captured_and_replayed():
         graph.replay()
         want = sa.sample_tokens(x, u, **kw)
         assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("rows", [1, 40, 200])
+@pytest.mark.parametrize("k,p,m", [(200, 0.95, 0.0), (3000, 1.0, 0.0), (9000, 0.9, 0.01), (0, 0.95, 0.02), (0, 0.4, 0.0),
+                                   (0, 1.0, 1e-6), (40, 1.0, 0.3), (2048, 0.999, 0.0)])
+def test_rows_by_cta_and_by_cluster(rows, k, p, m):
+    """Batches on both sides of the rules for the cluster's size, lists on both sides of what is sorted at once."""
+    rng = np.random.RandomState(rows + k)
+    x = torch.from_numpy(-1.3 * np.log(1 + rng.rand(rows, 30011) * 30011) + rng.randn(rows, 30011)).float().to(DEV)
+    x[::3, 700:] = float("-inf")  # all that is allowed lies in one place
+    check(x, rng.rand(rows), np.full(rows, 0.9), [k] * rows, [p] * rows, [m] * rows)
