@@ -26,10 +26,11 @@
 //
 // Arithmetic.  e is fp32 (the difference before the scale: a large logit must
 // not lose what tells it from its neighbours).  Partial sums of a thread are
-// fp32, everything above is 64-bit fixed point: the slice sums of Z in units
-// of 2^-40, masses under selection in units of Z 2^-43.  Integer sums are the
+// fp32, and so is Z, in a fixed order; masses that decide are 64-bit fixed
+// point: those of chunks in units of 2^-40, those of logits under selection
+// in units of Z 2^-43.  Integer sums are the
 // same in every order, so histogram atomics leave the result reproducible,
-// and 2^18 roundings lose at most 2^-22 (Z) or 2^-25 of the whole.  FP64 is
+// and 2^18 roundings lose at most 2^-22 (chunks) or 2^-25 of the whole.  FP64 is
 // not used: its rate on this GPU would cost more than all the rest.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
@@ -44,7 +45,7 @@ namespace {
 
 #ifndef SMP_PER
 #define SMP_PER 2
-#define SMP_MAX 8
+#define SMP_MAX 4
 #define SMP_SLICE 16384
 #endif
 
@@ -62,6 +63,7 @@ constexpr int kUnroll = 4;                // vectors a thread has in flight
 constexpr float kMassOne = 8796093022208.f;   // 2^43
 constexpr float kSumOne = 1099511627776.f;    // 2^40
 constexpr int kLowBits = 13;
+constexpr float kLowest = -3.402823466e38f;   // fp32's lowest finite value
 
 typedef unsigned long long u64;
 
@@ -85,8 +87,9 @@ struct Sorted {
 };
 
 struct Shared {
-  u64 exchange[2][kMaxCluster];
+  u64 exchange[2][kMaxCluster][2];
   u64 warp_u[kWarps], warp_v[kWarps];
+  uint32_t warp_key[kWarps];
   float chunk_max[kChunks][kWarps], chunk_sum[kChunks][kWarps];
   u64 chunk_mass[kChunks][kWarps];
   u64 cut, cut_mass;
@@ -107,6 +110,9 @@ struct Elem<0> {
   static SA_DEV void unpack(uint4 v, float* x) {
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
+  static SA_DEV float largest(uint4 v) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
   static SA_DEV float one(T v) { return v; }
   static SA_DEV T lowest() { return -INFINITY; }
 };
@@ -118,6 +124,15 @@ struct Elem<1> {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  static SA_DEV float largest(uint4 v) {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  static SA_DEV uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+    return d;
   }
   static SA_DEV float one(T v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
   static SA_DEV T lowest() { return 0xff80u; }
@@ -133,6 +148,16 @@ struct Elem<2> {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
       x[2 * i] = f.x, x[2 * i + 1] = f.y;
     }
+  }
+  static SA_DEV float largest(uint4 v) {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return fmaxf(f.x, f.y);
+  }
+  static SA_DEV uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+    return d;
   }
   static SA_DEV float one(T v) { return __half2float(*reinterpret_cast<const __half*>(&v)); }
   static SA_DEV T lowest() { return 0xfc00u; }
@@ -206,13 +231,14 @@ class Row {
     const bool by_count = k > 0 && k < vocab_, by_mass = top_p < 1.f, by_floor = min_p > 0.f;
     const bool chunks = !by_count && !by_mass && !by_floor;
 
-    const float thread_max = pass1(chunks);
-    cluster_.barrier_wait();  // every CTA of the cluster runs: its shared memory may be written
     if (!valid) {
+      cluster_.barrier_wait();
       if (rank_ == 0 && tid == 0) put(a, row, -1, NAN, NAN);
       return;
     }
-    reduce_max_and_sum();
+    const float thread_max = pass1(chunks);
+    cluster_.barrier_wait();  // every CTA of the cluster runs: its shared memory may be written
+    reduce(thread_max, by_count && k > 1 ? k : 0);
     if (z_ == 0.f || max_ == INFINITY || z_ != z_) {
       const float v = z_ == 0.f ? -INFINITY : NAN;  // nothing is allowed, or something is not a number
       if (rank_ == 0 && tid == 0) put(a, row, -1, v, v);
@@ -222,11 +248,7 @@ class Row {
 
     if (k == 1) {  // the largest, of equal ones the lowest index
       int at = vocab_;
-      each_vector([&](const float* v, int base) {
-#pragma unroll
-        for (int e = E::kVec - 1; e >= 0; --e)
-          if (v[e] == max_) at = min(at, base + e);
-      });
+      each_from(max_, [&](float, int index) { at = min(at, index); });
       at = block_min(at);
       int best = vocab_;
       exchange(static_cast<u64>(at), [&](u64 v) { best = min(best, static_cast<int>(v)); });
@@ -243,7 +265,7 @@ class Row {
     }
     // what lies below floor is not kept, nor does its mass count for top-p
     float floor = -INFINITY;
-    if (by_count) floor = count_floor(thread_max, k);
+    if (by_count) floor = count_floor();
     if (by_floor && !(by_count && by_mass)) floor = fmaxf(floor, mass_floor(min_mass_ * 0.999f));
     if (floor > -INFINITY && sample_list(a, row, floor, by_count ? k : vocab_, by_mass ? top_p : 1.f, by_count, share))
       return;
@@ -256,8 +278,8 @@ class Row {
       const float range = floor > -INFINITY ? max_ - floor : 30.f * temperature_;
       per_step_ = range > 0.f ? fminf((kBins - 1) / range, 1e30f) : 0.f;
       u64 kept = 0;
-      if (by_count) kept = search(true, k, 0.f);
-      if (by_mass) search(false, by_count ? part_of(kept, top_p) : 0, top_p);
+      if (by_count) kept = search(true, k, 0.f, by_mass);
+      if (by_mass) search(false, by_count ? part_of(kept, top_p) : 0, top_p, true);
     }
     chunk_masses();
     sample_chunks(a, row, share);
@@ -267,15 +289,15 @@ class Row {
   // Every CTA of the cluster gives a number and takes all of them in rank order.
   template <class F>
   SA_DEV void exchange(u64 v, F take) {
-    u64* buf = sh_.exchange[parity_];
-    parity_ ^= 1;  // the other half may still be read by a slower CTA
     if (ctas_ == 1) {
       take(v);
       return;
     }
-    if (threadIdx.x < ctas_) cluster_.map_shared_rank(buf, threadIdx.x)[rank_] = v;
+    u64 (*buf)[2] = sh_.exchange[parity_];
+    parity_ ^= 1;  // the other half may still be read by a slower CTA
+    if (threadIdx.x < ctas_) cluster_.map_shared_rank(&buf[0][0], threadIdx.x)[2 * rank_] = v;
     cluster_.sync();
-    for (unsigned r = 0; r < ctas_; ++r) take(buf[r]);
+    for (unsigned r = 0; r < ctas_; ++r) take(buf[r][0]);
   }
   SA_DEV void sync_all() {
     if (ctas_ == 1)
@@ -300,90 +322,137 @@ class Row {
   }
   SA_DEV int index_of(int v) const { return first_ + v * E::kVec - shift_; }
 
-  // f(values, index of the first) for the slice's vectors in [turn0, turn1) x threads; padding is -inf.
+  // f(vector, its number) for the slice's vectors in [turn0, turn1) x threads; padding is -inf.
   template <class F>
   SA_DEV void turns_of_vectors(int turn0, int turn1, F f) {
-    for (int t = turn0; t < turn1; t += kUnroll) {
+    const int tid = threadIdx.x, whole = end_ / E::kVec / kThreads;  // turns of whole vectors, the first one aside
+    const auto checked = [&](int t) {
+      const int v = t * kThreads + tid;
+      if (v < vectors_) f(load(v), v);
+    };
+    int t = turn0;
+    if (t == 0 && shift_ > 0 && t < turn1) checked(t++);
+    for (; t + kUnroll <= min(turn1, whole); t += kUnroll) {
       uint4 w[kUnroll];
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int v = (t + i) * kThreads + threadIdx.x;
-        if (v < vectors_) w[i] = load(v);
-      }
+      for (int i = 0; i < kUnroll; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(base_) + (t + i) * kThreads + tid);
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int v = (t + i) * kThreads + threadIdx.x;
-        if (v < vectors_) {
-          float x[E::kVec];
-          E::unpack(w[i], x);
-          f(x, index_of(v));
-        }
-      }
+      for (int i = 0; i < kUnroll; ++i) f(w[i], (t + i) * kThreads + tid);
     }
+#pragma unroll 1
+    for (; t < turn1; ++t) checked(t);
   }
   template <class F>
   SA_DEV void each_vector(F f) {
     turns_of_vectors(0, (vectors_ + kThreads - 1) / kThreads, f);
+  }
+  // f(x, index) for the slice's logits from floor on, above -inf.
+  template <class F>
+  SA_DEV void each_from(float floor, F f) {
+    each_vector([&](uint4 w, int v) {
+      if (!(E::largest(w) >= floor)) return;
+      float x[E::kVec];
+      E::unpack(w, x);
+#pragma unroll
+      for (int e = 0; e < E::kVec; ++e)
+        if (x[e] >= floor && x[e] > -INFINITY) f(x[e], index_of(v) + e);
+    });
   }
   SA_DEV int chunks() const {
     return ((vectors_ + kThreads - 1) / kThreads + chunk_turns_ - 1) / chunk_turns_;
   }
 
   // Maximum and sum of one pass, the sum relative to the running maximum; per
-  // chunk and warp, or (chunks false) per warp as chunk 0.
+  // chunk and warp, or (by_chunk false) per warp as chunk 0.
   SA_DEV float pass1(bool by_chunk) {
     const int warp = threadIdx.x >> 5, turns = (vectors_ + kThreads - 1) / kThreads;
     const int step = by_chunk ? chunk_turns_ : max(turns, 1);
-    float top = -3.402823466e38f;  // so that a difference with -inf is -inf
+    float top = kLowest;  // so that a difference with -inf is -inf
+    // In the ordinary range the exponent is one fused x * scale - ref, with
+    // ref the rounded top * scale; what ref was rounded by is put right at
+    // the end.  Beyond it (where ref's rounding would swamp the exponent) the
+    // difference is taken first.
+    float ref = 0.f;
+    bool fused = false;
     for (int c = 0; c * step < max(turns, 1); ++c) {
-      float sum = 0.f;
-      turns_of_vectors(c * step, min((c + 1) * step, turns), [&](const float* x, int) {
-        float m = x[0];
-#pragma unroll
-        for (int e = 1; e < E::kVec; ++e) m = fmaxf(m, x[e]);
+      float2 sum = make_float2(0.f, 0.f);
+      turns_of_vectors(c * step, min((c + 1) * step, turns), [&](uint4 w, int) {
+        const float m = E::largest(w);
+        float x[E::kVec];
+        E::unpack(w, x);
         if (m > top) {
-          sum *= ex2((top - m) * scale_);
+          const float next = m * scale_;
+          const bool next_fused = fabsf(next) < 1048576.f;
+          const float f = fused && next_fused ? ex2(ref - next) : ex2((top - m) * scale_);
+          sum.x *= f;
+          sum.y *= f;
           top = m;
+          ref = next;
+          fused = next_fused;
         }
+        if (fused) {
+          const float2 c2 = make_float2(scale_, scale_), r2 = make_float2(-ref, -ref);
 #pragma unroll
-        for (int e = 0; e < E::kVec; ++e) sum += ex2((x[e] - top) * scale_);
+          for (int e = 0; e < E::kVec; e += 2) {
+            const float2 t = ffma2(make_float2(x[e], x[e + 1]), c2, r2);
+            sum = fadd2(sum, make_float2(ex2(t.x), ex2(t.y)));
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < E::kVec; ++e) sum.x += ex2((x[e] - top) * scale_);
+        }
       });
+      float total = sum.x + sum.y;
+      if (fused) total *= ex2(-fmaf(top, scale_, -ref));
       const float warp_top = warp_max(top);
-      const float warp_total = warp_sum(sum * ex2((top - warp_top) * scale_));
+      const float warp_total = warp_sum(total * ex2((top - warp_top) * scale_));
       if ((threadIdx.x & 31) == 0) sh_.chunk_max[c][warp] = warp_top, sh_.chunk_sum[c][warp] = warp_total;
     }
     pass1_parts_ = (by_chunk ? chunks() : 1) * kWarps;
-    __syncthreads();
     return top;
   }
 
-  // max_ and z_ (0: no logit above -inf, NaN: a NaN or +inf among them), and
-  // the chunks' sums in fixed point, relative to max_.  Every warp does it all.
-  SA_DEV void reduce_max_and_sum() {
-    const int lane = threadIdx.x & 31;
+  // From pass 1, with one exchange: max_, z_ (0: no logit above -inf, NaN: a
+  // NaN or +inf among them), the chunks' sums relative to max_ in fixed
+  // point, and the bound of the k largest.  Every warp does it all.
+  SA_DEV void reduce(float thread_max, int k) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t key = warp_quota_key(thread_max, k);
+    if (lane == 0) sh_.warp_key[warp] = key;
+    __syncthreads();
     const float* maxima = &sh_.chunk_max[0][0];
     const float* sums = &sh_.chunk_sum[0][0];
-    float top = -3.402823466e38f;
+    float top = kLowest, sum = 0.f;
     for (int i = lane; i < pass1_parts_; i += 32) top = fmaxf(top, maxima[i]);
-    max_ = -3.402823466e38f;
-    exchange(__float_as_uint(warp_max(top)),
-             [&](u64 v) { max_ = fmaxf(max_, __uint_as_float(static_cast<uint32_t>(v))); });
-    u64 sum = 0;
-    bool bad = false;
-    for (int i = lane; i < pass1_parts_; i += 32) {
-      const float s = sums[i] * ex2((maxima[i] - max_) * scale_);
-      bad |= s != s;
-      const u64 fixed = static_cast<u64>(s * kSumOne);
-      sum += fixed;
-      if (threadIdx.x < 32) (&sh_.chunk_mass[0][0])[i] = fixed;
-    }
+    top = warp_max(top);
+    for (int i = lane; i < pass1_parts_; i += 32) sum += sums[i] * ex2((maxima[i] - top) * scale_);
     sum = warp_sum(sum);
-    u64 all = 0;
-    exchange(__any_sync(0xffffffffu, bad) ? ~0ull : sum, [&](u64 v) {
-      bad |= v == ~0ull;
-      all += v;
-    });
-    z_ = __any_sync(0xffffffffu, bad) ? NAN : static_cast<float>(all) * (1.f / kSumOne);
+    uint32_t least = __reduce_min_sync(0xffffffffu, lane < kWarps ? sh_.warp_key[lane] : 0xffffffffu);
+    if (ctas_ == 1) {
+      max_ = top;
+      z_ = sum;
+    } else {
+      u64 (*buf)[2] = sh_.exchange[parity_];
+      parity_ ^= 1;
+      if (threadIdx.x < ctas_) {
+        u64* to = cluster_.map_shared_rank(&buf[0][0], threadIdx.x) + 2 * rank_;
+        to[0] = static_cast<u64>(__float_as_uint(top)) << 32 | __float_as_uint(sum);
+        to[1] = least;
+      }
+      cluster_.sync();
+      max_ = kLowest;
+      for (unsigned r = 0; r < ctas_; ++r) {
+        max_ = fmaxf(max_, __uint_as_float(static_cast<uint32_t>(buf[r][0] >> 32)));
+        least = min(least, static_cast<uint32_t>(buf[r][1]));
+      }
+      z_ = 0.f;
+      for (unsigned r = 0; r < ctas_; ++r)
+        z_ += __uint_as_float(static_cast<uint32_t>(buf[r][0])) *
+              ex2((__uint_as_float(static_cast<uint32_t>(buf[r][0] >> 32)) - max_) * scale_);
+    }
+    count_key_ = least;
+    for (int i = threadIdx.x; i < pass1_parts_; i += kThreads)
+      (&sh_.chunk_mass[0][0])[i] = static_cast<u64>(sums[i] * ex2((maxima[i] - max_) * scale_) * kSumOne);
     __syncthreads();
   }
 
@@ -428,11 +497,11 @@ class Row {
     return f - fabsf(f) * 2.4e-7f;
   }
 
-  // A value that at least k logits reach: in each warp the k / warps-th
-  // largest of the lanes' maxima, and the least of those over the row's warps.
-  SA_DEV float count_floor(float thread_max, int k) {
+  // The k / warps-th largest of the lanes' maxima, as a key: at least k logits
+  // of the row reach the least of these over the row's warps.
+  SA_DEV uint32_t warp_quota_key(float thread_max, int k) const {
     const int warps = kWarps * ctas_, quota = (k + warps - 1) / warps;
-    if (quota > 32) return -INFINITY;
+    if (k <= 0 || quota > 32) return 0;
     const uint32_t key = order_key(thread_max);
     uint32_t lo = 0;
 #pragma unroll
@@ -440,14 +509,11 @@ class Row {
       const uint32_t mid = lo | 1u << bit;
       if (__popc(__ballot_sync(0xffffffffu, key >= mid)) >= quota) lo = mid;
     }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh_.warp_u[threadIdx.x >> 5] = lo;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) lo = min(lo, static_cast<uint32_t>(sh_.warp_u[w]));
-    uint32_t least = 0xffffffffu;
-    exchange(lo, [&](u64 v) { least = min(least, static_cast<uint32_t>(v)); });
-    const float f = key_value(least);
-    return f > -3.402823466e38f ? f : -INFINITY;  // some warp has too few logits above -inf
+    return lo;
+  }
+  SA_DEV float count_floor() const {
+    const float f = key_value(count_key_);
+    return f > kLowest ? f : -INFINITY;  // key 0, or some warp has too few logits above -inf
   }
 
   // Collects the logits from floor on, sorts them and samples from their
@@ -455,30 +521,29 @@ class Row {
   SA_DEV bool sample_list(const SampleArgs& a, int row, float floor, int k, float top_p, bool by_count, float share) {
     const int tid = threadIdx.x;
     if (tid == 0) sh_.gathered = 0;
+    __syncthreads();
+    each_from(floor, [&](float x, int index) {
+      const int at = atomicAdd(&sh_.gathered, 1);
+      if (at < kList) sh_.s.key[at] = full_key(x, index);
+    });
     sync_all();
-    {
-      int* n = cluster_.map_shared_rank(&sh_.gathered, 0);
-      u64* keys = cluster_.map_shared_rank(sh_.s.key, 0);
-      each_vector([&](const float* x, int base) {
-        float m = x[0];
+    // CTA 0 takes the others' lists behind its own
+    int counts[kMaxCluster], n = 0;
 #pragma unroll
-        for (int e = 1; e < E::kVec; ++e) m = fmaxf(m, x[e]);
-        if (m < floor) return;
+    for (int r = 0; r < kMaxCluster; ++r) {
+      counts[r] = r < static_cast<int>(ctas_) ? *cluster_.map_shared_rank(&sh_.gathered, r) : 0;
+      n += counts[r];
+    }
+    if (n <= kList && rank_ == 0) {
+      int at = counts[0];
 #pragma unroll
-        for (int e = 0; e < E::kVec; ++e)
-          if (x[e] >= floor) {
-            const int at = atomicAdd(n, 1);
-            if (at < kList) keys[at] = full_key(x[e], base + e);
-          }
-      });
+      for (int r = 1; r < kMaxCluster; ++r) {
+        const u64* from = cluster_.map_shared_rank(sh_.s.key, r < static_cast<int>(ctas_) ? r : 0);
+        for (int i = tid; i < counts[r]; i += kThreads) sh_.s.key[at + i] = from[i];
+        at += counts[r];
+      }
     }
-    sync_all();
-    int n = sh_.gathered;
-    if (ctas_ > 1) {
-      int all = 0;
-      exchange(rank_ == 0 ? static_cast<u64>(n) : 0, [&](u64 v) { all += static_cast<int>(v); });
-      n = all;
-    }
+    sync_all();  // the lists have been read
     if (n > kList) return false;
     if (rank_ != 0) return true;
 
@@ -587,11 +652,7 @@ class Row {
   // f(x, index) for the slice's candidates.
   template <class F>
   SA_DEV void each_candidate(F f) {
-    each_vector([&](const float* x, int base) {
-#pragma unroll
-      for (int e = 0; e < E::kVec; ++e)
-        if (x[e] >= floor_ && x[e] > -INFINITY) f(x[e], base + e);
-    });
+    each_from(floor_, f);
   }
 
   SA_DEV int step_of(float x) const { return static_cast<int>(fminf((max_ - x) * per_step_, kBins - 1.f)); }
@@ -599,15 +660,16 @@ class Row {
   // Histogram of what bin_of gives a bin (>= 0), summed over the cluster; the
   // first bin at which count or mass reaches the target, starting from before.
   template <class F>
-  SA_DEV Pick histogram(bool by_count, u64 target, float top_p, u64 count0, u64 mass0, F bin_of) {
+  SA_DEV Pick histogram(bool by_count, u64 target, float top_p, u64 count0, u64 mass0, bool masses, F bin_of) {
     const int tid = threadIdx.x;
     for (int i = tid; i < kBins; i += kThreads) sh_.h.count[i] = sh_.h.mass_hi[i] = sh_.h.mass_lo[i] = 0;
     __syncthreads();
     each_candidate([&](float x, int index) {
       const int bin = bin_of(x, index);
       if (bin < 0) return;
-      const u64 m = fixed(x);
       atomicAdd(&sh_.h.count[bin], 1u);
+      if (!masses) return;
+      const u64 m = fixed(x);
       atomicAdd(&sh_.h.mass_hi[bin], static_cast<uint32_t>(m >> kLowBits));
       atomicAdd(&sh_.h.mass_lo[bin], static_cast<uint32_t>(m & ((1u << kLowBits) - 1)));
     });
@@ -685,11 +747,12 @@ class Row {
 
   // Moves cut_ to the key of the last candidate that is kept and returns the
   // mass of the kept ones.  Candidates below the present cut do not count.
-  // Target 0: top_p of the mass of everything.
-  SA_DEV u64 search(bool by_count, u64 target, float top_p) {
+  // Target 0: top_p of the mass of everything.  Without `masses` (a cut by
+  // count alone) none are summed, and none is returned.
+  SA_DEV u64 search(bool by_count, u64 target, float top_p, bool masses) {
     const int tid = threadIdx.x;
     const u64 cut = cut_;
-    Pick p = histogram(by_count, target, top_p, 0, 0, [&](float x, int index) {
+    Pick p = histogram(by_count, target, top_p, 0, 0, masses, [&](float x, int index) {
       return full_key(x, index) >= cut ? step_of(x) : -1;
     });
     const int step = p.bin;
@@ -720,7 +783,7 @@ class Row {
     while (p.members > kGather) {  // keys differ, so each turn leaves fewer
       int shift = 0;
       while (((hi - lo) >> shift) >= kBins) ++shift;
-      p = histogram(by_count, p.target, 0.f, p.count, p.mass, [&](float x, int index) {
+      p = histogram(by_count, p.target, 0.f, p.count, p.mass, masses, [&](float x, int index) {
         const u64 key = full_key(x, index);
         return key >= cut && key >= lo && key <= hi && step_of(x) == step ? static_cast<int>((hi - key) >> shift) : -1;
       });
@@ -788,10 +851,13 @@ class Row {
     for (int c = 0; c < chunks(); ++c) {
       float sum = 0.f;
       turns_of_vectors(c * chunk_turns_, min((c + 1) * chunk_turns_, (vectors_ + kThreads - 1) / kThreads),
-                       [&](const float* x, int base) {
+                       [&](uint4 w, int v) {
+                         if (!(E::largest(w) >= floor_)) return;
+                         float x[E::kVec];
+                         E::unpack(w, x);
 #pragma unroll
                          for (int e = 0; e < E::kVec; ++e)
-                           if (x[e] >= floor_) sum += kept_mass(x[e], base + e);
+                           if (x[e] >= floor_) sum += kept_mass(x[e], index_of(v) + e);
                        });
       sum = warp_sum(sum);
       if ((threadIdx.x & 31) == 0) sh_.chunk_mass[c][threadIdx.x >> 5] = static_cast<u64>(sum * kSumOne);
@@ -876,6 +942,7 @@ class Row {
   unsigned rank_, ctas_;
   int parity_ = 0;
   int vocab_, first_, shift_, end_, vectors_, chunk_turns_, pass1_parts_;
+  uint32_t count_key_;
   float temperature_, scale_, max_, z_, to_fixed_, min_mass_, floor_ = -INFINITY, per_step_;
   u64 cut_;
 };
