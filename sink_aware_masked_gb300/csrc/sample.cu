@@ -81,7 +81,7 @@ struct Histogram {
   u64 key[kGather], key_mass[kGather], sorted[kGather], sorted_mass[kGather];
 };
 
-struct Sorted {
+struct alignas(16) Sorted {
   u64 key[kList];
   u64 bin[kThreads];  // masses by index
 };
@@ -89,7 +89,6 @@ struct Sorted {
 struct Shared {
   u64 exchange[2][kMaxCluster][2];
   u64 warp_u[kWarps], warp_v[kWarps];
-  uint32_t warp_key[kWarps];
   float chunk_max[kChunks][kWarps], chunk_sum[kChunks][kWarps];
   u64 chunk_mass[kChunks][kWarps];
   u64 cut, cut_mass;
@@ -416,9 +415,8 @@ class Row {
   // NaN or +inf among them), the chunks' sums relative to max_ in fixed
   // point, and the bound of the k largest.  Every warp does it all.
   SA_DEV void reduce(float thread_max, int k) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t key = warp_quota_key(thread_max, k);
-    if (lane == 0) sh_.warp_key[warp] = key;
+    const int lane = threadIdx.x & 31;
+    uint32_t least = quota_key(thread_max, k);
     __syncthreads();
     const float* maxima = &sh_.chunk_max[0][0];
     const float* sums = &sh_.chunk_sum[0][0];
@@ -427,7 +425,6 @@ class Row {
     top = warp_max(top);
     for (int i = lane; i < pass1_parts_; i += 32) sum += sums[i] * ex2((maxima[i] - top) * scale_);
     sum = warp_sum(sum);
-    uint32_t least = __reduce_min_sync(0xffffffffu, lane < kWarps ? sh_.warp_key[lane] : 0xffffffffu);
     if (ctas_ == 1) {
       max_ = top;
       z_ = sum;
@@ -497,23 +494,24 @@ class Row {
     return f - fabsf(f) * 2.4e-7f;
   }
 
-  // The k / warps-th largest of the lanes' maxima, as a key: at least k logits
-  // of the row reach the least of these over the row's warps.
-  SA_DEV uint32_t warp_quota_key(float thread_max, int k) const {
-    const int warps = kWarps * ctas_, quota = (k + warps - 1) / warps;
-    if (k <= 0 || quota > 32) return 0;
-    const uint32_t key = order_key(thread_max);
+  // A value that k / ctas of the threads' maxima reach (the largest such one,
+  // to the upper 16 bits of its key), as a key: at least k logits of the row
+  // reach the least of these over the row's CTAs.  0 where there is none.
+  SA_DEV uint32_t quota_key(float thread_max, int k) const {
+    const int quota = (k + ctas_ - 1) / ctas_;
+    if (k <= 0 || quota > kThreads) return 0;
+    const uint32_t key = thread_max > kLowest ? order_key(thread_max) : 0;
     uint32_t lo = 0;
-#pragma unroll
-    for (int bit = 31; bit >= 0; --bit) {
+#pragma unroll 1
+    for (int bit = 31; bit >= 16; --bit) {
       const uint32_t mid = lo | 1u << bit;
-      if (__popc(__ballot_sync(0xffffffffu, key >= mid)) >= quota) lo = mid;
+      if (__syncthreads_count(key >= mid) >= quota) lo = mid;
     }
     return lo;
   }
   SA_DEV float count_floor() const {
     const float f = key_value(count_key_);
-    return f > kLowest ? f : -INFINITY;  // key 0, or some warp has too few logits above -inf
+    return f > kLowest ? f : -INFINITY;  // key 0: some CTA has too few logits above -inf, or k is large
   }
 
   // Collects the logits from floor on, sorts them and samples from their
@@ -547,11 +545,7 @@ class Row {
     if (n > kList) return false;
     if (rank_ != 0) return true;
 
-    int size = 32;
-    while (size < n) size *= 2;
-    for (int i = n + tid; i < size; i += kThreads) sh_.s.key[i] = 0;
-    __syncthreads();
-    sort_keys(size);
+    sort_keys(n);
     // masses of the first k, in order: kPer entries per thread
     constexpr int kPer = kList / kThreads;
     u64 upto[kPer], own = 0;
@@ -618,19 +612,40 @@ class Row {
     return true;
   }
 
-  // Descending bitonic sort of sh_.s.key[0 .. size), size a power of two.
-  SA_DEV void sort_keys(int size) {
+  // Sorts sh_.s.key[0 .. n), largest first; the keys differ.
+  SA_DEV void sort_keys(int n) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (n <= kThreads) {  // a key's place is the number of larger ones
+      const u64 mine = tid < n ? sh_.s.key[tid] : 0;
+      if (tid == n) sh_.s.key[n] = 0;  // n + 1 <= kList
+      __syncthreads();
+      int place = 0;
+      if ((tid & ~31) < n)
+        for (int j = 0; j < n; j += 2) {
+          const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&sh_.s.key[j]);
+          place += (two.x > mine) + (two.y > mine);
+        }
+      __syncthreads();
+      if (tid < n) sh_.s.key[place] = mine;
+      __syncthreads();
+      return;
+    }
+    int size = 2 * kThreads;
+    while (size < n) size *= 2;
+    for (int i = n + tid; i < size; i += kThreads) sh_.s.key[i] = 0;
+    __syncthreads();
+#pragma unroll 1
     for (int k = 2; k <= size; k *= 2)
+#pragma unroll 1
       for (int j = k / 2; j > 0; j /= 2) {
-        for (int i = threadIdx.x; i < size / 2; i += kThreads) {
+        for (int i = tid; i < size / 2; i += kThreads) {
           const int lo = 2 * i - (i & (j - 1)), hi = lo + j;
           const u64 x = sh_.s.key[lo], y = sh_.s.key[hi];
           if ((x < y) == ((lo & k) == 0)) sh_.s.key[lo] = y, sh_.s.key[hi] = x;
         }
-        // pairs closer than 32 stay inside the 64 keys of one warp
-        if (j > 32)
-          __syncthreads();
-        else if (j == 1 && k >= 64)
+        // pairs at most 32 apart stay inside the 64 keys of one warp
+        if (j > 32 || (j == 1 && k >= 64))
           __syncthreads();
         else
           __syncwarp();
