@@ -43,21 +43,19 @@
 namespace sa {
 namespace {
 
-#ifndef SMP_PER
-#define SMP_PER 2
-#define SMP_MAX 4
-#define SMP_SLICE 16384
-#endif
-
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 4;
+constexpr int kSliceLogits = 16384;       // a slice this long is not shared out further
 constexpr int kIndexBits = 18;            // vocabularies up to 2^18
 constexpr int kBins = 1024;
 constexpr int kGather = kThreads;         // members that the last step of a search ranks, one per thread
 constexpr int kList = 2048;               // candidates that are sorted at once
+constexpr int kSlice = 8192;              // candidates of a slice that are kept for a search's passes
+constexpr int kRuns = 512;                // runs of indices; 512 of 512 are the largest vocabulary
+constexpr int kQueue = kSlice / kWarps;    // candidates a warp can hold back: 31 and a vector of each lane
 constexpr int kChunks = 16;               // runs of a slice whose masses are kept apart
 constexpr int kUnroll = 4;                // vectors a thread has in flight
 constexpr float kMassOne = 8796093022208.f;   // 2^43
@@ -83,7 +81,7 @@ struct Histogram {
 
 struct alignas(16) Sorted {
   u64 key[kList];
-  u64 bin[kThreads];  // masses by index
+  u64 bin[kRuns];  // masses by index
 };
 
 struct Shared {
@@ -94,10 +92,13 @@ struct Shared {
   u64 cut, cut_mass;
   Pick pick;
   int gathered, found, last;
+  int slice_n;
   union {
     Histogram h;
     Sorted s;
   };
+  float slice_x[kSlice];
+  uint16_t slice_at[kSlice];  // index in the slice
 };
 
 template <int kType>
@@ -272,6 +273,7 @@ class Row {
     if (!by_count && by_mass)
       floor = fmaxf(floor, mass_floor((1.f - top_p) * 0.99f * z_ / vocab_));
     floor_ = floor;
+    if (by_floor && !by_count && !by_mass) make_slice_list();
     if (by_count || by_mass) {
       // steps for the first histogram: the candidates' range, or what holds all mass that counts
       const float range = floor > -INFINITY ? max_ - floor : 30.f * temperature_;
@@ -279,6 +281,18 @@ class Row {
       u64 kept = 0;
       if (by_count) kept = search(true, k, 0.f, by_mass);
       if (by_mass) search(false, by_count ? part_of(kept, top_p) : 0, top_p, true);
+    }
+    if (listed_) {
+      __syncthreads();  // the histogram's place is used again
+      pick(a, row, share, first_, end_ - shift_, ctas_ > 1, [&](auto f) {
+        for (int i = tid; i < list_n_; i += kThreads) {
+          const float x = sh_.slice_x[i];
+          const int index = first_ + sh_.slice_at[i];
+          const float e = kept_mass(x, index);
+          if (e > 0.f) f(index, static_cast<u64>(e * to_fixed_), x);
+        }
+      });
+      return;
     }
     chunk_masses();
     sample_chunks(a, row, share);
@@ -570,46 +584,123 @@ class Row {
       if (i < min(n, k) && e[j] >= min_mass_ && e[j] > 0.f && (i == 0 || excluded < target)) ++kept;
     }
     kept = block_sum_int(kept);  // they are the first ones
-    // the kept masses by index: first over runs of indices, then inside the run that holds the target
-    const int width = (vocab_ + kThreads - 1) / kThreads;
-    u64 target_in = 0, total = 0;
-    int lo = 0;
-    for (int level = 0; level < 2; ++level) {
-      sh_.s.bin[tid] = 0;
-      __syncthreads();
+    pick(a, row, share, 0, vocab_, false, [&](auto f) {
       for (int i = tid; i < kept; i += kThreads) {
         const u64 key = sh_.s.key[i];
-        const int index = (1 << kIndexBits) - 1 - static_cast<int>(key & ((1u << kIndexBits) - 1));
-        const u64 m = static_cast<u64>(mass(key_value(static_cast<uint32_t>(key >> kIndexBits))) * to_fixed_);
+        const float x = key_value(static_cast<uint32_t>(key >> kIndexBits));
+        f((1 << kIndexBits) - 1 - static_cast<int>(key & ((1u << kIndexBits) - 1)), static_cast<u64>(mass(x) * to_fixed_),
+          x);
+      }
+    });
+    return true;
+  }
+
+  // The token among kept entries, indices [lo, lo + span): first the run of
+  // indices that holds the target, then the index in it.  each(f) calls
+  // f(index, mass, x) for the thread's entries; across: every CTA has some,
+  // in index order.
+  template <class Each>
+  SA_DEV void pick(const SampleArgs& a, int row, float share, int lo, int span, bool across, Each each) {
+    const int tid = threadIdx.x, width = max((span + kRuns - 1) / kRuns, 1);
+    constexpr int kRun = kRuns / kThreads;
+    u64 target = 0, total = 0;
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {
+      for (int i = tid; i < kRuns; i += kThreads) sh_.s.bin[i] = 0;
+      __syncthreads();
+      each([&](int index, u64 m, float) {
         if (level == 0)
-          atomicAdd(&sh_.s.bin[index / width], m);
+          atomicAdd(&sh_.s.bin[(index - lo) / width], m);
         else if (index >= lo && index < lo + width)
           sh_.s.bin[index - lo] = m;
-      }
-      if (tid == 0) sh_.found = kThreads;
+      });
       __syncthreads();
-      const u64 in = sh_.s.bin[tid], run = block_scan(in, level == 0 ? sh_.warp_u : sh_.warp_v);
+      u64 in = 0;
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) in += sh_.s.bin[tid * kRun + j];
+      u64* sums = level == 0 ? sh_.warp_u : sh_.warp_v;
+      u64 run = block_scan(in, sums) - in;
       if (level == 0) {
-        for (int w = 0; w < kWarps; ++w) total += sh_.warp_u[w];
-        target_in = u_of(total, share);
+        for (int w = 0; w < kWarps; ++w) total += sums[w];
+        u64 before = 0;
+        const u64 own = total;
+        if (across) {
+          unsigned r = 0;
+          total = 0;
+          exchange(own, [&](u64 v) {
+            if (r++ < rank_) before += v;
+            total += v;
+          });
+        }
+        target = u_of(total, share);
+        if (!(before <= target && before + own > target)) return;  // exactly one CTA holds it
+        target -= before;
       }
-      if (run > target_in && run - in <= target_in) {
-        sh_.found = tid;
-        sh_.cut_mass = run - in;
+#pragma unroll
+      for (int j = 0; j < kRun; ++j) {
+        const u64 next = run + sh_.s.bin[tid * kRun + j];
+        if (next > target && run <= target) {
+          sh_.found = tid * kRun + j;
+          sh_.cut_mass = run;
+        }
+        run = next;
       }
       __syncthreads();
       if (level == 0) {
-        lo = sh_.found * width;
-        target_in -= sh_.cut_mass;
+        lo += sh_.found * width;
+        target -= sh_.cut_mass;
         __syncthreads();
       }
     }
     const int token = lo + sh_.found;
-    for (int i = tid; i < kept; i += kThreads)
-      if ((1 << kIndexBits) - 1 - static_cast<int>(sh_.s.key[i] & ((1u << kIndexBits) - 1)) == token)
-        put_token(a, row, token, key_value(static_cast<uint32_t>(sh_.s.key[i] >> kIndexBits)),
-                  kept == 1 ? 1.f : __fdiv_rn(static_cast<float>(total), to_fixed_));
-    return true;
+    each([&](int index, u64 m, float x) {  // logq of a token that is kept alone is 0 exactly
+      if (index == token) put_token(a, row, token, x, m == total ? mass(x) : __fdiv_rn(static_cast<float>(total), to_fixed_));
+    });
+  }
+
+  // The slice's candidates (floor_ and above) into shared memory, if those of
+  // every slice fit.  A warp claims places for all its lanes at once.
+  SA_DEV void make_slice_list() {
+    const int lane = threadIdx.x & 31;
+    listed_ = floor_ > -INFINITY || end_ - shift_ <= kSlice;
+    if (threadIdx.x == 0) sh_.slice_n = 0;
+    __syncthreads();
+    if (listed_) {
+      each_vector_of_warp([&](uint4 w, int v) {
+        claim(w, v, [&](int total) {
+          int at = 0;
+          if (lane == 0) at = atomicAdd(&sh_.slice_n, total);
+          return __shfl_sync(0xffffffffu, at, 0);
+        }, sh_.slice_x, sh_.slice_at, kSlice);
+      });
+    }
+    __syncthreads();
+    list_n_ = sh_.slice_n;
+    const bool mine = listed_ && list_n_ <= kSlice;
+    listed_ = true;
+    exchange(mine, [&](u64 v) { listed_ &= v != 0; });
+  }
+
+  // f(vector, number) for every vector with a logit from floor_ on among the
+  // warp's 32; all lanes take part, those without a vector with padding.
+  template <class F>
+  SA_DEV void each_vector_of_warp(F f) {
+    const int turns = (vectors_ + kThreads - 1) / kThreads;
+    uint4 none;
+    T* fill = reinterpret_cast<T*>(&none);
+#pragma unroll
+    for (int e = 0; e < E::kVec; ++e) fill[e] = E::lowest();
+    for (int t = 0; t < turns; t += kUnroll) {
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i) {
+        const int v = (t + i) * kThreads + threadIdx.x;
+        w[i] = v < vectors_ ? load(v) : none;
+      }
+#pragma unroll
+      for (int i = 0; i < kUnroll; ++i)
+        if (__any_sync(0xffffffffu, E::largest(w[i]) >= floor_)) f(w[i], (t + i) * kThreads + threadIdx.x);
+    }
   }
 
   // Sorts sh_.s.key[0 .. n), largest first; the keys differ.
@@ -664,10 +755,60 @@ class Row {
     return s;
   }
 
-  // f(x, index) for the slice's candidates.
+  // f(x, index) for the slice's candidates: from their list, or, while there
+  // is none, from memory.  There a warp queues what it finds and calls f for
+  // 32 at a time, since among neighbours few lanes have a candidate.
   template <class F>
   SA_DEV void each_candidate(F f) {
-    each_from(floor_, f);
+    if (listed_) {
+      for (int i = threadIdx.x; i < list_n_; i += kThreads) f(sh_.slice_x[i], first_ + sh_.slice_at[i]);
+      return;
+    }
+    const int lane = threadIdx.x & 31;
+    float* queue_x = sh_.slice_x + (threadIdx.x >> 5) * kQueue;
+    uint16_t* queue_at = sh_.slice_at + (threadIdx.x >> 5) * kQueue;
+    int n = 0;
+    const auto drain = [&](int least) {
+      __syncwarp();
+      while (n >= least && n > 0) {
+        const int i = n - 32 + lane;
+        if (i >= 0) f(queue_x[i], first_ + queue_at[i]);
+        n = max(n - 32, 0);
+      }
+      __syncwarp();
+    };
+    each_vector_of_warp([&](uint4 w, int v) {
+      claim(w, v, [&](int total) {
+        const int at = n;
+        n += total;
+        return at;
+      }, queue_x, queue_at, kQueue);
+      if (n >= 32) drain(32);
+    });
+    drain(1);
+  }
+
+  // Writes a vector's candidates of all the warp's lanes to a list, from the
+  // place that claim_places(their number) gives; those beyond cap are dropped.
+  template <class F>
+  SA_DEV void claim(uint4 w, int v, F claim_places, float* xs, uint16_t* ats, int cap) {
+    float x[E::kVec];
+    E::unpack(w, x);
+    uint32_t mine = 0;
+#pragma unroll
+    for (int e = 0; e < E::kVec; ++e) mine |= static_cast<uint32_t>(x[e] >= floor_ && x[e] > -INFINITY) << e;
+    const int count = __popc(mine), upto = warp_scan(count);
+    int at = claim_places(__shfl_sync(0xffffffffu, upto, 31)) + upto - count;
+    const int index = index_of(v) - first_;
+#pragma unroll
+    for (int e = 0; e < E::kVec; ++e)
+      if (mine >> e & 1u) {
+        if (at < cap) {
+          xs[at] = x[e];
+          ats[at] = static_cast<uint16_t>(index + e);
+        }
+        ++at;
+      }
   }
 
   SA_DEV int step_of(float x) const { return static_cast<int>(fminf((max_ - x) * per_step_, kBins - 1.f)); }
@@ -771,6 +912,13 @@ class Row {
       return full_key(x, index) >= cut ? step_of(x) : -1;
     });
     const int step = p.bin;
+    if (!listed_ && step >= 0 && step < kBins - 1 && per_step_ > 0.f) {
+      // Nothing below this step counts any more (the last step holds all that lies beyond the range): what is left
+      // is mostly few enough for a list.
+      const float edge = max_ - (step + 1.01f) / per_step_;
+      floor_ = fmaxf(floor_, edge - fabsf(edge) * 2.4e-7f);
+      make_slice_list();
+    }
     u64 lo = 0, hi = ~0ull;
     if (p.members > kGather) {  // the members' range of keys
       u64 least = ~0ull, most = 0;
@@ -957,13 +1105,15 @@ class Row {
   unsigned rank_, ctas_;
   int parity_ = 0;
   int vocab_, first_, shift_, end_, vectors_, chunk_turns_, pass1_parts_;
+  int list_n_ = 0;
+  bool listed_ = false;
   uint32_t count_key_;
   float temperature_, scale_, max_, z_, to_fixed_, min_mass_, floor_ = -INFINITY, per_step_;
   u64 cut_;
 };
 
 template <int kType>
-__global__ void __launch_bounds__(kThreads, SMP_PER) sample_kernel(const SampleArgs a, int slice) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a, int slice) {
   extern __shared__ __align__(16) uint8_t smem[];
   Row<kType> row(*reinterpret_cast<Shared*>(smem));
   row.run(a, blockIdx.x / cg::this_cluster().num_blocks(), slice);
@@ -974,7 +1124,7 @@ cudaError_t launch_type(const SampleArgs& a, cudaStream_t s) {
   // CTAs per row go by the vocabulary alone, so that a row's result does not
   // depend on the batch around it.
   int ctas = 1;
-  while (ctas < SMP_MAX && ceil_div(a.vocab, ctas) > SMP_SLICE) ctas *= 2;
+  while (ctas < kMaxCluster && ceil_div(a.vocab, ctas) > kSliceLogits) ctas *= 2;
   const int vec = Elem<kType>::kVec;
   const int slice = ceil_div(ceil_div(a.vocab, ctas), vec) * vec;
   const auto kernel = sample_kernel<kType>;

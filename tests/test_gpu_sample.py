@@ -183,3 +183,12 @@ def test_rows_by_cta_and_by_cluster(rows, k, p, m):
     x = torch.from_numpy(-1.3 * np.log(1 + rng.rand(rows, 30011) * 30011) + rng.randn(rows, 30011)).float().to(DEV)
     x[::3, 700:] = float("-inf")  # all that is allowed lies in one place
     check(x, rng.rand(rows), np.full(rows, 0.9), [k] * rows, [p] * rows, [m] * rows)
+
+
+@pytest.mark.parametrize("t", [0.01, 1.0, 20.0])
+def test_cuts_far_below_the_largest_logit(t):
+    """One logit far above the rest: the first histogram's range ends before the cut, whose step then holds all below."""
+    rng = np.random.RandomState(9)
+    x = torch.from_numpy(rng.randn(4, 40003)).float().to(DEV)
+    x[:, 77] = 45.0 * max(t, 1.0)
+    check(x, [0.1, 0.9, 0.5, 1 - 2.0 ** -24], [t] * 4, [3000, 20000, 39000, 5000], [1.0, 1.0, 0.999, 1.0], [0.0] * 4)
