@@ -20,6 +20,7 @@ using namespace kv4;
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanPer = kKv4MaxRequests / kPlanThreads;  // requests per thread
 constexpr int kScanPages = 16;                            // counts per thread and step
+constexpr int kListPages = 4096;
 constexpr int kBloomBits = 32768;
 constexpr int kSaturated = 0x7fffffff;
 
@@ -27,6 +28,7 @@ struct PlanShared {
   int slot[kKv4MaxRequests];
   int upto[kKv4MaxRequests];  // pages asked for by the requests up to and including this one, saturating
   uint32_t seen[kBloomBits / 32], again[kBloomBits / 32];
+  int page[kListPages];  // free pages found, by rank
   int warp[32];
   int total;
 };
@@ -109,7 +111,8 @@ SA_DEV int request_of(const PlanShared& sh, int n, int rank) {
 }
 
 // Calls give(rank, page) for the lowest free pages, rank = 0 .. need - 1, and
-// returns how many there are, at most `need`.
+// returns how many there are, at most `need`.  Free pages come in runs, which
+// one thread finds: they go through a list, so that all threads hand out.
 template <class F>
 SA_DEV int hand_out(PlanShared& sh, const Kv4Cache& c, int need, F give) {
   int found = 0;
@@ -129,10 +132,16 @@ SA_DEV int hand_out(PlanShared& sh, const Kv4Cache& c, int need, F give) {
     }
     const int mine = __popc(free_bits);
     int rank = found + block_scan(mine, sh.warp, &sh.total) - mine;
-    while (free_bits != 0 && rank < need) {
-      const int k = __ffs(free_bits) - 1;
-      free_bits &= free_bits - 1;
-      give(rank++, static_cast<int>(p0) + k);
+    const int end = min(found + sh.total, need);
+    for (int first = found; first < end; first += kListPages) {
+      const int last = min(first + kListPages, end);
+      while (free_bits != 0 && rank < last) {  // the ranks below `first` are through
+        sh.page[rank++ - first] = static_cast<int>(p0) + __ffs(free_bits) - 1;
+        free_bits &= free_bits - 1;
+      }
+      __syncthreads();
+      for (int r = first + threadIdx.x; r < last; r += kPlanThreads) give(r, sh.page[r - first]);
+      __syncthreads();
     }
     found += sh.total;
   }
@@ -315,11 +324,13 @@ __global__ void __launch_bounds__(128) kv4_free_kernel(const Kv4Cache c, const i
 }
 
 // ------------------------------------------------------------ compaction
-// Three launches: live pages per chunk of counts; each live page's new number
-// (a chunk sums the chunks before it) with the list of live pages; then the
-// copies, shared evenly over the CTAs by the list, with tables and counts.
+// Each live page gets its new number (a chunk of counts sums the chunks
+// before it) and a place in the list of live pages; then come the copies,
+// shared evenly over the CTAs by the list, with tables and counts.  In pools
+// of more than kDirectPages a launch before those counts the chunks; in
+// smaller ones a chunk reads all counts before its own, which costs less.
 constexpr int kChunkThreads = 256;
-constexpr int kChunkPer = 16;
+constexpr int kChunkPer = 4;
 constexpr int kChunk = kChunkThreads * kChunkPer;
 
 struct CompactWs {
@@ -328,33 +339,45 @@ struct CompactWs {
   int32_t* list;       // [live] old numbers
 };
 
-SA_DEV int live_of(const Kv4Cache& c, int64_t p0, uint32_t& bits) {
-  bits = 0;
-  for (int k = 0; k < kChunkPer; ++k)
-    if (p0 + k < c.num_pages && c.refcount[p0 + k] > 0) bits |= 1u << k;
-  return __popc(bits);
+constexpr int kDirectPages = 32768;
+
+SA_DEV uint32_t live_bits(const Kv4Cache& c, int64_t p0) {
+  if (p0 + kChunkPer <= c.num_pages) {
+    const int4 v = *reinterpret_cast<const int4*>(c.refcount + p0);
+    return (v.x > 0) | (v.y > 0) << 1 | (v.z > 0) << 2 | (v.w > 0) << 3;
+  }
+  uint32_t bits = 0;
+  for (int k = 0; p0 + k < c.num_pages; ++k) bits |= static_cast<uint32_t>(c.refcount[p0 + k] > 0) << k;
+  return bits;
 }
 
 __global__ void __launch_bounds__(kChunkThreads) kv4_live_kernel(const Kv4Cache c, const CompactWs w) {
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kChunk + threadIdx.x * kChunkPer;
   __shared__ int warp[32], total;
-  uint32_t bits;
-  const int mine = live_of(c, static_cast<int64_t>(blockIdx.x) * kChunk + threadIdx.x * kChunkPer, bits);
-  block_scan(mine, warp, &total);
+  block_scan(__popc(live_bits(c, p0)), warp, &total);
   if (threadIdx.x == 0) w.per_chunk[blockIdx.x] = total;
 }
 
-__global__ void __launch_bounds__(kChunkThreads) kv4_place_kernel(const Kv4Cache c, const CompactWs w,
+__global__ void __launch_bounds__(kChunkThreads) kv4_place_kernel(const Kv4Cache c, const CompactWs w, bool direct,
                                                                   int32_t* __restrict__ count) {
   __shared__ int warp[32], total;
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kChunk + threadIdx.x * kChunkPer;
+  const uint32_t bits = live_bits(c, p0);
   int before = 0;
-  for (int i = threadIdx.x; i < static_cast<int>(blockIdx.x); i += kChunkThreads) before += w.per_chunk[i];
+  if (direct) {
+#pragma unroll 8
+    for (int i = 0; i < static_cast<int>(blockIdx.x); ++i)
+      before += __popc(live_bits(c, static_cast<int64_t>(i) * kChunk + threadIdx.x * kChunkPer));
+  } else {
+    for (int i = threadIdx.x; i < static_cast<int>(blockIdx.x); i += kChunkThreads) before += w.per_chunk[i];
+  }
   block_scan(before, warp, &total);
   const int base = total;
-  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * kChunk + threadIdx.x * kChunkPer;
-  uint32_t bits;
-  const int mine = live_of(c, p0, bits);
+  const int mine = __popc(bits);
   int at = base + block_scan(mine, warp, &total) - mine;
-  for (int k = 0; k < kChunkPer && p0 + k < c.num_pages; ++k) {
+#pragma unroll
+  for (int k = 0; k < kChunkPer; ++k) {
+    if (p0 + k >= c.num_pages) break;
     const bool live = bits >> k & 1u;
     w.place[p0 + k] = live ? at : -1;
     if (live) w.list[at++] = static_cast<int32_t>(p0 + k);
@@ -405,14 +428,15 @@ SA_DEV int cu_at(const TokenArgs& a, int b) {
   return a.cu == nullptr ? b * a.per : min(max(a.cu[b], 0), a.total);
 }
 
+// All lanes of a warp ask for one block.
 SA_DEV bool find_block(const Kv4Cache& c, const TokenArgs& a, int id, BlockPlace& out) {
-  int lo = 0, hi = a.n - 1;  // the last entry whose first number is <= id
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((cu_at(a, mid) >> 4) + 2 * mid <= id)
-      lo = mid;
-    else
-      hi = mid - 1;
+  int lo = 0, left = a.n;  // the last entry whose first number is <= id lies in [lo, lo + left)
+  while (left > 1) {       // 32 of them looked at at once
+    const int step = (left + 31) / 32, at = static_cast<int>(threadIdx.x & 31) * step;
+    const bool le = at == 0 || (at < left && (cu_at(a, lo + at) >> 4) + 2 * (lo + at) <= id);
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, le));
+    lo += last * step;
+    left = min(step, left - last * step);
   }
   const int r0 = cu_at(a, lo), r1 = max(cu_at(a, lo + 1), r0);
   const int slot = a.slots[lo], len = slot_len(c, slot);
@@ -424,56 +448,70 @@ SA_DEV bool find_block(const Kv4Cache& c, const TokenArgs& a, int id, BlockPlace
   return id >= (r0 >> 4) + 2 * lo && out.blk * kBlockTokens < len;
 }
 
-// x / d for one divisor and many x, correctly rounded, with r = 1 / d rounded
-// to nearest: one residual and one correction (P. Markstein, "Computation of
+// x / d for one divisor and many x (in pairs), correctly rounded, with r = 1 / d
+// rounded to nearest: one residual and one correction (P. Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", IBM J. Res.
 // Dev. 34 (1), 1990).  Quotients so small that the residual underflows are
 // far below the smallest scale and round to the code 0 either way.
-SA_DEV float div_by(float x, float d, float r) {
-  const float q = x * r;
-  return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
-}
-
-// Rounds 16-dim groups to e2m1 codes under one e4m3 scale.  bits: the largest
-// |y| of the group as an integer (a NaN or infinity compares above all else).
-struct GroupScale {
-  uint32_t byte;
-  float s, r;  // the scale's value and its reciprocal; 0 and 0 where all codes are 0
+struct Divisor {
+  float2 neg, r;  // -d and 1 / d, twice
+  SA_DEV explicit Divisor(float d) {
+    const float inv = __fdiv_rn(1.f, d);
+    neg = make_float2(-d, -d);
+    r = make_float2(inv, inv);
+  }
+  SA_DEV Divisor(float d, float inv) : neg(make_float2(-d, -d)), r(make_float2(inv, inv)) {}
+  SA_DEV float2 operator()(float2 x) const {
+    const float2 q = fmul2(x, r);
+    return ffma2(ffma2(q, neg, x), r, q);
+  }
 };
 
-SA_DEV GroupScale group_scale(uint32_t bits) {
+// |a| and |b|, the larger one; NaN if one of them is.
+SA_DEV float max_abs_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return d;
+}
+
+// The e4m3 scale of 16 dims whose largest |y| is `top` (NaN or infinite: not
+// all of them are finite).
+struct GroupScale {
+  uint32_t byte;
+  float s, r;  // the scale's value and its reciprocal; r = 0 makes all codes 0
+};
+
+SA_DEV GroupScale group_scale(float top) {
   GroupScale g;
-  const float top = fminf(__fdiv_rn(__uint_as_float(bits), 6.f), 448.f);
   uint16_t two;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(two) : "f"(0.f), "f"(top));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(two) : "f"(0.f), "f"(fminf(__fdiv_rn(top, 6.f), 448.f)));
   g.byte = two & 0xffu;
-  if (bits >= 0x7f800000u) g.byte = kNaNScale;
+  if (!(top < INFINITY)) g.byte = kNaNScale;
   g.s = f16x2_to_f32(e4m3x2(g.byte)).x;
   g.r = g.s > 0.f ? __fdiv_rn(1.f, g.s) : 0.f;
   return g;
 }
 
-SA_DEV uint32_t e2m1_codes(const float* y, const GroupScale& g) {  // 8 values -> 8 nibbles
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = div_by(y[2 * i], g.s, g.r), b = div_by(y[2 * i + 1], g.s, g.r);
-    uint32_t two;
-    asm("{\n .reg .b8 p;\n cvt.rn.satfinite.e2m1x2.f32 p, %1, %2;\n cvt.u32.u8 %0, p;\n}\n" : "=r"(two) : "f"(b), "f"(a));
-    w |= two << (8 * i);
-  }
+SA_DEV uint32_t e2m1_codes(const float2 (&y)[4], const GroupScale& g) {  // 8 values -> 8 nibbles
+  const Divisor by(g.s, g.r);
+  const float2 a = by(y[0]), b = by(y[1]), c = by(y[2]), d = by(y[3]);
+  uint32_t w;
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n mov.b32 %0, {b0, b1, b2, b3};\n}\n"
+      : "=r"(w)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
   return w;
 }
 
-SA_DEV uint32_t load8(const __nv_bfloat16* p, float factor, float r, float* y) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
+// y = x / factor of 8 dims; returns the largest |y| (NaN if one is).
+SA_DEV float scaled8(uint4 v, const Divisor& factor, float2 (&y)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t top = 0;
+  float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    y[2 * i] = div_by(__uint_as_float(w[i] << 16), factor, r);
-    y[2 * i + 1] = div_by(__uint_as_float(w[i] & 0xffff0000u), factor, r);
-    top = max(top, max(__float_as_uint(y[2 * i]) & 0x7fffffffu, __float_as_uint(y[2 * i + 1]) & 0x7fffffffu));
+    y[i] = factor(make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)));
+    top = max_abs_nan(top, max_abs_nan(y[i].x, y[i].y));
   }
   return top;
 }
@@ -496,20 +534,39 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4Cache c, const
   const auto row = [&](int token) {
     return (static_cast<int64_t>(pl.row0 + pos0 + token - pl.lo) * c.num_heads_kv + head) * kHeadDim;
   };
+  // all loads first
+  uint4 kv[2][2], vv[4];
+  bool in[2];
+  uint32_t v_in = 0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    in[h] = mine(g + 8 * h);
+    kv[h][0] = kv[h][1] = make_uint4(0, 0, 0, 0);
+    if (in[h]) {
+      const uint4* x = reinterpret_cast<const uint4*>(k + row(g + 8 * h) + 16 * t);
+      kv[h][0] = __ldcs(x);
+      kv[h][1] = __ldcs(x + 1);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int token = 2 * t + (i & 1) + 8 * (i >> 1);
+    vv[i] = make_uint4(0, 0, 0, 0);
+    if (mine(token)) {
+      vv[i] = __ldcs(reinterpret_cast<const uint4*>(v + row(token) + 8 * g));
+      v_in |= 1u << i;
+    }
+  }
   {  // keys: tokens g and g + 8, the 16 dims of scale t
-    const float factor = c.k_scale[head], r = __fdiv_rn(1.f, factor);
+    const Divisor factor(c.k_scale[head]);
     uint32_t codes[2][2], scale[2];
-    bool in[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      in[h] = mine(g + 8 * h);
-      if (!in[h]) continue;
-      float y[16];
-      const __nv_bfloat16* x = k + row(g + 8 * h) + 16 * t;
-      const uint32_t top = load8(x, factor, r, y);
-      const GroupScale gs = group_scale(max(top, load8(x + 8, factor, r, y + 8)));
-      codes[h][0] = e2m1_codes(y, gs);
-      codes[h][1] = e2m1_codes(y + 8, gs);
+      float2 y[2][4];
+      const float top = scaled8(kv[h][0], factor, y[0]);
+      const GroupScale gs = group_scale(max_abs_nan(top, scaled8(kv[h][1], factor, y[1])));
+      codes[h][0] = e2m1_codes(y[0], gs);
+      codes[h][1] = e2m1_codes(y[1], gs);
       scale[h] = gs.byte;
     }
     if (in[0] && in[1]) {
@@ -525,31 +582,24 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4Cache c, const
     }
   }
   {  // values: tokens 2t, 2t+1, 2t+8, 2t+9, 8 dims; the other 8 of their scale are lane ^ 4's
-    const float factor = c.v_scale[head], r = __fdiv_rn(1.f, factor);
+    const Divisor factor(c.v_scale[head]);
     uint32_t codes[4], scales = 0;
-    uint32_t in = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int token = 2 * t + (i & 1) + 8 * (i >> 1);
-      float y[8];
-      uint32_t top = 0;
-      const bool here = mine(token);
-      if (here) top = load8(v + row(token) + 8 * g, factor, r, y);
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
-      if (here) {
-        const GroupScale gs = group_scale(top);
-        codes[i] = e2m1_codes(y, gs);
-        scales |= gs.byte << (8 * i);
-        in |= 1u << i;
-      }
+      float2 y[4];
+      float top = scaled8(vv[i], factor, y);
+      top = max_abs_nan(top, __shfl_xor_sync(0xffffffffu, top, 4));
+      const GroupScale gs = group_scale(top);
+      codes[i] = e2m1_codes(y, gs);
+      scales |= gs.byte << (8 * i);
     }
-    if (in == 15u) {
+    if (v_in == 15u) {
       *reinterpret_cast<uint4*>(block + kVCodes + 16 * lane) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
       if ((g & 1) == 0) *reinterpret_cast<uint32_t*>(block + kVScales + 4 * (4 * (g >> 1) + t)) = scales;
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (in >> i & 1u) {
+        if (v_in >> i & 1u) {
           *reinterpret_cast<uint32_t*>(block + kVCodes + 16 * lane + 4 * i) = codes[i];
           if ((g & 1) == 0) block[kVScales + 4 * (4 * (g >> 1) + t) + i] = static_cast<uint8_t>(scales >> (8 * i));
         }
@@ -625,15 +675,20 @@ int64_t token_warps(const Kv4Cache& c, const TokenArgs& a) {
 
 cudaError_t launch_kv4_reserve(const Kv4Cache& c, const int32_t* slots, const int32_t* add, int n, int32_t* done,
                                cudaStream_t s) {
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(kv4_reserve_kernel, sizeof(PlanShared));
+  if (e != cudaSuccess) return e;
   kv4_reserve_kernel<<<1, kPlanThreads, sizeof(PlanShared), s>>>(c, slots, add, n, done);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_fork(const Kv4Cache& c, const int32_t* src, const int32_t* dst, int n, int32_t* done,
                             cudaStream_t s) {
-  kv4_fork_plan_kernel<<<1, kPlanThreads, sizeof(PlanShared), s>>>(c, src, dst, n, done);
-  cudaError_t e = cudaGetLastError();
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in(kv4_fork_plan_kernel, sizeof(PlanShared));
   if (e != cudaSuccess) return e;
+  kv4_fork_plan_kernel<<<1, kPlanThreads, sizeof(PlanShared), s>>>(c, src, dst, n, done);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long units = (static_cast<long long>(kBlockBytes) << c.blocks_log2) * c.num_heads_kv / 16;
   const int parts = static_cast<int>(std::min<long long>(ceil_div(units, kCopyThreads * kCopyUnroll), 64));
   kv4_fork_copy_kernel<<<dim3(n, parts), kCopyThreads, 0, s>>>(c, src, dst, done);
@@ -656,10 +711,13 @@ cudaError_t launch_kv4_compact(const Kv4Cache& from, const Kv4Cache& to, int32_t
   w.per_chunk = static_cast<int32_t*>(workspace);
   w.place = w.per_chunk + chunks;
   w.list = w.place + from.num_pages;
-  kv4_live_kernel<<<chunks, kChunkThreads, 0, s>>>(from, w);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  kv4_place_kernel<<<chunks, kChunkThreads, 0, s>>>(from, w, count);
+  const bool direct = from.num_pages <= kDirectPages;
+  cudaError_t e;
+  if (!direct) {
+    kv4_live_kernel<<<chunks, kChunkThreads, 0, s>>>(from, w);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  kv4_place_kernel<<<chunks, kChunkThreads, 0, s>>>(from, w, direct, count);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   kv4_compact_kernel<<<device_sms() * 8, kCopyThreads, 0, s>>>(from, to, w, count);
   return cudaGetLastError();

@@ -406,7 +406,7 @@ def test_pages_many_requests(n, pages):
     same_state(h, c)
 
 
-@pytest.mark.parametrize("page,heads,pool", [(16, 1, 30), (64, 3, 5000), (32, 8, 4097)])
+@pytest.mark.parametrize("page,heads,pool", [(16, 1, 30), (64, 3, 5000), (32, 8, 4097), (16, 1, 40001)])
 def test_compact(page, heads, pool):
     import sink_aware_masked_gb300 as sa
 
