@@ -63,6 +63,14 @@ def _tensor(name: str, t, dtype: torch.dtype, shape, dev) -> int:
     return t.data_ptr()
 
 
+def _output(name: str, t, make, dtype: torch.dtype, shape, dev):
+    """A caller's output, checked, or a new one made like ``make``: the tensor and its address."""
+    if t is None:
+        t = torch.empty_like(make)
+        return t, t.data_ptr()
+    return t, _tensor(name, t, dtype, shape, dev)
+
+
 def _vector(name: str, t, dtype: torch.dtype, dev) -> int:
     """The length of a 1-D tensor that is checked like any other."""
     if not (isinstance(t, torch.Tensor) and t.dim() == 1):
@@ -127,8 +135,8 @@ def kv4_reserve(cache: KV4Cache, slots, new_tokens, *, done=None):
     dev, i32 = cache.device, torch.int32
     n = _vector("slots", slots, i32, dev)
     sp, np_ = _tensor("slots", slots, i32, (n,), dev), _tensor("new_tokens", new_tokens, i32, (n,), dev)
-    done = torch.empty_like(slots) if done is None else done
-    _call("sinkattn_kv4_reserve", dev, cache._ref, sp, np_, n, _tensor("done", done, i32, (n,), dev))
+    done, op = _output("done", done, slots, i32, (n,), dev)
+    _call("sinkattn_kv4_reserve", dev, cache._ref, sp, np_, n, op)
     return done
 
 
@@ -137,8 +145,8 @@ def kv4_fork(cache: KV4Cache, src, dst, *, done=None):
     dev, i32 = cache.device, torch.int32
     n = _vector("src", src, i32, dev)
     sp, dp = _tensor("src", src, i32, (n,), dev), _tensor("dst", dst, i32, (n,), dev)
-    done = torch.empty_like(src) if done is None else done
-    _call("sinkattn_kv4_fork", dev, cache._ref, sp, dp, n, _tensor("done", done, i32, (n,), dev))
+    done, op = _output("done", done, src, i32, (n,), dev)
+    _call("sinkattn_kv4_fork", dev, cache._ref, sp, dp, n, op)
     return done
 
 
@@ -203,9 +211,9 @@ def kv4_read(cache: KV4Cache, slots, total: int, *, cu=None, k=None, v=None):
     shape = (int(total), cache.num_heads_kv, HEAD_DIM)
     cp = None if cu is None else _tensor("cu", cu, torch.int32, (n + 1,), dev)
     k = torch.empty(shape, dtype=bf16, device=dev) if k is None else k
-    v = torch.empty_like(k) if v is None else v
-    _call("sinkattn_kv4_read", dev, cache._ref, sp, n, cp, shape[0], _tensor("k", k, bf16, shape, dev),
-          _tensor("v", v, bf16, shape, dev))
+    kp = _tensor("k", k, bf16, shape, dev)
+    v, vp = _output("v", v, k, bf16, shape, dev)
+    _call("sinkattn_kv4_read", dev, cache._ref, sp, n, cp, shape[0], kp, vp)
     return k, v
 
 
@@ -239,17 +247,21 @@ def kv4_decode_fwd(cache: KV4Cache, slots, q, sink, *, q_per_seq: int, window: i
         raise ValueError(f"query heads ({hq}) must be a multiple of key/value heads ({cache.num_heads_kv})")
     n = _vector("slots", slots, torch.int32, dev)
     sp = _tensor("slots", slots, torch.int32, (n,), dev)
-    rows = n * int(q_per_seq)
+    q_per_seq, window, prefix = int(q_per_seq), int(window), int(prefix)
+    rows = n * q_per_seq
     shape = (rows, hq, HEAD_DIM)
     qp, kp = _tensor("q", q, torch.bfloat16, shape, dev), _tensor("sink", sink, torch.float32, (hq,), dev)
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((hq, rows), dtype=torch.float32, device=dev) if lse is None else lse
+    o, op = _output("o", o, q, torch.bfloat16, shape, dev)
+    if lse is None:
+        lse = torch.empty((hq, rows), dtype=torch.float32, device=dev)
+        lp = lse.data_ptr()
+    else:
+        lp = _tensor("lse", lse, torch.float32, (hq, rows), dev)
     if workspace is None:
         workspace = kv4_decode_workspace(cache, q)
     wn = _vector("workspace", workspace, torch.uint8, dev)
-    _call("sinkattn_kv4_decode_fwd", dev, cache._ref, sp, n, int(q_per_seq), hq, int(window), int(prefix),
-          _SCALE if scale is None else float(scale), qp, kp, _tensor("o", o, torch.bfloat16, shape, dev),
-          _tensor("lse", lse, torch.float32, (hq, rows), dev), _tensor("workspace", workspace, torch.uint8, (wn,), dev), wn)
+    _call("sinkattn_kv4_decode_fwd", dev, cache._ref, sp, n, q_per_seq, hq, window, prefix,
+          _SCALE if scale is None else scale, qp, kp, op, lp, _tensor("workspace", workspace, torch.uint8, (wn,), dev), wn)
     return o, lse
 
 
@@ -282,11 +294,9 @@ def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=
     min_p = torch.zeros_like(u) if min_p is None else min_p
     tp, kp = _tensor("temperature", temperature, f32, one, dev), _tensor("top_k", top_k, i32, one, dev)
     pp, mp = _tensor("top_p", top_p, f32, one, dev), _tensor("min_p", min_p, f32, one, dev)
-    tokens = torch.empty_like(top_k) if tokens is None else tokens
-    logp = torch.empty_like(u) if logp is None else logp
-    logq = torch.empty_like(u) if logq is None else logq
-    to, lp, lq = (_tensor("tokens", tokens, i32, one, dev), _tensor("logp", logp, f32, one, dev),
-                  _tensor("logq", logq, f32, one, dev))
+    tokens, to = _output("tokens", tokens, top_k, i32, one, dev)
+    logp, lp = _output("logp", logp, u, f32, one, dev)
+    logq, lq = _output("logq", logq, u, f32, one, dev)
     _on_gpu("logits", logits)
     _call("sinkattn_sample_tokens", dev, logits.data_ptr(), kind, B, V, logits.stride(0) if B > 1 else V, up, tp, kp, pp,
           mp, to, lp, lq)
