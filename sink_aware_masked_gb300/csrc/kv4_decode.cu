@@ -37,9 +37,9 @@ using namespace kv4;
 
 constexpr int kRowPad = 68;       // floats per row in shared memory
 constexpr float kSlack = 8.f;     // log2 units a score may exceed its row's reference
-// Partial rows that the CTAs of one SM can leave, two pairs cut each: at most
-// 4 CTAs of 8 rows, 2 of 16 or 1 of 32.
-constexpr int kPartRowsPerSm = 64;
+// Partial rows that the CTAs of one SM can leave in the workspace: two pairs
+// cut each, 8 NT rows a pair (launch_variant checks it).
+constexpr int kPartRowsPerSm = 192;
 
 // Blocks of the longest pair up to which warps work alone, each on whole pairs.
 constexpr int kAloneBlocks = 48;
@@ -455,7 +455,11 @@ SA_DEV void finish_row(const DecK& p, int b, int head, int row, int d0, const Pi
   for (int e = 0; e < kD / 2; ++e) v[e] = f.sum == 0.f ? 0u : pack_bf16(f.acc[2 * e] * w, f.acc[2 * e + 1] * w);
   if constexpr (kD == 2) *reinterpret_cast<uint32_t*>(o) = v[0];
   if constexpr (kD == 4) *reinterpret_cast<uint2*>(o) = make_uint2(v[0], v[1]);
-  if constexpr (kD == 8) *reinterpret_cast<uint4*>(o) = make_uint4(v[0], v[1], v[2], v[3]);
+  if constexpr (kD >= 8) {
+#pragma unroll
+    for (int e = 0; e < kD / 8; ++e)
+      *reinterpret_cast<uint4*>(o + 8 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+  }
   if (d0 == 0) p.lse[static_cast<int64_t>(h) * p.num_seqs * p.n + at] = lse;
 }
 
@@ -476,19 +480,39 @@ SA_DEV Piece<kD> merge_pieces(F part_of, int c0, int c1, int row, int d0) {
   all.ref = -INFINITY;
 #pragma unroll
   for (int d = 0; d < kD; ++d) all.acc[d] = 0.f;
-  for (int c = c0; c <= c1; ++c) all.ref = fmaxf(all.ref, __ldcg(part_of(c) + kRows * kHeadDim + 2 * row));
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float* from = part_of(c);
-    const float2 st = __ldcg(reinterpret_cast<const float2*>(from + kRows * kHeadDim + 2 * row));
-    // a piece that saw nothing holds zeros, or a NaN that must come through
-    const float f = st.x == -INFINITY ? (st.y == 0.f ? 0.f : 1.f) : ex2(st.x - all.ref);
-    all.sum += f * st.y;
+  constexpr int kAtOnce = 64 / kD;  // pieces in flight: their number, not their size, is what a merge waits for
+#pragma unroll 1
+  for (int first = c0; first <= c1; first += kAtOnce) {
+    float2 st[kAtOnce], v[kAtOnce][kD / 2];
 #pragma unroll
-    for (int d = 0; d < kD; d += 2) {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(from + row * kHeadDim + d0 + d));
-      all.acc[d] += f * v.x;
-      all.acc[d + 1] += f * v.y;
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float* from = part_of(min(first + i, c1));
+      st[i] = __ldcg(reinterpret_cast<const float2*>(from + kRows * kHeadDim + 2 * row));
+#pragma unroll
+      for (int d = 0; d < kD / 2; ++d)
+        v[i][d] = __ldcg(reinterpret_cast<const float2*>(from + row * kHeadDim + d0 + 2 * d));
+    }
+    float top = all.ref;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, st[i].x);
+    const float old = all.ref == -INFINITY ? 1.f : ex2(all.ref - top);
+    all.ref = top;
+    all.sum *= old;
+#pragma unroll
+    for (int d = 0; d < kD; ++d) all.acc[d] *= old;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      // a piece that saw nothing holds zeros, or a NaN that must come through
+      float f = st[i].x == -INFINITY ? (st[i].y == 0.f ? 0.f : 1.f) : ex2(st[i].x - top);
+      if (first + i > c1) f = 0.f, st[i].y = 0.f;
+      all.sum += f * st[i].y;
+#pragma unroll
+      for (int d = 0; d < kD / 2; ++d) {
+        if (first + i <= c1) {
+          all.acc[2 * d] += f * v[i][d].x;
+          all.acc[2 * d + 1] += f * v[i][d].y;
+        }
+      }
     }
   }
   return all;
@@ -870,6 +894,7 @@ template <int NT, int kWarps, int kPerSm>
 cudaError_t launch_variant(const DecK& p, cudaStream_t s) {
   constexpr size_t kFixed = static_cast<size_t>(kWarps) * (kStages * kTurnBytes + 8 * NT * (kRowPad + 2) * 4);
   const auto kernel = kv4_decode_kernel<NT, kWarps, kPerSm>;
+  static_assert(2 * kPerSm * 8 * NT <= kPartRowsPerSm, "the workspace has no room for every CTA's cut pairs");
   static SmemOptIn opt_in;
   const cudaError_t e = opt_in(kernel, kFixed + kKv4MaxRequests * sizeof(SeqInfo));
   if (e != cudaSuccess) return e;
@@ -910,8 +935,8 @@ cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, int* st
   const int nt = p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : 4;
   p.row_groups = ceil_div(p.rows, 8 * nt);
   if (nt == 1) return launch_variant<1, 4, 3>(p, s);
-  if (nt == 2) return launch_variant<2, 8, 1>(p, s);
-  return launch_variant<4, 8, 1>(p, s);
+  if (nt == 2) return launch_variant<2, 4, 2>(p, s);
+  return launch_variant<4, 4, 2>(p, s);
 }
 
 }  // namespace sa
