@@ -216,7 +216,9 @@ sinkattn_status sinkattn_grpo_loss(const sinkattn_grpo_problem* g, const float* 
  * sinkattn_grpo_loss takes as logp_old.
  *
  * All state is on the device and every call is asynchronous, so a step can be
- * captured into a CUDA graph and replayed while the sequences grow.
+ * captured into a CUDA graph and replayed while the sequences grow (make the
+ * first call of each kind on a device outside any capture: it asks once for
+ * the kernel's shared memory).
  *
  * Format.  pages is [num_pages][num_heads_kv][page_size / 16] blocks of 16
  * tokens, 1152 bytes each.  With g = 0..7, t = 0..3, lane = 4 g + t:

@@ -41,6 +41,11 @@ constexpr float kSlack = 8.f;     // log2 units a score may exceed its row's ref
 // cut each, 8 NT rows a pair (launch_variant checks it).
 constexpr int kPartRowsPerSm = 192;
 
+// What beginning a pair costs a CTA, in blocks.  A CTA whose share holds the
+// end of one pair and the begin of the next gets that many blocks less
+// (32 x 8192 keys: 43.0 us without, 42.4 with 24, 42.0 with 40, 42.1 with 64).
+constexpr int kPairCost = 40;
+
 // Blocks of the longest pair up to which warps work alone, each on whole pairs.
 constexpr int kAloneBlocks = 48;
 
@@ -59,7 +64,7 @@ struct DecK {
 };
 
 SA_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -67,7 +72,7 @@ SA_DEV void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32
 
 // The same with nothing to add to.
 SA_DEV void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
@@ -175,20 +180,25 @@ SA_DEV void block_step(Rows<NT>& r, const Tile (&tile)[U], const uint32_t (&qf)[
   const int g = lane_g();
   // scores before their row's coefficient: s[u][nt][e] key g of block u, s[u][nt][2 + e] key g + 8, row e
   float s[U][NT][4];
+  uint32_t x[U][4], y[U][4], z[U][4], w[U][4], sa[U], sb[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     uint32_t ks = tile[u].ks;
     if (kMasked && mk.missing[u]) ks = kNaNScale * 0x0101u;
     const uint32_t two = e4m3x2(ks);
-    const uint32_t sa = __byte_perm(two, 0, 0x1010), sb = __byte_perm(two, 0, 0x3232);
-    uint32_t x[4], y[4], z[4], w[4];
-    e2m1x8(tile[u].k.x, x);
-    e2m1x8(tile[u].k.z, z);
-    e2m1x8(tile[u].k.y, y);
-    e2m1x8(tile[u].k.w, w);
+    sa[u] = __byte_perm(two, 0, 0x1010);
+    sb[u] = __byte_perm(two, 0, 0x3232);
+    e2m1x8(tile[u].k.x, x[u]);
+    e2m1x8(tile[u].k.z, z[u]);
+    e2m1x8(tile[u].k.y, y[u]);
+    e2m1x8(tile[u].k.w, w[u]);
+  }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t a0 = hmul2(x[j], sa), a1 = hmul2(z[j], sb), a2 = hmul2(y[j], sa), a3 = hmul2(w[j], sb);
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {  // the blocks' chains of products run side by side
+      const uint32_t a0 = hmul2(x[u][j], sa[u]), a1 = hmul2(z[u][j], sb[u]);
+      const uint32_t a2 = hmul2(y[u][j], sa[u]), a3 = hmul2(w[u][j], sb[u]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (j == 0)
@@ -197,7 +207,6 @@ SA_DEV void block_step(Rows<NT>& r, const Tile (&tile)[U], const uint32_t (&qf)[
           mma_f16(s[u][nt], a0, a1, a2, a3, qf[nt][j][0], qf[nt][j][1]);
       }
     }
-  }
   bool move = false;
   float top[NT][2];
 #pragma unroll
@@ -311,7 +320,7 @@ struct Batch {
 
 // The part of a pair that a worker takes: blocks [blk0, blk1) of `blocks`.
 struct Segment {
-  long long x;  // its place in the line that is shared out
+  long long x;  // where its pair begins in the line that is shared out
   int b, in_seq, blk0, blk1, blocks, slot, head, row0;
   Span span;
 };
@@ -615,13 +624,16 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) kv4_decode_kernel(const D
   // a turn at least for every warp, unless that leaves pairs without a worker of their own
   const long long want = alone ? pairs : max((work + kTurnBlocks * kWarps - 1) / (kTurnBlocks * kWarps), pairs);
   const int most = static_cast<int>(gridDim.x) * (alone ? kWarps : 1);
-  // the line that is shared out: all blocks, or all pairs
-  const Shares shares(alone ? pairs : work, static_cast<int>(min(static_cast<long long>(most), want)));
+  const int n_workers = static_cast<int>(min(static_cast<long long>(most), want));
+  // The line that is shared out: all pairs, or all blocks, where the blocks of
+  // each pair stand behind `pad` places for what beginning a pair costs a CTA.
+  const int pad = !alone && work >= 4LL * kPairCost * n_workers ? kPairCost : 0;
+  const Shares shares(alone ? pairs : work + pairs * pad, n_workers);
   const int worker = alone ? warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) : blockIdx.x;
   if (worker >= shares.workers) return;  // a whole CTA, or a warp of one that never meets the others again
   const long long x_end = shares.start(worker + 1);
 
-  // The segment at x, the first of the rest of pair in_seq of sequence b.
+  // The worker's part of pair in_seq of sequence b, which begins at x of the line, from blk0 on.
   const auto segment_at = [&](long long x, int b, int in_seq, int blk0) {
     Segment s;
     const SeqInfo info = seqs[b];
@@ -632,18 +644,18 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) kv4_decode_kernel(const D
     s.slot = info.slot;
     s.span = visible_span(p, info.len);
     s.blocks = max(s.span.count(), 1);
-    s.blk1 = alone ? s.blocks : static_cast<int>(min(static_cast<long long>(s.blocks), blk0 + (x_end - x)));
+    s.blk1 = alone ? s.blocks : static_cast<int>(min(static_cast<long long>(s.blocks), x_end - x - pad));
     s.head = p.row_groups == 1 ? in_seq : in_seq / p.row_groups;
     s.row0 = (in_seq - s.head * p.row_groups) * kRows;
     return s;
   };
   Segment seg;
-  {  // the pair that holds the share's first block
+  {  // the pair that holds the share's first place
     const long long x = shares.start(worker);
     int lo = 0, hi = p.num_seqs - 1;
     while (!alone && lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (seqs[mid].upto * per_seq <= x)
+      if ((seqs[mid].upto + static_cast<long long>(mid) * pad) * per_seq <= x)
         lo = mid;
       else
         hi = mid - 1;
@@ -652,12 +664,13 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) kv4_decode_kernel(const D
       lo = static_cast<int>(x / per_seq);
       seg = segment_at(x, lo, static_cast<int>(x - static_cast<long long>(lo) * per_seq), 0);
     } else {
-      const long long off = x - seqs[lo].upto * per_seq;
-      const int blocks = max(visible_span(p, seqs[lo].len).count(), 1);
-      int in_seq = min(static_cast<int>(__fdividef(static_cast<float>(off), static_cast<float>(blocks))), per_seq - 1);
-      while (static_cast<long long>(in_seq) * blocks > off) --in_seq;
-      while (static_cast<long long>(in_seq + 1) * blocks <= off) ++in_seq;
-      seg = segment_at(x, lo, in_seq, static_cast<int>(off - static_cast<long long>(in_seq) * blocks));
+      const long long off = x - (seqs[lo].upto + static_cast<long long>(lo) * pad) * per_seq;
+      const long long places = max(visible_span(p, seqs[lo].len).count(), 1) + pad;
+      int in_seq = min(static_cast<int>(__fdividef(static_cast<float>(off), static_cast<float>(places))), per_seq - 1);
+      while (in_seq * places > off) --in_seq;
+      while ((in_seq + 1) * places <= off) ++in_seq;
+      const long long in_pair = off - in_seq * places;
+      seg = segment_at(x - in_pair, lo, in_seq, static_cast<int>(max(in_pair - pad, 0LL)));
     }
   }
 
@@ -762,8 +775,8 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) kv4_decode_kernel(const D
 
     // the next segment is on its way while this one is finished
     const Segment done = seg;
-    const long long x_next = done.x + (alone ? 1 : done.blk1 - done.blk0);
-    const bool more = x_next < x_end;
+    const long long x_next = done.x + (alone ? 1 : done.blocks + pad);
+    const bool more = done.blk1 == done.blocks && x_next + pad < x_end;
     if (more) {
       const bool same = done.in_seq + 1 < per_seq;
       seg = segment_at(x_next, same ? done.b : done.b + 1, same ? done.in_seq + 1 : 0, 0);
@@ -774,15 +787,14 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) kv4_decode_kernel(const D
     // A pair that is cut is published when the worker is through, with one
     // fence and no copies in flight for it to wait for.
     const bool whole = done.blk0 == 0 && done.blk1 == done.blocks;
-    const long long p0 = done.x - done.blk0;
-    float* mine = p.part + (2 * static_cast<int64_t>(worker) + (done.blk0 == 0 && done.x > shares.start(worker))) * kPartFloats;
+    float* mine = p.part + (2 * static_cast<int64_t>(worker) + (done.x > shares.start(worker) ? 1 : 0)) * kPartFloats;
     if (!whole) {
       if (tid == 0) {
         Cut c;
         c.pair = static_cast<long long>(done.b) * per_seq + done.in_seq;
-        c.p0 = p0;
-        c.c0 = shares.owner(p0);
-        c.c1 = shares.owner(p0 + done.blocks - 1);
+        c.p0 = done.x;
+        c.c0 = shares.owner(done.x + pad);
+        c.c1 = shares.owner(done.x + pad + done.blocks - 1);
         c.b = done.b;
         c.head = done.head;
         c.row0 = done.row0;
@@ -936,7 +948,7 @@ cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, int* st
   p.row_groups = ceil_div(p.rows, 8 * nt);
   if (nt == 1) return launch_variant<1, 4, 3>(p, s);
   if (nt == 2) return launch_variant<2, 4, 2>(p, s);
-  return launch_variant<4, 4, 2>(p, s);
+  return launch_variant<4, 8, 1>(p, s);
 }
 
 }  // namespace sa

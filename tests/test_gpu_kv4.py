@@ -348,6 +348,33 @@ def test_decode_many_sequences():
     check_decode(c, slots[-50:], 1, 2, -1, 0, q[-50:], sink, o[-50:], lse[:, -50:])
 
 
+@pytest.mark.parametrize("n,window,prefix", [(1, -1, 0), (2, -1, 0), (4, 30000, 5)])
+def test_decode_long_against_the_bf16_kernel(n, window, prefix):
+    """Shares of many blocks, pairs cut at many places.  The values are exact in bf16 here (factors 1), so the bf16
+    decode works on the same numbers; its P is rounded to bf16 (2^-8 of the values) where this one's is in f16."""
+    import sink_aware_masked_gb300 as sa
+
+    rng = np.random.RandomState(13)
+    lens, hkv, hq = [40011, 31, 52000, 38005, 700, 44444], 8, 64
+    c = sa.KV4Cache.empty(sum(-(-x // 64) for x in lens), len(lens), 1000, hkv, page_size=64)
+    slots = i32(list(range(len(lens))))
+    assert sa.kv4_reserve(c, slots, i32(lens)).tolist() == [1] * len(lens)
+    cu = [0] + [int(x) for x in np.cumsum(lens)]
+    g = torch.Generator(device=DEV).manual_seed(3)
+    k, v = (torch.randn((cu[-1], hkv, 64), generator=g, device=DEV).to(torch.bfloat16) for _ in range(2))
+    sa.kv4_append(c, slots, k, v, cu_new=i32(cu))
+    k, v = sa.kv4_read(c, slots, cu[-1], cu=i32(cu))
+    q = bf16(rng.randn(len(lens) * n, hq, 64) * 2).to(DEV)
+    sink = dev(rng.randn(hq), torch.float32)
+    o, lse = sa.kv4_decode_fwd(c, slots, q, sink, q_per_seq=n, window=window, prefix=prefix)
+    o2, lse2 = sa.sinkattn_decode_fwd(q, k, v, sink, q_per_seq=n, cu_seqlens=i32(cu), cu_seqlens_host=cu, window=window,
+                                      prefix=prefix)
+    assert (o.float() - o2.float()).abs().max() <= 3 * 2.0 ** -8 * v.float().abs().max()
+    # the mean over the rows is far below the largest error: a block lost or taken twice would show
+    assert (o.float() - o2.float()).abs().mean() <= 2.0 ** -8 * o2.float().abs().mean()
+    assert (lse - lse2).abs().max() <= 1e-4
+
+
 # ---------------------------------------------------------------- pages
 def same_state(h, c):
     assert np.array_equal(h.seqlens.cpu().numpy(), c.lens)
@@ -542,3 +569,66 @@ def test_a_group_of_rollouts():
     assert torch.isfinite(dlogp).all() and abs(float(stats[0])) < 1e-5
     sa.kv4_free(c, rollouts)
     assert int((c.refcount > 0).sum()) == -(-P // 16) and int(c.refcount.max()) == 1
+
+
+def test_nothing_is_written_outside_the_outputs():
+    """Sentinels around every output, the workspace, and the pool's pages that are not the call's."""
+    import sink_aware_masked_gb300 as sa
+
+    rng = np.random.RandomState(30)
+
+    def guarded(shape, dtype, zero=False):
+        n = int(np.prod(shape)) * torch.empty((), dtype=dtype).element_size()
+        buf = torch.full((4096 + n + 4096,), 0xA5, dtype=torch.uint8, device=DEV)
+        t = buf[4096:4096 + n].view(dtype).view(shape)
+        if zero:
+            t.zero_()
+        return t, buf
+
+    kept = []
+
+    def out(shape, dtype, zero=False):
+        t, buf = guarded(shape, dtype, zero)
+        kept.append((buf, t.numel() * t.element_size()))
+        return t
+
+    lens, hkv = [1000, 17, 333, 64], 2
+    c = shuffled(rng, lens, 16, hkv)
+    pages, table = out(c.pages.shape, torch.uint8), out(c.table.shape, torch.int32)
+    seqlens, refcount = out(c.lens.shape, torch.int32), out(c.ref.shape, torch.int32)
+    for t, a in ((pages, c.pages), (table, c.table), (seqlens, c.lens), (refcount, c.ref)):
+        t.copy_(dev(a))
+    h = sa.KV4Cache(pages, table, seqlens, refcount, dev(c.k_scale), dev(c.v_scale))
+    slots = i32([0, 1, 2, 3])
+    for n in (1, 3, 8):
+        q = bf16(rng.randn(4 * n, 16, 64)).to(DEV)
+        ws = out(tuple(sa.kv4_decode_workspace(h, q).shape), torch.uint8, zero=True)
+        o, lse = out(q.shape, torch.bfloat16), out((16, 4 * n), torch.float32)
+        sa.kv4_decode_fwd(h, slots, q, torch.zeros(16, device=DEV), q_per_seq=n, o=o, lse=lse, workspace=ws)
+    cu = i32([0, 5, 22, 122, 123])
+    k, v = out((123, hkv, 64), torch.bfloat16), out((123, hkv, 64), torch.bfloat16)
+    sa.kv4_read(h, slots, 123, cu=cu, k=k, v=v)
+    before = h.pages.clone()
+    sa.kv4_append(h, slots, k, v, cu_new=cu)
+    mine = torch.zeros(h.pages.shape[0], dtype=torch.bool)
+    for s, n in enumerate([5, 17, 100, 1]):
+        for pos in range(lens[s] - n, lens[s]):
+            mine[c.table[s, pos // 16]] = True
+    assert torch.equal(h.pages[~mine.to(DEV)], before[~mine.to(DEV)])
+    done = out((4,), torch.int32)
+    sa.kv4_reserve(h, slots, i32([0, 40, 3, 1]), done=done)
+    sa.kv4_free(h, i32([1]))
+    sa.kv4_fork(h, i32([2, 0, 0, 9]), i32([1, 1, 3, 0]), done=done)
+    to = sa.KV4Cache(out(c.pages.shape, torch.uint8), out(c.table.shape, torch.int32), out(c.lens.shape, torch.int32),
+                     out(c.ref.shape, torch.int32), h.k_scale, h.v_scale)
+    size = 2 * c.pages.shape[0] * 4 + 4096
+    sa.kv4_compact(h, to, count=out((1,), torch.int32), workspace=out((size,), torch.uint8))
+    for B, V in ((3, 50001), (2, 5)):
+        x, one = torch.randn((B, V), device=DEV), torch.ones(B, device=DEV)
+        for p in (0.9, 1.0):
+            sa.sample_tokens(x, one * 0.5, top_p=one * p, tokens=out((B,), torch.int32), logp=out((B,), torch.float32),
+                             logq=out((B,), torch.float32))
+    torch.cuda.synchronize()
+    assert sa.sinkattn_get_device_status() == 0
+    for buf, n in kept:
+        assert (buf[:4096] == 0xA5).all() and (buf[4096 + n:] == 0xA5).all()
