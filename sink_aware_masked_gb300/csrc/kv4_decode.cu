@@ -27,6 +27,12 @@
 // many pairs with few blocks each, a single warp, which takes whole pairs and
 // merges nothing.  A pair cut between CTAs leaves partial results in the
 // workspace, and the last CTA of the pair to arrive merges them in order.
+//
+// Measured (GB300): 32 x 8192 keys, 64/8 heads, 42.0 us (151 MB, 22.4 us at the
+// copy rate): 53 of an SM's cycles per block, 147 instructions, of them 69
+// conversions and scalings and 8 products; without conversions and products a
+// block takes 41, the memory's rate.  8 x 32768 keys x 4 rows 84.4 us, 200
+// windowed sequences 10.6 us, one sequence of 37 keys 6.7 us.
 #include "kv4.cuh"
 #include "tc.cuh"
 
@@ -46,7 +52,8 @@ constexpr int kPartRowsPerSm = 192;
 // (32 x 8192 keys: 43.0 us without, 42.4 with 24, 42.0 with 40, 42.1 with 64).
 constexpr int kPairCost = 40;
 
-// Blocks of the longest pair up to which warps work alone, each on whole pairs.
+// Blocks of the longest pair up to which warps work alone, each on whole pairs
+// (200 sequences of 10 visible blocks: 10.6 us, by CTAs and shares 40.9).
 constexpr int kAloneBlocks = 48;
 
 struct DecK {
@@ -944,6 +951,10 @@ cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, int* st
   p.window = a.window;
   p.prefix = a.prefix;
   p.scale = a.scale;
+  // Tiles of 8, 16 or 32 rows; wider ones come as row groups.  An SM holds 12
+  // warps at 8 rows (42.0 us; 16 warps at 128 registers 45.4), 8 at 16 rows
+  // (2 CTAs of 4: 57.2 us at 32 x 8192 x 2 rows, 1 of 8: 62.1) and 8 at 32
+  // (1 CTA of 8: 85.5 us at 8 x 32768 x 4 rows, 2 of 4: 91.7).
   const int nt = p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : 4;
   p.row_groups = ceil_div(p.rows, 8 * nt);
   if (nt == 1) return launch_variant<1, 4, 3>(p, s);

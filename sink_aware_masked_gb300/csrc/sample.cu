@@ -24,6 +24,11 @@
 //   again by their exact key (x's bits and the index, so all keys differ)
 //   until they are few.  A last pass sums what is kept.
 //
+// Measured (GB300): 1 x 50257 fp32 with top-k and top-p 13.9 us; 256 x 201088
+// bf16 (103 MB, 15 us at the copy rate): no selection 62 us, greedy 47, top-k
+// 200 83, min-p 66, top-p alone 218.  Pass 1 runs at HBM speed; what a row
+// waits for is the latency of its phases, with two CTAs on an SM.
+//
 // Arithmetic.  e is fp32 (the difference before the scale: a large logit must
 // not lose what tells it from its neighbours).  Partial sums of a thread are
 // fp32, and so is Z, in a fixed order; masses that decide are 64-bit fixed
