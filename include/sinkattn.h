@@ -347,8 +347,9 @@ sinkattn_status sinkattn_kv4_decode_fwd(const sinkattn_kv4_cache* cache, const i
  * as logp_old; logq = log(e / kept mass) (0 where one token is kept).  Logits
  * of -inf are never chosen; a row of nothing else gives token -1 and -inf.  A
  * row with a NaN or +inf logit, a NaN parameter, a negative or infinite
- * temperature gives token -1 and NaN.  u outside [0, 1) is clamped.  vocab
- * <= 2^18, row_stride >= vocab, any alignment of the rows. */
+ * temperature gives token -1 and NaN.  u outside [0, 1) is clamped, fp32
+ * subnormals count as 0.  vocab <= 2^18, row_stride >= vocab, any alignment of
+ * the rows. */
 sinkattn_status sinkattn_sample_tokens(const void* logits, int32_t dtype, int32_t rows, int32_t vocab,
                                        int64_t row_stride, const float* u, const float* temperature,
                                        const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,

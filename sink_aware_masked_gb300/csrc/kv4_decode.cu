@@ -17,9 +17,9 @@
 // S, O and the statistics are fp32.
 //
 // The softmax keeps a reference score m per row that need not be the
-// maximum: it moves (and O and l are rescaled) only when a score exceeds it
-// by a factor of 2^8, which keeps P below f16's range and leaves one compare and one vote
-// per block in the ordinary case.
+// maximum: it moves (and O and l are rescaled) only when a probability would
+// exceed 2^8, which keeps P inside f16's range and leaves one compare and one
+// vote per two blocks in the ordinary case.
 //
 // Work: the visible blocks of all (sequence, kv head, row group) pairs in one
 // line, cut into equal shares, one per worker.  A worker is a CTA, whose warps
@@ -332,9 +332,10 @@ struct Segment {
   Span span;
 };
 
-// A warp's way through its blocks of a segment (turns part, part + parts,
-// ..., each the part of four aligned blocks that the segment has): page numbers are loaded two batches ahead; the blocks come through
-// the ring by bulk copies, one lane per block, two turns in flight.
+// A warp's way through its blocks of a segment (turns part, part + parts, ...,
+// each the part of four aligned blocks that the segment has): page numbers are
+// loaded two batches ahead; the blocks come through the ring by bulk copies,
+// two turns in flight.
 class Stream {
  public:
   SA_DEV Stream(const DecK& p, const uint8_t* ring, uint32_t bars, const tc::Abort& abort, int part, int parts)
@@ -469,13 +470,9 @@ SA_DEV void finish_row(const DecK& p, int b, int head, int row, int d0, const Pi
   uint32_t v[kD / 2];
 #pragma unroll
   for (int e = 0; e < kD / 2; ++e) v[e] = f.sum == 0.f ? 0u : pack_bf16(f.acc[2 * e] * w, f.acc[2 * e + 1] * w);
-  if constexpr (kD == 2) *reinterpret_cast<uint32_t*>(o) = v[0];
+  static_assert(kD == 4 || kD == 8, "one store");
   if constexpr (kD == 4) *reinterpret_cast<uint2*>(o) = make_uint2(v[0], v[1]);
-  if constexpr (kD >= 8) {
-#pragma unroll
-    for (int e = 0; e < kD / 8; ++e)
-      *reinterpret_cast<uint4*>(o + 8 * e) = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-  }
+  if constexpr (kD == 8) *reinterpret_cast<uint4*>(o) = make_uint4(v[0], v[1], v[2], v[3]);
   if (d0 == 0) p.lse[static_cast<int64_t>(h) * p.num_seqs * p.n + at] = lse;
 }
 
@@ -573,7 +570,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) kv4_decode_kernel(const D
   constexpr int kRows = 8 * NT;
   constexpr int kAloneRows = NT <= 2 ? 2 * NT : 1;  // rows a lane finishes when its warp works alone
   constexpr int kPartFloats = kRows * (kHeadDim + 2);
-  constexpr int kDims = kRows * kHeadDim / kThreads;  // dims per thread when a CTA merges: 2, 4 or 8
+  constexpr int kDims = kRows * kHeadDim / kThreads;  // dims per thread when a CTA merges: 4 or 8
   extern __shared__ __align__(16) uint8_t smem[];
   // the warps' rings, merge area [warps][rows][kRowPad], statistics [warps][rows][2], then the sequences
   float* acc_sh = reinterpret_cast<float*>(smem + kWarps * kStages * kTurnBytes);
