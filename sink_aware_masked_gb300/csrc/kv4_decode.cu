@@ -736,7 +736,9 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) kv4_decode_kernel(const D
         qf[nt][i][0] = pack_f16(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
         qf[nt][i][1] = pack_f16(__uint_as_float(w[4 + i] << 16) * up, __uint_as_float(w[4 + i] & 0xffff0000u) * up);
       }
-      const float mine = down * (p.scale * kLog2e * k_factor);
+      // Not below the least normal number: such scores are nothing beside 1 either way, and 0 times a masked key's
+      // -inf would be a NaN.
+      const float mine = fmaxf(down * (p.scale * kLog2e) * k_factor, 1.17549435e-38f);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         coef[nt][r] = __shfl_sync(0xffffffffu, mine, 4 * (2 * t + r));

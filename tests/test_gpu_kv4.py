@@ -255,6 +255,26 @@ def test_decode_ranges_of_q_and_sink():
     assert (o[4] == 0).all()
 
 
+@pytest.mark.parametrize("factor", [1.0, 2.0 ** -8, 2.0 ** -40, 2.0 ** -120])
+@pytest.mark.parametrize("n,hq", [(1, 8), (2, 8), (4, 16)])
+def test_decode_rows_of_zeros_and_tiny_queries(n, hq, factor):
+    """Such a row's scores are 0, or nothing beside 1: it is the mean of what it sees, and no masked key is in it."""
+    import sink_aware_masked_gb300 as sa
+
+    rng = np.random.RandomState(13)
+    c = shuffled(rng, [37, 5, 200], 16, 2, factors=False)
+    c.k_scale = np.full(2, factor, dtype=np.float32)
+    x = rng.randn(3 * n, hq, 64)
+    x[:, 0] = 0
+    x[:, 1] *= 2.0 ** -126
+    x[:, 2] *= 2.0 ** -133  # bf16 subnormals
+    x[:, hq - 1] = 0
+    q, sink = bf16(x).to(DEV), dev(rng.randn(hq), torch.float32)
+    for window, prefix in ((-1, 0), (20, 3)):
+        o, lse = sa.kv4_decode_fwd(handle(c), i32([0, 1, 2]), q, sink, q_per_seq=n, window=window, prefix=prefix)
+        check_decode(c, [0, 1, 2], n, hq, window, prefix, q, sink, o, lse)
+
+
 @pytest.mark.parametrize("n,hq", [(1, 8), (3, 8), (4, 16)])
 def test_decode_not_finite_only_where_it_is_seen(n, hq):
     """A NaN value, key or query, and a missing page, reach exactly the rows (and dims) that see them."""
