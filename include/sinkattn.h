@@ -276,7 +276,8 @@ sinkattn_status sinkattn_kv4_reserve(const sinkattn_kv4_cache* cache, const int3
  * read as they were before the call.  done[i] = 0, and nothing changes for
  * the entry, where a slot is out of range, dst[i] is not empty or is named
  * earlier in the call, or the pages run out (then every later entry that
- * needs one gets none either). */
+ * needs one gets none either).  Where the source's open page is not in the
+ * pool, the copy's is -1. */
 sinkattn_status sinkattn_kv4_fork(const sinkattn_kv4_cache* cache, const int32_t* src, const int32_t* dst, int32_t n,
                                   int32_t* done, void* stream);
 

@@ -297,7 +297,13 @@ __global__ void __launch_bounds__(kCopyThreads) kv4_fork_copy_kernel(const Kv4Ca
   const int open = len & (c.page_size - 1);
   if (open == 0) return;
   const int old_page = row[full], new_page = out[full];
-  if (old_page < 0 || old_page >= c.num_pages) return;
+  if (old_page < 0 || old_page >= c.num_pages) {  // nothing to copy: these tokens read as NaN from the copy too
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+      out[full] = -1;
+      c.refcount[new_page] = 0;
+    }
+    return;
+  }
   const int per_head = ((open + kBlockTokens - 1) / kBlockTokens) * (kBlockBytes / 16);
   const int64_t head = static_cast<int64_t>(kBlockBytes) << c.blocks_log2;
   copy_units(c.pages + old_page * head * c.num_heads_kv, c.pages + new_page * head * c.num_heads_kv,

@@ -432,6 +432,29 @@ def test_pages_any_order_of_calls(seed):
         assert np.array_equal(h.pages.cpu().numpy(), c.pages)
 
 
+def test_fork_of_a_slot_whose_open_page_is_missing():
+    """Its tokens read as NaN from the copy as from the source, never as what a page held before."""
+    import sink_aware_masked_gb300 as sa
+
+    rng = np.random.RandomState(3)
+    c = shuffled(rng, [40, 0, 0, 21], 16, 2)
+    c.pages[c.ref == 0] = 0x11
+    h = handle(c)
+    lost = int(h.page_table[0, 2])
+    h.page_table[0, 2] = c.pages.shape[0] + 5
+    assert sa.kv4_fork(h, i32([0, 3]), i32([1, 2])).tolist() == [1, 1]
+    assert h.seqlens.tolist() == [40, 40, 21, 21]
+    assert int(h.page_table[1, 2]) == -1
+    want = c.ref.copy()
+    want[c.table[0, :2]] += 1
+    want[c.table[3, 0]] += 1
+    want[int(h.page_table[2, 1])] += 1  # the second entry's page; the first one's is free again
+    assert c.ref[int(h.page_table[2, 1])] == 0 and h.refcount.tolist() == want.tolist() and c.ref[lost] == 1
+    for x, y in zip(sa.kv4_read(h, i32([0, 1]), 80), sa.kv4_read(handle(c), i32([0]), 40)):
+        for got in (x[:40], x[40:]):
+            assert torch.equal(got[:32], y[:32]) and torch.isnan(got[32:].float()).all()
+
+
 @pytest.mark.parametrize("n,pages", [(4096, 70000), (1025, 1500), (2048, 17)])
 def test_pages_many_requests(n, pages):
     import sink_aware_masked_gb300 as sa
