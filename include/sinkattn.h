@@ -245,7 +245,8 @@ sinkattn_status sinkattn_grpo_loss(const sinkattn_grpo_problem* g, const float* 
  * there are not written and read as NaN.  Limits: page_size 16, 32, 64, 128
  * or 256; max_pages * page_size <= 2^30; 4096 entries per call; head_dim 64.
  * All pointers of the cache are 16-byte aligned; int32 and fp32 lists
- * elsewhere 4-byte aligned. */
+ * elsewhere 4-byte aligned.  Calls that change a cache must not overlap on the
+ * GPU with other calls on it. */
 typedef struct {
   void* pages;            /* uint8 [num_pages][num_heads_kv][page_size * 72] */
   int32_t* page_table;    /* [num_slots][max_pages] */

@@ -86,7 +86,19 @@ class KV4Cache:
     [num_pages], k_scale and v_scale float32 [Hkv] (finite, positive: a value
     is code * e4m3 scale * its head's factor).  The cache keeps these tensors
     and works on them in place; ``empty`` makes the tensors of a new one.
+    Calls that change a cache follow one another, and the calls that read it,
+    on one stream or by events.
     """
+
+    _FIXED = frozenset(("pages", "page_table", "seqlens", "refcount", "k_scale", "v_scale", "device", "num_pages",
+                        "num_heads_kv", "page_size", "num_slots", "max_pages"))
+
+    def __setattr__(self, name, value):
+        # The library holds the tensors' addresses: another tensor in their place would not be seen, and the one
+        # that is used would be freed.
+        if name in self._FIXED and self.__dict__.get(name, value) is not value:
+            raise AttributeError(f"{name} of a KV4Cache cannot be replaced: write into the tensor it was made with")
+        super().__setattr__(name, value)
 
     def __init__(self, pages, page_table, seqlens, refcount, k_scale, v_scale):
         dev = pages.device if isinstance(pages, torch.Tensor) else None

@@ -214,3 +214,20 @@ def test_sampling_by_hand():
     assert ref.sample(x, 0.999, 1.0, 0, 0.5, 0.0)[0] == 2
     token, logp, logq = ref.sample(x, 0.05, 1.0, 0, 1.0, 0.5)
     assert token == 1 and abs(logp - np.log(0.4)) < 1e-12 and abs(logq - np.log(0.5)) < 1e-12
+
+
+def test_a_caches_tensors_cannot_be_replaced():
+    """The library keeps their addresses; a write in place, also by an augmented assignment, is fine."""
+    c = object.__new__(rollout.KV4Cache)
+    c.seqlens, c.num_heads_kv = torch.zeros(3, dtype=torch.int32), 300
+    first = c.seqlens
+    c.seqlens += 2
+    c.seqlens[1] = 5
+    assert c.seqlens is first and first.tolist() == [2, 5, 2]
+    with pytest.raises(AttributeError, match="seqlens of a KV4Cache cannot be replaced"):
+        c.seqlens = c.seqlens + 1
+    with pytest.raises(AttributeError, match="num_heads_kv"):
+        c.num_heads_kv = 1
+    assert c.seqlens is first and c.num_heads_kv == 300
+    c.note = 1
+    c.note = 2
