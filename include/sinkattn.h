@@ -231,7 +231,7 @@ sinkattn_status sinkattn_grpo_loss(const sinkattn_grpo_problem* g, const float* 
  * A byte holds two e2m1 codes, the lower dim in the low nibble (0, 0.5, 1,
  * 1.5, 2, 3, 4, 6 and a sign); a scale is e4m3 and serves 16 dims of a token.
  * A value is code * scale * (the head's fp32 factor k_scale or v_scale, which
- * is finite and positive).
+ * lies between 2^-100 and 2^100).
  *
  * Pages.  Slot s holds seqlens[s] tokens in the pages page_table[s][0 ..
  * ceil(seqlens[s] / page_size) - 1]; the other entries mean nothing.
@@ -305,8 +305,8 @@ sinkattn_status sinkattn_kv4_compact(const sinkattn_kv4_cache* from, const sinka
  * rows each.  Rows behind the last offset are not read.  Per 16 dims with
  * y = x / factor: scale = e4m3(min(max|y| / 6, 448)), code = e2m1(y / scale),
  * both rounded to nearest even, codes saturating, 0 where the scale is 0.  16
- * dims that hold a NaN or an infinity read back as NaN.  A slot may be named
- * once per call. */
+ * dims with a y that is a NaN or an infinity in fp32 read back as NaN.  A slot
+ * may be named once per call. */
 sinkattn_status sinkattn_kv4_append(const sinkattn_kv4_cache* cache, const int32_t* slots, int32_t num_seqs,
                                     const int32_t* cu_new, int32_t total, const void* k, const void* v, void* stream);
 
@@ -348,10 +348,10 @@ sinkattn_status sinkattn_kv4_decode_fwd(const sinkattn_kv4_cache* cache, const i
  * tokens int32; logp = log(e / sum of all e), what sinkattn_grpo_loss takes
  * as logp_old; logq = log(e / kept mass) (0 where one token is kept).  Logits
  * of -inf are never chosen; a row of nothing else gives token -1 and -inf.  A
- * row with a NaN or +inf logit, a NaN parameter, a negative or infinite
- * temperature gives token -1 and NaN.  u outside [0, 1) is clamped, fp32
- * subnormals count as 0.  vocab <= 2^18, row_stride >= vocab, any alignment of
- * the rows. */
+ * row with a NaN or +inf logit, a NaN parameter or a temperature that is
+ * negative or above 1e36 gives token -1 and NaN.  u outside [0, 1) is clamped,
+ * fp32 subnormals count as 0.  vocab <= 2^18, row_stride >= vocab, any
+ * alignment of the rows. */
 sinkattn_status sinkattn_sample_tokens(const void* logits, int32_t dtype, int32_t rows, int32_t vocab,
                                        int64_t row_stride, const float* u, const float* temperature,
                                        const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,

@@ -202,7 +202,7 @@ def kept_tokens(x, u, temperature, top_k, top_p, min_p):
 def sample_invalid(x, u, temperature, top_k, top_p, min_p):
     """What an invalid row gives for logp and logq (token -1): NaN, or -inf where nothing is allowed; None if valid."""
     x = np.asarray(x, dtype=np.float64)
-    if np.isnan([u, temperature, top_p, min_p]).any() or temperature < 0 or np.isinf(temperature):
+    if np.isnan([u, temperature, top_p, min_p]).any() or not 0 <= temperature <= 1e36:
         return float("nan")
     if np.isnan(x).any() or np.isposinf(x).any():
         return float("nan")

@@ -228,7 +228,8 @@ class Row {
 
     const float temperature = a.temperature[row], top_p = a.top_p[row], min_p = a.min_p[row], u = a.u[row];
     int k = a.top_k[row];
-    const bool valid = temperature >= 0.f && temperature < INFINITY && top_p == top_p && min_p == min_p && u == u;
+    // up to 1e36, so that 1 / T stays a normal number and a difference that overflows has no mass either way
+    const bool valid = temperature >= 0.f && temperature <= 1e36f && top_p == top_p && min_p == min_p && u == u;
     const bool greedy = temperature == 0.f;
     temperature_ = greedy || !valid ? 1.f : temperature;
     scale_ = fminf(__fdiv_rn(kLog2e, temperature_), 1e38f);

@@ -83,7 +83,7 @@ class KV4Cache:
 
     pages uint8 [num_pages, Hkv, page_size * 72], page_table int32
     [num_slots, max_pages], seqlens int32 [num_slots], refcount int32
-    [num_pages], k_scale and v_scale float32 [Hkv] (finite, positive: a value
+    [num_pages], k_scale and v_scale float32 [Hkv] (2^-100 to 2^100: a value
     is code * e4m3 scale * its head's factor).  The cache keeps these tensors
     and works on them in place; ``empty`` makes the tensors of a new one.
     Calls that change a cache follow one another, and the calls that read it,

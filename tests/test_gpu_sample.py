@@ -130,6 +130,19 @@ def test_ends_of_u_and_of_the_parameters():
     assert abs(logp[5] - np.log(0.25)) < 1e-6 and logp[4] == 0 and logq[6] == 0 and logq[7] == 0
 
 
+def test_the_largest_temperatures():
+    """1e36 still is one, with masked logits of -inf and of fp32's lowest value; what lies beyond is refused."""
+    rng = np.random.RandomState(6)
+    x = torch.from_numpy(rng.randn(10, 40009)).float().to(DEV)
+    x[:, 5::3] = float("-inf")
+    x[:, 6::3] = torch.finfo(torch.float32).min
+    t = [1e36] * 6 + [1e37, 1.3e38, 3.4e38, 1e36]
+    k, p, m = [0, 100, 0, 0, 9000, 30, 0, 0, 0, 0], [1, 1, 0.9, 1, 0.5, 0.4, 1, 1, 0.9, 0.01], [0, 0, 0, 0.1] + [0] * 6
+    tok, logp, _ = run(x, [0.5] * 10, t, k, p, m)
+    assert (tok[[6, 7, 8]] == -1).all() and np.isnan(logp[[6, 7, 8]]).all() and (tok[[0, 1, 2, 3, 4, 5, 9]] >= 0).all()
+    check(x, rng.rand(10), t, k, p, m)
+
+
 def test_rows_stand_alone_and_repeat_bit_by_bit():
     rng = np.random.RandomState(5)
     x = torch.from_numpy(rng.randn(300, 10007) * 3).float().to(DEV)
