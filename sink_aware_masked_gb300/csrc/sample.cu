@@ -341,13 +341,17 @@ class Row {
   }
   SA_DEV int index_of(int v) const { return first_ + v * E::kVec - shift_; }
 
-  // f(vector, its number) for the slice's vectors in [turn0, turn1) x threads; padding is -inf.
+  // f(vectors, number of the first) for the slice's vectors in [turn0, turn1) x threads, some of the thread's at
+  // once, which are kThreads apart; padding is -inf.
   template <class F>
-  SA_DEV void turns_of_vectors(int turn0, int turn1, F f) {
+  SA_DEV void turns_of_groups(int turn0, int turn1, F f) {
     const int tid = threadIdx.x, whole = end_ / E::kVec / kThreads;  // turns of whole vectors, the first one aside
     const auto checked = [&](int t) {
       const int v = t * kThreads + tid;
-      if (v < vectors_) f(load(v), v);
+      if (v < vectors_) {
+        const uint4 w[1] = {load(v)};
+        f(w, v);
+      }
     };
     int t = turn0;
     if (t == 0 && shift_ > 0 && t < turn1) checked(t++);
@@ -355,11 +359,18 @@ class Row {
       uint4 w[kUnroll];
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(base_) + (t + i) * kThreads + tid);
-#pragma unroll
-      for (int i = 0; i < kUnroll; ++i) f(w[i], (t + i) * kThreads + tid);
+      f(w, t * kThreads + tid);
     }
 #pragma unroll 1
     for (; t < turn1; ++t) checked(t);
+  }
+  // f(vector, its number), one by one.
+  template <class F>
+  SA_DEV void turns_of_vectors(int turn0, int turn1, F f) {
+    turns_of_groups(turn0, turn1, [&](const auto& w, int v) {
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(sizeof(w) / sizeof(uint4)); ++i) f(w[i], v + i * kThreads);
+    });
   }
   template <class F>
   SA_DEV void each_vector(F f) {
@@ -395,10 +406,11 @@ class Row {
     bool fused = false;
     for (int c = 0; c * step < max(turns, 1); ++c) {
       float2 sum = make_float2(0.f, 0.f);
-      turns_of_vectors(c * step, min((c + 1) * step, turns), [&](uint4 w, int) {
-        const float m = E::largest(w);
-        float x[E::kVec];
-        E::unpack(w, x);
+      turns_of_groups(c * step, min((c + 1) * step, turns), [&](const auto& w, int) {
+        constexpr int kGroup = sizeof(w) / sizeof(uint4);
+        float m = E::largest(w[0]);
+#pragma unroll
+        for (int i = 1; i < kGroup; ++i) m = fmaxf(m, E::largest(w[i]));
         if (m > top) {
           const float next = m * scale_;
           const bool next_fused = fabsf(next) < 1048576.f;
@@ -409,16 +421,22 @@ class Row {
           ref = next;
           fused = next_fused;
         }
-        if (fused) {
-          const float2 c2 = make_float2(scale_, scale_), r2 = make_float2(-ref, -ref);
+        const float2 c2 = make_float2(scale_, scale_), r2 = make_float2(-ref, -ref);
+        const bool by_fma = fused;
 #pragma unroll
-          for (int e = 0; e < E::kVec; e += 2) {
-            const float2 t = ffma2(make_float2(x[e], x[e + 1]), c2, r2);
-            sum = fadd2(sum, make_float2(ex2(t.x), ex2(t.y)));
+        for (int i = 0; i < kGroup; ++i) {
+          float x[E::kVec];
+          E::unpack(w[i], x);
+          if (by_fma) {
+#pragma unroll
+            for (int e = 0; e < E::kVec; e += 2) {
+              const float2 t = ffma2(make_float2(x[e], x[e + 1]), c2, r2);
+              sum = fadd2(sum, make_float2(ex2(t.x), ex2(t.y)));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < E::kVec; ++e) sum.x += ex2((x[e] - top) * scale_);
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < E::kVec; ++e) sum.x += ex2((x[e] - top) * scale_);
         }
       });
       float total = sum.x + sum.y;
@@ -768,6 +786,10 @@ class Row {
   SA_DEV void each_candidate(F f) {
     if (listed_) {
       for (int i = threadIdx.x; i < list_n_; i += kThreads) f(sh_.slice_x[i], first_ + sh_.slice_at[i]);
+      return;
+    }
+    if (floor_ == -INFINITY) {  // every logit is one (256 x 201088, top-k 5000: 181 us; by the queue 281)
+      each_from(floor_, f);
       return;
     }
     const int lane = threadIdx.x & 31;
