@@ -937,7 +937,7 @@ class Row {
     const int tid = threadIdx.x;
     const u64 cut = cut_;
     Pick p = histogram(by_count, target, top_p, 0, 0, masses, [&](float x, int index) {
-      return full_key(x, index) >= cut ? step_of(x) : -1;
+      return cut == 0 || full_key(x, index) >= cut ? step_of(x) : -1;
     });
     const int step = p.bin;
     if (!listed_ && step >= 0 && step < kBins - 1 && per_step_ > 0.f) {
@@ -1031,7 +1031,7 @@ class Row {
   }
 
   SA_DEV float kept_mass(float x, int index) const {
-    if (static_cast<u64>(order_key(x)) < (cut_ >> kIndexBits) || full_key(x, index) < cut_) return 0.f;
+    if (cut_ != 0 && (static_cast<u64>(order_key(x)) < (cut_ >> kIndexBits) || full_key(x, index) < cut_)) return 0.f;
     const float e = mass(x);
     return e >= min_mass_ ? e : 0.f;
   }
