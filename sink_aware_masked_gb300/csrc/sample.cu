@@ -24,10 +24,12 @@
 //   again by their exact key (x's bits and the index, so all keys differ)
 //   until they are few.  A last pass sums what is kept.
 //
-// Measured (GB300): 1 x 50257 fp32 with top-k and top-p 13.9 us; 256 x 201088
-// bf16 (103 MB, 15 us at the copy rate): no selection 62 us, greedy 47, top-k
-// 200 83, min-p 66, top-p alone 218.  Pass 1 runs at HBM speed; what a row
-// waits for is the latency of its phases, with two CTAs on an SM.
+// Measured (GB300): 1 x 50257 fp32 with top-k and top-p 13.7 us; 256 x 201088
+// bf16 (103 MB, 15 us at the copy rate): no selection 60 us, greedy 46, top-k
+// 200 80, min-p 63, top-p alone 214, top-k 5000 180.  The first rows' pass 1
+// runs at HBM speed, later ones' is bound by issue and latency (with the next
+// rows brought into L2 ahead the time is the same); what a row waits for is
+// the latency of its phases, with two CTAs on an SM.
 //
 // Arithmetic.  e is fp32 (the difference before the scale: a large logit must
 // not lose what tells it from its neighbours).  Partial sums of a thread are
