@@ -231,7 +231,7 @@ sinkattn_status sinkattn_grpo_loss(const sinkattn_grpo_problem* g, const float* 
  * A byte holds two e2m1 codes, the lower dim in the low nibble (0, 0.5, 1,
  * 1.5, 2, 3, 4, 6 and a sign); a scale is e4m3 and serves 16 dims of a token.
  * A value is code * scale * (the head's fp32 factor k_scale or v_scale, which
- * lies between 2^-100 and 2^100).
+ * lies between 2^-100 and 2^100); what is below 2^-126 counts as 0.
  *
  * Pages.  Slot s holds seqlens[s] tokens in the pages page_table[s][0 ..
  * ceil(seqlens[s] / page_size) - 1]; the other entries mean nothing.
