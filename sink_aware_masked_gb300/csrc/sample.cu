@@ -34,8 +34,9 @@
 // Arithmetic.  e is fp32 (the difference before the scale: a large logit must
 // not lose what tells it from its neighbours).  Partial sums of a thread are
 // fp32, and so is Z, in a fixed order; masses that decide are 64-bit fixed
-// point: those of chunks in units of 2^-40, those of logits under selection
-// in units of Z 2^-43.  Integer sums are the
+// point: those of chunks in units of 2^-40, inside the chunk that holds the
+// token as fine as its mass allows, those of logits under selection in units
+// of Z 2^-43.  Integer sums are the
 // same in every order, so histogram atomics leave the result reproducible,
 // and 2^18 roundings lose at most 2^-22 (chunks) or 2^-25 of the whole.  FP64 is
 // not used: its rate on this GPU would cost more than all the rest.
@@ -1077,8 +1078,16 @@ class Row {
     if (!(before <= target && before + slice > target)) return;  // exactly one CTA holds the target
     const unsigned beyond = __ballot_sync(0xffffffffu, before + chunk_upto > target);
     const int chunk = __ffs(beyond) - 1;
-    before += __shfl_sync(0xffffffffu, chunk_upto - mine, chunk);
-    if (tid == 0) sh_.found = sh_.last = -1;
+    // From here on the masses before the chunk are left out, and the unit is as fine as 64 bits allow: the chunk's
+    // mass, at least 1 in the old unit, becomes 2^57 to 2^58 in the new one.  So logits whose masses are 0 each in
+    // the old unit, and more than 0 only together, are met by the walk one by one.  (The warps' sums lost less than
+    // one old unit each, so that the walk's own sum stays below 17 * 2^58.)
+    const u64 chunk_mass = __shfl_sync(0xffffffffu, mine, chunk);
+    const int finer = __clzll(chunk_mass) - 6;  // the chunk's mass is below 2^58
+    const u64 goal = (target - before - __shfl_sync(0xffffffffu, chunk_upto - mine, chunk)) << finer;
+    const float one = kSumOne * __int_as_float((127 + finer) << 23);
+    before = 0;
+    if (tid == 0) sh_.found = -1, sh_.last = max(chunk * chunk_turns_ * kThreads * E::kVec, shift_);
     __syncthreads();
     const int turns = (vectors_ + kThreads - 1) / kThreads;
     for (int t = chunk * chunk_turns_; t < min((chunk + 1) * chunk_turns_, turns); ++t) {
@@ -1090,7 +1099,7 @@ class Row {
         E::unpack(load(v), x);
 #pragma unroll
         for (int i = 0; i < E::kVec; ++i) {
-          e[i] = x[i] >= floor_ ? static_cast<u64>(kept_mass(x[i], index_of(v) + i) * kSumOne) : 0;
+          e[i] = x[i] >= floor_ ? static_cast<u64>(kept_mass(x[i], index_of(v) + i) * one) : 0;
           own += e[i];
           if (e[i] > 0) last = i;
         }
@@ -1098,13 +1107,13 @@ class Row {
       const u64 upto = before + block_scan(own, sh_.warp_u);
       if (last >= 0) {
         atomicMax(&sh_.last, v * E::kVec + last);
-        if (upto > target && upto - own <= target) {
+        if (upto > goal && upto - own <= goal) {
           u64 run = upto - own;
           bool hit = false;
 #pragma unroll
           for (int i = 0; i < E::kVec; ++i) {
             run += e[i];
-            if (!hit && run > target) sh_.found = v * E::kVec + i, hit = true;
+            if (!hit && run > goal) sh_.found = v * E::kVec + i, hit = true;
           }
         }
       }
@@ -1113,9 +1122,9 @@ class Row {
       for (int w = 0; w < kWarps; ++w) before += sh_.warp_u[w];
       __syncthreads();
     }
-    // the chunk's sum was rounded elsewhere: where the walk falls short of the target, the last kept one
+    // the chunk's sum was rounded elsewhere: where the walk falls short of the goal, the last kept one
     const int at = sh_.found >= 0 ? sh_.found : sh_.last;
-    if (tid == 0 && at >= 0)
+    if (tid == 0)
       put_token(a, row, first_ + at - shift_, E::one(base_[at]), static_cast<float>(total) * (1.f / kSumOne));
   }
 

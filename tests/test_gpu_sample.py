@@ -205,3 +205,37 @@ def test_cuts_far_below_the_largest_logit(t):
     x = torch.from_numpy(rng.randn(4, 40003)).float().to(DEV)
     x[:, 77] = 45.0 * max(t, 1.0)
     check(x, [0.1, 0.9, 0.5, 1 - 2.0 ** -24], [t] * 4, [3000, 20000, 39000, 5000], [1.0, 1.0, 0.999, 1.0], [0.0] * 4)
+
+
+def sentinel_outputs(rows):
+    return dict(tokens=torch.full((rows,), -77, dtype=torch.int32, device=DEV),
+                logp=torch.full((rows,), 7e7, device=DEV), logq=torch.full((rows,), 7e7, device=DEV))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("vocab,peak,height,gap", [
+    (16384, 12000, 28.5, 16384), (201088, 150000, 30.0, 16384), (201088, 3, 28.5, 201088), (201088, 201080, 28.5, 201088),
+    (40009, 20000, 30.0, 40009)])
+@pytest.mark.parametrize("k,m", [(0, 0.0), (-9, 0.0), (0, 1e-30)])
+def test_masses_that_count_together_alone(vocab, peak, height, gap, k, m, dtype):
+    """Logits more than 27.7 below the largest have masses under 2^-40 of its mass, yet thousands of them together
+    have more: where u lies among them the row still gets a token, the first one for u = 0.  `gap` logits from the
+    first on are 0 (the others are masked), one is `height`; k < 0: all but -k of the allowed ones are kept."""
+    import sink_aware_masked_gb300 as sa
+
+    u = [0.0, 2.0 ** -24, 0.5, 1 - 2.0 ** -24, -3.0, 7.0]
+    n = len(u)
+    x = torch.full((n, vocab), float("-inf"), dtype=dtype, device=DEV)
+    x[:, :gap] = 0
+    x[:, peak] = height
+    full = lambda v, t=torch.float32: torch.full((n,), v, dtype=t, device=DEV)  # noqa: E731
+    top_k = gap + k if k < 0 else 0
+    out = sentinel_outputs(n)
+    sa.sample_tokens(x, torch.tensor(u, device=DEV), temperature=full(1.0), top_k=full(top_k, torch.int32),
+                     top_p=full(1.0), min_p=full(m), **out)
+    tokens = out["tokens"].tolist()
+    # every output is written; a logarithm is off by TOL at most (see above), so one of a probability is below TOL
+    assert all(0 <= t < vocab for t in tokens) and (out["logp"] <= TOL).all() and (out["logq"] <= TOL).all(), tokens
+    # a warp's masses together reach 2^-40 from the first logits on, so that u = 0 finds the very first
+    assert tokens[0] == tokens[4] == (0 if peak != 3 else tokens[0]) and tokens[2] == peak
+    check(x, u, [1.0] * n, [top_k] * n, [1.0] * n, [m] * n)
