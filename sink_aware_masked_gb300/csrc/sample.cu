@@ -417,7 +417,13 @@ class Row {
         if (m > top) {
           const float next = m * scale_;
           const bool next_fused = fabsf(next) < 1048576.f;
-          const float f = fused && next_fused ? ex2(ref - next) : ex2((top - m) * scale_);
+          float by = ref - next;
+          if (!fused || !next_fused) {  // from top's or ref's basis to m's or next's: ref and next are rounded
+            by = (top - m) * scale_;
+            if (fused) by -= fmaf(top, scale_, -ref);
+            if (next_fused) by += fmaf(m, scale_, -next);
+          }
+          const float f = ex2(by);
           sum.x *= f;
           sum.y *= f;
           top = m;

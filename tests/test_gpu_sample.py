@@ -239,3 +239,22 @@ def test_masses_that_count_together_alone(vocab, peak, height, gap, k, m, dtype)
     # a warp's masses together reach 2^-40 from the first logits on, so that u = 0 finds the very first
     assert tokens[0] == tokens[4] == (0 if peak != 3 else tokens[0]) and tokens[2] == peak
     check(x, u, [1.0] * n, [top_k] * n, [1.0] * n, [m] * n)
+
+
+@pytest.mark.parametrize("vocab", [16384, 40009, 262144])
+@pytest.mark.parametrize("t", [1.0, 0.001, 300.0])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_logits_around_the_end_of_the_fused_exponents(sign, t, vocab):
+    """Where |x| log2(e) / T passes 2^20 the exponent is computed another way: a thread whose maximum crosses the
+    border, up or down, keeps the whole of what it has summed before.  The logits are spaced as fp32 has them there
+    (2^-24 of their value, 0.06 T), all within 4 T of the border; nothing below is cut but where k says so."""
+    rng = np.random.RandomState(11)
+    t32, m = float(np.float32(t)), np.linspace(-4.0, 4.0, vocab)
+    edge = sign * 2.0 ** 20 / np.log2(np.e) * t32
+    rows = [m, m[::-1], rng.permutation(m)]
+    for at in (0.1, 0.3, 0.6, 0.9):  # two levels, one on either side
+        rows += [np.where(np.arange(vocab) < at * vocab, lo, -lo) for lo in (-1.0, -0.1)]
+    x = torch.from_numpy(edge + np.stack(rows) * t32).float().to(DEV)
+    r = len(x)
+    for k, floor in ((0, 0.0), (vocab - 7, 0.0), (0, 1e-9), (100, 0.0)):
+        check(x, rng.rand(r), [t] * r, [k] * r, [1.0] * r, [floor] * r)
