@@ -278,7 +278,8 @@ sinkattn_status sinkattn_kv4_reserve(const sinkattn_kv4_cache* cache, const int3
  * the entry, where a slot is out of range, dst[i] is not empty or is named
  * earlier in the call, or the pages run out (then every later entry that
  * needs one gets none either).  Where the source's open page is not in the
- * pool, the copy's is -1. */
+ * pool, the copy's is -1.  A `done` that shares memory with src or dst is
+ * refused (INVALID_ARG). */
 sinkattn_status sinkattn_kv4_fork(const sinkattn_kv4_cache* cache, const int32_t* src, const int32_t* dst, int32_t n,
                                   int32_t* done, void* stream);
 

@@ -55,6 +55,12 @@ sinkattn_status check_list(int32_t n, const void* list) {
   return SINKATTN_OK;
 }
 
+// Whether two lists of n int32 share memory.
+bool lists_overlap(const int32_t* a, const int32_t* b, int32_t n) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return (x < y ? y - x : x - y) < static_cast<uintptr_t>(n) * 4;
+}
+
 sinkattn_status tokens_common(const sinkattn_kv4_cache* cache, const int32_t* slots, int32_t n, const int32_t* cu,
                               int32_t total, const void* k, const void* v, sa::Kv4Cache& c) {
   sinkattn_status st = check_cache(cache, c);
@@ -96,6 +102,8 @@ sinkattn_status sinkattn_kv4_fork(const sinkattn_kv4_cache* cache, const int32_t
       (st = check_list(n, done)) != SINKATTN_OK)
     return st;
   if (n == 0) return SINKATTN_OK;
+  // the second of fork's launches reads src and dst again
+  if (lists_overlap(done, src, n) || lists_overlap(done, dst, n)) return SINKATTN_ERR_INVALID_ARG;
   return from_cuda(sa::launch_kv4_fork(c, src, dst, n, done, static_cast<cudaStream_t>(stream)));
 }
 

@@ -231,3 +231,12 @@ def test_a_caches_tensors_cannot_be_replaced():
     assert c.seqlens is first and c.num_heads_kv == 300
     c.note = 1
     c.note = 2
+
+
+@pytest.mark.parametrize("n,src,dst,done", [(1, 0, 64, 0), (1, 0, 64, 64), (8, 0, 64, 28), (8, 0, 64, 92), (8, 64, 0, 36),
+                                            (4096, 0, 1 << 20, 4 * 4095)])
+def test_fork_refuses_a_done_that_overlaps_its_lists(lib, n, src, dst, done):
+    """Its second launch reads src and dst after the first one has written done."""
+    c = ctypes.byref(cache())
+    assert lib.sinkattn_kv4_fork(c, FAKE + src, FAKE + dst, n, FAKE + done, None) == INVALID
+    assert lib.sinkattn_kv4_fork(c, FAKE, FAKE, 0, FAKE, None) == OK  # nothing is read or written
