@@ -231,7 +231,8 @@ def kv4_read(cache: KV4Cache, slots, total: int, *, cu=None, k=None, v=None):
 
 def kv4_decode_workspace(cache: KV4Cache, q) -> torch.Tensor:
     """A zero-filled workspace for kv4_decode_fwd with queries shaped like q."""
-    size = int(_lib.load().sinkattn_kv4_decode_workspace_size(int(q.shape[0]), int(q.shape[1])))
+    with torch.cuda.device(cache.device):  # the size goes by that device's number of SMs
+        size = int(_lib.load().sinkattn_kv4_decode_workspace_size(int(q.shape[0]), int(q.shape[1])))
     if size == 0:
         raise ValueError(f"kv4_decode_workspace: no workspace for queries of shape {list(q.shape)}")
     return torch.zeros(size, dtype=torch.uint8, device=cache.device)

@@ -240,3 +240,32 @@ def test_fork_refuses_a_done_that_overlaps_its_lists(lib, n, src, dst, done):
     c = ctypes.byref(cache())
     assert lib.sinkattn_kv4_fork(c, FAKE + src, FAKE + dst, n, FAKE + done, None) == INVALID
     assert lib.sinkattn_kv4_fork(c, FAKE, FAKE, 0, FAKE, None) == OK  # nothing is read or written
+
+
+def test_decode_workspace_is_sized_on_the_caches_device(monkeypatch):
+    """The size depends on the device's number of SMs: the cache's device is asked, whichever is current."""
+    current = ["cuda:0"]
+
+    class Device:
+        def __init__(self, device):
+            self.device = str(device)
+
+        def __enter__(self):
+            current.append(self.device)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    class Library:
+        @staticmethod
+        def sinkattn_kv4_decode_workspace_size(rows, heads):
+            return {"cuda:0": 100, "cuda:1": 300}[current[-1]] + rows * heads
+
+    made = {}
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(_lib, "load", lambda: Library)
+    monkeypatch.setattr(torch, "zeros", lambda size, dtype, device: made.update(size=size, device=str(device)))
+    c = object.__new__(rollout.KV4Cache)
+    c.device = torch.device("cuda:1")
+    rollout.kv4_decode_workspace(c, torch.empty(2, 8, 64))
+    assert made == dict(size=316, device="cuda:1") and current == ["cuda:0"]
