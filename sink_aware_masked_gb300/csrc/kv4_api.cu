@@ -22,8 +22,6 @@ sinkattn_status check_cache(const sinkattn_kv4_cache* c, sa::Kv4Cache& out) {
     return SINKATTN_ERR_UNSUPPORTED;
   if (c->num_heads_kv > sa::kMaxHeadsQ) return SINKATTN_ERR_UNSUPPORTED;
   if (static_cast<long long>(c->max_pages) * c->page_size > (1LL << 30)) return SINKATTN_ERR_UNSUPPORTED;
-  if (static_cast<long long>(c->num_pages) * c->num_heads_kv * (c->page_size / 16) > 0xffffffffLL)
-    return SINKATTN_ERR_UNSUPPORTED;  // blocks are numbered in 32 bits (2^32 of them are 4.9 TB)
   if (!c->pages || !c->page_table || !c->seqlens || !c->refcount || !c->k_scale || !c->v_scale)
     return SINKATTN_ERR_INVALID_ARG;
   if (!aligned16(c->pages) || !aligned16(c->page_table) || !aligned16(c->seqlens) || !aligned16(c->refcount) ||

@@ -269,3 +269,14 @@ def test_decode_workspace_is_sized_on_the_caches_device(monkeypatch):
     c.device = torch.device("cuda:1")
     rollout.kv4_decode_workspace(c, torch.empty(2, 8, 64))
     assert made == dict(size=316, device="cuda:1") and current == ["cuda:0"]
+
+
+@pytest.mark.parametrize("kw", [dict(num_pages=2 ** 31 - 1, num_heads_kv=256, page_size=256), dict(num_pages=2 ** 31 - 1),
+                                dict(num_pages=2 ** 28, num_heads_kv=2, page_size=256)])
+def test_pools_of_any_size_are_taken(lib, kw):
+    """Blocks are addressed in 64 bits; the header names no limit of a pool but its int32 count of pages."""
+    c = ctypes.byref(cache(**kw))
+    assert lib.sinkattn_kv4_free(c, None, 0, None) == OK and lib.sinkattn_kv4_reserve(c, None, None, 0, None, None) == OK
+    assert lib.sinkattn_kv4_append(c, FAKE, 1, None, 0, None, None, None) == OK
+    pages = kw["num_pages"]
+    assert lib.sinkattn_kv4_compact_workspace_size(c) == 4 * (-(-pages // 1024) + 2 * pages)
