@@ -36,6 +36,8 @@
 #include "kv4.cuh"
 #include "tc.cuh"
 
+#include <algorithm>
+
 namespace sa {
 namespace {
 
@@ -43,9 +45,10 @@ using namespace kv4;
 
 constexpr int kRowPad = 68;       // floats per row in shared memory
 constexpr float kSlack = 8.f;     // log2 units a score may exceed its row's reference
-// Partial rows that the CTAs of one SM can leave in the workspace: two pairs
-// cut each, 8 NT rows a pair (launch_variant checks it).
-constexpr int kPartRowsPerSm = 192;
+// CTAs that an SM holds of the variants with 8, 16 and 32 rows, and the partial
+// rows that they can leave in the workspace: two cut pairs each.
+constexpr int kPerSm8 = 3, kPerSm16 = 2, kPerSm32 = 1;
+constexpr int kPartRowsPerSm = 2 * std::max({8 * kPerSm8, 16 * kPerSm16, 32 * kPerSm32});
 
 // What beginning a pair costs a CTA, in blocks.  A CTA whose share holds the
 // end of one pair and the begin of the next gets that many blocks less
@@ -956,9 +959,9 @@ cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, int* st
   // (1 CTA of 8: 85.5 us at 8 x 32768 x 4 rows, 2 of 4: 91.7).
   const int nt = p.rows <= 8 ? 1 : p.rows <= 16 ? 2 : 4;
   p.row_groups = ceil_div(p.rows, 8 * nt);
-  if (nt == 1) return launch_variant<1, 4, 3>(p, s);
-  if (nt == 2) return launch_variant<2, 4, 2>(p, s);
-  return launch_variant<4, 8, 1>(p, s);
+  if (nt == 1) return launch_variant<1, 4, kPerSm8>(p, s);
+  if (nt == 2) return launch_variant<2, 4, kPerSm16>(p, s);
+  return launch_variant<4, 8, kPerSm32>(p, s);
 }
 
 }  // namespace sa

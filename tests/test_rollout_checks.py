@@ -280,3 +280,10 @@ def test_pools_of_any_size_are_taken(lib, kw):
     assert lib.sinkattn_kv4_append(c, FAKE, 1, None, 0, None, None, None) == OK
     pages = kw["num_pages"]
     assert lib.sinkattn_kv4_compact_workspace_size(c) == 4 * (-(-pages // 1024) + 2 * pages)
+
+
+def test_decode_workspace_holds_what_the_ctas_can_leave(lib):
+    """At most 64 partial rows of 64 accumulators and two statistics per SM (two cut pairs a CTA), beside the counters."""
+    size = lib.sinkattn_kv4_decode_workspace_size
+    assert 0 < size(0, 1) <= 152 * 64 * 66 * 4 + 256
+    assert size(100, 64) == size(0, 1) + 100 * 64 * 4
