@@ -462,21 +462,26 @@ struct Piece {
   float acc[kD], sum, ref;
 };
 
-// Writes dims d0 .. d0 + kD - 1 of a finished row: o = alpha * acc / sum, and lse.
+// Writes dims d0 .. d0 + kD - 1 of a finished row: o = factor * sigmoid(lse - sink) * acc / sum, and lse.
 template <int kD>
 SA_DEV void finish_row(const DecK& p, int b, int head, int row, int d0, const Piece<kD>& f, float sink, float factor) {
-  const int i = row / p.group, h = head * p.group + row % p.group;
+  const int i = row / p.group, h_q = head * p.group + row % p.group;
   const int64_t at = static_cast<int64_t>(b) * p.n + i;
   const float lse = f.sum == 0.f ? -INFINITY : (f.ref + lg2(f.sum)) * kLn2;
-  const float w = __fdividef(factor, f.sum * (1.f + __expf(sink - lse)));
-  __nv_bfloat16* o = p.o + (at * p.hq + h) * kHeadDim + d0;
+  // sigmoid(lse - sink) = a^2 / (1 + h^2) with h = e^(-|sink - lse| / 2) and a = h where the sink is the larger one,
+  // else 1.  Neither what a sink far above leaves, e^(lse - sink), nor factor / sum need be in fp32's range: one a
+  // goes with the sum, which brings the accumulators to the values' size, the other with the factor.
+  const float x = sink - lse, h = __expf(-0.5f * fabsf(x)), a = x > 0.f ? h : 1.f;
+  const float mean = __fdividef(a, f.sum * (1.f + h * h)), w = factor * a;
+  __nv_bfloat16* o = p.o + (at * p.hq + h_q) * kHeadDim + d0;
   uint32_t v[kD / 2];
 #pragma unroll
-  for (int e = 0; e < kD / 2; ++e) v[e] = f.sum == 0.f ? 0u : pack_bf16(f.acc[2 * e] * w, f.acc[2 * e + 1] * w);
+  for (int e = 0; e < kD / 2; ++e)
+    v[e] = f.sum == 0.f ? 0u : pack_bf16(f.acc[2 * e] * mean * w, f.acc[2 * e + 1] * mean * w);
   static_assert(kD == 4 || kD == 8, "one store");
   if constexpr (kD == 4) *reinterpret_cast<uint2*>(o) = make_uint2(v[0], v[1]);
   if constexpr (kD == 8) *reinterpret_cast<uint4*>(o) = make_uint4(v[0], v[1], v[2], v[3]);
-  if (d0 == 0) p.lse[static_cast<int64_t>(h) * p.num_seqs * p.n + at] = lse;
+  if (d0 == 0) p.lse[static_cast<int64_t>(h_q) * p.num_seqs * p.n + at] = lse;
 }
 
 // Partial results in the workspace: kRows x 64 accumulators, then (ref, sum) per row.

@@ -675,3 +675,45 @@ def test_nothing_is_written_outside_the_outputs():
     assert sa.sinkattn_get_device_status() == 0
     for buf, n in kept:
         assert (buf[:4096] == 0xA5).all() and (buf[4096 + n:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("n,lens", [(1, [1]), (1, [900, 2]), (2, [900, 40]), (4, [5000, 7])])
+def test_decode_sinks_that_leave_almost_nothing(n, lens):
+    """sigmoid(l - sink) down to 2^-133 still multiplies: o = e^(l - sink) softmax(s) V is in bf16's normal range under
+    the factor.  The exponential's argument is off by a few 2^-24 of itself (up to 92), so the relative error is under
+    2^-15 beside the roundings of both results to bf16."""
+    import sink_aware_masked_gb300 as sa
+
+    rng = np.random.RandomState(31)
+    hq = 8
+    c = shuffled(rng, lens, 16, 1, factors=False)
+    c.v_scale = np.array([2.0 ** 30], dtype=np.float32)
+    q = bf16(rng.randn(len(lens) * n, hq, 64)).to(DEV)
+    base = torch.full((hq,), -1e30, device=DEV)
+    slots = i32(list(range(len(lens))))
+    h = handle(c)
+    plain, lse = sa.kv4_decode_fwd(h, slots, q, base, q_per_seq=n)
+    for above in (20.0, 60.0, 80.0, 86.0):
+        sink = torch.full((hq,), float(lse.max()) + above, device=DEV)
+        o, lse2 = sa.kv4_decode_fwd(h, slots, q, sink, q_per_seq=n)
+        assert torch.equal(lse2, lse)
+        w = torch.exp(lse.double() - sink.double()[:, None])
+        want = plain.double() * (w / (1 + w)).t()[:, :, None]
+        assert ((o.double() - want).abs() <= (2 * 2.0 ** -8 + 2.0 ** -15) * want.abs() + 2.0 ** -126).all(), above
+
+
+@pytest.mark.parametrize("n", [1, 2, 4])
+def test_decode_small_factors_over_many_keys(n):
+    """The mean of many equal values under a value factor of 2^-100 is that value: factor / (sum of probabilities)
+    may leave fp32's range on the way, the result does not."""
+    import sink_aware_masked_gb300 as sa
+
+    L = 1 << 20
+    c = sa.KV4Cache.empty(L // 256, 1, L // 256, 1, page_size=256, v_scale=torch.full((1,), 2.0 ** -100, device=DEV))
+    sa.kv4_reserve(c, i32([0]), i32([L]))
+    x = torch.zeros((L, 1, 64), dtype=torch.bfloat16, device=DEV)
+    sa.kv4_append(c, i32([0]), x, torch.full_like(x, 1.5 * 2.0 ** -100))
+    q = torch.zeros((100 * n, 8, 64), dtype=torch.bfloat16, device=DEV)
+    o, lse = sa.kv4_decode_fwd(c, i32([0] * 100), q, torch.full((8,), -1e30, device=DEV), q_per_seq=n)
+    assert ((o.double() / (1.5 * 2.0 ** -100) - 1).abs() <= 2.0 ** -8 + 2.0 ** -11).all()
+    assert (lse - np.log(L)).abs().max() < 1e-4
