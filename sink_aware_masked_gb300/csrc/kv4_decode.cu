@@ -13,13 +13,17 @@
 // Keys and dims are the 16-wide side, so 8 query rows fill the matrix
 // instruction's 8-wide side and none of it is padding.  code * scale has at
 // most 6 significant bits and is exact in f16; q is brought into f16's range
-// by a power of two per row (its 8 bits fit); P is rounded to f16 (2^-11);
-// S, O and the statistics are fp32.
+// by a power of two per row (its 8 bits fit); P is rounded to f16; S, O and the
+// statistics are fp32.
 //
 // The softmax keeps a reference score m per row that need not be the
-// maximum: it moves (and O and l are rescaled) only when a probability would
-// exceed 2^8, which keeps P inside f16's range and leaves one compare and one
-// vote per two blocks in the ordinary case.
+// maximum: it moves (and O and l are rescaled) only when a score exceeds it by
+// more than 8 log2 units, which leaves one compare and one vote per two blocks
+// in the ordinary case.  A key at the reference has P = 2^7, so P stays below
+// 2^15, inside f16's range, and has most of that range below it: P is off by
+// 2^-11 of itself, or, where it is weaker than 2^-21 of the largest and f16
+// is subnormal, by 2^-32 of the largest (one strong key over a million weak
+// ones leaves these their share in O as in l).
 //
 // Work: the visible blocks of all (sequence, kv head, row group) pairs in one
 // line, cut into equal shares, one per worker.  A worker is a CTA, whose warps
@@ -45,6 +49,8 @@ using namespace kv4;
 
 constexpr int kRowPad = 68;       // floats per row in shared memory
 constexpr float kSlack = 8.f;     // log2 units a score may exceed its row's reference
+constexpr float kRefLog2 = 7.f;   // log2 of the probability that stands for the reference,
+constexpr float kRefScale = 1.f / 128.f;  // 2^-kRefLog2
 // CTAs that an SM holds of the variants with 8, 16 and 32 rows, and the partial
 // rows that they can leave in the workspace: two cut pairs each.
 constexpr int kPerSm8 = 3, kPerSm16 = 2, kPerSm32 = 1;
@@ -265,9 +271,9 @@ SA_DEV void block_step(Rows<NT>& r, const Tile (&tile)[U], const uint32_t (&qf)[
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        // subtracted first: the largest of huge scores has to give exactly 2^0
-        s[u][nt][e] = ex2((s[u][nt][e] - r.ref[nt][e]) * coef[nt][e]);
-        s[u][nt][2 + e] = ex2((s[u][nt][2 + e] - r.ref[nt][e]) * coef[nt][e]);
+        // subtracted first: the largest of huge scores has to give exactly 2^7
+        s[u][nt][e] = ex2(fmaf(s[u][nt][e] - r.ref[nt][e], coef[nt][e], kRefLog2));
+        s[u][nt][2 + e] = ex2(fmaf(s[u][nt][2 + e] - r.ref[nt][e], coef[nt][e], kRefLog2));
         r.sum[nt][e] += s[u][nt][e] + s[u][nt][2 + e];
       }
       pf[u][nt][0] = transpose8(pack_f16(s[u][nt][0], s[u][nt][1]));
@@ -456,7 +462,8 @@ class Stream {
 };
 
 // A row's running softmax over some of its keys: kD of the accumulator's
-// dims.  ref is -inf where none of the keys was seen.
+// dims.  ref is -inf where none of the keys was seen; a key at ref counts as
+// 2^kRefLog2 in sum and acc.
 template <int kD>
 struct Piece {
   float acc[kD], sum, ref;
@@ -467,7 +474,7 @@ template <int kD>
 SA_DEV void finish_row(const DecK& p, int b, int head, int row, int d0, const Piece<kD>& f, float sink, float factor) {
   const int i = row / p.group, h_q = head * p.group + row % p.group;
   const int64_t at = static_cast<int64_t>(b) * p.n + i;
-  const float lse = f.sum == 0.f ? -INFINITY : (f.ref + lg2(f.sum)) * kLn2;
+  const float lse = f.sum == 0.f ? -INFINITY : (f.ref + lg2(f.sum * kRefScale)) * kLn2;
   // sigmoid(lse - sink) = a^2 / (1 + h^2) with h = e^(-|sink - lse| / 2) and a = h where the sink is the larger one,
   // else 1.  Neither what a sink far above leaves, e^(lse - sink), nor factor / sum need be in fp32's range: one a
   // goes with the sum, which brings the accumulators to the values' size, the other with the factor.

@@ -717,3 +717,40 @@ def test_decode_small_factors_over_many_keys(n):
     o, lse = sa.kv4_decode_fwd(c, i32([0] * 100), q, torch.full((8,), -1e30, device=DEV), q_per_seq=n)
     assert ((o.double() / (1.5 * 2.0 ** -100) - 1).abs() <= 2.0 ** -8 + 2.0 ** -11).all()
     assert (lse - np.log(L)).abs().max() < 1e-4
+
+
+@pytest.mark.parametrize("entries,n,far,score", [(500, 1, 262144, 17.53125), (500, 2, 262144, 17.53125),
+                                                 (250, 4, 262144, 17.53125), (1, 1, 262144, 17.53125),
+                                                 (3, 1, 700, 17.53125), (3, 2, 700, 5.25), (3, 4, 700, 5.25), (3, 1, 700, 5.625)])
+def test_decode_one_strong_key_over_many_weak_ones(entries, n, far, score):
+    """One key takes nearly all and its value is 0, as with the first token of trained models: what is left is the
+    many others' share.  The largest probability stands in f16 as 2^7 at least, so one that is weaker is off by half
+    a step, 2^-11 of itself or 2^-25 where f16 is subnormal, 2^-32 of the largest: o is off by
+    (2 ds + 2^-11 + 2^-20) sum p |v| + far 2^-32 max|v| and its own rounding (ds as above).  l is a running sum in
+    fp32, one addition per block and lane: an addition is off by 2^-24 of the sum at most, and here, where all weak
+    keys are alike, always to the same side, so that lse is off by that much for every block of a warp: a pair's
+    blocks are shared by 4 warps at least, those of a short one (700 keys) by none."""
+    import sink_aware_masked_gb300 as sa
+
+    hq, a, at = 8, 1.5, 40 if far < 1000 else 5
+    q1 = score / 8 / a  # 64 dims, scale 1/8
+    assert float(torch.tensor(q1).to(torch.bfloat16)) == q1
+    c = sa.KV4Cache.empty(-(-far // 64), 1, -(-far // 64), 1, page_size=64)
+    assert sa.kv4_reserve(c, i32([0]), i32([far])).tolist() == [1]
+    k, v = torch.zeros((far, 1, 64), dtype=torch.bfloat16, device=DEV), torch.full((far, 1, 64), a, dtype=torch.bfloat16, device=DEV)
+    k[at], v[at] = a, 0  # 6 * 2^-2: exact in the cache
+    sa.kv4_append(c, i32([0]), k, v)
+    q = torch.full((entries * n, hq, 64), q1, dtype=torch.bfloat16, device=DEV)
+    sink = torch.full((hq,), -1e30, device=DEV)
+    o, lse = sa.kv4_decode_fwd(c, i32([0] * entries), q, sink, q_per_seq=n)
+    weak = (far - n + np.arange(n)).astype(np.float64)  # weak keys that row i sees
+    total = np.exp(score) + weak
+    p = np.tile(weak / total, entries)[:, None, None]
+    want, want_l = p * a, np.tile(np.log(total), entries)[None]
+    ds = 64 * 2.0 ** -23 * score
+    tol = (2 * ds + 2.0 ** -11 + 2.0 ** -20) * p * a + far * 2.0 ** -32 * a + 2.0 ** -8 * want
+    err = np.abs(o.double().cpu().numpy() - want)
+    assert (err <= tol).all(), float((err / tol).max())
+    err = np.abs(lse.double().cpu().numpy() - want_l)
+    additions = far / 16 / (4 if far > 1000 else 1)
+    assert (err <= ds + 2.0 ** -21 * (np.abs(want_l) + 4) + additions * 2.0 ** -24).all(), float(err.max())
