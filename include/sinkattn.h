@@ -342,7 +342,8 @@ sinkattn_status sinkattn_kv4_decode_fwd(const sinkattn_kv4_cache* cache, const i
  *   e_i = exp((x_i - max x) / temperature), order: larger x first, of equal
  *   ones the lower index; top_k keeps the first top_k (<= 0 or >= vocab: all);
  *   top_p the shortest run of those whose mass is at least top_p of theirs
- *   (>= 1: all, <= 0: the first one); min_p those with e_i >= min(min_p, 1).
+ *   (>= 1: all, <= 0: the first one); min_p those with e_i >= min_p (>= 1:
+ *   those that equal the largest).
  *   The token is the first index whose kept mass up to and including it
  *   exceeds u times the kept mass.  temperature 0: the first in the order,
  *   with e at temperature 1.

@@ -291,6 +291,8 @@ class Row {
       if (by_count) kept = search(true, k, 0.f, by_mass);
       if (by_mass) search(false, by_count ? part_of(kept, top_p) : 0, top_p, true);
     }
+    const u64 least = min_p_cut();
+    cut_ = cut_ > least ? cut_ : least;
     if (listed_) {
       __syncthreads();  // the histogram's place is used again
       pick(a, row, share, first_, end_ - shift_, ctas_ > 1, [&](auto f) {
@@ -524,6 +526,9 @@ class Row {
   }
 
   SA_DEV float mass(float x) const { return ex2((x - max_) * scale_); }
+  // min-p of 1 keeps what equals the largest, by its key, since a smaller logit's e may round to 1 (a large temperature,
+  // a near tie).
+  SA_DEV u64 min_p_cut() const { return min_mass_ >= 1.f ? static_cast<u64>(order_key(max_)) << kIndexBits : 0; }
   SA_DEV u64 fixed(float x) const { return static_cast<u64>(mass(x) * to_fixed_); }
 
   SA_DEV int block_min(int x) {
@@ -609,12 +614,14 @@ class Row {
     for (int w = 0; w < kWarps; ++w) all += sh_.warp_u[w];
     // top-p counts against the first k, or, without top-k, against everything
     const u64 target = top_p < 1.f ? part_of(by_count ? all : whole_mass(all), top_p) : ~0ull;
+    const u64 least = min_p_cut();
     int kept = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = tid * kPer + j;
       const u64 excluded = before + (j > 0 ? upto[j > 0 ? j - 1 : 0] : 0);
-      if (i < min(n, k) && e[j] >= min_mass_ && e[j] > 0.f && (i == 0 || excluded < target)) ++kept;
+      if (i < min(n, k) && e[j] >= min_mass_ && e[j] > 0.f && (i == 0 || excluded < target) && sh_.s.key[i] >= least)
+        ++kept;
     }
     kept = block_sum_int(kept);  // they are the first ones
     pick(a, row, share, 0, vocab_, false, [&](auto f) {

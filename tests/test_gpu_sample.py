@@ -258,3 +258,30 @@ def test_logits_around_the_end_of_the_fused_exponents(sign, t, vocab):
     r = len(x)
     for k, floor in ((0, 0.0), (vocab - 7, 0.0), (0, 1e-9), (100, 0.0)):
         check(x, rng.rand(r), [t] * r, [k] * r, [1.0] * r, [floor] * r)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [100, 5000, 40009])
+def test_min_p_of_one_keeps_the_largest_alone(vocab, dtype):
+    """Also where a smaller logit's e is 1 to fp32's, or to 64 bits', last place: a large temperature, a neighbouring
+    fp32 value.  So what min-p keeps of the oracle's other choices is told by the logits, not by their e."""
+    rng = np.random.RandomState(vocab)
+    x = torch.from_numpy(rng.randn(14, vocab)).to(dtype).to(DEV)
+    if dtype == torch.float32:
+        x[7:] = 1.0 + 2.0 ** -23 * torch.from_numpy(rng.randint(0, 3, (7, vocab))).float().to(DEV)
+    else:
+        x[7:] = torch.from_numpy(rng.randint(0, 3, (7, vocab))).to(dtype).to(DEV)
+    k = [0, 50, 4000, 0, 30, 4500, 0] * 2
+    p = [1.0, 1.0, 1.0, 0.9, 0.9, 0.99999, 0.0] * 2
+    for t in (1e10, 1e36, 40.0):
+        for m in (1.0, 3.0):
+            u = rng.rand(14).astype(np.float32)
+            token, logp, logq = run(x, u, [t] * 14, k, p, [m] * 14)
+            for r, row in enumerate(x.double().cpu().numpy()):
+                kept = ref.kept_tokens(row, 0.0, float(np.float32(t)), k[r], float(np.float32(p[r])), 0.0)[2]
+                kept = kept[row[kept] == row.max()]
+                n = len(kept)
+                assert token[r] == kept[int(float(u[r]) * n)], (t, m, r, token[r], n)
+                assert abs(logq[r] + np.log(n)) <= TOL + 2.0 ** -23 * np.log(n)
+                total = np.exp((row - row.max()) / float(np.float32(t))).sum()
+                assert abs(logp[r] + np.log(total)) <= TOL + 2.0 ** -23 * np.log(total)
