@@ -9,9 +9,9 @@
 //   token = the first index, in index order, whose kept mass up to and
 //   including it exceeds u times the kept mass
 //
-// A row belongs to a CTA, or to a cluster of CTAs where there are few rows.
-// Pass 1 reads it from HBM and leaves the maximum, Z and every thread's own
-// maximum; later passes find it in L2.
+// A row belongs to a CTA, or, where the vocabulary is longer than one CTA's
+// slice, to a cluster of two or four.  Pass 1 reads it from HBM and leaves the
+// maximum, Z and every thread's own maximum; later passes find it in L2.
 //
 //   Nothing to select: the token lies in the chunk whose mass, known from
 //   pass 1, holds u Z; that chunk alone is read again.

@@ -285,3 +285,16 @@ def test_min_p_of_one_keeps_the_largest_alone(vocab, dtype):
                 assert abs(logq[r] + np.log(n)) <= TOL + 2.0 ** -23 * np.log(n)
                 total = np.exp((row - row.max()) / float(np.float32(t))).sum()
                 assert abs(logp[r] + np.log(total)) <= TOL + 2.0 ** -23 * np.log(total)
+
+
+@pytest.mark.parametrize("vocab", [16384, 16385, 32768, 32769])
+@pytest.mark.parametrize("k,p,m", [(200, 0.95, 0.0), (3000, 1.0, 0.0), (9000, 0.9, 0.01), (0, 0.95, 0.02), (0, 0.4, 0.0),
+                                   (0, 1.0, 1e-6), (40, 1.0, 0.3), (2048, 0.999, 0.0), (0, 1.0, 0.0), (1, 1.0, 0.0)])
+def test_clusters_of_every_size(k, p, m, vocab):
+    """Vocabularies on both sides of the borders between one, two and four CTAs a row, at any alignment of the rows;
+    lists on both sides of what is sorted at once."""
+    rng = np.random.RandomState(vocab + k)
+    x = -1.3 * np.log(1 + rng.rand(6, vocab + 3) * vocab) + rng.randn(6, vocab + 3)
+    x[::3, 700:] = float("-inf")  # all that is allowed lies in one place
+    for dtype in (torch.float32, torch.float16):
+        check(torch.from_numpy(x).to(dtype).to(DEV)[:, :vocab], rng.rand(6), [0.9] * 6, [k] * 6, [p] * 6, [m] * 6)
