@@ -213,7 +213,9 @@ sinkattn_status sinkattn_grpo_loss(const sinkattn_grpo_problem* g, const float* 
  * The 4-bit paged key/value cache and what a rollout does with it.  One
  * prompt's pages are shared by the rollouts of its GRPO group; every new
  * token attends to the cache and is sampled with the log-probability that
- * sinkattn_grpo_loss takes as logp_old.
+ * sinkattn_grpo_loss takes as logp_old.  A cache is one layer's: a model keeps
+ * one per layer, each with its own tables and counts, and reserves, forks,
+ * frees and compacts each of them.
  *
  * All state is on the device and every call is asynchronous, so a step can be
  * captured into a CUDA graph and replayed while the sequences grow (make the
@@ -322,8 +324,9 @@ sinkattn_status sinkattn_kv4_read(const sinkattn_kv4_cache* cache, const int32_t
  * for sequences.  q and o bf16 [num_seqs * q_per_seq, num_heads_q, 64], lse
  * fp32 [num_heads_q, num_seqs * q_per_seq]; row b * q_per_seq + i is position
  * seqlens[slots[b]] - q_per_seq + i.  Rows at negative positions (an idle
- * entry, a sequence shorter than q_per_seq) get o = 0, lse = -inf.  The
- * lengths are read on the device.  (num_heads_q / num_heads_kv) * q_per_seq
+ * entry, a sequence shorter than q_per_seq) get o = 0, lse = -inf.  Scores are
+ * fp32: a row that sees one beyond fp32's range in log2 units may read as NaN.
+ * The lengths are read on the device.  (num_heads_q / num_heads_kv) * q_per_seq
  * <= 128.  The workspace (sinkattn_kv4_decode_workspace_size bytes for
  * num_rows = num_seqs * q_per_seq, 16-byte aligned, its size depends on the
  * device's SM count) is zero-filled once; every call leaves it usable for

@@ -526,8 +526,10 @@ SA_DEV float scaled8(uint4 v, const Divisor& factor, float2 (&y)[4]) {
 }
 
 // Measured: 83 k tokens x 8 heads in 46.8 us (220 MB, 32.5 us at the copy
-// rate), bound by issue (56 % of the slots; one dim per instruction 63 us);
-// 64 x 1 tokens in about 4 us, a chain of loads (offset, slot, length, page).
+// rate), bound by the loads' latency: a third of the warps, 56 % of the issue
+// slots, most stalls on the rows' loads, which a warp with one block has nothing
+// to overlap with (one dim per instruction: 63 us).  64 x 1 tokens in about 4 us,
+// a chain of loads (offset, slot, length, page).
 __global__ void __launch_bounds__(256) kv4_append_kernel(const Kv4Cache c, const TokenArgs a,
                                                          const __nv_bfloat16* __restrict__ k,
                                                          const __nv_bfloat16* __restrict__ v, int64_t warps) {

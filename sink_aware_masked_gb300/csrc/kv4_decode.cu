@@ -32,11 +32,13 @@
 // merges nothing.  A pair cut between CTAs leaves partial results in the
 // workspace, and the last CTA of the pair to arrive merges them in order.
 //
-// Measured (GB300): 32 x 8192 keys, 64/8 heads, 42.0 us (151 MB, 22.4 us at the
+// Measured (GB300): 32 x 8192 keys, 64/8 heads, 42.2 us (151 MB, 22.4 us at the
 // copy rate): 53 of an SM's cycles per block, 147 instructions, of them 69
 // conversions and scalings and 8 products; without conversions and products a
-// block takes 41, the memory's rate.  8 x 32768 keys x 4 rows 84.4 us, 200
-// windowed sequences 10.6 us, one sequence of 37 keys 6.7 us.
+// block takes 41, the memory's rate.  It is bound by dependent instructions: 2.1
+// of 4 a clock, most stalls the wait for a warp's own last one, 12 warps an SM.
+// 8 x 32768 keys x 4 rows 84.4 us, 200 windowed sequences 10.6 us, one sequence
+// of 37 keys 6.5 us.
 #include "kv4.cuh"
 #include "tc.cuh"
 

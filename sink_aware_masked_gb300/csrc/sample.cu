@@ -25,8 +25,9 @@
 //   until they are few.  A last pass sums what is kept.
 //
 // Measured (GB300): 1 x 50257 fp32 with top-k and top-p 13.7 us; 256 x 201088
-// bf16 (103 MB, 15 us at the copy rate): no selection 60 us, greedy 46, top-k
-// 200 80, min-p 63, top-p alone 214, top-k 5000 180.  The first rows' pass 1
+// bf16 at T = 0.9 (103 MB, 15 us at the copy rate; three batches in turn, so that
+// none is found in L2): no selection 61 us, greedy 47, top-k 200 81, min-p 0.02
+// 64, top-p 0.95 215, top-k 5000 180, all of these mixed 119.  The first rows' pass 1
 // runs at HBM speed, later ones' is bound by issue and latency (with the next
 // rows brought into L2 ahead the time is the same); what a row waits for is
 // the latency of its phases, with two CTAs on an SM.
@@ -804,7 +805,7 @@ class Row {
       for (int i = threadIdx.x; i < list_n_; i += kThreads) f(sh_.slice_x[i], first_ + sh_.slice_at[i]);
       return;
     }
-    if (floor_ == -INFINITY) {  // every logit is one (256 x 201088, top-k 5000: 181 us; by the queue 281)
+    if (floor_ == -INFINITY) {  // every logit is one (256 x 201088, top-k 5000: 180 us; by the queue 281)
       each_from(floor_, f);
       return;
     }

@@ -79,7 +79,7 @@ def _vector(name: str, t, dtype: torch.dtype, dev) -> int:
 
 
 class KV4Cache:
-    """Keys and values of up to ``num_slots`` sequences in 4 bits, in shared pages.
+    """One layer's keys and values of up to ``num_slots`` sequences in 4 bits, in shared pages.
 
     pages uint8 [num_pages, Hkv, page_size * 72], page_table int32
     [num_slots, max_pages], seqlens int32 [num_slots], refcount int32
