@@ -313,7 +313,7 @@ def _run_own(state):
     op = state["op"]
     if op == "verify":
         if "workspace" not in state:
-            state["workspace"] = sa.verify_workspace(state["logits"], state["temp"].numel())
+            state["workspace"] = sa.verify_workspace(state["logits"])
         return sa.verify_tokens(state["logits"], state["drafts"], state["u"], state["cu"],
                                 draft_logits=state["draft_logits"], temperature=state["temp"],
                                 workspace=state["workspace"])
@@ -326,7 +326,7 @@ def _run_own(state):
         sa.kv_write(pages, state["slot_map"], state["k"], state["v"])
         return state["k_pages"], state["v_pages"]
     if "workspace" not in state:
-        state["workspace"] = sa.kv_decode_workspace(pages, state["q"])
+        state["workspace"] = sa.kv_decode_workspace(pages)
     return sa.kv_decode_fwd(pages, state["slots"], state["q"], state["sink"], q_per_seq=state["rows_hi"],
                             cu_rows=state["cu"] if state["ragged"] else None, window=state["window"],
                             prefix=state["prefix"], workspace=state["workspace"])
