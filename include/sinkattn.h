@@ -41,7 +41,7 @@
  * returns SINKATTN_ERR_CUDA.  Nothing aborts, exits or traps on the device.
  *
  * First call on a device: the calls whose kernels wait (fwd, bwd, decode,
- * kv4 decode, GRPO, the wait self-test) look up the device address of the library's
+ * kv4 and paged decode, GRPO, the wait self-test) look up the device address of the library's
  * status word once per device, with that device current, through
  * cudaGetSymbolAddress (thread-safe).  Make the first such call on each
  * device outside any stream capture; later calls only launch kernels.
@@ -361,6 +361,129 @@ sinkattn_status sinkattn_sample_tokens(const void* logits, int32_t dtype, int32_
                                        int64_t row_stride, const float* u, const float* temperature,
                                        const int32_t* top_k, const float* top_p, const float* min_p, int32_t* tokens,
                                        float* logp, float* logq, void* stream);
+
+/* ----------------------------------------- rollout with drafted tokens
+ * Pages of bf16 keys and values, the type that sinkattn_fwd and sinkattn_bwd
+ * work in, and the verification of drafted tokens.  One step of a rollout:
+ *   sinkattn_kv_plan        where the new tokens of every slot go
+ *   sinkattn_kv_write       their keys and values
+ *   sinkattn_kv_decode_fwd  attention of all of them
+ *   sinkattn_verify_tokens  which drafts stand; those that do not are the next
+ *                           plan's `drop`
+ * All state is on the device and every call is asynchronous, so a step can be
+ * captured into a CUDA graph and replayed while the sequences grow (make the
+ * first call of each kind on a device outside any capture).
+ *
+ * Pages.  Place p of the pool is row p % page_size of page p / page_size.
+ * Slot s holds seqlens[s] tokens in the pages block_table[s][0 ..
+ * ceil(seqlens[s] / page_size) - 1]; the other entries mean nothing.  owner[p]
+ * is the slot that holds page p, -1 where it is free.  New pages are
+ * block_table and owner all -1, seqlens all 0.  A caller that keeps tables of
+ * its own (pages shared between slots, for instance) can leave sinkattn_kv_plan
+ * out: write and decode read the table and the lengths only.
+ *
+ * Rows of several sequences stand one after another: those of entry b are
+ * cu[b] .. cu[b + 1] - 1 (int32 on the device, nondecreasing).  Entries of
+ * `slots` outside [0, num_slots) are idle: they read as an empty sequence.  A
+ * page number outside [0, num_pages), or a position beyond the table, is never
+ * accessed: tokens there are not written and read as NaN.  Limits: page_size
+ * 16, 32, 64, 128 or 256; max_pages * page_size <= 2^30, num_pages * page_size
+ * < 2^31; 4096 entries per call; head_dim 64.  All pointers of the struct are
+ * 16-byte aligned; int32 and fp32 lists elsewhere 4-byte aligned.  Calls that
+ * change pages must not overlap on the GPU with other calls on them. */
+typedef struct {
+  void* k_pages;         /* bf16 [num_pages][page_size][num_heads_kv][64] */
+  void* v_pages;         /* the same */
+  int32_t* block_table;  /* [num_slots][max_pages] */
+  int32_t* seqlens;      /* [num_slots] */
+  int32_t* owner;        /* [num_pages] */
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t num_heads_kv;
+  int32_t num_slots;
+  int32_t max_pages;
+} sinkattn_kv_pages;
+
+/* plan: slot slots[i] drops its last drop[i] tokens (all, if it has fewer;
+ * drop NULL or negative: none) and gets new_tokens[i] new ones.  First the
+ * pages that no token is left in go back, then the requests get theirs, the
+ * lowest-numbered free ones, in the order of the requests; one that does not
+ * fit, and every later one that needs a page, gets none.  live[i] = slots[i],
+ * or -1 where the request was not served: its pages ran out, or its length
+ * would pass the table (the slot is left without what it dropped), or the slot
+ * is out of range or named earlier in the call, or the count is negative
+ * (nothing changes).  cu (int32 [n + 1]) is the running total of the requests'
+ * rows, max(new_tokens, 0) each, served or not.  slot_map[r] is the place of
+ * row r, positions[r] its position in the sequence, r < total; -1 for rows of
+ * requests that were not served and for rows behind cu[n].  live may be slots
+ * itself; otherwise outputs share no memory with inputs. */
+sinkattn_status sinkattn_kv_plan(const sinkattn_kv_pages* pages, const int32_t* slots, const int32_t* drop,
+                                 const int32_t* new_tokens, int32_t n, int32_t* live, int32_t* cu, int32_t* slot_map,
+                                 int32_t* positions, int32_t total, void* stream);
+
+/* write: row r of k and v (bf16, num_heads_kv * 64 values, rows k_stride and
+ * v_stride values apart, multiples of 8) goes to place slot_map[r]; rows whose
+ * place is not in the pool are skipped.  Places differ. */
+sinkattn_status sinkattn_kv_write(const sinkattn_kv_pages* pages, const int32_t* slot_map, int32_t rows, const void* k,
+                                  int64_t k_stride, const void* v, int64_t v_stride, void* stream);
+
+/* Decode forward over the pages: as sinkattn_decode_fwd (causal) with slots
+ * for sequences.  q and o bf16 [rows, num_heads_q, 64], lse fp32 [num_heads_q,
+ * rows].  Entry b has rows cu_rows[b] .. cu_rows[b + 1] - 1, at most q_per_seq
+ * of them, or without cu_rows q_per_seq rows (rows = num_seqs * q_per_seq);
+ * the i-th of n rows is position seqlens[slots[b]] - n + i.  Rows at negative
+ * positions (an idle entry, a sequence shorter than n) get o = 0, lse = -inf.
+ * Rows outside every entry's, and rows of an entry beyond q_per_seq, are left
+ * as they were.  What a row does not see does not reach it, whatever it holds;
+ * scores are fp32: a row that sees one beyond fp32's range in log2 units may
+ * read as NaN; outputs below 2^-126 may be 0.  (num_heads_q / num_heads_kv) * q_per_seq <= 128.  The
+ * workspace (sinkattn_kv_decode_workspace_size bytes, 16-byte aligned, its size
+ * depends on the device's SM count) is zero-filled once; every call leaves it
+ * usable for later calls of any shape with as many kv heads or fewer, not for
+ * calls that overlap on the GPU.  Results do not depend on the order in which
+ * the GPU runs the parts of the work. */
+size_t sinkattn_kv_decode_workspace_size(int32_t num_heads_kv);
+sinkattn_status sinkattn_kv_decode_fwd(const sinkattn_kv_pages* pages, const int32_t* slots, const int32_t* cu_rows,
+                                       int32_t num_seqs, int32_t q_per_seq, int32_t rows, int32_t num_heads_q,
+                                       int64_t window, int64_t prefix, float scale, const void* q, const float* sink,
+                                       void* o, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Verification of drafted tokens.  logits [rows][row_stride] (the first
+ * `vocab` of each row; dtype 0 fp32, 1 bf16, 2 fp16) are the target's, entry
+ * b's rows cu_rows[b] .. cu_rows[b + 1] - 1: n rows, of which the first n - 1
+ * have a draft each.  drafts (int32 [num_drafts]) and draft_logits
+ * [num_drafts][draft_stride] hold the drafts of all entries one after another.
+ * With p and q the softmax of a row's logits and draft logits at temperature
+ * temperature[b], or without draft_logits (NULL) q = 1 at the draft:
+ *   a draft d stands if u[r] q(d) < p(d), r its row.  The first of an entry
+ *   that does not ends it, with a token drawn from max(p - q, 0) (without
+ *   draft_logits: from p without d); if all stand, its last row gives one drawn
+ *   from p.  Drawn from w: the first index whose cumulated w exceeds the whole
+ *   of w times u of the entry's LAST row; from p where w is 0 everywhere.
+ *   temperature 0: a draft stands if it is the largest logit (the lowest index
+ *   of equal ones), and that is the token drawn; p at temperature 1.
+ * Tokens so emitted follow distribution p, whatever the drafts were drawn from
+ * with q.  tokens [rows]: the drafts that stand, then the token drawn, then -1;
+ * logp [rows] their log p (what sinkattn_grpo_loss takes as logp_old), 0 behind
+ * them.  accepted, rejected [num_seqs]: drafts that stand and that do not.
+ * Rows outside every entry's are left as they were; an entry without rows has
+ * accepted = rejected = 0.
+ * Logits of -inf are never drawn; so a choice of tokens (a grammar, a top-k) is
+ * made by -inf in both rows.  A draft outside [0, vocab) does not stand.  An
+ * entry ends with token -1 at a row of nothing but -inf (logp -inf), and at a
+ * row with a NaN or +inf logit, a draft row of such kind or of nothing but -inf,
+ * or a temperature that is NaN, negative or above 1e36 (logp NaN).  u outside
+ * [0, 1) is clamped (a NaN to 0), fp32 subnormals count as 0.  vocab <= 2^18,
+ * rows <= 2^20, strides >= vocab, any alignment of the rows.  The workspace
+ * (sinkattn_verify_workspace_size bytes, 16-byte aligned) needs no filling; not
+ * for calls that overlap on the GPU. */
+size_t sinkattn_verify_workspace_size(int32_t dtype, int32_t rows, int32_t vocab);
+sinkattn_status sinkattn_verify_tokens(const void* logits, int64_t row_stride, const void* draft_logits,
+                                       int64_t draft_stride, int32_t dtype, int32_t rows, int32_t num_drafts,
+                                       int32_t vocab, const int32_t* drafts, const int32_t* cu_rows, int32_t num_seqs,
+                                       const float* u, const float* temperature, int32_t* tokens, float* logp,
+                                       int32_t* accepted, int32_t* rejected, void* workspace, size_t workspace_bytes,
+                                       void* stream);
 
 /* Packed-sequence front end (multi-turn trajectories of different lengths,
  * SinkFlex-RL section 3).  seqlens: device int32 [num_seqs];

@@ -27,6 +27,13 @@ from .api import (  # noqa: F401
     sinkattn_unpack,
     sinkattn_varlen_plan,
 )
+from .pages import (  # noqa: F401
+    KVPages,
+    kv_decode_fwd,
+    kv_decode_workspace,
+    kv_plan,
+    kv_write,
+)
 from .rollout import (  # noqa: F401
     KV4Cache,
     kv4_append,
@@ -38,4 +45,6 @@ from .rollout import (  # noqa: F401
     kv4_read,
     kv4_reserve,
     sample_tokens,
+    verify_tokens,
+    verify_workspace,
 )

@@ -67,9 +67,25 @@ class Kv4Cache(ctypes.Structure):
     ]
 
 
+class KvPages(ctypes.Structure):
+    _fields_ = [
+        ("k_pages", ctypes.c_void_p),
+        ("v_pages", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("seqlens", ctypes.c_void_p),
+        ("owner", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("num_heads_kv", ctypes.c_int32),
+        ("num_slots", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+    ]
+
+
 _PP = ctypes.POINTER(Problem)
 _GP = ctypes.POINTER(GrpoProblem)
 _KP = ctypes.POINTER(Kv4Cache)
+_VP = ctypes.POINTER(KvPages)
 _f32 = ctypes.c_float
 SIGNATURES = {
     "sinkattn_fwd_workspace_size": (_sz, [_PP]),
@@ -94,6 +110,14 @@ SIGNATURES = {
                                                _sz, _vp]),
     "sinkattn_sample_tokens": (ctypes.c_int, [_vp, _i32, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                               _vp]),
+    "sinkattn_kv_plan": (ctypes.c_int, [_VP, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp]),
+    "sinkattn_kv_write": (ctypes.c_int, [_VP, _vp, _i32, _vp, _i64, _vp, _i64, _vp]),
+    "sinkattn_kv_decode_workspace_size": (_sz, [_i32]),
+    "sinkattn_kv_decode_fwd": (ctypes.c_int, [_VP, _vp, _vp, _i32, _i32, _i32, _i32, _i64, _i64, _f32, _vp, _vp, _vp,
+                                              _vp, _vp, _sz, _vp]),
+    "sinkattn_verify_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "sinkattn_verify_tokens": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp,
+                                              _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "sinkattn_varlen_plan": (ctypes.c_int, [_vp, _i32, _vp, _vp]),
     "sinkattn_pack": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp]),
     "sinkattn_unpack": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp]),

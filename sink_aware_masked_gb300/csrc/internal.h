@@ -1,6 +1,7 @@
 // Parameters handed from the C-ABI layer to the kernel launchers.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -197,6 +198,52 @@ struct Kv4DecodeArgs {
 size_t kv4_decode_workspace_bytes(long long rows, int hq);
 cudaError_t launch_kv4_decode(const Kv4Cache& c, const Kv4DecodeArgs& a, int* status, cudaStream_t s);
 
+// Pages of bf16 keys and values (pages.cu, pages_decode.cu) after validation.
+struct KvPages {
+  __nv_bfloat16* k;      // [num_pages, page_size, num_heads_kv, 64]
+  __nv_bfloat16* v;
+  int32_t* block_table;  // [num_slots, max_pages]
+  int32_t* seqlens;      // [num_slots]
+  int32_t* owner;        // [num_pages] slot, or -1
+  int num_pages, page_size, num_heads_kv, num_slots, max_pages;
+  int page_log2;  // page_size = 1 << page_log2
+};
+
+struct KvPlanArgs {
+  const int32_t* slots;       // [n]
+  const int32_t* drop;        // [n] or nullptr
+  const int32_t* new_tokens;  // [n]
+  int n, total;
+  int32_t* live;       // [n]
+  int32_t* cu;         // [n + 1]
+  int32_t* slot_map;   // [total]
+  int32_t* positions;  // [total]
+};
+cudaError_t launch_kv_plan(const KvPages& c, const KvPlanArgs& a, cudaStream_t s);
+
+struct KvWriteArgs {
+  const int32_t* slot_map;  // [rows]
+  const __nv_bfloat16* k;   // [rows][num_heads_kv, 64], rows k_stride elements apart
+  const __nv_bfloat16* v;
+  int64_t k_stride, v_stride;
+  int rows;
+};
+cudaError_t launch_kv_write(const KvPages& c, const KvWriteArgs& a, cudaStream_t s);
+
+struct KvDecodeArgs {
+  const int32_t* slots;  // [num_seqs]
+  const int32_t* cu;     // [num_seqs + 1] or nullptr: n rows each
+  const void* q;         // [rows, Hq, 64]
+  const float* sink;
+  void* o;
+  float* lse;            // [Hq, rows]
+  void* workspace;
+  int num_seqs, rows, n, hq, window, prefix;  // n: rows of a sequence, at most
+  float scale;
+};
+size_t kv_decode_workspace_bytes(int hkv);
+cudaError_t launch_kv_decode(const KvPages& c, const KvDecodeArgs& a, int* status, cudaStream_t s);
+
 // Token sampling (sample.cu).
 struct SampleArgs {
   const void* logits;  // [rows, stride], the first `vocab` of each row
@@ -213,6 +260,26 @@ struct SampleArgs {
   float* logq;
 };
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
+
+// Verification of drafted tokens (verify.cu).
+struct VerifyArgs {
+  const void* logits;        // [rows, stride], the first `vocab` of each row
+  const void* draft_logits;  // [num_drafts, draft_stride] or nullptr
+  int dtype;                 // 0 fp32, 1 bf16, 2 fp16
+  int rows, num_drafts, vocab, num_seqs;
+  long long stride, draft_stride;  // elements
+  const int32_t* drafts;     // [num_drafts]
+  const int32_t* cu;         // [num_seqs + 1]
+  const float* u;            // [rows]
+  const float* temperature;  // [num_seqs]
+  int32_t* tokens;           // [rows]
+  float* logp;               // [rows]
+  int32_t* accepted;         // [num_seqs]
+  int32_t* rejected;         // [num_seqs]
+  float4* parts;             // [rows][2][slices]
+};
+size_t verify_workspace_bytes(int dtype, int rows, int vocab);
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
 
 // Optional events recorded around the main kernels (measurement hook).
 struct ProfileEvents {

@@ -6,13 +6,15 @@
 #include <cstdint>
 
 #include "../../include/sinkattn.h"
+#include "checks.h"
 #include "internal.h"
 
-namespace {
+using sa::aligned16;
+using sa::aligned4;
+using sa::check_list;
+using sa::from_cuda;
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-inline sinkattn_status from_cuda(cudaError_t e) { return e == cudaSuccess ? SINKATTN_OK : SINKATTN_ERR_CUDA; }
+namespace {
 
 // Validates `c` and fills `out`.  Touches no CUDA API.
 sinkattn_status check_cache(const sinkattn_kv4_cache* c, sa::Kv4Cache& out) {
@@ -41,15 +43,6 @@ sinkattn_status check_cache(const sinkattn_kv4_cache* c, sa::Kv4Cache& out) {
   out.page_log2 = 0;
   while ((1 << out.page_log2) < c->page_size) ++out.page_log2;
   out.blocks_log2 = out.page_log2 - 4;
-  return SINKATTN_OK;
-}
-
-// A list of n slots (or other int32 per request).
-sinkattn_status check_list(int32_t n, const void* list) {
-  if (n < 0) return SINKATTN_ERR_INVALID_ARG;
-  if (n > sa::kKv4MaxRequests) return SINKATTN_ERR_UNSUPPORTED;
-  if (n > 0 && !list) return SINKATTN_ERR_INVALID_ARG;
-  if (!aligned4(list)) return SINKATTN_ERR_ALIGNMENT;
   return SINKATTN_OK;
 }
 

@@ -1,0 +1,925 @@
+// Decode forward over pages of bf16 keys and values: the new rows of each
+// sequence against its whole history, with the mask, sink and lse of the
+// contiguous decode forward; 1 row a sequence in an ordinary step, several
+// where drafted tokens are attended to, and not the same number everywhere.
+//
+//   s = scale <q, K_k>,  l = log sum_{visible} e^s,  o = sigmoid(l - sink) softmax(s) V
+//
+// 256 bytes per key and kv head, and 4 x 64 x rows operations on them: a
+// stream over the pages, bound by HBM up to some 64 rows.  Keys and values
+// come as TMA boxes of 32 tokens (two of 16 where a page has 16), each warp
+// through a ring of its own, and are multiplied by warp-level matrix
+// instructions with keys and dims on the 16-wide side, so that 8 query rows
+// fill the 8-wide side:
+//   S^T [16 keys x 8 rows] = K [16 x 64] Q^T,   O^T [64 dims x 8 rows] += V^T [64 x 16] P^T
+//
+// The softmax keeps a reference score m per row that need not be the maximum:
+// it moves (and O and the sums are rescaled) only when a score exceeds it by
+// more than 8 log2 units.  A key at the reference has P = 2^-8, so P is at
+// most 1.  P is rounded to bf16 for the product (off by 2^-9 of itself at
+// most), and O is divided by the sum of the rounded P, so that one key alone
+// gives its value exactly; lse takes the fp32 sum of the unrounded ones.
+//
+// Work: the visible turns (32 tokens) of all (sequence, kv head) pairs in one
+// line, cut into equal shares, one per worker.  A worker is a CTA, whose warps
+// take a pair's turns in turn and merge in shared memory; or, where there are
+// many pairs with few turns each, a single warp, which takes whole pairs.  A
+// pair cut between CTAs leaves partial results in the workspace, and the last
+// CTA of the pair to arrive merges them in order.  Above 32 rows two or four
+// warps share a ring and split the rows.
+#include "shares.cuh"
+#include "tc.cuh"
+#include "tmap.h"
+
+#include <algorithm>
+
+#include "internal.h"
+
+namespace sa {
+namespace {
+
+constexpr int kTurn = 32;                          // tokens of a turn
+constexpr int kTurnHalf = kTurn * kHeadDim * 2;    // bytes of its keys (or values)
+constexpr int kTurnBytes = 2 * kTurnHalf;
+constexpr int kBoxBytes = kTurnHalf / 2;           // 16 tokens
+constexpr int kRowPad = 68;                        // floats per row in shared memory
+constexpr float kSlack = 8.f;                      // log2 units a score may exceed its row's reference
+constexpr int kPartPad = 4;                        // floats of statistics per row of a partial result
+// Partial rows that the CTAs of one SM can leave in the workspace: two cut pairs each.
+constexpr int kPartRowsPerSm = 256;
+
+// What beginning a pair costs a CTA, in turns.
+constexpr int kPairCost = 6;
+// Turns of the longest pair up to which warps work alone, each on whole pairs.
+constexpr int kAloneTurns = 24;
+
+struct PageDecK {
+  CUtensorMap tm_k, tm_v;
+  const int32_t* block_table;
+  const int32_t* seqlens;
+  const int32_t* slots;
+  const int32_t* cu;
+  const __nv_bfloat16* q;
+  const float* sink;
+  __nv_bfloat16* o;
+  float* lse;
+  float* part;
+  int* counters;  // [pairs]
+  int* status;
+  int num_pages, page_log2, num_slots, max_pages, num_heads_kv;
+  int num_seqs, total_rows, n, hq, group, window, prefix;
+  float coef;  // scale * log2 e
+};
+
+// D (+)= A B, A 16 x 16 (keys or dims), B 16 x 8.
+SA_DEV void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// 8x8 16-bit transpose across the warp.
+SA_DEV uint32_t transpose8(uint32_t v) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(d) : "r"(v));
+  return d;
+}
+
+SA_DEV float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+SA_DEV float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+SA_DEV float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+// v without its infinities and NaNs (0 in their place).
+SA_DEV uint32_t finite_bf16x2(uint32_t v) {
+  uint32_t r = v;
+  if ((v & 0x7f80u) == 0x7f80u) r &= 0xffff0000u;
+  if ((v & 0x7f800000u) == 0x7f800000u) r &= 0xffffu;
+  return r;
+}
+
+// A sequence of the call: its slot, length, and rows row0 .. row0 + n - 1 of q.
+struct Seq {
+  int slot, len, row0, n;
+};
+
+SA_DEV Seq sequence(const PageDecK& p, int b) {
+  Seq s;
+  s.slot = p.slots[b];
+  s.len = 0;
+  if (s.slot >= 0 && s.slot < p.num_slots)
+    s.len = min(static_cast<long long>(max(p.seqlens[s.slot], 0)), static_cast<long long>(p.max_pages) << p.page_log2);
+  if (p.cu == nullptr) {
+    s.row0 = b * p.n;
+    s.n = p.n;
+  } else {
+    s.row0 = min(max(p.cu[b], 0), p.total_rows);
+    s.n = min(max(p.cu[b + 1], s.row0), p.total_rows) - s.row0;
+  }
+  return s;
+}
+
+// The turns of a sequence that its last n positions can see: [0, pre) and [lo, end).
+struct Span {
+  int pre, lo, end;
+  SA_DEV int count() const { return pre + end - lo; }
+  SA_DEV int turn(int i) const { return i < pre ? i : i - pre + lo; }
+};
+
+SA_DEV Span visible_span(const PageDecK& p, const Seq& q) {
+  Span s;
+  s.end = q.n > 0 ? q.len / kTurn + (q.len % kTurn != 0) : 0;
+  const int first = max(q.len - q.n, 0);  // the earliest of the positions
+  s.lo = min(p.window < 0 ? 0 : max(first - p.window, 0) / kTurn, s.end);
+  const int pre = min(p.prefix, q.len);
+  s.pre = min(pre / kTurn + (pre % kTurn != 0), s.lo);
+  return s;
+}
+
+// The part of a pair that a worker takes: turns [t0, t1) of `turns`.
+struct Segment {
+  long long x;  // where its pair begins in the line that is shared out
+  int b, head, t0, t1, turns;
+  Seq seq;
+  Span span;
+};
+
+// A turn as a warp sees it.
+struct Turn {
+  int key0;      // position of its first key
+  int loaded;    // tokens of it that are in the ring: its first 16, all 32 (a bit each)
+  bool masked;   // some (row, key) is not visible, or a half is not in the ring
+};
+
+// A warp's way through its turns of a segment (part, part + parts, ...): page
+// numbers are loaded a batch of 32 turns ahead; the boxes come through the
+// ring, kStages turns in flight.  Of the kShare warps that use one ring the
+// first starts the copies, once all have read what a stage held.
+template <int kShare, int kStages>
+class Stream {
+ public:
+  SA_DEV Stream(const PageDecK& p, uint32_t ring, uint32_t bars, const tc::Abort& abort, int part, int parts, bool leads)
+      : p_(p), ring_(ring), bars_(bars), abort_(abort), part_(part), parts_(parts), leads_(leads) {}
+
+  // Starts a segment's first copies; none of an earlier one is in flight.
+  SA_DEV void begin(const Segment& s) {
+    seg_ = s;
+    const int all = s.t1 - s.t0;
+    turns_ = s.seq.n > 0 && s.seq.len > 0 && all > part_ && !dead_ ? (all - part_ + parts_ - 1) / parts_ : 0;
+    if (turns_ == 0) return;
+    load_places(0);
+    cur0_ = to_row(next0_, 0, 0);
+    cur1_ = to_row(next1_, 0, 1);
+    if (turns_ > 32) load_places(32);
+    __syncwarp();  // every lane is done with the ring
+    const int now = min(turns_, kStages);
+    for (int d = 0; d < now; ++d) fetch(d, used_ + d, cur0_, cur1_);
+  }
+
+  // Calls step(address of the turn's keys, turn) for every turn.
+  template <class F>
+  SA_DEV void run(F step) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int i = 0; i < turns_; ++i) {
+      const int stage = used_ % kStages;
+      if ((i & 31) == 16 && turns_ > i + 16) {  // the next batch's places are here by now
+        next0_ = to_row(next0_, i + 16, 0);
+        next1_ = to_row(next1_, i + 16, 1);
+      }
+      if (!tc::mbar_wait_warp(full(stage), used_ / kStages & 1, abort_)) {
+        // Out of time, which the status word says: nothing more is started,
+        // and what is in flight has as long again to land.
+        dead_ = true;
+        const long long t0 = clock64();
+        for (int use = used_, last = used_ + min(kStages, turns_ - i); use < last;)
+          if (tc::mbar_try_wait(full(use % kStages), use / kStages & 1) || clock64() - t0 > tc::kTimeoutCycles) ++use;
+        break;
+      }
+      Turn t;
+      const int r0 = __shfl_sync(0xffffffffu, cur0_, i & 31), r1 = __shfl_sync(0xffffffffu, cur1_, i & 31);
+      t.key0 = seg_.span.turn(place(i)) * kTurn;
+      t.loaded = (r0 >= 0) | (r1 >= 0) << 1;
+      const int key1 = t.key0 + kTurn - 1;
+      // seen by all rows: the earliest position causally, the last one's window
+      t.masked = t.loaded != 3 || key1 > seg_.seq.len - seg_.seq.n ||
+                 !(p_.window < 0 || t.key0 >= seg_.seq.len - 1 - p_.window || key1 < p_.prefix);
+      step(ring_ + stage * kTurnBytes, t);
+      __syncwarp();  // every lane is done with the stage
+      if (kShare > 1 && lane == 0) tc::mbar_arrive(empty(stage));
+      if (i + kStages < turns_) {
+        const bool same = (i & 31) + kStages < 32;
+        fetch((i + kStages) & 31, used_ + kStages, same ? cur0_ : next0_, same ? cur1_ : next1_);
+      }
+      ++used_;
+      if ((i & 31) == 31) {
+        cur0_ = next0_;
+        cur1_ = next1_;
+        if (turns_ > i + 33) load_places(i + 33);
+      }
+    }
+  }
+
+ private:
+  SA_DEV uint32_t full(int stage) const { return bars_ + 8 * stage; }
+  SA_DEV uint32_t empty(int stage) const { return bars_ + 8 * (kStages + stage); }
+  SA_DEV int place(int i) const { return seg_.t0 + part_ + parts_ * i; }  // the i-th turn as a number in the pair
+  // The pages of the lane's turn of the batch from the j0-th on: of its first token, and of its 17th.
+  SA_DEV void load_places(int j0) {
+    const int i = j0 + (threadIdx.x & 31);
+    next0_ = next1_ = -1;
+    if (i >= turns_) return;
+    const int pos = seg_.span.turn(place(i)) * kTurn, col = pos >> p_.page_log2, col1 = (pos + 16) >> p_.page_log2;
+    const int32_t* row = p_.block_table + static_cast<int64_t>(seg_.seq.slot) * p_.max_pages;
+    next0_ = row[col];  // a visible turn's first token is below the length, and that is inside the table
+    if (pos + 16 < seg_.seq.len) next1_ = col1 == col ? next0_ : row[col1];
+  }
+  // The pool's row of a half's first token, -1 where it has none.
+  SA_DEV int to_row(int page, int j0, int half) const {
+    const int i = j0 + (threadIdx.x & 31);
+    if (i >= turns_ || page < 0 || page >= p_.num_pages) return -1;
+    const int pos = seg_.span.turn(place(i)) * kTurn + 16 * half;
+    return (page << p_.page_log2) + (pos & ((1 << p_.page_log2) - 1));
+  }
+  // Starts the copies of a turn of the batch, the ring's use-th.
+  SA_DEV void fetch(int in_batch, int use, int rows0, int rows1) {
+    const int r0 = __shfl_sync(0xffffffffu, rows0, in_batch), r1 = __shfl_sync(0xffffffffu, rows1, in_batch);
+    if (kShare > 1) {
+      if (!leads_) return;
+      if (use >= kStages && !tc::mbar_wait_warp(empty(use % kStages), (use / kStages - 1) & 1, abort_)) {
+        // the wait for this turn's bytes finds the abort word set
+        return;
+      }
+    }
+    if ((threadIdx.x & 31) != 0) return;
+    const uint32_t bar = full(use % kStages), to = ring_ + use % kStages * kTurnBytes;
+    const int c = seg_.head * kHeadDim;
+    if (p_.page_log2 > 4) {  // one page, one box of 32 rows (what lies behind the length is read and masked)
+      tc::mbar_expect_tx(bar, r0 >= 0 ? kTurnBytes : 0);
+      if (r0 >= 0) {
+        tc::tma_load_2d(to, &p_.tm_k, c, r0, bar);
+        tc::tma_load_2d(to + kTurnHalf, &p_.tm_v, c, r0, bar);
+      }
+    } else {
+      tc::mbar_expect_tx(bar, ((r0 >= 0) + (r1 >= 0)) * 2 * kBoxBytes);
+      if (r0 >= 0) {
+        tc::tma_load_2d(to, &p_.tm_k, c, r0, bar);
+        tc::tma_load_2d(to + kTurnHalf, &p_.tm_v, c, r0, bar);
+      }
+      if (r1 >= 0) {
+        tc::tma_load_2d(to + kBoxBytes, &p_.tm_k, c, r1, bar);
+        tc::tma_load_2d(to + kTurnHalf + kBoxBytes, &p_.tm_v, c, r1, bar);
+      }
+    }
+  }
+
+  const PageDecK& p_;
+  uint32_t ring_, bars_;
+  tc::Abort abort_;
+  int part_, parts_, used_ = 0, turns_ = 0;
+  bool leads_, dead_ = false;
+  int cur0_ = -1, cur1_ = -1, next0_ = -1, next1_ = -1;
+  Segment seg_;
+};
+
+// What a warp keeps of its rows.  Row 8 nt + 2 t + e of the warp's is lane
+// (g, t)'s entry [nt][e] (the same in all g) except the sums, which are over
+// the lane's own keys until they are reduced.
+template <int NT>
+struct Rows {
+  float o[NT][4][4];   // O^T: [i][e] dim 16 i + g, [i][2 + e] dim 16 i + g + 8
+  float sum[NT][2];    // of P
+  float sum_o[NT][2];  // of P rounded to bf16
+  float ref[NT][2];    // reference score (before the coefficient), 0 while the row has seen no key
+  float limit[NT][2];  // score beyond which ref moves, -inf while the row has seen no key
+};
+
+template <int NT>
+SA_DEV void rows_clear(Rows<NT>& r) {
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r.o[nt][i][e] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      r.sum[nt][e] = r.sum_o[nt][e] = r.ref[nt][e] = 0.f;
+      r.limit[nt][e] = -INFINITY;
+    }
+  }
+}
+
+struct Visible {
+  int window, prefix;
+  SA_DEV bool sees(int at, int key) const {  // at < len: -1 for a row that is not there
+    return key <= at && (window < 0 || key >= at - window || key < prefix);
+  }
+};
+
+// One turn: two blocks of 16 keys, whose chains of products run side by side.
+// kMasked: some (row, key) of them is not visible, or a half is not there.
+// pos[nt][e]: the rows' positions.
+template <int NT, bool kMasked>
+SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[NT][4][2], int tiles, float coef, float slack,
+                      const int (&pos)[NT][2], const Turn& turn, const Visible& vis) {
+  constexpr int U = kTurn / 16;
+  const int lane = threadIdx.x & 31, g = lane >> 2;
+  // Rows of 128 bytes, 16-byte chunks XORed with the row's low three bits.
+  const uint32_t row_k = (lane & 7) + (lane & 8), chunk_k = lane >> 4;
+  const uint32_t row_v = (lane & 7) + (lane >> 4) * 8, chunk_v = lane >> 3 & 1;
+  // scores before the coefficient: s[u][nt][e] key g of block u, s[u][nt][2 + e] key g + 8, row 2 t + e
+  float s[U][NT][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint32_t a[4];
+      ldsm_x4(keys + (16 * u + row_k) * 128 + (((2 * j + chunk_k) ^ (lane & 7)) << 4), a[0], a[1], a[2], a[3]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (NT > 2 && nt >= tiles) continue;
+        if (j == 0)
+          mma_first(s[u][nt], a, qf[nt][j][0], qf[nt][j][1]);
+        else
+          mma16816(s[u][nt], a, qf[nt][j][0], qf[nt][j][1]);
+      }
+    }
+  bool move = false;
+  float top[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (NT > 2 && nt >= tiles) continue;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (kMasked) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key = turn.key0 + 16 * u + 8 * h + g;
+            float& x = s[u][nt][2 * h + e];
+            if (!vis.sees(pos[nt][e], key))
+              x = -INFINITY;
+            else if (!(turn.loaded >> u & 1))
+              x = __int_as_float(0x7fffffff);  // its page is not in the pool
+          }
+      }
+      top[nt][e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
+      move |= top[nt][e] > r.limit[nt][e];
+    }
+  }
+  if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (NT > 2 && nt >= tiles) continue;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float m = top[nt][e];
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (m > r.limit[nt][e]) {
+          // a row that has seen nothing holds zeros (or a NaN, which stays)
+          const float f = r.limit[nt][e] == -INFINITY ? 0.f : ex2((r.ref[nt][e] - m) * coef);
+          r.ref[nt][e] = m;
+          r.limit[nt][e] = m + slack;
+          r.sum[nt][e] *= f;
+          r.sum_o[nt][e] *= f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            r.o[nt][i][e] *= f;
+            r.o[nt][i][2 + e] *= f;
+          }
+        }
+      }
+    }
+  }
+  uint32_t pf[U][NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (NT > 2 && nt >= tiles) continue;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          // subtracted first: the largest of huge scores has to give exactly 2^-8
+          float& x = s[u][nt][2 * h + e];
+          x = ex2(fmaf(x - r.ref[nt][e], coef, -kSlack));
+          r.sum[nt][e] += x;
+        }
+        const uint32_t two = pack_bf16(s[u][nt][2 * h], s[u][nt][2 * h + 1]);
+        r.sum_o[nt][0] += bf16_lo(two);
+        r.sum_o[nt][1] += bf16_hi(two);
+        pf[u][nt][h] = transpose8(two);
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t a[4];
+      ldsm_x4_t(keys + kTurnHalf + (16 * u + row_v) * 128 + (((2 * i + chunk_v) ^ (lane & 7)) << 4), a[0], a[1], a[2],
+                a[3]);
+      if (kMasked) {
+        // What a masked key holds must not reach a row that does not see it,
+        // and 0 times an infinity or a NaN would: they are taken out of the
+        // product and added below to the rows that do see them.
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          if (!(turn.loaded >> u & 1)) {
+            a[m] = 0u;  // nothing was loaded
+          } else {
+            const uint32_t clean = finite_bf16x2(a[m]);
+            odd |= clean != a[m];
+            a[m] = clean;
+          }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (NT > 2 && nt >= tiles) continue;
+        mma16816(r.o[nt][i], a, pf[u][nt][0], pf[u][nt][1]);
+      }
+    }
+    if (kMasked && __any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+      for (int key = 0; key < 16; ++key) {
+        const uint32_t row = keys + kTurnHalf + (16 * u + key) * 128;
+#pragma unroll 1
+        for (int d = 0; d < 8; ++d) {  // dims 8 d + g: [d / 2][2 (d % 2) + e]
+          uint32_t two;
+          asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(two) : "r"(row + ((d ^ (key & 7)) << 4) + 2 * g));
+          const float v = bf16_lo(two);
+          if (isfinite(v)) continue;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                  if (2 * i + h == d && vis.sees(pos[nt][e], turn.key0 + 16 * u + key)) r.o[nt][i][2 * h + e] += v;
+        }
+      }
+    }
+  }
+}
+
+// A row's running softmax over some of its keys: kD of the accumulator's dims.
+// ref is in log2 units, -inf where none of the keys was seen; a key at ref
+// counts as 2^-kSlack in the sums and acc.
+template <int kD>
+struct Piece {
+  float acc[kD], sum, sum_o, ref;
+};
+
+// Writes dims d0 .. d0 + kD - 1 of a finished row: o = sigmoid(lse - sink) * acc / sum_o, and lse.
+template <int kD>
+SA_DEV void finish_row(const PageDecK& p, const Seq& q, int head, int row, int d0, const Piece<kD>& f) {
+  const int i = row / p.group, h_q = head * p.group + row % p.group;
+  const int64_t at = static_cast<int64_t>(q.row0) + i;
+  const float lse = f.sum == 0.f ? -INFINITY : (f.ref + kSlack + lg2(f.sum)) * kLn2;
+  // sigmoid(lse - sink) = a^2 / (1 + h^2) with h = e^(-|sink - lse| / 2) and a = h where the sink is the larger one,
+  // else 1.  What a sink far above leaves, e^(lse - sink), need not be in fp32's range where the mean is large: one a
+  // goes with the sum, the other comes last.
+  const float x = __ldg(p.sink + h_q) - lse, h = __expf(-0.5f * fabsf(x)), a = x > 0.f ? h : 1.f;
+  const float mean = __fdividef(a, f.sum_o * (1.f + h * h));
+  uint32_t v[kD / 2];
+#pragma unroll
+  for (int e = 0; e < kD / 2; ++e)
+    v[e] = f.sum == 0.f ? 0u : pack_bf16(f.acc[2 * e] * mean * a, f.acc[2 * e + 1] * mean * a);
+  __nv_bfloat16* o = p.o + (at * p.hq + h_q) * kHeadDim + d0;
+  if constexpr (kD == 4) {
+    *reinterpret_cast<uint2*>(o) = make_uint2(v[0], v[1]);
+  } else {
+    static_assert(kD % 8 == 0, "16-byte stores");
+#pragma unroll
+    for (int e = 0; e < kD / 8; ++e)
+      reinterpret_cast<uint4*>(o)[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+  }
+  if (d0 == 0) p.lse[static_cast<int64_t>(h_q) * p.total_rows + at] = lse;
+}
+
+// Partial results in the workspace: kRows x 64 accumulators, then (ref, sum, sum_o, 0) per row.
+template <int kRows, int kD>
+SA_DEV void put_piece(float* part, int row, int d0, const Piece<kD>& f) {
+#pragma unroll
+  for (int d = 0; d < kD; d += 4)
+    __stcg(reinterpret_cast<float4*>(part + row * kHeadDim + d0 + d),
+           make_float4(f.acc[d], f.acc[d + 1], f.acc[d + 2], f.acc[d + 3]));
+  if (d0 == 0)
+    __stcg(reinterpret_cast<float4*>(part + kRows * kHeadDim + kPartPad * row), make_float4(f.ref, f.sum, f.sum_o, 0.f));
+}
+
+// What a piece with reference `ref` and sum `sum` counts beside one with reference `top`: a piece that saw nothing
+// holds zeros, or a NaN that must come through.
+SA_DEV float weight_of(float ref, float sum, float top) {
+  return ref == -INFINITY ? (sum == 0.f ? 0.f : 1.f) : ex2(ref - top);
+}
+
+// The pieces of workers c0 .. c1, in order.
+template <int kRows, int kD, class F>
+SA_DEV Piece<kD> merge_pieces(F part_of, int c0, int c1, int row, int d0) {
+  Piece<kD> all;
+  all.sum = all.sum_o = 0.f;
+  all.ref = -INFINITY;
+#pragma unroll
+  for (int d = 0; d < kD; ++d) all.acc[d] = 0.f;
+  constexpr int kAtOnce = kD >= 16 ? 2 : 32 / kD;  // pieces in flight: their number, not their size, is what a merge waits for
+#pragma unroll 1
+  for (int first = c0; first <= c1; first += kAtOnce) {
+    float4 st[kAtOnce], v[kAtOnce][kD / 4];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const float* from = part_of(min(first + i, c1));
+      st[i] = __ldcg(reinterpret_cast<const float4*>(from + kRows * kHeadDim + kPartPad * row));
+#pragma unroll
+      for (int d = 0; d < kD / 4; ++d)
+        v[i][d] = __ldcg(reinterpret_cast<const float4*>(from + row * kHeadDim + d0 + 4 * d));
+    }
+    float top = all.ref;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, st[i].x);
+    const float old = all.ref == -INFINITY ? 1.f : ex2(all.ref - top);
+    all.ref = top;
+    all.sum *= old;
+    all.sum_o *= old;
+#pragma unroll
+    for (int d = 0; d < kD; ++d) all.acc[d] *= old;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (first + i > c1) break;
+      const float f = weight_of(st[i].x, st[i].y, top);
+      all.sum += f * st[i].y;
+      all.sum_o += f * st[i].z;
+#pragma unroll
+      for (int d = 0; d < kD / 4; ++d) {
+        all.acc[4 * d] += f * v[i][d].x;
+        all.acc[4 * d + 1] += f * v[i][d].y;
+        all.acc[4 * d + 2] += f * v[i][d].z;
+        all.acc[4 * d + 3] += f * v[i][d].w;
+      }
+    }
+  }
+  return all;
+}
+
+struct Cut {  // a pair that other workers have parts of
+  long long pair, p0;  // its number and its place in the line
+  int c0, c1, b, head;
+};
+
+// NT: tiles of 8 rows a warp has; kShare: warps that share a ring and split the rows; kTeams: rings of a CTA.
+template <int NT, int kShare, int kTeams, int kStages, int kPerSm>
+__global__ void __launch_bounds__(kShare* kTeams * 32, kPerSm) kv_decode_kernel(const __grid_constant__ PageDecK p) {
+  constexpr int kWarps = kShare * kTeams, kThreads = kWarps * 32;
+  constexpr int kWarpRows = 8 * NT, kRows = kWarpRows * kShare;
+  constexpr int kPartFloats = kRows * (kHeadDim + kPartPad);
+  constexpr int kDims = kRows * kHeadDim / kThreads;  // dims per thread when a CTA merges
+  constexpr bool kMayAlone = kShare == 1 && NT <= 2;
+  extern __shared__ uint8_t smem_raw[];
+  // the rings (boxes are swizzled by their address: 1024-byte aligned), merge area [teams][rows][kRowPad], statistics
+  // [teams][rows][4], then the places of the sequences in the line
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* acc_sh = reinterpret_cast<float*>(smem + kTeams * kStages * kTurnBytes);
+  float4* stat_sh = reinterpret_cast<float4*>(acc_sh + kTeams * kRows * kRowPad);
+  long long* upto = reinterpret_cast<long long*>(stat_sh + kTeams * kRows);  // turns of the sequences before
+  __shared__ long long warp_sum[kWarps];
+  __shared__ __align__(8) uint64_t bars[kTeams * 2 * kStages];
+  __shared__ Cut cuts[2];
+  __shared__ int last_sh[2], abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int team = warp / kShare, share = warp % kShare;
+
+  if (tid == 0) {
+    for (int i = 0; i < kTeams; ++i)
+      for (int s = 0; s < kStages; ++s) {
+        tc::mbar_init(smem_u32(&bars[i * 2 * kStages + s]), 1);
+        tc::mbar_init(smem_u32(&bars[i * 2 * kStages + kStages + s]), kShare);
+      }
+    tc::fence_mbar_init();
+    abort_flag = 0;
+    tc::tma_prefetch_map(&p.tm_k);
+    tc::tma_prefetch_map(&p.tm_v);
+  }
+  // turns per sequence (an empty one counts as one: its rows are written too) and their running total
+  long long turns_all = 0;
+  int longest = 0;
+  for (int base = 0; base < p.num_seqs; base += kThreads) {
+    const int b = base + tid;
+    long long x = b < p.num_seqs ? max(visible_span(p, sequence(p, b)).count(), 1) : 0;
+    const long long mine = x;
+    longest = max(longest, static_cast<int>(x));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    long long before = turns_all;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += warp_sum[w];
+      turns_all += warp_sum[w];
+    }
+    if (b < p.num_seqs) upto[b] = before + x - mine;
+    __syncthreads();
+  }
+  const bool few = __syncthreads_and(longest <= kAloneTurns) != 0;
+  const int heads = p.num_heads_kv;  // pairs per sequence
+  const long long work = turns_all * heads, pairs = static_cast<long long>(p.num_seqs) * heads;
+  // many pairs, all of them short
+  const bool alone = kMayAlone && few && pairs >= gridDim.x;
+  // a turn at least for every team, unless that leaves pairs without a worker of their own
+  const long long want = alone ? pairs : max((work + kTeams - 1) / kTeams, pairs);
+  const int most = static_cast<int>(gridDim.x) * (alone ? kWarps : 1);
+  const int n_workers = static_cast<int>(min(static_cast<long long>(most), want));
+  // The line that is shared out: all pairs, or all turns, where the turns of
+  // each pair stand behind `pad` places for what beginning a pair costs a CTA.
+  const int pad = !alone && work >= 4LL * kPairCost * n_workers ? kPairCost : 0;
+  const Shares shares(alone ? pairs : work + pairs * pad, n_workers);
+  const int worker = alone ? warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) : blockIdx.x;
+  if (worker >= shares.workers) return;  // a whole CTA, or a warp of one that never meets the others again
+  const long long x_end = shares.start(worker + 1);
+
+  // The worker's part of pair `head` of sequence b, which begins at x of the line, from t0 on.
+  const auto segment_at = [&](long long x, int b, int head, int t0) {
+    Segment s;
+    s.x = x;
+    s.b = b;
+    s.head = head;
+    s.t0 = t0;
+    s.seq = sequence(p, b);
+    s.span = visible_span(p, s.seq);
+    s.turns = max(s.span.count(), 1);
+    s.t1 = alone ? s.turns : static_cast<int>(min(static_cast<long long>(s.turns), x_end - x - pad));
+    return s;
+  };
+  Segment seg;
+  {  // the pair that holds the share's first place
+    const long long x = shares.start(worker);
+    if (alone) {
+      const int b = static_cast<int>(x / heads);
+      seg = segment_at(x, b, static_cast<int>(x - static_cast<long long>(b) * heads), 0);
+    } else {
+      int lo = 0, hi = p.num_seqs - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if ((upto[mid] + static_cast<long long>(mid) * pad) * heads <= x)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      const long long off = x - (upto[lo] + static_cast<long long>(lo) * pad) * heads;
+      const long long places = max(visible_span(p, sequence(p, lo)).count(), 1) + pad;
+      int head = min(static_cast<int>(__fdividef(static_cast<float>(off), static_cast<float>(places))), heads - 1);
+      while (head * places > off) --head;
+      while ((head + 1) * places <= off) ++head;
+      const long long in_pair = off - head * places;
+      seg = segment_at(x - in_pair, lo, head, static_cast<int>(max(in_pair - pad, 0LL)));
+    }
+  }
+
+  const int row_w = share * kWarpRows;  // the warp's first row
+  const int merge_row = tid / (kThreads / kRows), merge_dim = tid % (kThreads / kRows) * kDims;
+  const float slack = __fdividef(kSlack, p.coef);
+  const Visible vis{p.window, p.prefix};
+  Stream<kShare, kStages> stream(p, smem_u32(smem) + team * kStages * kTurnBytes, smem_u32(&bars[team * 2 * kStages]),
+                                 tc::Abort{&abort_flag, p.status}, alone ? 0 : team, alone ? 1 : kTeams, share == 0);
+  int n_cuts = 0;
+  stream.begin(seg);
+  while (true) {
+    // the warp's query rows: lane (g, t) has dims 16 j + 2 t, + 1 and + 8, + 9 of row g of each tile
+    const int rows = p.group * seg.seq.n;
+    const int tiles = min(max((rows - row_w + 7) / 8, 0), NT);
+    uint32_t qf[NT][4][2];
+    int pos[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = row_w + 8 * nt + g;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) qf[nt][j][0] = qf[nt][j][1] = 0u;
+      if (row < rows) {
+        const int i = row / p.group, h = seg.head * p.group + row - i * p.group;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(
+            p.q + ((static_cast<int64_t>(seg.seq.row0) + i) * p.hq + h) * kHeadDim + 2 * t);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          qf[nt][j][0] = __ldg(src + 8 * j);
+          qf[nt][j][1] = __ldg(src + 8 * j + 4);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int rr = row_w + 8 * nt + 2 * t + e;
+        pos[nt][e] = rr < rows ? seg.seq.len - seg.seq.n + rr / p.group : -1;
+      }
+    }
+
+    Rows<NT> r;
+    rows_clear(r);
+    stream.run([&](uint32_t keys, const Turn& turn) {
+      if (kShare > 1 && tiles == 0) return;
+      if (turn.masked)
+        turn_step<NT, true>(r, keys, qf, tiles, p.coef, slack, pos, turn, vis);
+      else
+        turn_step<NT, false>(r, keys, qf, tiles, p.coef, slack, pos, turn, vis);
+    });
+
+    // the next segment is on its way while this one is finished
+    const Segment done = seg;
+    const long long x_next = done.x + (alone ? 1 : done.turns + pad);
+    const bool more = done.t1 == done.turns && x_next + pad < x_end;
+    if (more) {
+      const bool same = done.head + 1 < heads;
+      seg = segment_at(x_next, same ? done.b : done.b + 1, same ? done.head + 1 : 0, 0);
+      stream.begin(seg);
+    }
+
+    // A pair that is cut is published when the worker is through, with one
+    // fence and no copies in flight for it to wait for.
+    const bool whole = done.t0 == 0 && done.t1 == done.turns;
+    float* mine = p.part + (2 * static_cast<int64_t>(worker) + (done.x > shares.start(worker) ? 1 : 0)) * kPartFloats;
+    if (!whole) {
+      if (tid == 0) {
+        Cut c;
+        c.pair = static_cast<long long>(done.b) * heads + done.head;
+        c.p0 = done.x;
+        c.c0 = shares.owner(done.x + pad);
+        c.c1 = shares.owner(done.x + pad + done.turns - 1);
+        c.b = done.b;
+        c.head = done.head;
+        cuts[n_cuts] = c;
+      }
+      ++n_cuts;
+    }
+
+    // sums over the keys, and the accumulators by row
+    const int at0 = (alone ? warp : team) * kRows + row_w;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float sum = r.sum[nt][e], sum_o = r.sum_o[nt][e];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+          sum += __shfl_xor_sync(0xffffffffu, sum, o);
+          sum_o += __shfl_xor_sync(0xffffffffu, sum_o, o);
+        }
+        const int at = at0 + 8 * nt + 2 * t + e;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc_sh[at * kRowPad + 16 * i + g] = r.o[nt][i][e];
+          acc_sh[at * kRowPad + 16 * i + g + 8] = r.o[nt][i][2 + e];
+        }
+        if (g == 0)
+          stat_sh[at] = make_float4(r.limit[nt][e] == -INFINITY ? -INFINITY : r.ref[nt][e] * p.coef, sum, sum_o, 0.f);
+      }
+    if (kMayAlone && alone) {
+      __syncwarp();
+      // lane: 16 dims of row lane / 4 of each tile
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = 8 * nt + (lane >> 2), d0 = 16 * (lane & 3);
+        const float4 st = stat_sh[at0 + row];
+        Piece<16> f;
+        f.ref = st.x, f.sum = st.y, f.sum_o = st.z;
+#pragma unroll
+        for (int d = 0; d < 16; ++d) f.acc[d] = acc_sh[(at0 + row) * kRowPad + d0 + d];
+        if (row < rows) finish_row<16>(p, done.seq, done.head, row, d0, f);
+      }
+      __syncwarp();
+    } else {
+      __syncthreads();
+      // thread: one row, kDims of its dims
+      Piece<kDims> f;
+      f.sum = f.sum_o = 0.f;
+      f.ref = -INFINITY;
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) f.acc[d] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kTeams; ++w) f.ref = fmaxf(f.ref, stat_sh[w * kRows + merge_row].x);
+#pragma unroll
+      for (int w = 0; w < kTeams; ++w) {
+        const float4 st = stat_sh[w * kRows + merge_row];
+        const float m = weight_of(st.x, st.y, f.ref);
+        f.sum += m * st.y;
+        f.sum_o += m * st.z;
+#pragma unroll
+        for (int d = 0; d < kDims; ++d) f.acc[d] += m * acc_sh[(w * kRows + merge_row) * kRowPad + merge_dim + d];
+      }
+      if (merge_row < rows) {
+        if (whole)
+          finish_row<kDims>(p, done.seq, done.head, merge_row, merge_dim, f);
+        else
+          put_piece<kRows, kDims>(mine, merge_row, merge_dim, f);
+      }
+      if (more) __syncthreads();  // the merge area is free again
+    }
+    if (!more) break;
+  }
+
+  if (n_cuts == 0) return;
+  const auto arrive = [&](const Cut& c) {  // by one thread, after a barrier: is this worker the pair's last?
+    __threadfence();  // the worker's piece, ordered before by the barrier, is there for whoever sees the count
+    const bool last = atomicAdd(p.counters + c.pair, 1) == c.c1 - c.c0;
+    __threadfence();
+    if (last) p.counters[c.pair] = 0;
+    return last;
+  };
+  // a worker's first pair left its piece in the first of its two places, a later one in the second
+  const auto part_of = [&](const Cut& c) {
+    return [&p, &shares, p0 = c.p0](int w) {
+      return p.part + (2 * static_cast<int64_t>(w) + (p0 > shares.start(w) ? 1 : 0)) * kPartFloats;
+    };
+  };
+  __syncthreads();
+  if (tid < n_cuts) last_sh[tid] = arrive(cuts[tid]);
+  __syncthreads();
+  for (int i = 0; i < n_cuts; ++i) {
+    if (!last_sh[i]) continue;
+    const Cut c = cuts[i];
+    const Seq q = sequence(p, c.b);
+    if (merge_row < p.group * q.n)
+      finish_row<kDims>(p, q, c.head, merge_row, merge_dim,
+                        merge_pieces<kRows, kDims>(part_of(c), c.c0, c.c1, merge_row, merge_dim));
+  }
+}
+
+template <int NT, int kShare, int kTeams, int kStages, int kPerSm>
+cudaError_t launch_variant(const PageDecK& p, cudaStream_t s) {
+  constexpr int kRows = 8 * NT * kShare;
+  constexpr size_t kFixed = 1024 + static_cast<size_t>(kTeams) * (kStages * kTurnBytes + kRows * (kRowPad * 4 + 16));
+  const auto kernel = kv_decode_kernel<NT, kShare, kTeams, kStages, kPerSm>;
+  static_assert(2 * kPerSm * kRows <= kPartRowsPerSm, "the workspace has no room for every CTA's cut pairs");
+  static_assert(kFixed + kKv4MaxRequests * sizeof(long long) <= 227 * 1024, "shared memory");
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(kernel, kFixed + kKv4MaxRequests * sizeof(long long));
+  if (e != cudaSuccess) return e;
+  kernel<<<device_sms() * kPerSm, kShare * kTeams * 32, kFixed + p.num_seqs * sizeof(long long), s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// Partial results first, in a place that depends on the GPU alone, then the
+// counters (zero between calls, one per pair): a workspace zeroed once serves
+// every call with as many kv heads or fewer.
+static size_t part_bytes() {
+  return static_cast<size_t>(device_sms()) * kPartRowsPerSm * (kHeadDim + kPartPad) * 4;
+}
+
+size_t kv_decode_workspace_bytes(int hkv) { return part_bytes() + static_cast<size_t>(kKv4MaxRequests) * hkv * 4; }
+
+cudaError_t launch_kv_decode(const KvPages& c, const KvDecodeArgs& a, int* status, cudaStream_t s) {
+  PageDecK p;
+  const long long places = static_cast<long long>(c.num_pages) << c.page_log2;
+  const int box = std::min(c.page_size, kTurn);
+  if (!make_rows_map(&p.tm_k, c.k, places, c.num_heads_kv, box) ||
+      !make_rows_map(&p.tm_v, c.v, places, c.num_heads_kv, box))
+    return cudaErrorInvalidValue;
+  p.block_table = c.block_table;
+  p.seqlens = c.seqlens;
+  p.slots = a.slots;
+  p.cu = a.cu;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.sink = a.sink;
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.part = static_cast<float*>(a.workspace);
+  p.counters = reinterpret_cast<int*>(static_cast<uint8_t*>(a.workspace) + part_bytes());
+  p.status = status;
+  p.num_pages = c.num_pages;
+  p.page_log2 = c.page_log2;
+  p.num_slots = c.num_slots;
+  p.max_pages = c.max_pages;
+  p.num_heads_kv = c.num_heads_kv;
+  p.num_seqs = a.num_seqs;
+  p.total_rows = a.rows;
+  p.n = a.n;
+  p.hq = a.hq;
+  p.group = a.hq / c.num_heads_kv;
+  p.window = a.window;
+  p.prefix = a.prefix;
+  // Not below the least normal number: such scores are nothing beside 1 either way, and 0 times a masked key's -inf
+  // would be a NaN.
+  p.coef = std::max(a.scale * kLog2e, 1.17549435e-38f);
+  const int rows = p.group * a.n;
+  if (rows <= 8) return launch_variant<1, 1, 4, 3, 2>(p, s);
+  if (rows <= 16) return launch_variant<2, 1, 4, 2, 2>(p, s);
+  if (rows <= 32) return launch_variant<4, 1, 4, 2, 2>(p, s);
+  if (rows <= 64) return launch_variant<4, 2, 4, 3, 1>(p, s);
+  return launch_variant<4, 4, 2, 6, 1>(p, s);
+}
+
+}  // namespace sa

@@ -1,0 +1,696 @@
+// Verification of drafted tokens against the target's probabilities, from
+// given random numbers, with the log-probabilities of the tokens that stand.
+//
+//   p = softmax(x / T), q = softmax(y / T) (without draft logits: 1 at the draft)
+//   draft d of a row stands if u q(d) < p(d); at the first that does not the
+//   sequence gets a token from w = max(p - q, 0) instead (without draft
+//   logits: p without d), after the last draft one from w = p:
+//   the first index whose cumulated w exceeds u' times the whole of w.
+//   T = 0: a draft stands if it is the largest logit's first index, and that is the token.
+//
+// All rows are read once, which is what the call cannot do without: 2 or 4
+// bytes a logit and one exponential each.  A first launch does that, a CTA per
+// (row, slice of the vocabulary): the slice's maximum and the sum relative to
+// it, from registers.  A second launch gives each sequence to a cluster: it
+// tests the drafts and draws the last token from the one row (or pair of
+// rows) in which it stopped, read again, mostly from L2.
+//
+// Arithmetic.  Where the tests are concerned fp32 sums do: a test is decided
+// wrongly only where u q and p agree to some 2^-22.  The draw is another
+// matter: among 200 k cumulated masses one border or another lies within 2^-24
+// of every place, so the masses are 64-bit fixed point in units of 2^-45 of
+// the whole, and
+//   - the exponent is kept in two parts (x - max times log2 e / T loses 2^-24
+//     of up to 20 otherwise), which leaves the hardware exponential's error,
+//     some 2^-23 of the mass;
+//   - masses above 2^-13 of the whole, of which there are few, take an
+//     exponential of two fp32 parts (off by some 2^-40);
+//   - max(p - q, 0) needs the ratio of the two sums as exactly: they are
+//     summed again in the same way from the two rows.
+// Integer sums are the same in every order.  FP64 is left to single values: its
+// rate on this GPU would cost more than all the rest.
+#include <cooperative_groups.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace sa {
+namespace {
+
+namespace cg = cooperative_groups;
+
+typedef unsigned long long u64;
+
+constexpr float kLowest = -3.402823466e38f;  // fp32's lowest finite value
+
+template <int kType>
+struct Elem;
+template <>
+struct Elem<0> {
+  typedef float T;
+  static constexpr int kVec = 4;
+  static SA_DEV void unpack(uint4 v, float* x) {
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+  }
+  static SA_DEV float one(T v) { return v; }
+  static SA_DEV T lowest() { return -INFINITY; }
+};
+template <>
+struct Elem<1> {
+  typedef uint16_t T;
+  static constexpr int kVec = 8;
+  static SA_DEV void unpack(uint4 v, float* x) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  static SA_DEV float one(T v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+  static SA_DEV T lowest() { return 0xff80u; }
+};
+template <>
+struct Elem<2> {
+  typedef uint16_t T;
+  static constexpr int kVec = 8;
+  static SA_DEV void unpack(uint4 v, float* x) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+  }
+  static SA_DEV float one(T v) { return __half2float(*reinterpret_cast<const __half*>(&v)); }
+  static SA_DEV T lowest() { return 0xfc00u; }
+};
+
+SA_DEV float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+SA_DEV int warp_min(int x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = min(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+template <class T>
+SA_DEV T warp_sum(T x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// The softmax's scale log2 e / T in two parts.  Valid temperatures: 0 (greedy,
+// with the probabilities of temperature 1) up to 1e36.
+struct Scale {
+  float hi, lo, temperature;
+  bool valid, greedy;
+  SA_DEV explicit Scale(float t) {
+    valid = t >= 0.f && t <= 1e36f;
+    greedy = t == 0.f;
+    temperature = greedy || !valid ? 1.f : t;
+    const double s = 1.4426950408889634 / static_cast<double>(temperature);
+    hi = fminf(static_cast<float>(s), 1e38f);
+    lo = s < 1e38 ? static_cast<float>(s - static_cast<double>(hi)) : 0.f;
+  }
+};
+
+// A sequence's rows [row0, row0 + n) and drafts [draft0, ...): the drafts of
+// all sequences stand one after another, n - 1 of a sequence that has rows.
+struct Rows {
+  int row0, n, draft0;
+};
+
+// What the first launch leaves of a row's slice.
+struct alignas(16) Part {
+  float top, sum;  // largest logit (kLowest at least), sum of 2^((x - top) scale)
+  int arg, pad;    // where the first of the largest is, in rows of temperature 0
+};
+
+// ---------------------------------------------------------------- all rows
+constexpr int kStatThreads = 256;
+constexpr int kStatVecs = 8;  // 16-byte vectors a thread holds
+
+template <int kType>
+__host__ __device__ constexpr int slice_logits() {
+  return kStatThreads * kStatVecs * Elem<kType>::kVec;
+}
+
+template <int kType>
+__global__ void __launch_bounds__(kStatThreads) verify_rows_kernel(const VerifyArgs a, int slices) {
+  typedef Elem<kType> E;
+  typedef typename E::T T;
+  constexpr int kWarps = kStatThreads / 32;
+  __shared__ float red[kWarps];
+  __shared__ int red_i[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int item = blockIdx.x >> 1, row = item / slices, slice = item - row * slices;
+  const bool draft = blockIdx.x & 1;
+  // the row's sequence, and how many with rows come before it
+  int seqs = 0, full = 0;
+  for (int j = tid; j < a.num_seqs; j += kStatThreads) {
+    const int upto = a.cu[j + 1];
+    if (upto <= row) {
+      ++seqs;
+      full += upto > a.cu[j];
+    }
+  }
+  const int both = warp_sum(seqs << 16 | full);
+  if (lane == 0) red_i[warp] = both;
+  __syncthreads();
+  int b = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) b += red_i[w] >> 16, before += red_i[w] & 0xffff;
+  if (b >= a.num_seqs || row < a.cu[0]) return;
+  if (draft && (a.draft_logits == nullptr || row + 1 >= a.cu[b + 1])) return;
+  const Scale sc(a.temperature[b]);
+  if (!sc.valid || (draft && sc.greedy)) return;
+  const int d = row - a.cu[0] - before;  // the row's draft
+  if (draft && d >= a.num_drafts) return;
+  const T* x = draft ? static_cast<const T*>(a.draft_logits) + static_cast<int64_t>(d) * a.draft_stride
+                     : static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.stride;
+
+  // 16-byte vectors as they are aligned in memory, what is outside the row -inf
+  const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) / sizeof(T)) % E::kVec);
+  const T* base = x - shift;
+  const int end = shift + a.vocab;
+  const int v0 = slice * kStatThreads * kStatVecs;
+  uint4 w[kStatVecs];
+#pragma unroll
+  for (int i = 0; i < kStatVecs; ++i) {
+    const int v = v0 + i * kStatThreads + tid;
+    if (v * E::kVec >= shift && (v + 1) * E::kVec <= end) {
+      w[i] = __ldg(reinterpret_cast<const uint4*>(base) + v);
+    } else {
+      union {
+        uint4 q;
+        T t[E::kVec];
+      } part;
+#pragma unroll
+      for (int e = 0; e < E::kVec; ++e) {
+        const int at = v * E::kVec + e;
+        part.t[e] = at >= shift && at < end ? base[at] : E::lowest();
+      }
+      w[i] = part.q;
+    }
+  }
+  float top = kLowest;
+#pragma unroll
+  for (int i = 0; i < kStatVecs; ++i) {
+    float f[E::kVec];
+    E::unpack(w[i], f);
+#pragma unroll
+    for (int e = 0; e < E::kVec; ++e) top = fmaxf(top, f[e]);
+  }
+  top = warp_max(top);
+  if (lane == 0) red[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) top = fmaxf(top, red[i]);
+  float2 sum = make_float2(0.f, 0.f);
+  const float2 minus = make_float2(-top, -top), by = make_float2(sc.hi, sc.hi);
+#pragma unroll
+  for (int i = 0; i < kStatVecs; ++i) {
+    float f[E::kVec];
+    E::unpack(w[i], f);
+#pragma unroll
+    for (int e = 0; e < E::kVec; e += 2) {
+      const float2 t = fmul2(fadd2(make_float2(f[e], f[e + 1]), minus), by);
+      sum = fadd2(sum, make_float2(ex2(t.x), ex2(t.y)));
+    }
+  }
+  int arg = 0x7fffffff;
+  if (sc.greedy) {
+#pragma unroll
+    for (int i = kStatVecs - 1; i >= 0; --i) {
+      float f[E::kVec];
+      E::unpack(w[i], f);
+#pragma unroll
+      for (int e = E::kVec - 1; e >= 0; --e)
+        if (f[e] == top) arg = (v0 + i * kStatThreads + tid) * E::kVec + e - shift;
+    }
+    arg = warp_min(arg);
+  }
+  __syncthreads();
+  const float total = warp_sum(sum.x + sum.y);
+  if (lane == 0) red[warp] = total, red_i[warp] = arg;
+  __syncthreads();
+  if (tid != 0) return;
+  Part p{top, 0.f, 0x7fffffff, 0};
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) p.sum += red[i], p.arg = min(p.arg, red_i[i]);
+  a.parts[(static_cast<int64_t>(row) * 2 + draft) * slices + slice] =
+      make_float4(p.top, p.sum, __int_as_float(p.arg), 0.f);
+}
+
+// ---------------------------------------------------------------- exponentials
+// 2^(k / 16) in two parts, from repeated square roots.
+constexpr double root2(double x) {  // Newton's iteration, x in [1, 2]
+  double r = x;
+  for (int i = 0; i < 40; ++i) r = 0.5 * (r + x / r);
+  return r;
+}
+struct Powers {
+  float hi[16], lo[16];
+  constexpr Powers() : hi(), lo() {
+    const double step = root2(root2(root2(root2(2.0))));
+    double v = 1.0;
+    for (int k = 0; k < 16; ++k) {
+      hi[k] = static_cast<float>(v);
+      lo[k] = static_cast<float>(v - static_cast<double>(hi[k]));
+      v *= step;
+    }
+  }
+};
+__constant__ Powers kPowers{};
+
+struct Pair {
+  float hi, lo;
+};
+
+// t = (x - top) scale in two parts.
+SA_DEV Pair exponent(float x, float top, const Scale& s) {
+  const float d = __fadd_rn(x, -top), b = __fadd_rn(d, -x);
+  const float d_lo = __fadd_rn(__fadd_rn(x, -__fadd_rn(d, -b)), -__fadd_rn(top, b));  // what d was rounded by
+  const float hi = __fmul_rn(d, s.hi);
+  return {hi, __fmaf_rn(d, s.hi, -hi) + __fmaf_rn(d, s.lo, d_lo * s.hi)};
+}
+// 2^t to some 2^-23 of itself; 0 below fp32's normal numbers.
+SA_DEV float power(Pair t) {
+  const float e = ex2(t.hi);
+  return t.hi > -126.f ? fmaf(e, t.lo * kLn2, e) : 0.f;
+}
+// 2^t to some 2^-40 of itself, t in (-60, 0]: 2^(n + k/16) (1 + g + g^2/2 + ...), g = ln 2 times the rest of t,
+// |g| <= ln 2 / 32.
+SA_DEV Pair power_pair(Pair t) {
+  const float m = rintf(t.hi * 16.f), rest = fmaf(m, -0.0625f, t.hi) + t.lo;  // the first difference is exact
+  const float rest_lo = t.lo - (rest - fmaf(m, -0.0625f, t.hi));
+  const int i = static_cast<int>(m), k = i & 15;
+  constexpr float kLn2Lo = static_cast<float>(0.693147180559945309 - static_cast<double>(kLn2));
+  const float g = __fmul_rn(rest, kLn2), g_lo = fmaf(rest, kLn2, -g) + fmaf(rest, kLn2Lo, rest_lo * kLn2);
+  const float more = fmaf(g * g, fmaf(g, fmaf(g, fmaf(g, 1.f / 120, 1.f / 24), 1.f / 6), 0.5f), g_lo);  // e^g - 1 - g
+  const float hi = kPowers.hi[k], lo = kPowers.lo[k];
+  const float a = __fmul_rn(hi, g), a_lo = fmaf(hi, g, -a);
+  const float sum = __fadd_rn(hi, a), sum_lo = a - (sum - hi);  // |hi| > |a|
+  const float rest2 = sum_lo + (a_lo + fmaf(hi, more, fmaf(lo, g, lo)));
+  const float scale = __int_as_float((127 + (i >> 4)) << 23);
+  return {sum * scale, rest2 * scale};
+}
+SA_DEV long long to_units(Pair e, float unit) { return __float2ll_rn(e.hi * unit) + __float2ll_rn(e.lo * unit); }
+
+// ---------------------------------------------------------------- a sequence
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+constexpr int kUnroll = 2;
+constexpr float kHeavy = 1.f / 8192.f;  // of the whole
+constexpr int kUnitLog2 = 45;           // masses in units of 2^-45 of (about) the whole
+
+struct RowStat {
+  float top, sum;
+  int arg;
+  SA_DEV bool none() const { return sum == 0.f; }
+  SA_DEV bool bad() const { return !(sum >= 0.f) || sum > 3e38f; }
+};
+
+struct Shared {
+  u64 exchange[2][kMaxCluster][2];
+  u64 warp_mass[kWarps], warp_mass_q[kWarps];
+  int count[kWarps];
+  int first;
+};
+
+template <int kType>
+class Sequence {
+ public:
+  typedef Elem<kType> E;
+  typedef typename E::T T;
+
+  SA_DEV Sequence(Shared& sh, const VerifyArgs& a, int slices)
+      : sh_(sh), a_(a), cluster_(cg::this_cluster()), slices_(slices), rank_(cluster_.block_rank()),
+        ctas_(cluster_.num_blocks()) {}
+
+  SA_DEV void run(int b) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (ctas_ > 1) cluster_.barrier_arrive();
+    int full = 0;
+    for (int j = tid; j < b; j += kThreads) full += a_.cu[j + 1] > a_.cu[j];
+    full = warp_sum(full);
+    if (lane == 0) sh_.count[warp] = full;
+    const int row0 = max(a_.cu[b], 0), n = min(a_.cu[b + 1], a_.rows) - row0;
+    if (tid == 0) sh_.first = max(n - 1, 0);
+    if (ctas_ > 1) cluster_.barrier_wait();  // every CTA of the cluster runs: its shared memory may be written
+    __syncthreads();
+    int draft0 = row0 - a_.cu[0];  // one draft fewer than rows in every sequence before that has rows
+    for (int w = 0; w < kWarps; ++w) draft0 -= sh_.count[w];
+    if (n <= 0) {
+      if (rank_ == 0 && tid == 0) a_.accepted[b] = a_.rejected[b] = 0;
+      return;
+    }
+    const Scale sc(a_.temperature[b]);
+    // the drafts, a warp each; what an earlier stop makes void is overwritten below
+    for (int i = warp; i < n - 1; i += kWarps) {
+      bool stands = false;
+      if (sc.valid && draft0 + i < a_.num_drafts) {
+        const int token = a_.drafts[draft0 + i];
+        const RowStat p = stat(row0 + i, false, sc);
+        if (!p.bad() && !p.none() && token >= 0 && token < a_.vocab) {
+          const float x = logit(row0 + i, token);
+          if (sc.greedy) {
+            stands = token == p.arg;
+          } else {
+            double q = 1.0;
+            bool known = true;
+            if (a_.draft_logits != nullptr) {
+              const RowStat s = stat(row0 + i, true, sc);
+              known = !s.bad() && !s.none();
+              q = share(draft_logit(draft0 + i, token), s, sc);
+            }
+            stands = known && static_cast<double>(unit_of(a_.u[row0 + i])) * q < share(x, p, sc);
+          }
+          if (stands && rank_ == 0 && lane == 0) {
+            a_.tokens[row0 + i] = token;
+            a_.logp[row0 + i] = log_share(x, p, sc);
+          }
+        }
+      }
+      if (!stands && lane == 0) atomicMin(&sh_.first, i);
+    }
+    __syncthreads();
+    const int j = sh_.first, row = row0 + j;
+    if (rank_ == 0) {
+      for (int i = j + 1 + tid; i < n; i += kThreads) {
+        a_.tokens[row0 + i] = -1;
+        a_.logp[row0 + i] = 0.f;
+      }
+      if (tid == 0) {
+        a_.accepted[b] = j;
+        a_.rejected[b] = n - 1 - j;
+      }
+    }
+    const bool refused = j < n - 1;
+    if (!sc.valid || (refused && draft0 + j >= a_.num_drafts)) return put(row, -1, NAN);
+    const RowStat p = stat(row, false, sc);
+    if (p.bad()) return put(row, -1, NAN);
+    if (p.none()) return put(row, -1, -INFINITY);
+    if (sc.greedy) return put(row, p.arg, log_share(p.top, p, sc));
+    Weights w;
+    w.p = p;
+    w.unit = unit_for(p.sum);
+    w.heavy = p.sum * kHeavy;
+    w.without = -1;
+    w.minus_q = false;
+    x_ = static_cast<const T*>(a_.logits) + static_cast<int64_t>(row) * a_.stride;
+    y_ = nullptr;
+    if (refused && a_.draft_logits == nullptr) w.without = a_.drafts[draft0 + j];
+    if (refused && a_.draft_logits != nullptr) {
+      const RowStat q = stat(row, true, sc);
+      if (q.bad() || q.none()) return put(row, -1, NAN);
+      w.q = q;
+      w.minus_q = true;
+      w.heavy_q = q.sum * kHeavy;
+      y_ = static_cast<const T*>(a_.draft_logits) + static_cast<int64_t>(draft0 + j) * a_.draft_stride;
+      sum_ratio(w, sc);
+    }
+    if (!draw(w, sc, row, unit_of(a_.u[row0 + n - 1]))) {
+      // nothing is left of w: the target's own probabilities
+      w.minus_q = false;
+      w.without = -1;
+      draw(w, sc, row, unit_of(a_.u[row0 + n - 1]));
+    }
+  }
+
+ private:
+  struct Weights {
+    RowStat p, q;
+    float unit, heavy, heavy_q;  // masses are e times unit; e from which a mass is heavy
+    Pair ratio;                  // of the sums: p - q is e_p - ratio e_q, but for a factor
+    int without;                 // the draft that is taken out, or -1
+    bool minus_q;
+  };
+
+  static SA_DEV float unit_of(float u) { return fminf(fmaxf(u, 0.f), 0.99999994f); }
+  // A power of two that brings the whole, `sum`, to 2^kUnitLog2 or just below.
+  static SA_DEV float unit_for(float sum) {
+    const int e = (__float_as_int(sum) >> 23) - 127 + 1;  // sum < 2^e, and at least 2^-1 (the largest counts 1)
+    return __int_as_float((127 + kUnitLog2 - e) << 23);
+  }
+
+  SA_DEV RowStat stat(int row, bool draft, const Scale& sc) const {  // by a whole warp
+    const float4* parts = a_.parts + (static_cast<int64_t>(row) * 2 + draft) * slices_;
+    RowStat r{kLowest, 0.f, 0x7fffffff};
+    for (int i = threadIdx.x & 31; i < slices_; i += 32) r.top = fmaxf(r.top, parts[i].x);
+    r.top = warp_max(r.top);
+    for (int i = threadIdx.x & 31; i < slices_; i += 32) {
+      const float4 f = parts[i];
+      r.sum += f.y * ex2((f.x - r.top) * sc.hi);
+      if (f.x == r.top) r.arg = min(r.arg, __float_as_int(f.z));
+    }
+    r.sum = warp_sum(r.sum);
+    r.arg = warp_min(r.arg);
+    return r;
+  }
+  SA_DEV float logit(int row, int token) const {
+    return E::one(static_cast<const T*>(a_.logits)[static_cast<int64_t>(row) * a_.stride + token]);
+  }
+  SA_DEV float draft_logit(int draft, int token) const {
+    return E::one(static_cast<const T*>(a_.draft_logits)[static_cast<int64_t>(draft) * a_.draft_stride + token]);
+  }
+  static SA_DEV double share(float x, const RowStat& s, const Scale& sc) {
+    return exp((static_cast<double>(x) - static_cast<double>(s.top)) / static_cast<double>(sc.temperature)) /
+           static_cast<double>(s.sum);
+  }
+  static SA_DEV float log_share(float x, const RowStat& s, const Scale& sc) {
+    return __fdiv_rn(x - s.top, sc.temperature) - logf(s.sum);
+  }
+  SA_DEV void put(int row, int token, float logp) const {
+    if (rank_ != 0 || threadIdx.x != 0) return;
+    a_.tokens[row] = token;
+    a_.logp[row] = logp;
+  }
+
+  // Every CTA of the cluster gives two numbers and takes all of them in rank order.
+  template <class F>
+  SA_DEV void exchange(u64 v, u64 w, F take) {
+    if (ctas_ == 1) {
+      take(v, w);
+      return;
+    }
+    u64 (*buf)[2] = sh_.exchange[parity_];
+    parity_ ^= 1;  // the other half may still be read by a slower CTA
+    if (threadIdx.x < ctas_) {
+      u64* to = cluster_.map_shared_rank(&buf[0][0], threadIdx.x) + 2 * rank_;
+      to[0] = v;
+      to[1] = w;
+    }
+    cluster_.sync();
+    for (unsigned r = 0; r < ctas_; ++r) take(buf[r][0], buf[r][1]);
+  }
+
+  // The vectors of the row (counted from its first logit) that the warp has, one run of them.
+  SA_DEV void my_run(int& v0, int& v1) const {
+    const int vectors = (a_.vocab + E::kVec - 1) / E::kVec, parts = ctas_ * kWarps;
+    const int each = (vectors + parts - 1) / parts;
+    v0 = min((static_cast<int>(rank_) * kWarps + static_cast<int>(threadIdx.x >> 5)) * each, vectors);
+    v1 = min(v0 + each, vectors);
+  }
+  // Logits of vector v; -inf behind the row's end.
+  SA_DEV void load(const T* row, int v, float* f) const {
+    const int at = v * E::kVec;
+    if ((reinterpret_cast<uintptr_t>(row) & 15u) == 0 && at + E::kVec <= a_.vocab) {
+      E::unpack(__ldg(reinterpret_cast<const uint4*>(row) + v), f);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E::kVec; ++e) f[e] = at + e < a_.vocab ? E::one(row[at + e]) : -INFINITY;
+    }
+  }
+
+  // e in units.
+  SA_DEV long long mass(float x, const RowStat& s, float heavy, float unit, const Scale& sc) const {
+    const Pair t = exponent(x, s.top, sc);
+    const float e = power(t);
+    return e < heavy ? __float2uint_rn(e * unit) : to_units(power_pair(t), unit);
+  }
+  // What a token weighs, in units.
+  SA_DEV long long weight(float x, float y, int index, const Weights& w, const Scale& sc) const {
+    if (!w.minus_q) return index == w.without ? 0 : mass(x, w.p, w.heavy, w.unit, sc);
+    const Pair tp = exponent(x, w.p.top, sc), tq = exponent(y, w.q.top, sc);
+    const float ep = power(tp), eq = power(tq);
+    if (ep < w.heavy && eq < w.heavy_q) {
+      const float r = fmaf(-eq, w.ratio.lo, fmaf(-eq, w.ratio.hi, ep));
+      return __float2uint_rn(fmaxf(r, 0.f) * w.unit);
+    }
+    Pair p = {ep, 0.f}, q = {eq, 0.f};
+    if (ep >= w.heavy) p = power_pair(tp);
+    if (eq >= w.heavy_q) q = power_pair(tq);
+    const float c = __fmul_rn(q.hi, w.ratio.hi), c_lo = fmaf(q.hi, w.ratio.hi, -c) + fmaf(q.hi, w.ratio.lo, q.lo * w.ratio.hi);
+    return max(to_units(p, w.unit) - to_units({c, c_lo}, w.unit), 0LL);
+  }
+
+  // The ratio of the two rows' sums.
+  SA_DEV void sum_ratio(Weights& w, const Scale& sc) {
+    const float unit_q = unit_for(w.q.sum);
+    int v0, v1;
+    my_run(v0, v1);
+    u64 p = 0, q = 0;
+#pragma unroll kUnroll
+    for (int v = v0 + (threadIdx.x & 31); v < v1; v += 32) {
+      float x[E::kVec], y[E::kVec];
+      load(x_, v, x);
+      load(y_, v, y);
+#pragma unroll
+      for (int e = 0; e < E::kVec; ++e) {
+        p += mass(x[e], w.p, w.heavy, w.unit, sc);
+        q += mass(y[e], w.q, w.heavy_q, unit_q, sc);
+      }
+    }
+    block_totals(p, q);
+    u64 all_p = 0, all_q = 0;
+    exchange(p, q, [&](u64 a, u64 b) { all_p += a, all_q += b; });
+    const double ratio = (static_cast<double>(all_p) / static_cast<double>(w.unit)) /
+                         (static_cast<double>(all_q) / static_cast<double>(unit_q));
+    w.ratio.hi = static_cast<float>(ratio);
+    w.ratio.lo = static_cast<float>(ratio - static_cast<double>(w.ratio.hi));
+  }
+  // Sums over the CTA, the same in all threads; the warps' own stay in sh_.warp_mass.
+  SA_DEV void block_totals(u64& p, u64& q) {
+    __syncthreads();
+    p = warp_sum(p);
+    q = warp_sum(q);
+    if ((threadIdx.x & 31) == 0) sh_.warp_mass[threadIdx.x >> 5] = p, sh_.warp_mass_q[threadIdx.x >> 5] = q;
+    __syncthreads();
+    p = q = 0;
+    for (int i = 0; i < kWarps; ++i) p += sh_.warp_mass[i], q += sh_.warp_mass_q[i];
+  }
+
+  // Draws the token of `row`; false (for all CTAs alike) if nothing has weight.
+  SA_DEV bool draw(const Weights& w, const Scale& sc, int row, float u) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int v0, v1;
+    my_run(v0, v1);
+    const auto vector_weights = [&](int v, long long* m) {
+      float x[E::kVec], y[E::kVec];
+      load(x_, v, x);
+      if (w.minus_q) load(y_, v, y);
+#pragma unroll
+      for (int e = 0; e < E::kVec; ++e) m[e] = weight(x[e], w.minus_q ? y[e] : 0.f, v * E::kVec + e, w, sc);
+    };
+    u64 own = 0, none = 0;
+#pragma unroll kUnroll
+    for (int v = v0 + lane; v < v1; v += 32) {
+      long long m[E::kVec];
+      vector_weights(v, m);
+#pragma unroll
+      for (int e = 0; e < E::kVec; ++e) own += m[e];
+    }
+    block_totals(own, none);
+    u64 total = 0, before = 0;
+    unsigned r = 0;
+    exchange(own, 0, [&](u64 v, u64) {
+      if (r++ < rank_) before += v;
+      total += v;
+    });
+    if (total == 0) return false;
+    // floor(total u), below total
+    const u64 target = __umul64hi(total << 4, static_cast<u64>(u * 4294967296.f) << 28);
+    if (target < before || target >= before + own) return true;  // another CTA has it
+    for (int i = 0; i < warp; ++i) before += sh_.warp_mass[i];
+    if (target < before || target >= before + sh_.warp_mass[warp]) return true;
+    for (int v = v0 + lane;; v += 32) {  // the warp that has it: some vector does
+      long long m[E::kVec];
+      u64 mine = 0;
+      if (v < v1) {
+        vector_weights(v, m);
+#pragma unroll
+        for (int e = 0; e < E::kVec; ++e) mine += m[e];
+      }
+      u64 upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      u64 at = before + upto - mine;
+      const bool here = target >= at && target < at + mine;
+      if (here) {
+        int token = -1;
+#pragma unroll
+        for (int e = 0; e < E::kVec; ++e) {
+          if (token < 0 && target < at + m[e]) token = v * E::kVec + e;
+          at += m[e];
+        }
+        a_.tokens[row] = token;
+        a_.logp[row] = log_share(E::one(x_[token]), w.p, sc);
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+      if (__any_sync(0xffffffffu, here) || v - lane >= v1) break;
+    }
+    return true;
+  }
+
+  Shared& sh_;
+  const VerifyArgs& a_;
+  cg::cluster_group cluster_;
+  int slices_;
+  unsigned rank_, ctas_;
+  int parity_ = 0;
+  const T* x_ = nullptr;
+  const T* y_ = nullptr;
+};
+
+template <int kType>
+__global__ void __launch_bounds__(kThreads) verify_draw_kernel(const __grid_constant__ VerifyArgs a, int slices) {
+  __shared__ Shared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int ctas = cluster.num_blocks();
+  {
+    Sequence<kType> s(sh, a, slices);
+    s.run(blockIdx.x / ctas);
+  }
+  if (ctas > 1) cluster.sync();  // no CTA leaves while another may still write to its shared memory
+}
+
+template <int kType>
+int slices_for(int vocab) {
+  return ceil_div(static_cast<long long>(vocab) + Elem<kType>::kVec - 1, slice_logits<kType>());
+}
+
+template <int kType>
+cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
+  const int slices = slices_for<kType>(a.vocab);
+  if (a.rows > 0)
+    verify_rows_kernel<kType><<<static_cast<unsigned>(2LL * a.rows * slices), kStatThreads, 0, s>>>(a, slices);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  int ctas = 1;
+  while (ctas < kMaxCluster && ctas * 8192 < a.vocab) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, verify_draw_kernel<kType>, a, slices);
+}
+
+}  // namespace
+
+size_t verify_workspace_bytes(int dtype, int rows, int vocab) {
+  const int slices = dtype == 0 ? slices_for<0>(vocab) : slices_for<1>(vocab);
+  return static_cast<size_t>(rows) * 2 * slices * sizeof(Part);
+}
+
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
+  if (a.dtype == 0) return launch_type<0>(a, s);
+  if (a.dtype == 1) return launch_type<1>(a, s);
+  return launch_type<2>(a, s);
+}
+
+}  // namespace sa

@@ -314,3 +314,77 @@ def sample_tokens(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=
     _call("sinkattn_sample_tokens", dev, logits.data_ptr(), kind, B, V, logits.stride(0) if B > 1 else V, up, tp, kp, pp,
           mp, to, lp, lq)
     return tokens, logp, logq
+
+
+def _logit_rows(name: str, t):
+    """Checks logits [rows, vocab] with contiguous rows: their type's number and their row stride."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor [rows, vocab]")
+    kind = _LOGIT_TYPES.get(t.dtype)
+    if kind is None:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected float32, bfloat16 or float16")
+    rows, vocab = t.shape
+    if (vocab > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < vocab):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return kind, t.stride(0) if rows > 1 else vocab
+
+
+def verify_workspace(logits) -> torch.Tensor:
+    """A workspace for verify_tokens with target logits like these."""
+    kind, _ = _logit_rows("logits", logits)
+    rows, vocab = logits.shape
+    size = int(_lib.load().sinkattn_verify_workspace_size(kind, rows, vocab))
+    if size == 0 and rows > 0:
+        raise ValueError(f"verify_workspace: no workspace for logits of shape {list(logits.shape)}")
+    return torch.empty(max(size, 16), dtype=torch.uint8, device=logits.device)
+
+
+def verify_tokens(logits, drafts, u, cu_rows, *, draft_logits=None, temperature=None, tokens=None, logp=None,
+                  accepted=None, rejected=None, workspace=None):
+    """Which drafted tokens stand, and the token that follows them: returns (tokens, logp, accepted, rejected).
+
+    logits [R, V] fp32, bf16 or fp16, rows contiguous (any row stride): the
+    target's.  Entry b has rows cu_rows[b] .. cu_rows[b + 1] - 1 (int32 [B + 1],
+    on the device), and one draft fewer: drafts int32 [D], those of all entries
+    one after another, with the logits they were drawn from, draft_logits [D, V]
+    (the same type), or without (drafts that were looked up).  u fp32 [R] random
+    numbers in [0, 1): a row's for its draft, an entry's last one for the token
+    that is drawn.  temperature fp32 [B] (default 1; 0: the largest logit), for
+    both.  tokens int32 [R]: the drafts that stand, the token drawn, -1 behind
+    it; logp fp32 [R] their log-probabilities under the target (grpo_loss's
+    logp_old), 0 behind them; accepted and rejected int32 [B].  An invalid row
+    ends its entry with token -1 and logp NaN, one without an allowed token
+    with -1 and -inf.
+    """
+    kind, stride = _logit_rows("logits", logits)
+    R, V = logits.shape
+    dev = logits.device
+    f32, i32 = torch.float32, torch.int32
+    D, B = _vector("drafts", drafts, i32, dev), _vector("cu_rows", cu_rows, i32, dev) - 1
+    if B < 0:
+        raise ValueError("cu_rows has shape [0], expected one offset more than there are entries")
+    xp, xs = None, V
+    if draft_logits is not None:
+        if draft_logits.dtype is not logits.dtype:
+            raise TypeError(f"draft_logits has dtype {draft_logits.dtype}, expected {logits.dtype}")
+        _, xs = _logit_rows("draft_logits", draft_logits)
+        if draft_logits.shape != (D, V) or draft_logits.device != dev:
+            raise ValueError(f"draft_logits has shape {list(draft_logits.shape)} on {draft_logits.device}, "
+                             f"expected {[D, V]} on {dev}")
+        xp = draft_logits.data_ptr()
+    dp, up = _tensor("drafts", drafts, i32, (D,), dev), _tensor("u", u, f32, (R,), dev)
+    cp = _tensor("cu_rows", cu_rows, i32, (B + 1,), dev)
+    temperature = torch.ones(B, dtype=f32, device=dev) if temperature is None else temperature
+    tp = _tensor("temperature", temperature, f32, (B,), dev)
+    logp, lp = _output("logp", logp, u, f32, (R,), dev)
+    tokens = torch.empty(R, dtype=i32, device=dev) if tokens is None else tokens
+    accepted = torch.empty(B, dtype=i32, device=dev) if accepted is None else accepted
+    to, ap = _tensor("tokens", tokens, i32, (R,), dev), _tensor("accepted", accepted, i32, (B,), dev)
+    rejected, rp = _output("rejected", rejected, accepted, i32, (B,), dev)
+    _on_gpu("logits", logits)
+    if workspace is None:
+        workspace = verify_workspace(logits)
+    wn = _vector("workspace", workspace, torch.uint8, dev)
+    _call("sinkattn_verify_tokens", dev, logits.data_ptr(), stride, xp, xs, kind, R, D, V, dp, cp, B, up, tp, to, lp, ap,
+          rp, _tensor("workspace", workspace, torch.uint8, (wn,), dev), wn)
+    return tokens, logp, accepted, rejected
