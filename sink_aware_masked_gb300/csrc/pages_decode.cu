@@ -68,10 +68,13 @@ struct PageDecK {
   int* status;
   int num_pages, page_log2, num_slots, max_pages, num_heads_kv;
   int num_seqs, total_rows, n, hq, group, window, prefix;
-  float coef;  // scale * log2 e
+  uint32_t group_magic;  // ceil(2^16 / group)
+  float coef;            // scale * log2 e
+  // row / group, exact while row * group <= 2^16 (rows and groups are up to 128)
+  SA_DEV int row_of_seq(int row) const { return static_cast<int>(row * group_magic >> 16); }
 };
 
-// D (+)= A B, A 16 x 16 (keys or dims), B 16 x 8.
+// D = A B, A 16 x 16 (keys), B 16 x 8.
 SA_DEV void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
@@ -102,9 +105,10 @@ SA_DEV uint32_t finite_bf16x2(uint32_t v) {
   return r;
 }
 
-// A sequence of the call: its slot, length, and rows row0 .. row0 + n - 1 of q.
+// A sequence of the call: its slot, length, and rows row0 .. row0 + n - 1 of q;
+// `rows` of a pair (query heads times rows of q) are computed.
 struct Seq {
-  int slot, len, row0, n;
+  int slot, len, row0, n, rows;
 };
 
 SA_DEV Seq sequence(const PageDecK& p, int b) {
@@ -120,6 +124,7 @@ SA_DEV Seq sequence(const PageDecK& p, int b) {
     s.row0 = min(max(p.cu[b], 0), p.total_rows);
     s.n = min(max(p.cu[b + 1], s.row0), p.total_rows) - s.row0;
   }
+  s.rows = p.group * min(s.n, p.n);
   return s;
 }
 
@@ -286,16 +291,17 @@ class Stream {
   Segment seg_;
 };
 
-// What a warp keeps of its rows.  Row 8 nt + 2 t + e of the warp's is lane
-// (g, t)'s entry [nt][e] (the same in all g) except the sums, which are over
-// the lane's own keys until they are reduced.
+constexpr float kUnseen = -3.402823466e38f;
+
+// What a warp keeps of its rows.  Rows 2 t and 2 t + 1 of its tile nt of 8 rows
+// are lane (g, t)'s entry [nt], .x and .y (the same in all g) except the sums,
+// which are over the lane's own keys until they are reduced.
 template <int NT>
 struct Rows {
-  float o[NT][4][4];   // O^T: [i][e] dim 16 i + g, [i][2 + e] dim 16 i + g + 8
-  float sum[NT][2];    // of P
-  float sum_o[NT][2];  // of P rounded to bf16
-  float ref[NT][2];    // reference score (before the coefficient), 0 while the row has seen no key
-  float limit[NT][2];  // score beyond which ref moves, -inf while the row has seen no key
+  float o[NT][4][4];  // O^T: [i][e] dim 16 i + g, [i][2 + e] dim 16 i + g + 8
+  float2 sum[NT];     // of P
+  float2 sum_o[NT];   // of P rounded to bf16
+  float2 ref[NT];     // reference score (before the coefficient), kUnseen while the row has seen no key
 };
 
 template <int NT>
@@ -306,34 +312,54 @@ SA_DEV void rows_clear(Rows<NT>& r) {
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) r.o[nt][i][e] = 0.f;
+    r.sum[nt] = r.sum_o[nt] = make_float2(0.f, 0.f);
+    r.ref[nt] = make_float2(kUnseen, kUnseen);
+  }
+}
+
+// The keys of a turn that row position `at` sees (-1: none), as bits.
+SA_DEV uint32_t seen_bits(int at, int key0, int window, int prefix) {
+  uint32_t bits = bits_below(at - key0 + 1);
+  if (window >= 0) bits &= ~bits_below(at - window - key0) | bits_below(prefix - key0);
+  return bits;
+}
+
+// Moves a row's reference: all that was summed relative to the old one.
+template <int NT>
+SA_DEV void move_reference(Rows<NT>& r, int nt, int e, float top, float coef, float slack) {
+  float m = top;
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+  float& ref = e ? r.ref[nt].y : r.ref[nt].x;
+  if (m > ref + slack || (ref == kUnseen && m > kUnseen)) {
+    // a row that has seen nothing holds zeros (or a NaN, which stays)
+    const float f = ref == kUnseen ? 0.f : ex2((ref - m) * coef);
+    ref = m;
+    (e ? r.sum[nt].y : r.sum[nt].x) *= f;
+    (e ? r.sum_o[nt].y : r.sum_o[nt].x) *= f;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      r.sum[nt][e] = r.sum_o[nt][e] = r.ref[nt][e] = 0.f;
-      r.limit[nt][e] = -INFINITY;
+    for (int i = 0; i < 4; ++i) {
+      r.o[nt][i][e] *= f;
+      r.o[nt][i][2 + e] *= f;
     }
   }
 }
 
-struct Visible {
-  int window, prefix;
-  SA_DEV bool sees(int at, int key) const {  // at < len: -1 for a row that is not there
-    return key <= at && (window < 0 || key >= at - window || key < prefix);
-  }
-};
-
-// One turn: two blocks of 16 keys, whose chains of products run side by side.
-// kMasked: some (row, key) of them is not visible, or a half is not there.
-// pos[nt][e]: the rows' positions.
-template <int NT, bool kMasked>
-SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[NT][4][2], int tiles, float coef, float slack,
-                      const int (&pos)[NT][2], const Turn& turn, const Visible& vis) {
+// One turn and tiles [kFirst, kFirst + HT) of the warp's: two blocks of 16
+// keys, whose chains of products run side by side.  kMasked: some (row, key) of
+// them is not visible, or a half is not there; pos(nt, e): the rows' positions.
+template <int NT, int kFirst, int HT, bool kMasked, class Pos>
+SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2], int tiles, float coef, float slack,
+                      const Pos& pos, const Turn& turn, int window, int prefix) {
   constexpr int U = kTurn / 16;
+  constexpr bool kSkip = NT > 2;  // tiles without rows are left out
   const int lane = threadIdx.x & 31, g = lane >> 2;
   // Rows of 128 bytes, 16-byte chunks XORed with the row's low three bits.
   const uint32_t row_k = (lane & 7) + (lane & 8), chunk_k = lane >> 4;
   const uint32_t row_v = (lane & 7) + (lane >> 4) * 8, chunk_v = lane >> 3 & 1;
   // scores before the coefficient: s[u][nt][e] key g of block u, s[u][nt][2 + e] key g + 8, row 2 t + e
-  float s[U][NT][4];
+  float s[U][HT][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -341,8 +367,8 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[NT][4][2]
       uint32_t a[4];
       ldsm_x4(keys + (16 * u + row_k) * 128 + (((2 * j + chunk_k) ^ (lane & 7)) << 4), a[0], a[1], a[2], a[3]);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (NT > 2 && nt >= tiles) continue;
+      for (int nt = 0; nt < HT; ++nt) {
+        if (kSkip && kFirst + nt >= tiles) continue;
         if (j == 0)
           mma_first(s[u][nt], a, qf[nt][j][0], qf[nt][j][1]);
         else
@@ -350,128 +376,111 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[NT][4][2]
       }
     }
   bool move = false;
-  float top[NT][2];
+  float top[HT][2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    if (NT > 2 && nt >= tiles) continue;
+  for (int nt = 0; nt < HT; ++nt) {
+    if (kSkip && kFirst + nt >= tiles) continue;
+    if (kMasked) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (kMasked) {
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t bits = seen_bits(pos(kFirst + nt, e), turn.key0, window, prefix) >> g;
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int key = turn.key0 + 16 * u + 8 * h + g;
             float& x = s[u][nt][2 * h + e];
-            if (!vis.sees(pos[nt][e], key))
-              x = -INFINITY;
-            else if (!(turn.loaded >> u & 1))
-              x = __int_as_float(0x7fffffff);  // its page is not in the pool
+            if (!(turn.loaded >> u & 1)) x = __int_as_float(0x7fffffff);  // its page is not in the pool
+            if (!(bits >> (16 * u + 8 * h) & 1u)) x = -INFINITY;
           }
       }
-      top[nt][e] = fmaxf(fmaxf(s[0][nt][e], s[0][nt][2 + e]), fmaxf(s[1][nt][e], s[1][nt][2 + e]));
-      move |= top[nt][e] > r.limit[nt][e];
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      top[nt][e] = fmaxf(fmax3(s[0][nt][e], s[0][nt][2 + e], s[1][nt][e]), s[1][nt][2 + e]);
+      const float ref = e ? r.ref[kFirst + nt].y : r.ref[kFirst + nt].x;
+      move |= top[nt][e] > ref + slack || (ref == kUnseen && top[nt][e] > kUnseen);
     }
   }
   if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (NT > 2 && nt >= tiles) continue;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float m = top[nt][e];
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        if (m > r.limit[nt][e]) {
-          // a row that has seen nothing holds zeros (or a NaN, which stays)
-          const float f = r.limit[nt][e] == -INFINITY ? 0.f : ex2((r.ref[nt][e] - m) * coef);
-          r.ref[nt][e] = m;
-          r.limit[nt][e] = m + slack;
-          r.sum[nt][e] *= f;
-          r.sum_o[nt][e] *= f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            r.o[nt][i][e] *= f;
-            r.o[nt][i][2 + e] *= f;
-          }
-        }
-      }
+    for (int nt = 0; nt < HT; ++nt) {
+      if (kSkip && kFirst + nt >= tiles) continue;
+      move_reference(r, kFirst + nt, 0, top[nt][0], coef, slack);
+      move_reference(r, kFirst + nt, 1, top[nt][1], coef, slack);
     }
   }
-  uint32_t pf[U][NT][2];
+  uint32_t pf[U][HT][2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    if (NT > 2 && nt >= tiles) continue;
+  for (int nt = 0; nt < HT; ++nt) {
+    if (kSkip && kFirst + nt >= tiles) continue;
+    const int n = kFirst + nt;
+    const float2 minus = make_float2(-r.ref[n].x, -r.ref[n].y), c2 = make_float2(coef, coef);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          // subtracted first: the largest of huge scores has to give exactly 2^-8
-          float& x = s[u][nt][2 * h + e];
-          x = ex2(fmaf(x - r.ref[nt][e], coef, -kSlack));
-          r.sum[nt][e] += x;
-        }
-        const uint32_t two = pack_bf16(s[u][nt][2 * h], s[u][nt][2 * h + 1]);
-        r.sum_o[nt][0] += bf16_lo(two);
-        r.sum_o[nt][1] += bf16_hi(two);
+        // subtracted first: the largest of huge scores has to give exactly 2^-8
+        const float2 d = fadd2(make_float2(s[u][nt][2 * h], s[u][nt][2 * h + 1]), minus);
+        const float2 x = ffma2(d, c2, make_float2(-kSlack, -kSlack));
+        const float2 p = make_float2(ex2(x.x), ex2(x.y));
+        r.sum[n] = fadd2(r.sum[n], p);
+        const uint32_t two = pack_bf16(p.x, p.y);
+        r.sum_o[n] = fadd2(r.sum_o[n], make_float2(bf16_lo(two), bf16_hi(two)));
         pf[u][nt][h] = transpose8(two);
       }
     }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    bool odd = false;
+    uint32_t a[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t a[4];
-      ldsm_x4_t(keys + kTurnHalf + (16 * u + row_v) * 128 + (((2 * i + chunk_v) ^ (lane & 7)) << 4), a[0], a[1], a[2],
-                a[3]);
-      if (kMasked) {
-        // What a masked key holds must not reach a row that does not see it,
-        // and 0 times an infinity or a NaN would: they are taken out of the
-        // product and added below to the rows that do see them.
+    for (int i = 0; i < 4; ++i)
+      ldsm_x4_t(keys + kTurnHalf + (16 * u + row_v) * 128 + (((2 * i + chunk_v) ^ (lane & 7)) << 4), a[i][0], a[i][1],
+                a[i][2], a[i][3]);
+    if (kMasked) {
+      // What a masked key holds must not reach a row that does not see it, and
+      // 0 times an infinity or a NaN would: they are taken out of the product
+      // and added to the rows that do see them.
+      const bool there = turn.loaded >> u & 1;
+      uint32_t odd = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          if (!(turn.loaded >> u & 1)) {
-            a[m] = 0u;  // nothing was loaded
-          } else {
-            const uint32_t clean = finite_bf16x2(a[m]);
-            odd |= clean != a[m];
-            a[m] = clean;
+          if (!there) a[i][m] = 0u;
+          odd |= (a[i][m] & 0x7fff7fffu) + 0x00800080u;  // an exponent of ones carries into the sign's place
+        }
+      if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0u)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int m = 0; m < 4; ++m) a[i][m] = finite_bf16x2(a[i][m]);
+#pragma unroll 1
+        for (int key = 0; key < 16; ++key) {
+          const uint32_t row = keys + kTurnHalf + (16 * u + key) * 128;
+          const int at = turn.key0 + 16 * u + key;
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {  // dims 8 d + g: [d / 2][2 (d % 2) + e]
+            uint32_t two;
+            asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(two) : "r"(row + ((d ^ (key & 7)) << 4) + 2 * g));
+            const float v = bf16_lo(two);
+            if (!((two & 0x7f80u) == 0x7f80u)) continue;
+#pragma unroll
+            for (int nt = 0; nt < HT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (seen_bits(pos(kFirst + nt, e), at, window, prefix) & 1u) r.o[kFirst + nt][d >> 1][2 * (d & 1) + e] += v;
           }
         }
       }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (NT > 2 && nt >= tiles) continue;
-        mma16816(r.o[nt][i], a, pf[u][nt][0], pf[u][nt][1]);
-      }
     }
-    if (kMasked && __any_sync(0xffffffffu, odd)) {
-#pragma unroll 1
-      for (int key = 0; key < 16; ++key) {
-        const uint32_t row = keys + kTurnHalf + (16 * u + key) * 128;
-#pragma unroll 1
-        for (int d = 0; d < 8; ++d) {  // dims 8 d + g: [d / 2][2 (d % 2) + e]
-          uint32_t two;
-          asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(two) : "r"(row + ((d ^ (key & 7)) << 4) + 2 * g));
-          const float v = bf16_lo(two);
-          if (isfinite(v)) continue;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                  if (2 * i + h == d && vis.sees(pos[nt][e], turn.key0 + 16 * u + key)) r.o[nt][i][2 * h + e] += v;
-        }
+      for (int nt = 0; nt < HT; ++nt) {
+        if (kSkip && kFirst + nt >= tiles) continue;
+        mma16816(r.o[kFirst + nt][i], a[i], pf[u][nt][0], pf[u][nt][1]);
       }
-    }
   }
 }
 
@@ -483,21 +492,36 @@ struct Piece {
   float acc[kD], sum, sum_o, ref;
 };
 
-// Writes dims d0 .. d0 + kD - 1 of a finished row: o = sigmoid(lse - sink) * acc / sum_o, and lse.
-template <int kD>
-SA_DEV void finish_row(const PageDecK& p, const Seq& q, int head, int row, int d0, const Piece<kD>& f) {
-  const int i = row / p.group, h_q = head * p.group + row % p.group;
-  const int64_t at = static_cast<int64_t>(q.row0) + i;
-  const float lse = f.sum == 0.f ? -INFINITY : (f.ref + kSlack + lg2(f.sum)) * kLn2;
+// A reference score in log2 units, -inf where the row has seen no key.
+SA_DEV float log2_ref(float ref, float coef) { return ref == kUnseen ? -INFINITY : ref * coef; }
+
+// What finishes a row from its sums: o is acc times first, then times last; and lse.
+struct Finish {
+  float first, last, lse;
+};
+
+SA_DEV Finish finish_of(float ref, float sum, float sum_o, float sink) {
+  Finish f;
+  f.lse = sum == 0.f ? -INFINITY : (ref + kSlack + lg2(sum)) * kLn2;
   // sigmoid(lse - sink) = a^2 / (1 + h^2) with h = e^(-|sink - lse| / 2) and a = h where the sink is the larger one,
   // else 1.  What a sink far above leaves, e^(lse - sink), need not be in fp32's range where the mean is large: one a
   // goes with the sum, the other comes last.
-  const float x = __ldg(p.sink + h_q) - lse, h = __expf(-0.5f * fabsf(x)), a = x > 0.f ? h : 1.f;
-  const float mean = __fdividef(a, f.sum_o * (1.f + h * h));
+  const float x = sink - f.lse, h = __expf(-0.5f * fabsf(x)), a = x > 0.f ? h : 1.f;
+  f.first = sum == 0.f ? 0.f : __fdividef(a, sum_o * (1.f + h * h));
+  f.last = sum == 0.f ? 0.f : a;
+  return f;
+}
+
+// Writes dims d0 .. d0 + kD - 1 of a finished row: o = sigmoid(lse - sink) * acc / sum_o, and lse.
+template <int kD>
+SA_DEV void finish_row(const PageDecK& p, const Seq& q, int head, int row, int d0, const Piece<kD>& f) {
+  const int i = p.row_of_seq(row), h_q = head * p.group + row - i * p.group;
+  const int64_t at = static_cast<int64_t>(q.row0) + i;
+  const Finish w = finish_of(f.ref, f.sum, f.sum_o, __ldg(p.sink + h_q));
   uint32_t v[kD / 2];
 #pragma unroll
   for (int e = 0; e < kD / 2; ++e)
-    v[e] = f.sum == 0.f ? 0u : pack_bf16(f.acc[2 * e] * mean * a, f.acc[2 * e + 1] * mean * a);
+    v[e] = pack_bf16(f.acc[2 * e] * w.first * w.last, f.acc[2 * e + 1] * w.first * w.last);
   __nv_bfloat16* o = p.o + (at * p.hq + h_q) * kHeadDim + d0;
   if constexpr (kD == 4) {
     *reinterpret_cast<uint2*>(o) = make_uint2(v[0], v[1]);
@@ -507,7 +531,34 @@ SA_DEV void finish_row(const PageDecK& p, const Seq& q, int head, int row, int d
     for (int e = 0; e < kD / 8; ++e)
       reinterpret_cast<uint4*>(o)[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
   }
-  if (d0 == 0) p.lse[static_cast<int64_t>(h_q) * p.total_rows + at] = lse;
+  if (d0 == 0) p.lse[static_cast<int64_t>(h_q) * p.total_rows + at] = w.lse;
+}
+
+// Writes the rows of a warp that had all keys of a pair: 8x8 transposes bring a row's dims together.
+template <int NT>
+SA_DEV void finish_tiles(const PageDecK& p, const Seq& q, int head, int rows, const Rows<NT>& r) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    if (8 * nt >= rows) break;
+    Finish w[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int row = 8 * nt + 2 * t + e, i = p.row_of_seq(row), h_q = head * p.group + row - i * p.group;
+      w[e] = finish_of(log2_ref(e ? r.ref[nt].y : r.ref[nt].x, p.coef), e ? r.sum[nt].y : r.sum[nt].x, e ? r.sum_o[nt].y : r.sum_o[nt].x,
+                       row < rows ? __ldg(p.sink + h_q) : 0.f);
+      if (g == 0 && row < rows) p.lse[static_cast<int64_t>(h_q) * p.total_rows + q.row0 + i] = w[e].lse;
+    }
+    const int row = 8 * nt + g, i = p.row_of_seq(row), h_q = head * p.group + row - i * p.group;
+    uint32_t* o = reinterpret_cast<uint32_t*>(p.o + ((static_cast<int64_t>(q.row0) + i) * p.hq + h_q) * kHeadDim);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {  // dims 8 c + g of rows 2 t, 2 t + 1 -> dims 8 c + 2 t, + 1 of row g
+      const float x = r.o[nt][c >> 1][2 * (c & 1)] * w[0].first * w[0].last;
+      const float y = r.o[nt][c >> 1][2 * (c & 1) + 1] * w[1].first * w[1].last;
+      const uint32_t two = transpose8(pack_bf16(x, y));
+      if (row < rows) o[4 * c + t] = two;
+    }
+  }
 }
 
 // Partial results in the workspace: kRows x 64 accumulators, then (ref, sum, sum_o, 0) per row.
@@ -575,31 +626,94 @@ SA_DEV Piece<kD> merge_pieces(F part_of, int c0, int c1, int row, int d0) {
 }
 
 struct Cut {  // a pair that other workers have parts of
-  long long pair, p0;  // its number and its place in the line
+  long long p0;  // its place in its head's line
   int c0, c1, b, head;
 };
 
-// NT: tiles of 8 rows a warp has; kShare: warps that share a ring and split the rows; kTeams: rings of a CTA.
-template <int NT, int kShare, int kTeams, int kStages, int kPerSm>
-__global__ void __launch_bounds__(kShare* kTeams * 32, kPerSm) kv_decode_kernel(const __grid_constant__ PageDecK p) {
-  constexpr int kWarps = kShare * kTeams, kThreads = kWarps * 32;
-  constexpr int kWarpRows = 8 * NT, kRows = kWarpRows * kShare;
-  constexpr int kPartFloats = kRows * (kHeadDim + kPartPad);
-  constexpr int kDims = kRows * kHeadDim / kThreads;  // dims per thread when a CTA merges
+constexpr int kUptoStep = 4;  // every fourth sequence's place in the line is kept
+
+// How a CTA is made up.  NT: tiles of 8 rows a warp has, taken in halves from
+// five on (the queries of a half come from shared memory then); kShare: warps
+// that share a ring and split the tiles; kTeams: rings of a CTA.
+template <int NT_, int kShare_, int kTeams_, int kStages_, int kPerSm_>
+struct Shape {
+  static constexpr int NT = NT_, kShare = kShare_, kTeams = kTeams_, kStages = kStages_, kPerSm = kPerSm_;
+  static constexpr int kHalves = NT > 4 ? 2 : 1, HT = NT / kHalves;
+  static constexpr int kWarps = kShare * kTeams, kThreads = kWarps * 32;
+  static constexpr int kRows = 8 * NT * kShare;
+  // Teams that merge by rows in shared memory; where there are twice as many, the others' results are added to
+  // theirs before.
+  static constexpr int kSlots = kTeams > 4 || kShare > 1 ? kTeams / 2 : kTeams;
+  static constexpr int kPerRow = kThreads / kRows >= 16 ? 16 : kThreads / kRows >= 8 ? 8 : kThreads / kRows >= 4 ? 4 : 2;
+  static constexpr int kDims = kHeadDim / kPerRow;  // dims per thread when a CTA merges
+  static_assert(kThreads >= 2 * kRows, "a row's threads");
+  static constexpr int kPartFloats = kRows * (kHeadDim + kPartPad);
+  static constexpr size_t kRing = static_cast<size_t>(kTeams) * kStages * kTurnBytes;
+  static constexpr size_t kMerge = static_cast<size_t>(kSlots) * kRows * (kRowPad * 4 + 16);
+  static constexpr size_t kQueries = kHalves > 1 ? kRows * kHeadDim * 2 : 0;
+  static_assert(2 * kPerSm * kRows <= kPartRowsPerSm, "the workspace has no room for every CTA's cut pairs");
+};
+
+// The warp's query rows in registers: lane (g, t) has dims 16 j + 2 t, + 1 and
+// + 8, + 9 of row g of each tile (tile nt is number nt * step + first of the pair's).
+template <int HT>
+SA_DEV void load_queries(const PageDecK& p, const Seq& q, int head, int rows, int first, int step,
+                         uint32_t (&qf)[HT][4][2]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int nt = 0; nt < HT; ++nt) {
+    const int row = 8 * (nt * step + first) + g;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) qf[nt][j][0] = qf[nt][j][1] = 0u;
+    if (row < rows) {
+      const int i = p.row_of_seq(row), h = head * p.group + row - i * p.group;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          p.q + ((static_cast<int64_t>(q.row0) + i) * p.hq + h) * kHeadDim + 2 * t);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        qf[nt][j][0] = __ldg(src + 8 * j);
+        qf[nt][j][1] = __ldg(src + 8 * j + 4);
+      }
+    }
+  }
+}
+
+// The same from shared memory, where row 8 tile + i of the pair lies at 128 bytes a row, swizzled.
+template <int HT>
+SA_DEV void fetch_queries(uint32_t queries, int first, int step, uint32_t (&qf)[HT][4][2]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int nt = 0; nt < HT; ++nt)
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const uint32_t row = 8 * (nt * step + first) + (lane & 7);
+      ldsm_x4(queries + row * 128 + (((2 * j + (lane >> 3)) ^ (lane & 7)) << 4), qf[nt][j][0], qf[nt][j][1],
+              qf[nt][j + 1][0], qf[nt][j + 1][1]);
+    }
+}
+
+// kAlone: every warp takes whole pairs, by the host's word that all are short.
+template <class S, bool kAlone>
+__global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const __grid_constant__ PageDecK p) {
+  constexpr int NT = S::NT, HT = S::HT, kShare = S::kShare, kTeams = S::kTeams, kStages = S::kStages;
+  constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kRows = S::kRows, kSlots = S::kSlots, kDims = S::kDims;
   constexpr bool kMayAlone = kShare == 1 && NT <= 2;
+  static_assert(!kAlone || kMayAlone, "a warp alone has the tiles of all rows");
   extern __shared__ uint8_t smem_raw[];
-  // the rings (boxes are swizzled by their address: 1024-byte aligned), merge area [teams][rows][kRowPad], statistics
-  // [teams][rows][4], then the places of the sequences in the line
+  // the rings (boxes are swizzled by their address: 1024-byte aligned), queries [rows][64], merge area
+  // [slots][rows][kRowPad] and statistics [slots][rows][4], then the places of the sequences in the line
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* acc_sh = reinterpret_cast<float*>(smem + kTeams * kStages * kTurnBytes);
-  float4* stat_sh = reinterpret_cast<float4*>(acc_sh + kTeams * kRows * kRowPad);
-  long long* upto = reinterpret_cast<long long*>(stat_sh + kTeams * kRows);  // turns of the sequences before
+  uint8_t* queries = smem + S::kRing;
+  float* acc_sh = reinterpret_cast<float*>(queries + S::kQueries);
+  float4* stat_sh = reinterpret_cast<float4*>(acc_sh + kSlots * kRows * kRowPad);
+  long long* upto = reinterpret_cast<long long*>(stat_sh + kSlots * kRows);  // turns of the sequences before
   __shared__ long long warp_sum[kWarps];
   __shared__ __align__(8) uint64_t bars[kTeams * 2 * kStages];
   __shared__ Cut cuts[2];
   __shared__ int last_sh[2], abort_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int team = warp / kShare, share = warp % kShare;
+  const int heads = p.num_heads_kv;
 
   if (tid == 0) {
     for (int i = 0; i < kTeams; ++i)
@@ -614,46 +728,81 @@ __global__ void __launch_bounds__(kShare* kTeams * 32, kPerSm) kv_decode_kernel(
   }
   // turns per sequence (an empty one counts as one: its rows are written too) and their running total
   long long turns_all = 0;
-  int longest = 0;
-  for (int base = 0; base < p.num_seqs; base += kThreads) {
-    const int b = base + tid;
-    long long x = b < p.num_seqs ? max(visible_span(p, sequence(p, b)).count(), 1) : 0;
-    const long long mine = x;
-    longest = max(longest, static_cast<int>(x));
+  bool alone = kAlone;
+  if (!kAlone) {
+    int longest = 0;
+    for (int base = 0; base < p.num_seqs; base += kThreads) {
+      const int b = base + tid;
+      long long x = b < p.num_seqs ? max(visible_span(p, sequence(p, b)).count(), 1) : 0;
+      const long long mine = x;
+      longest = max(longest, static_cast<int>(x));
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) warp_sum[warp] = x;
+      __syncthreads();
+      long long before = turns_all;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += warp_sum[w];
+        turns_all += warp_sum[w];
+      }
+      if (b < p.num_seqs && b % kUptoStep == 0) upto[b / kUptoStep] = before + x - mine;
+      __syncthreads();
     }
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    long long before = turns_all;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += warp_sum[w];
-      turns_all += warp_sum[w];
-    }
-    if (b < p.num_seqs) upto[b] = before + x - mine;
+    // many pairs, all of them short
+    const bool few = __syncthreads_and(longest <= kAloneTurns) != 0;
+    alone = kMayAlone && few && static_cast<long long>(p.num_seqs) * heads >= gridDim.x;
+  } else {
     __syncthreads();
   }
-  const bool few = __syncthreads_and(longest <= kAloneTurns) != 0;
-  const int heads = p.num_heads_kv;  // pairs per sequence
-  const long long work = turns_all * heads, pairs = static_cast<long long>(p.num_seqs) * heads;
-  // many pairs, all of them short
-  const bool alone = kMayAlone && few && pairs >= gridDim.x;
-  // a turn at least for every team, unless that leaves pairs without a worker of their own
-  const long long want = alone ? pairs : max((work + kTeams - 1) / kTeams, pairs);
-  const int most = static_cast<int>(gridDim.x) * (alone ? kWarps : 1);
-  const int n_workers = static_cast<int>(min(static_cast<long long>(most), want));
-  // The line that is shared out: all pairs, or all turns, where the turns of
-  // each pair stand behind `pad` places for what beginning a pair costs a CTA.
-  const int pad = !alone && work >= 4LL * kPairCost * n_workers ? kPairCost : 0;
-  const Shares shares(alone ? pairs : work + pairs * pad, n_workers);
-  const int worker = alone ? warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x) : blockIdx.x;
-  if (worker >= shares.workers) return;  // a whole CTA, or a warp of one that never meets the others again
-  const long long x_end = shares.start(worker + 1);
 
-  // The worker's part of pair `head` of sequence b, which begins at x of the line, from t0 on.
-  const auto segment_at = [&](long long x, int b, int head, int t0) {
+  const float slack = __fdividef(kSlack, p.coef);
+  const uint32_t q_sh = smem_u32(queries);
+  Stream<kShare, kStages> stream(p, smem_u32(smem) + team * kStages * kTurnBytes, smem_u32(&bars[team * 2 * kStages]),
+                                 tc::Abort{&abort_flag, p.status}, alone ? 0 : team, alone ? 1 : kTeams, share == 0);
+  Rows<NT> r;
+  // All turns of a segment that are the warp's, summed up in r.
+  const auto process = [&](const Segment& seg) {
+    const int rows = seg.seq.rows;
+    const int tiles = min(max(((rows + 7) / 8 - share + kShare - 1) / kShare, 0), NT);
+    uint32_t qf[HT][4][2];
+    if (S::kHalves == 1) load_queries<HT>(p, seg.seq, seg.head, rows, share, kShare, qf);
+    const int first = seg.seq.len - seg.seq.n;
+    const auto pos = [&](int nt, int e) {
+      const int row = 8 * (nt * kShare + share) + 2 * t + e;
+      return row < rows ? first + p.row_of_seq(row) : -1;
+    };
+    rows_clear(r);
+    stream.run([&](uint32_t keys, const Turn& turn) {
+      if (tiles == 0) return;
+      if constexpr (S::kHalves > 1) fetch_queries<HT>(q_sh, share, kShare, qf);
+      if (turn.masked)
+        turn_step<NT, 0, HT, true>(r, keys, qf, tiles, p.coef, slack, pos, turn, p.window, p.prefix);
+      else
+        turn_step<NT, 0, HT, false>(r, keys, qf, tiles, p.coef, slack, pos, turn, p.window, p.prefix);
+      if constexpr (S::kHalves > 1) {
+        if (tiles <= HT) return;
+        fetch_queries<HT>(q_sh, HT * kShare + share, kShare, qf);
+        if (turn.masked)
+          turn_step<NT, HT, HT, true>(r, keys, qf, tiles, p.coef, slack, pos, turn, p.window, p.prefix);
+        else
+          turn_step<NT, HT, HT, false>(r, keys, qf, tiles, p.coef, slack, pos, turn, p.window, p.prefix);
+      }
+    });
+    // sums over the keys
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        r.sum[nt].x += __shfl_xor_sync(0xffffffffu, r.sum[nt].x, o);
+        r.sum[nt].y += __shfl_xor_sync(0xffffffffu, r.sum[nt].y, o);
+        r.sum_o[nt].x += __shfl_xor_sync(0xffffffffu, r.sum_o[nt].x, o);
+        r.sum_o[nt].y += __shfl_xor_sync(0xffffffffu, r.sum_o[nt].y, o);
+      }
+  };
+  const auto segment_of = [&](int b, int head, long long x, int t0) {
     Segment s;
     s.x = x;
     s.b = b;
@@ -661,145 +810,191 @@ __global__ void __launch_bounds__(kShare* kTeams * 32, kPerSm) kv_decode_kernel(
     s.t0 = t0;
     s.seq = sequence(p, b);
     s.span = visible_span(p, s.seq);
-    s.turns = max(s.span.count(), 1);
-    s.t1 = alone ? s.turns : static_cast<int>(min(static_cast<long long>(s.turns), x_end - x - pad));
+    s.turns = s.t1 = max(s.span.count(), 1);
     return s;
   };
-  Segment seg;
-  {  // the pair that holds the share's first place
-    const long long x = shares.start(worker);
-    if (alone) {
-      const int b = static_cast<int>(x / heads);
-      seg = segment_at(x, b, static_cast<int>(x - static_cast<long long>(b) * heads), 0);
-    } else {
-      int lo = 0, hi = p.num_seqs - 1;
+
+  if constexpr (kMayAlone) {
+    if (alone) {  // a warp meets no other one from here on
+      const long long pairs = static_cast<long long>(p.num_seqs) * heads;
+      const long long step = static_cast<long long>(gridDim.x) * kWarps;
+      long long pair = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
+      if (pair >= pairs) return;
+      const auto pair_at = [&](long long i) {
+        const int b = static_cast<int>(i / heads);
+        return segment_of(b, static_cast<int>(i - static_cast<long long>(b) * heads), 0, 0);
+      };
+      Segment seg = pair_at(pair);
+      stream.begin(seg);
+      while (true) {
+        process(seg);
+        const Segment done = seg;
+        pair += step;
+        if (pair < pairs) {  // on its way while this one is finished
+          seg = pair_at(pair);
+          stream.begin(seg);
+        }
+        finish_tiles<NT>(p, done.seq, done.head, done.seq.rows, r);
+        if (pair >= pairs) return;
+      }
+    }
+  }
+  if constexpr (!kAlone) {
+    // Every head's turns make one line, in which the turns of each sequence
+    // stand behind `pad` places for what beginning a pair costs a CTA.  All
+    // heads' lines are cut alike, into equal shares, and neighbouring CTAs take
+    // the same share of neighbouring heads, which lie side by side in memory.
+    // (More heads than CTAs: a line is not cut, and a CTA takes several.)
+    const int ctas = static_cast<int>(gridDim.x), lanes_of_heads = min(heads, ctas);
+    const int group = static_cast<int>(blockIdx.x) / lanes_of_heads, head0 = static_cast<int>(blockIdx.x) - group * lanes_of_heads;
+    // a turn at least for every team, unless that leaves pairs without a worker of their own
+    const long long want = max((turns_all + kTeams - 1) / kTeams, static_cast<long long>(p.num_seqs));
+    const int n_workers = heads > ctas ? 1 : static_cast<int>(min(static_cast<long long>(ctas / lanes_of_heads), want));
+    const int pad = turns_all >= 4LL * kPairCost * n_workers ? kPairCost : 0;
+    const Shares shares(turns_all + static_cast<long long>(p.num_seqs) * pad, n_workers);
+    if (group >= n_workers) return;
+    const long long x_begin = shares.start(group), x_end = shares.start(group + 1);
+    int b_first;  // the sequence that holds the share's first place
+    long long x_first;
+    {
+      int lo = 0, hi = (p.num_seqs - 1) / kUptoStep;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if ((upto[mid] + static_cast<long long>(mid) * pad) * heads <= x)
+        if (upto[mid] + static_cast<long long>(mid) * kUptoStep * pad <= x_begin)
           lo = mid;
         else
           hi = mid - 1;
       }
-      const long long off = x - (upto[lo] + static_cast<long long>(lo) * pad) * heads;
-      const long long places = max(visible_span(p, sequence(p, lo)).count(), 1) + pad;
-      int head = min(static_cast<int>(__fdividef(static_cast<float>(off), static_cast<float>(places))), heads - 1);
-      while (head * places > off) --head;
-      while ((head + 1) * places <= off) ++head;
-      const long long in_pair = off - head * places;
-      seg = segment_at(x - in_pair, lo, head, static_cast<int>(max(in_pair - pad, 0LL)));
+      b_first = lo * kUptoStep;
+      x_first = upto[lo] + static_cast<long long>(b_first) * pad;
+      for (int i = 1; i < kUptoStep && b_first + 1 < p.num_seqs; ++i) {
+        const long long next = x_first + max(visible_span(p, sequence(p, b_first)).count(), 1) + pad;
+        if (next > x_begin) break;
+        x_first = next;
+        ++b_first;
+      }
     }
-  }
-
-  const int row_w = share * kWarpRows;  // the warp's first row
-  const int merge_row = tid / (kThreads / kRows), merge_dim = tid % (kThreads / kRows) * kDims;
-  const float slack = __fdividef(kSlack, p.coef);
-  const Visible vis{p.window, p.prefix};
-  Stream<kShare, kStages> stream(p, smem_u32(smem) + team * kStages * kTurnBytes, smem_u32(&bars[team * 2 * kStages]),
-                                 tc::Abort{&abort_flag, p.status}, alone ? 0 : team, alone ? 1 : kTeams, share == 0);
-  int n_cuts = 0;
-  stream.begin(seg);
-  while (true) {
-    // the warp's query rows: lane (g, t) has dims 16 j + 2 t, + 1 and + 8, + 9 of row g of each tile
-    const int rows = p.group * seg.seq.n;
-    const int tiles = min(max((rows - row_w + 7) / 8, 0), NT);
-    uint32_t qf[NT][4][2];
-    int pos[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = row_w + 8 * nt + g;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) qf[nt][j][0] = qf[nt][j][1] = 0u;
-      if (row < rows) {
-        const int i = row / p.group, h = seg.head * p.group + row - i * p.group;
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(
-            p.q + ((static_cast<int64_t>(seg.seq.row0) + i) * p.hq + h) * kHeadDim + 2 * t);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          qf[nt][j][0] = __ldg(src + 8 * j);
-          qf[nt][j][1] = __ldg(src + 8 * j + 4);
+    // The worker's part of a pair that begins at x of the line.
+    const auto segment_at = [&](int b, int head, long long x) {
+      Segment s = segment_of(b, head, x, static_cast<int>(max(x_begin - x - pad, 0LL)));
+      s.t1 = static_cast<int>(min(static_cast<long long>(s.turns), x_end - x - pad));
+      return s;
+    };
+    const int merge_row = min(tid / S::kPerRow, kRows), merge_dim = tid % S::kPerRow * kDims;  // kRows: none
+    int n_cuts = 0;
+    Segment seg = segment_at(b_first, head0, x_first);
+    stream.begin(seg);
+    while (true) {
+      if (S::kHalves > 1) {
+        // the pair's queries into shared memory, zeros behind the last row
+        const int rows = seg.seq.rows;
+        for (int u = tid; u < kRows * 8; u += kThreads) {
+          const int row = u >> 3, c = u & 7;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (row < rows) {
+            const int i = p.row_of_seq(row), h = seg.head * p.group + row - i * p.group;
+            v = __ldg(reinterpret_cast<const uint4*>(p.q + ((static_cast<int64_t>(seg.seq.row0) + i) * p.hq + h) * kHeadDim) + c);
+          }
+          *reinterpret_cast<uint4*>(queries + swz(row, c)) = v;
         }
+        __syncthreads();
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int rr = row_w + 8 * nt + 2 * t + e;
-        pos[nt][e] = rr < rows ? seg.seq.len - seg.seq.n + rr / p.group : -1;
+      process(seg);
+
+      // the next segment is on its way while this one is finished
+      const Segment done = seg;
+      const int rows = done.seq.rows;
+      const long long x_next = done.x + done.turns + pad;
+      bool more = done.t1 == done.turns && done.b + 1 < p.num_seqs && x_next + pad < x_end;
+      if (more) {
+        seg = segment_at(done.b + 1, done.head, x_next);
+      } else if (done.head + ctas < heads) {  // more heads than CTAs
+        more = true;
+        seg = segment_at(b_first, done.head + ctas, x_first);
       }
-    }
+      if (more) stream.begin(seg);
 
-    Rows<NT> r;
-    rows_clear(r);
-    stream.run([&](uint32_t keys, const Turn& turn) {
-      if (kShare > 1 && tiles == 0) return;
-      if (turn.masked)
-        turn_step<NT, true>(r, keys, qf, tiles, p.coef, slack, pos, turn, vis);
-      else
-        turn_step<NT, false>(r, keys, qf, tiles, p.coef, slack, pos, turn, vis);
-    });
-
-    // the next segment is on its way while this one is finished
-    const Segment done = seg;
-    const long long x_next = done.x + (alone ? 1 : done.turns + pad);
-    const bool more = done.t1 == done.turns && x_next + pad < x_end;
-    if (more) {
-      const bool same = done.head + 1 < heads;
-      seg = segment_at(x_next, same ? done.b : done.b + 1, same ? done.head + 1 : 0, 0);
-      stream.begin(seg);
-    }
-
-    // A pair that is cut is published when the worker is through, with one
-    // fence and no copies in flight for it to wait for.
-    const bool whole = done.t0 == 0 && done.t1 == done.turns;
-    float* mine = p.part + (2 * static_cast<int64_t>(worker) + (done.x > shares.start(worker) ? 1 : 0)) * kPartFloats;
-    if (!whole) {
-      if (tid == 0) {
-        Cut c;
-        c.pair = static_cast<long long>(done.b) * heads + done.head;
-        c.p0 = done.x;
-        c.c0 = shares.owner(done.x + pad);
-        c.c1 = shares.owner(done.x + pad + done.turns - 1);
-        c.b = done.b;
-        c.head = done.head;
-        cuts[n_cuts] = c;
-      }
-      ++n_cuts;
-    }
-
-    // sums over the keys, and the accumulators by row
-    const int at0 = (alone ? warp : team) * kRows + row_w;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float sum = r.sum[nt][e], sum_o = r.sum_o[nt][e];
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          sum_o += __shfl_xor_sync(0xffffffffu, sum_o, o);
+      // A pair that is cut is published when the worker is through, with one
+      // fence and no copies in flight for it to wait for.
+      const bool whole = done.t0 == 0 && done.t1 == done.turns;
+      float* mine = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (done.x > x_begin ? 1 : 0)) * S::kPartFloats;
+      if (!whole) {
+        if (tid == 0) {
+          Cut c;
+          c.p0 = done.x;
+          c.c0 = shares.owner(done.x + pad);
+          c.c1 = shares.owner(done.x + pad + done.turns - 1);
+          c.b = done.b;
+          c.head = done.head;
+          cuts[n_cuts] = c;
         }
-        const int at = at0 + 8 * nt + 2 * t + e;
+        ++n_cuts;
+      }
+
+      if constexpr (kSlots < kTeams) {
+        // the upper teams' results, lane for lane, to the lower ones
+        float* slot = acc_sh + ((team % kSlots) * kShare + share) * (NT * 16 * 32) + 4 * lane;
+        float4* stat = stat_sh + ((team % kSlots) * kShare + share) * (NT * 8);
+        if (team >= kSlots) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc_sh[at * kRowPad + 16 * i + g] = r.o[nt][i][e];
-          acc_sh[at * kRowPad + 16 * i + g + 8] = r.o[nt][i][2 + e];
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<float4*>(slot + (nt * 4 + i) * 128) =
+                  make_float4(r.o[nt][i][0], r.o[nt][i][1], r.o[nt][i][2], r.o[nt][i][3]);
+            if (g == 0) {
+              stat[nt * 8 + 2 * t] = make_float4(r.ref[nt].x, r.sum[nt].x, r.sum_o[nt].x, 0.f);
+              stat[nt * 8 + 2 * t + 1] = make_float4(r.ref[nt].y, r.sum[nt].y, r.sum_o[nt].y, 0.f);
+            }
+          }
         }
-        if (g == 0)
-          stat_sh[at] = make_float4(r.limit[nt][e] == -INFINITY ? -INFINITY : r.ref[nt][e] * p.coef, sum, sum_o, 0.f);
-      }
-    if (kMayAlone && alone) {
-      __syncwarp();
-      // lane: 16 dims of row lane / 4 of each tile
+        __syncthreads();
+        if (team < kSlots) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int row = 8 * nt + (lane >> 2), d0 = 16 * (lane & 3);
-        const float4 st = stat_sh[at0 + row];
-        Piece<16> f;
-        f.ref = st.x, f.sum = st.y, f.sum_o = st.z;
+          for (int nt = 0; nt < NT; ++nt) {
+            float own[2], other[2];
 #pragma unroll
-        for (int d = 0; d < 16; ++d) f.acc[d] = acc_sh[(at0 + row) * kRowPad + d0 + d];
-        if (row < rows) finish_row<16>(p, done.seq, done.head, row, d0, f);
+            for (int e = 0; e < 2; ++e) {
+              const float4 st = stat[nt * 8 + 2 * t + e];
+              float& ref = e ? r.ref[nt].y : r.ref[nt].x;
+              float& sum = e ? r.sum[nt].y : r.sum[nt].x;
+              float& sum_o = e ? r.sum_o[nt].y : r.sum_o[nt].x;
+              const float top = fmaxf(ref, st.x), unit = log2_ref(top, p.coef);
+              own[e] = weight_of(log2_ref(ref, p.coef), sum, unit);
+              other[e] = weight_of(log2_ref(st.x, p.coef), st.y, unit);
+              sum = own[e] * sum + other[e] * st.y;
+              sum_o = own[e] * sum_o + other[e] * st.z;
+              ref = top;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float4 v = *reinterpret_cast<const float4*>(slot + (nt * 4 + i) * 128);
+              r.o[nt][i][0] = own[0] * r.o[nt][i][0] + other[0] * v.x;
+              r.o[nt][i][1] = own[1] * r.o[nt][i][1] + other[1] * v.y;
+              r.o[nt][i][2] = own[0] * r.o[nt][i][2] + other[0] * v.z;
+              r.o[nt][i][3] = own[1] * r.o[nt][i][3] + other[1] * v.w;
+            }
+          }
+        }
+        __syncthreads();
       }
-      __syncwarp();
-    } else {
+      if (team < kSlots) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int at = team * kRows + 8 * (nt * kShare + share) + 2 * t + e;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              acc_sh[at * kRowPad + 16 * i + g] = r.o[nt][i][e];
+              acc_sh[at * kRowPad + 16 * i + g + 8] = r.o[nt][i][2 + e];
+            }
+            if (g == 0) {
+              stat_sh[at] = make_float4(log2_ref(e ? r.ref[nt].y : r.ref[nt].x, p.coef), e ? r.sum[nt].y : r.sum[nt].x,
+                                        e ? r.sum_o[nt].y : r.sum_o[nt].x, 0.f);
+            }
+          }
+      }
       __syncthreads();
       // thread: one row, kDims of its dims
       Piece<kDims> f;
@@ -807,16 +1002,23 @@ __global__ void __launch_bounds__(kShare* kTeams * 32, kPerSm) kv_decode_kernel(
       f.ref = -INFINITY;
 #pragma unroll
       for (int d = 0; d < kDims; ++d) f.acc[d] = 0.f;
+      const int row_sh = min(merge_row, kRows - 1);
 #pragma unroll
-      for (int w = 0; w < kTeams; ++w) f.ref = fmaxf(f.ref, stat_sh[w * kRows + merge_row].x);
+      for (int w = 0; w < kSlots; ++w) f.ref = fmaxf(f.ref, stat_sh[w * kRows + row_sh].x);
 #pragma unroll
-      for (int w = 0; w < kTeams; ++w) {
-        const float4 st = stat_sh[w * kRows + merge_row];
+      for (int w = 0; w < kSlots; ++w) {
+        const float4 st = stat_sh[w * kRows + row_sh];
         const float m = weight_of(st.x, st.y, f.ref);
         f.sum += m * st.y;
         f.sum_o += m * st.z;
 #pragma unroll
-        for (int d = 0; d < kDims; ++d) f.acc[d] += m * acc_sh[(w * kRows + merge_row) * kRowPad + merge_dim + d];
+        for (int d = 0; d < kDims; d += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(acc_sh + (w * kRows + row_sh) * kRowPad + merge_dim + d);
+          f.acc[d] += m * v.x;
+          f.acc[d + 1] += m * v.y;
+          f.acc[d + 2] += m * v.z;
+          f.acc[d + 3] += m * v.w;
+        }
       }
       if (merge_row < rows) {
         if (whole)
@@ -824,49 +1026,49 @@ __global__ void __launch_bounds__(kShare* kTeams * 32, kPerSm) kv_decode_kernel(
         else
           put_piece<kRows, kDims>(mine, merge_row, merge_dim, f);
       }
-      if (more) __syncthreads();  // the merge area is free again
+      if (!more) break;
+      __syncthreads();  // the merge area is free again, and the queries
     }
-    if (!more) break;
-  }
 
-  if (n_cuts == 0) return;
-  const auto arrive = [&](const Cut& c) {  // by one thread, after a barrier: is this worker the pair's last?
-    __threadfence();  // the worker's piece, ordered before by the barrier, is there for whoever sees the count
-    const bool last = atomicAdd(p.counters + c.pair, 1) == c.c1 - c.c0;
-    __threadfence();
-    if (last) p.counters[c.pair] = 0;
-    return last;
-  };
-  // a worker's first pair left its piece in the first of its two places, a later one in the second
-  const auto part_of = [&](const Cut& c) {
-    return [&p, &shares, p0 = c.p0](int w) {
-      return p.part + (2 * static_cast<int64_t>(w) + (p0 > shares.start(w) ? 1 : 0)) * kPartFloats;
+    if (n_cuts == 0) return;
+    const auto arrive = [&](const Cut& c) {  // by one thread, after a barrier: is this worker the pair's last?
+      int* counter = p.counters + static_cast<int64_t>(c.b) * heads + c.head;
+      __threadfence();  // the worker's piece, ordered before by the barrier, is there for whoever sees the count
+      const bool last = atomicAdd(counter, 1) == c.c1 - c.c0;
+      __threadfence();
+      if (last) *counter = 0;
+      return last;
     };
-  };
-  __syncthreads();
-  if (tid < n_cuts) last_sh[tid] = arrive(cuts[tid]);
-  __syncthreads();
-  for (int i = 0; i < n_cuts; ++i) {
-    if (!last_sh[i]) continue;
-    const Cut c = cuts[i];
-    const Seq q = sequence(p, c.b);
-    if (merge_row < p.group * q.n)
-      finish_row<kDims>(p, q, c.head, merge_row, merge_dim,
-                        merge_pieces<kRows, kDims>(part_of(c), c.c0, c.c1, merge_row, merge_dim));
+    // a worker's first pair left its piece in the first of its two places, a later one in the second
+    const auto part_of = [&](const Cut& c) {
+      return [&p, &shares, heads, p0 = c.p0, head = c.head](int w) {
+        return p.part + (2 * (static_cast<int64_t>(w) * heads + head) + (p0 > shares.start(w) ? 1 : 0)) * S::kPartFloats;
+      };
+    };
+    __syncthreads();
+    if (tid < n_cuts) last_sh[tid] = arrive(cuts[tid]);
+    __syncthreads();
+    for (int i = 0; i < n_cuts; ++i) {
+      if (!last_sh[i]) continue;
+      const Cut c = cuts[i];
+      const Seq q = sequence(p, c.b);
+      if (merge_row < q.rows)
+        finish_row<kDims>(p, q, c.head, merge_row, merge_dim,
+                          merge_pieces<kRows, kDims>(part_of(c), c.c0, c.c1, merge_row, merge_dim));
+    }
   }
 }
 
-template <int NT, int kShare, int kTeams, int kStages, int kPerSm>
-cudaError_t launch_variant(const PageDecK& p, cudaStream_t s) {
-  constexpr int kRows = 8 * NT * kShare;
-  constexpr size_t kFixed = 1024 + static_cast<size_t>(kTeams) * (kStages * kTurnBytes + kRows * (kRowPad * 4 + 16));
-  const auto kernel = kv_decode_kernel<NT, kShare, kTeams, kStages, kPerSm>;
-  static_assert(2 * kPerSm * kRows <= kPartRowsPerSm, "the workspace has no room for every CTA's cut pairs");
-  static_assert(kFixed + kKv4MaxRequests * sizeof(long long) <= 227 * 1024, "shared memory");
+template <class S, bool kAlone>
+cudaError_t launch_kernel(const PageDecK& p, cudaStream_t s) {
+  constexpr size_t kFixed = 1024 + S::kRing + (kAlone ? 0 : S::kQueries + S::kMerge);
+  static_assert(kFixed + kKv4MaxRequests / kUptoStep * sizeof(long long) <= 227 * 1024, "shared memory");
+  const auto kernel = kv_decode_kernel<S, kAlone>;
+  const auto bytes = [](int seqs) { return kFixed + (kAlone ? 0 : ceil_div(seqs, kUptoStep) * sizeof(long long)); };
   static SmemOptIn opt_in;
-  const cudaError_t e = opt_in(kernel, kFixed + kKv4MaxRequests * sizeof(long long));
+  const cudaError_t e = opt_in(kernel, bytes(kKv4MaxRequests));
   if (e != cudaSuccess) return e;
-  kernel<<<device_sms() * kPerSm, kShare * kTeams * 32, kFixed + p.num_seqs * sizeof(long long), s>>>(p);
+  kernel<<<device_sms() * S::kPerSm, S::kThreads, bytes(p.num_seqs), s>>>(p);
   return cudaGetLastError();
 }
 
@@ -914,12 +1116,20 @@ cudaError_t launch_kv_decode(const KvPages& c, const KvDecodeArgs& a, int* statu
   // Not below the least normal number: such scores are nothing beside 1 either way, and 0 times a masked key's -inf
   // would be a NaN.
   p.coef = std::max(a.scale * kLog2e, 1.17549435e-38f);
+  p.group_magic = static_cast<uint32_t>(ceil_div(1 << 16, p.group));
   const int rows = p.group * a.n;
-  if (rows <= 8) return launch_variant<1, 1, 4, 3, 2>(p, s);
-  if (rows <= 16) return launch_variant<2, 1, 4, 2, 2>(p, s);
-  if (rows <= 32) return launch_variant<4, 1, 4, 2, 2>(p, s);
-  if (rows <= 64) return launch_variant<4, 2, 4, 3, 1>(p, s);
-  return launch_variant<4, 4, 2, 6, 1>(p, s);
+  // what a sequence's rows can see at most, in turns
+  const long long table = static_cast<long long>(c.max_pages) << c.page_log2;
+  const long long most = a.window < 0 ? ceil_div(table, kTurn)
+                                      : ceil_div(std::min<long long>(a.prefix, table), kTurn) +
+                                            ceil_div(static_cast<long long>(a.window) + a.n, kTurn) + 1;
+  const bool alone = most <= kAloneTurns && static_cast<long long>(a.num_seqs) * c.num_heads_kv >= device_sms();
+  if (rows <= 8) return alone ? launch_kernel<Shape<1, 1, 4, 2, 3>, true>(p, s) : launch_kernel<Shape<1, 1, 4, 3, 2>, false>(p, s);
+  if (rows <= 16) return alone ? launch_kernel<Shape<2, 1, 4, 2, 3>, true>(p, s) : launch_kernel<Shape<2, 1, 4, 2, 2>, false>(p, s);
+  if (rows <= 32) return launch_kernel<Shape<4, 1, 4, 2, 2>, false>(p, s);
+  if (rows <= 48) return launch_kernel<Shape<6, 1, 8, 2, 1>, false>(p, s);
+  if (rows <= 64) return launch_kernel<Shape<4, 2, 4, 3, 1>, false>(p, s);
+  return launch_kernel<Shape<4, 4, 2, 6, 1>, false>(p, s);
 }
 
 }  // namespace sa

@@ -242,6 +242,7 @@ def test_decode(page, heads, group, lens, counts, window, prefix):
 @pytest.mark.parametrize("batch,length,page,heads,group,n", [(5, 9000, 64, 2, 8, 1), (1, 40000, 16, 1, 8, 1),
                                                              (2, 12001, 128, 2, 8, 2), (3, 7000, 64, 2, 8, 4),
                                                              (2, 9001, 64, 2, 8, 7), (1, 20001, 32, 1, 64, 2),
+                                                             (2, 9001, 64, 2, 8, 5), (3, 8000, 16, 1, 6, 8),
                                                              (300, 40, 16, 2, 4, 1), (400, 70, 16, 2, 8, 2)])
 def test_decode_cut_between_ctas(batch, length, page, heads, group, n):
     """Long sequences, whose pairs are cut and merged, and many short ones, which warps take alone."""
@@ -272,7 +273,37 @@ def test_rows_outside_the_entries_are_left_alone():
     assert (o[rest] == 5).all() and (lse[:, rest] == 5).all()
 
 
-@pytest.mark.parametrize("n,group", [(1, 8), (2, 8), (4, 8), (8, 8), (3, 32)])
+def test_rows_beyond_q_per_seq_are_left_alone():
+    import sink_aware_masked_gb300 as sa
+
+    rng = np.random.RandomState(4)
+    c = shuffled(rng, [50, 20], 16, 2)
+    q, sink = bf16(rng, 7, 6, 64).to(DEV), dev(rng.randn(6), torch.float32)
+    h, cu = handle(c), i32([0, 3, 7])
+    want, want_l = sa.kv_decode_fwd(h, i32([0, 1]), q, sink, q_per_seq=4, cu_rows=cu)
+    check_decode(c, [0, 1], [3, 4], 6, -1, 0, q, sink, want, want_l)
+    for most in (1, 2, 3):
+        o, lse = torch.full_like(q, 5.0), torch.full((6, 7), 5.0, device=DEV)
+        sa.kv_decode_fwd(h, i32([0, 1]), q, sink, q_per_seq=most, cu_rows=cu, o=o, lse=lse)
+        there = torch.tensor([i < most for i in (0, 1, 2, 0, 1, 2, 3)], device=DEV)
+        assert torch.equal(lse[:, there], want_l[:, there]) and (lse[:, ~there] == 5).all()
+        assert torch.equal(o[there], want[there]) and (o[~there] == 5).all()
+
+
+@pytest.mark.parametrize("heads,group,n", [(40, 1, 1), (200, 1, 2), (160, 1, 1), (3, 16, 6)])
+def test_many_kv_heads(heads, group, n):
+    """More kv heads than there are shares, or than CTAs."""
+    import sink_aware_masked_gb300 as sa
+
+    rng = np.random.RandomState(heads)
+    lens = [333, 65, 0, 1200]
+    c = shuffled(rng, lens, 32, heads)
+    q, sink = bf16(rng, 4 * n, heads * group, 64).to(DEV), dev(rng.randn(heads * group), torch.float32)
+    o, lse = sa.kv_decode_fwd(handle(c), i32([3, 1, 2, 0]), q, sink, q_per_seq=n)
+    check_decode(c, [3, 1, 2, 0], [n] * 4, heads * group, -1, 0, q, sink, o, lse)
+
+
+@pytest.mark.parametrize("n,group", [(1, 8), (2, 8), (4, 8), (6, 8), (8, 8), (3, 32)])
 @pytest.mark.parametrize("window,prefix", [(-1, 0), (9, 2)])
 def test_what_is_not_seen_does_not_matter(n, group, window, prefix):
     """NaN and infinities behind the length, below the window and after a row's own position."""
