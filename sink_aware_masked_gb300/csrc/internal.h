@@ -276,7 +276,7 @@ struct VerifyArgs {
   float* logp;               // [rows]
   int32_t* accepted;         // [num_seqs]
   int32_t* rejected;         // [num_seqs]
-  float4* parts;             // [rows][2][slices]
+  float4* parts;             // [rows + num_drafts][slices]: largest logit, sum relative to it, where it is
 };
 size_t verify_workspace_bytes(int dtype, int rows, int vocab);
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);

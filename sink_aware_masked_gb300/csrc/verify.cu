@@ -18,17 +18,17 @@
 // Arithmetic.  Where the tests are concerned fp32 sums do: a test is decided
 // wrongly only where u q and p agree to some 2^-22.  The draw is another
 // matter: among 200 k cumulated masses one border or another lies within 2^-24
-// of every place, so the masses are 64-bit fixed point in units of 2^-45 of
-// the whole, and
+// of every place, so the masses are 64-bit fixed point in units of 2^-40 of
+// the whole (one rounding a vector of 16 bytes), and
 //   - the exponent is kept in two parts (x - max times log2 e / T loses 2^-24
 //     of up to 20 otherwise), which leaves the hardware exponential's error,
 //     some 2^-23 of the mass;
-//   - masses above 2^-13 of the whole, of which there are few, take an
-//     exponential of two fp32 parts (off by some 2^-40);
+//   - masses from 2^-12 of the whole on, of which there are few, are listed and
+//     take an exponential of two fp32 parts (off by some 2^-40);
 //   - max(p - q, 0) needs the ratio of the two sums as exactly: they are
 //     summed again in the same way from the two rows.
-// Integer sums are the same in every order.  FP64 is left to single values: its
-// rate on this GPU would cost more than all the rest.
+// Integer sums are the same in every order.  FP64 is not used: its rate on this
+// GPU would cost more than all the rest.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
@@ -55,6 +55,9 @@ struct Elem<0> {
   static SA_DEV void unpack(uint4 v, float* x) {
     x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
+  static SA_DEV float largest(uint4 v) {
+    return fmaxf(fmax3(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z)), __uint_as_float(v.w));
+  }
   static SA_DEV float one(T v) { return v; }
   static SA_DEV T lowest() { return -INFINITY; }
 };
@@ -66,6 +69,15 @@ struct Elem<1> {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(w[i] << 16), x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  static SA_DEV float largest(uint4 v) {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  static SA_DEV uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+    return d;
   }
   static SA_DEV float one(T v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
   static SA_DEV T lowest() { return 0xff80u; }
@@ -81,6 +93,16 @@ struct Elem<2> {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
       x[2 * i] = f.x, x[2 * i + 1] = f.y;
     }
+  }
+  static SA_DEV float largest(uint4 v) {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+    return fmaxf(f.x, f.y);
+  }
+  static SA_DEV uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+    return d;
   }
   static SA_DEV float one(T v) { return __half2float(*reinterpret_cast<const __half*>(&v)); }
   static SA_DEV T lowest() { return 0xfc00u; }
@@ -112,9 +134,10 @@ struct Scale {
     valid = t >= 0.f && t <= 1e36f;
     greedy = t == 0.f;
     temperature = greedy || !valid ? 1.f : t;
-    const double s = 1.4426950408889634 / static_cast<double>(temperature);
-    hi = fminf(static_cast<float>(s), 1e38f);
-    lo = s < 1e38 ? static_cast<float>(s - static_cast<double>(hi)) : 0.f;
+    constexpr float kLog2eLo = static_cast<float>(1.4426950408889634074 - static_cast<double>(kLog2e));
+    const float q = __fdiv_rn(kLog2e, temperature);
+    hi = fminf(q, 1e38f);
+    lo = q < 1e38f ? __fdiv_rn(fmaf(-q, temperature, kLog2e) + kLog2eLo, temperature) : 0.f;
   }
 };
 
@@ -124,14 +147,9 @@ struct Rows {
   int row0, n, draft0;
 };
 
-// What the first launch leaves of a row's slice.
-struct alignas(16) Part {
-  float top, sum;  // largest logit (kLowest at least), sum of 2^((x - top) scale)
-  int arg, pad;    // where the first of the largest is, in rows of temperature 0
-};
-
 // ---------------------------------------------------------------- all rows
 constexpr int kStatThreads = 256;
+constexpr int kStatWarps = kStatThreads / 32;
 constexpr int kStatVecs = 8;  // 16-byte vectors a thread holds
 
 template <int kType>
@@ -139,39 +157,58 @@ __host__ __device__ constexpr int slice_logits() {
   return kStatThreads * kStatVecs * Elem<kType>::kVec;
 }
 
+// Sum of 2^((x - top) scale) over the vectors a thread holds.
 template <int kType>
-__global__ void __launch_bounds__(kStatThreads) verify_rows_kernel(const VerifyArgs a, int slices) {
+SA_DEV float sum_powers(const uint4 (&w)[kStatVecs], float top, float scale) {
   typedef Elem<kType> E;
-  typedef typename E::T T;
-  constexpr int kWarps = kStatThreads / 32;
-  __shared__ float red[kWarps];
-  __shared__ int red_i[kWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int item = blockIdx.x >> 1, row = item / slices, slice = item - row * slices;
-  const bool draft = blockIdx.x & 1;
-  // the row's sequence, and how many with rows come before it
-  int seqs = 0, full = 0;
-  for (int j = tid; j < a.num_seqs; j += kStatThreads) {
-    const int upto = a.cu[j + 1];
-    if (upto <= row) {
-      ++seqs;
-      full += upto > a.cu[j];
+  float2 sum = make_float2(0.f, 0.f);
+  const float2 by = make_float2(scale, scale);
+  const float ref = top * scale;
+  if (fabsf(ref) < 1048576.f) {
+    // one fused x scale - ref, put right at the end for what ref was rounded by
+    const float2 minus = make_float2(-ref, -ref);
+#pragma unroll
+    for (int i = 0; i < kStatVecs; ++i) {
+      float f[E::kVec];
+      E::unpack(w[i], f);
+#pragma unroll
+      for (int e = 0; e < E::kVec; e += 2) {
+        const float2 t = ffma2(make_float2(f[e], f[e + 1]), by, minus);
+        sum = fadd2(sum, make_float2(ex2(t.x), ex2(t.y)));
+      }
+    }
+    return (sum.x + sum.y) * ex2(-fmaf(top, scale, -ref));
+  }
+  // where ref's rounding would swamp the exponent the difference comes first
+  const float2 minus = make_float2(-top, -top);
+#pragma unroll
+  for (int i = 0; i < kStatVecs; ++i) {
+    float f[E::kVec];
+    E::unpack(w[i], f);
+#pragma unroll
+    for (int e = 0; e < E::kVec; e += 2) {
+      const float2 t = fmul2(fadd2(make_float2(f[e], f[e + 1]), minus), by);
+      sum = fadd2(sum, make_float2(ex2(t.x), ex2(t.y)));
     }
   }
-  const int both = warp_sum(seqs << 16 | full);
-  if (lane == 0) red_i[warp] = both;
-  __syncthreads();
-  int b = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) b += red_i[w] >> 16, before += red_i[w] & 0xffff;
-  if (b >= a.num_seqs || row < a.cu[0]) return;
-  if (draft && (a.draft_logits == nullptr || row + 1 >= a.cu[b + 1])) return;
-  const Scale sc(a.temperature[b]);
-  if (!sc.valid || (draft && sc.greedy)) return;
-  const int d = row - a.cu[0] - before;  // the row's draft
-  if (draft && d >= a.num_drafts) return;
-  const T* x = draft ? static_cast<const T*>(a.draft_logits) + static_cast<int64_t>(d) * a.draft_stride
-                     : static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.stride;
+  return sum.x + sum.y;
+}
+
+// CTA: slice `slice` of target row or draft `index`.  The row is on its way
+// while the first warp finds the sequence that it belongs to.
+template <int kType>
+__global__ void __launch_bounds__(kStatThreads, 4) verify_rows_kernel(const VerifyArgs a, int slices) {
+  typedef Elem<kType> E;
+  typedef typename E::T T;
+  __shared__ float red[kStatWarps];
+  __shared__ int red_i[kStatWarps];
+  __shared__ int seq_sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int item = blockIdx.x / slices, slice = blockIdx.x - item * slices;
+  const bool draft = item >= a.rows;
+  const int index = draft ? item - a.rows : item;
+  const T* x = draft ? static_cast<const T*>(a.draft_logits) + static_cast<int64_t>(index) * a.draft_stride
+                     : static_cast<const T*>(a.logits) + static_cast<int64_t>(index) * a.stride;
 
   // 16-byte vectors as they are aligned in memory, what is outside the row -inf
   const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) / sizeof(T)) % E::kVec);
@@ -197,31 +234,42 @@ __global__ void __launch_bounds__(kStatThreads) verify_rows_kernel(const VerifyA
       w[i] = part.q;
     }
   }
+  if (warp == 0) {
+    // the sequences that end at or before the row, or (one draft fewer than rows each) before the draft
+    const int first = a.cu[0];
+    int seqs = 0, behind = 0;
+    for (int j0 = 0; j0 < a.num_seqs; j0 += 32) {
+      const int j = j0 + lane;
+      int rows = 0, upto = 0x7fffffff;
+      if (j < a.num_seqs) {
+        upto = a.cu[j + 1];
+        rows = upto - a.cu[j];
+      }
+      if (draft) {
+        const uint32_t full = __ballot_sync(0xffffffffu, rows > 0);
+        if (j < a.num_seqs) upto -= first + behind + __popc(full & (2u << lane) - 1u);
+        behind += __popc(full);
+      }
+      const uint32_t done = __ballot_sync(0xffffffffu, j < a.num_seqs && upto <= index);
+      seqs += __popc(done);
+      if (done != 0xffffffffu) break;
+    }
+    if (!draft && index < first) seqs = a.num_seqs;
+    if (lane == 0) seq_sh = seqs;
+  }
   float top = kLowest;
 #pragma unroll
-  for (int i = 0; i < kStatVecs; ++i) {
-    float f[E::kVec];
-    E::unpack(w[i], f);
-#pragma unroll
-    for (int e = 0; e < E::kVec; ++e) top = fmaxf(top, f[e]);
-  }
+  for (int i = 0; i < kStatVecs; ++i) top = fmaxf(top, E::largest(w[i]));
   top = warp_max(top);
   if (lane == 0) red[warp] = top;
   __syncthreads();
+  const int b = seq_sh;
+  if (b >= a.num_seqs) return;  // a row of no entry
+  const Scale sc(a.temperature[b]);
+  if (!sc.valid || (draft && sc.greedy)) return;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) top = fmaxf(top, red[i]);
-  float2 sum = make_float2(0.f, 0.f);
-  const float2 minus = make_float2(-top, -top), by = make_float2(sc.hi, sc.hi);
-#pragma unroll
-  for (int i = 0; i < kStatVecs; ++i) {
-    float f[E::kVec];
-    E::unpack(w[i], f);
-#pragma unroll
-    for (int e = 0; e < E::kVec; e += 2) {
-      const float2 t = fmul2(fadd2(make_float2(f[e], f[e + 1]), minus), by);
-      sum = fadd2(sum, make_float2(ex2(t.x), ex2(t.y)));
-    }
-  }
+  for (int i = 0; i < kStatWarps; ++i) top = fmaxf(top, red[i]);
+  const float sum = warp_sum(sum_powers<kType>(w, top, sc.hi));
   int arg = 0x7fffffff;
   if (sc.greedy) {
 #pragma unroll
@@ -235,15 +283,13 @@ __global__ void __launch_bounds__(kStatThreads) verify_rows_kernel(const VerifyA
     arg = warp_min(arg);
   }
   __syncthreads();
-  const float total = warp_sum(sum.x + sum.y);
-  if (lane == 0) red[warp] = total, red_i[warp] = arg;
+  if (lane == 0) red[warp] = sum, red_i[warp] = arg;
   __syncthreads();
   if (tid != 0) return;
-  Part p{top, 0.f, 0x7fffffff, 0};
+  float total = 0.f;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) p.sum += red[i], p.arg = min(p.arg, red_i[i]);
-  a.parts[(static_cast<int64_t>(row) * 2 + draft) * slices + slice] =
-      make_float4(p.top, p.sum, __int_as_float(p.arg), 0.f);
+  for (int i = 0; i < kStatWarps; ++i) total += red[i], arg = min(arg, red_i[i]);
+  a.parts[static_cast<int64_t>(item) * slices + slice] = make_float4(top, total, __int_as_float(arg), 0.f);
 }
 
 // ---------------------------------------------------------------- exponentials
@@ -299,15 +345,19 @@ SA_DEV Pair power_pair(Pair t) {
   const float scale = __int_as_float((127 + (i >> 4)) << 23);
   return {sum * scale, rest2 * scale};
 }
+SA_DEV Pair to_pair(u64 m) {
+  const float hi = __ull2float_rn(m);
+  return {hi, __ll2float_rn(static_cast<long long>(m - static_cast<u64>(hi)))};
+}
 SA_DEV long long to_units(Pair e, float unit) { return __float2ll_rn(e.hi * unit) + __float2ll_rn(e.lo * unit); }
 
 // ---------------------------------------------------------------- a sequence
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kUnroll = 2;
-constexpr float kHeavy = 1.f / 8192.f;  // of the whole
-constexpr int kUnitLog2 = 45;           // masses in units of 2^-45 of (about) the whole
+constexpr int kHeavyLog2 = 12;  // masses from 2^-12 of the whole on are heavy
+constexpr int kUnitLog2 = 40;   // masses in units of 2^-40 of (about) the whole
+constexpr int kList = 2048;     // vectors with heavy masses that a CTA keeps a list of
 
 struct RowStat {
   float top, sum;
@@ -320,7 +370,8 @@ struct Shared {
   u64 exchange[2][kMaxCluster][2];
   u64 warp_mass[kWarps], warp_mass_q[kWarps];
   int count[kWarps];
-  int first;
+  int first, listed;
+  uint32_t list[kList];  // vector in the CTA's run << 8 | its heavy logits, a bit each
 };
 
 template <int kType>
@@ -341,7 +392,8 @@ class Sequence {
     full = warp_sum(full);
     if (lane == 0) sh_.count[warp] = full;
     const int row0 = max(a_.cu[b], 0), n = min(a_.cu[b + 1], a_.rows) - row0;
-    if (tid == 0) sh_.first = max(n - 1, 0);
+    if (tid == 0) sh_.first = max(n - 1, 0), sh_.listed = 0;
+    my_run();
     if (ctas_ > 1) cluster_.barrier_wait();  // every CTA of the cluster runs: its shared memory may be written
     __syncthreads();
     int draft0 = row0 - a_.cu[0];  // one draft fewer than rows in every sequence before that has rows
@@ -356,20 +408,24 @@ class Sequence {
       bool stands = false;
       if (sc.valid && draft0 + i < a_.num_drafts) {
         const int token = a_.drafts[draft0 + i];
-        const RowStat p = stat(row0 + i, false, sc);
+        const RowStat p = stat(row0 + i, sc);
         if (!p.bad() && !p.none() && token >= 0 && token < a_.vocab) {
           const float x = logit(row0 + i, token);
           if (sc.greedy) {
             stands = token == p.arg;
           } else {
-            double q = 1.0;
-            bool known = true;
-            if (a_.draft_logits != nullptr) {
-              const RowStat s = stat(row0 + i, true, sc);
-              known = !s.bad() && !s.none();
-              q = share(draft_logit(draft0 + i, token), s, sc);
+            const float u = unit_of(a_.u[row0 + i]);
+            const Pair tp = exponent(x, p.top, sc);
+            if (a_.draft_logits == nullptr) {
+              stands = u * p.sum < power(tp);
+            } else {
+              // u q < p by their ratio, which stays in range where both are small
+              const RowStat s = stat(a_.rows + draft0 + i, sc);
+              const float y = draft_logit(draft0 + i, token);
+              const Pair tq = exponent(y, s.top, sc);
+              const float ratio = y == -INFINITY ? INFINITY : ex2((tp.hi - tq.hi) + (tp.lo - tq.lo)) * __fdiv_rn(s.sum, p.sum);
+              stands = !s.bad() && !s.none() && x > -INFINITY && u < ratio;
             }
-            stands = known && static_cast<double>(unit_of(a_.u[row0 + i])) * q < share(x, p, sc);
           }
           if (stands && rank_ == 0 && lane == 0) {
             a_.tokens[row0 + i] = token;
@@ -393,32 +449,36 @@ class Sequence {
     }
     const bool refused = j < n - 1;
     if (!sc.valid || (refused && draft0 + j >= a_.num_drafts)) return put(row, -1, NAN);
-    const RowStat p = stat(row, false, sc);
+    const RowStat p = stat(row, sc);
     if (p.bad()) return put(row, -1, NAN);
     if (p.none()) return put(row, -1, -INFINITY);
     if (sc.greedy) return put(row, p.arg, log_share(p.top, p, sc));
     Weights w;
     w.p = p;
     w.unit = unit_for(p.sum);
-    w.heavy = p.sum * kHeavy;
+    w.heavy = heavy_from(p, sc);
     w.without = -1;
     w.minus_q = false;
     x_ = static_cast<const T*>(a_.logits) + static_cast<int64_t>(row) * a_.stride;
     y_ = nullptr;
     if (refused && a_.draft_logits == nullptr) w.without = a_.drafts[draft0 + j];
     if (refused && a_.draft_logits != nullptr) {
-      const RowStat q = stat(row, true, sc);
+      const RowStat q = stat(a_.rows + draft0 + j, sc);
       if (q.bad() || q.none()) return put(row, -1, NAN);
       w.q = q;
       w.minus_q = true;
-      w.heavy_q = q.sum * kHeavy;
+      w.heavy_q = heavy_from(q, sc);
       y_ = static_cast<const T*>(a_.draft_logits) + static_cast<int64_t>(draft0 + j) * a_.draft_stride;
       sum_ratio(w, sc);
     }
     if (!draw(w, sc, row, unit_of(a_.u[row0 + n - 1]))) {
-      // nothing is left of w: the target's own probabilities
+      // nothing is left of w: the target's own probabilities (and the list holds what was heavy in q too)
       w.minus_q = false;
       w.without = -1;
+      listed_ = false;
+      __syncthreads();
+      if (tid == 0) sh_.listed = 0;
+      __syncthreads();
       draw(w, sc, row, unit_of(a_.u[row0 + n - 1]));
     }
   }
@@ -426,12 +486,18 @@ class Sequence {
  private:
   struct Weights {
     RowStat p, q;
-    float unit, heavy, heavy_q;  // masses are e times unit; e from which a mass is heavy
-    Pair ratio;                  // of the sums: p - q is e_p - ratio e_q, but for a factor
-    int without;                 // the draft that is taken out, or -1
+    float unit;            // masses are e times unit
+    float heavy, heavy_q;  // logits from which a mass is heavy
+    Pair ratio;            // of the sums: p - q is e_p - ratio e_q, but for a factor
+    int without;           // the draft that is taken out, or -1
     bool minus_q;
   };
 
+  static SA_DEV float heavy_from(const RowStat& s, const Scale& sc) {
+    float l;
+    asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(l) : "f"(s.sum));
+    return s.top + __fdiv_rn(l - kHeavyLog2, sc.hi);
+  }
   static SA_DEV float unit_of(float u) { return fminf(fmaxf(u, 0.f), 0.99999994f); }
   // A power of two that brings the whole, `sum`, to 2^kUnitLog2 or just below.
   static SA_DEV float unit_for(float sum) {
@@ -439,8 +505,9 @@ class Sequence {
     return __int_as_float((127 + kUnitLog2 - e) << 23);
   }
 
-  SA_DEV RowStat stat(int row, bool draft, const Scale& sc) const {  // by a whole warp
-    const float4* parts = a_.parts + (static_cast<int64_t>(row) * 2 + draft) * slices_;
+  // Of target row `item`, or of draft item - rows; by a whole warp.
+  SA_DEV RowStat stat(int item, const Scale& sc) const {
+    const float4* parts = a_.parts + static_cast<int64_t>(item) * slices_;
     RowStat r{kLowest, 0.f, 0x7fffffff};
     for (int i = threadIdx.x & 31; i < slices_; i += 32) r.top = fmaxf(r.top, parts[i].x);
     r.top = warp_max(r.top);
@@ -458,10 +525,6 @@ class Sequence {
   }
   SA_DEV float draft_logit(int draft, int token) const {
     return E::one(static_cast<const T*>(a_.draft_logits)[static_cast<int64_t>(draft) * a_.draft_stride + token]);
-  }
-  static SA_DEV double share(float x, const RowStat& s, const Scale& sc) {
-    return exp((static_cast<double>(x) - static_cast<double>(s.top)) / static_cast<double>(sc.temperature)) /
-           static_cast<double>(s.sum);
   }
   static SA_DEV float log_share(float x, const RowStat& s, const Scale& sc) {
     return __fdiv_rn(x - s.top, sc.temperature) - logf(s.sum);
@@ -490,12 +553,12 @@ class Sequence {
     for (unsigned r = 0; r < ctas_; ++r) take(buf[r][0], buf[r][1]);
   }
 
-  // The vectors of the row (counted from its first logit) that the warp has, one run of them.
-  SA_DEV void my_run(int& v0, int& v1) const {
+  // The vectors of a row (counted from its first logit) that the warp has, one run of them.
+  SA_DEV void my_run() {
     const int vectors = (a_.vocab + E::kVec - 1) / E::kVec, parts = ctas_ * kWarps;
-    const int each = (vectors + parts - 1) / parts;
-    v0 = min((static_cast<int>(rank_) * kWarps + static_cast<int>(threadIdx.x >> 5)) * each, vectors);
-    v1 = min(v0 + each, vectors);
+    run_ = (vectors + parts - 1) / parts;
+    v0_ = min((static_cast<int>(rank_) * kWarps + static_cast<int>(threadIdx.x >> 5)) * run_, vectors);
+    v1_ = min(v0_ + run_, vectors);
   }
   // Logits of vector v; -inf behind the row's end.
   SA_DEV void load(const T* row, int v, float* f) const {
@@ -508,52 +571,153 @@ class Sequence {
     }
   }
 
-  // e in units.
-  SA_DEV long long mass(float x, const RowStat& s, float heavy, float unit, const Scale& sc) const {
-    const Pair t = exponent(x, s.top, sc);
-    const float e = power(t);
-    return e < heavy ? __float2uint_rn(e * unit) : to_units(power_pair(t), unit);
-  }
-  // What a token weighs, in units.
-  SA_DEV long long weight(float x, float y, int index, const Weights& w, const Scale& sc) const {
-    if (!w.minus_q) return index == w.without ? 0 : mass(x, w.p, w.heavy, w.unit, sc);
-    const Pair tp = exponent(x, w.p.top, sc), tq = exponent(y, w.q.top, sc);
-    const float ep = power(tp), eq = power(tq);
-    if (ep < w.heavy && eq < w.heavy_q) {
-      const float r = fmaf(-eq, w.ratio.lo, fmaf(-eq, w.ratio.hi, ep));
-      return __float2uint_rn(fmaxf(r, 0.f) * w.unit);
+  // 2^((x - top) scale) of two logits to some 2^-23 of itself, 0 far below; d_least is where that is.
+  static SA_DEV float2 light(float x, float y, float top, float d_least, const Scale& sc) {
+    float2 d = fadd2(make_float2(x, y), make_float2(-top, -top));
+    float2 d_lo = make_float2(0.f, 0.f);
+    if constexpr (kType == 0) {
+      // what d was rounded by; the difference of two 16-bit logits is exact where it matters (neither below 2^-13 of
+      // the other)
+      const float2 b = fadd2(d, make_float2(-x, -y));
+      const float2 c = fadd2(d, make_float2(-b.x, -b.y));
+      d_lo = fadd2(fadd2(make_float2(x, y), make_float2(-c.x, -c.y)), fadd2(make_float2(-top, -top), make_float2(-b.x, -b.y)));
+      d_lo = make_float2(x > -INFINITY ? d_lo.x : 0.f, y > -INFINITY ? d_lo.y : 0.f);
     }
-    Pair p = {ep, 0.f}, q = {eq, 0.f};
-    if (ep >= w.heavy) p = power_pair(tp);
-    if (eq >= w.heavy_q) q = power_pair(tq);
+    d = make_float2(fmaxf(d.x, d_least), fmaxf(d.y, d_least));
+    const float2 s2 = make_float2(sc.hi, sc.hi);
+    const float2 hi = fmul2(d, s2);
+    float2 lo = ffma2(d, make_float2(sc.lo, sc.lo), ffma2(d, s2, make_float2(-hi.x, -hi.y)));
+    if constexpr (kType == 0) lo = ffma2(d_lo, s2, lo);
+    const float2 e = make_float2(ex2(hi.x), ex2(hi.y));
+    return ffma2(e, fmul2(lo, make_float2(kLn2, kLn2)), e);
+  }
+  static SA_DEV float least_difference(const Scale& sc) { return fmaxf(__fdiv_rn(-150.f, sc.hi), -3e38f); }
+
+  // What a token weighs, in units, where its mass is heavy.
+  SA_DEV long long heavy_weight(float x, float y, int index, const Weights& w, const Scale& sc) const {
+    if (index == w.without) return 0;
+    const Pair p = power_pair(exponent(x, w.p.top, sc));
+    if (!w.minus_q) return to_units(p, w.unit);
+    const Pair q = power_pair(exponent(y, w.q.top, sc));
     const float c = __fmul_rn(q.hi, w.ratio.hi), c_lo = fmaf(q.hi, w.ratio.hi, -c) + fmaf(q.hi, w.ratio.lo, q.lo * w.ratio.hi);
     return max(to_units(p, w.unit) - to_units({c, c_lo}, w.unit), 0LL);
+  }
+  // A vector's logits, and which of them are heavy, a bit each.
+  SA_DEV uint32_t load_both(int v, const Weights& w, float (&x)[E::kVec], float (&y)[E::kVec]) const {
+    load(x_, v, x);
+    bool any = largest(x) >= w.heavy;
+    if (w.minus_q) {
+      load(y_, v, y);
+      any |= largest(y) >= w.heavy_q;
+    }
+    uint32_t bits = 0;
+    if (any) {
+#pragma unroll
+      for (int e = 0; e < E::kVec; ++e)
+        bits |= static_cast<uint32_t>(x[e] >= w.heavy || (w.minus_q && y[e] >= w.heavy_q)) << e;
+    }
+    return bits;
+  }
+  static SA_DEV float largest(const float (&x)[E::kVec]) {
+    float m = fmaxf(x[0], x[1]);
+#pragma unroll
+    for (int e = 2; e < E::kVec; e += 2) m = fmax3(m, x[e], x[e + 1]);
+    return m;
+  }
+  // What the logits of a vector weigh that are not heavy, before the unit.
+  SA_DEV void light_weights(int v, uint32_t heavy, const float (&x)[E::kVec], const float (&y)[E::kVec], const Weights& w,
+                            float d_least, const Scale& sc, float2 (&r)[E::kVec / 2]) const {
+#pragma unroll
+    for (int e = 0; e < E::kVec; e += 2) {
+      float2 m = light(x[e], x[e + 1], w.p.top, d_least, sc);
+      if (w.minus_q) {
+        const float2 q = light(y[e], y[e + 1], w.q.top, d_least, sc), n = make_float2(-q.x, -q.y);
+        m = ffma2(n, make_float2(w.ratio.lo, w.ratio.lo), ffma2(n, make_float2(w.ratio.hi, w.ratio.hi), m));
+        m = make_float2(fmaxf(m.x, 0.f), fmaxf(m.y, 0.f));
+      }
+      r[e / 2] = m;
+    }
+    if (heavy != 0) {
+#pragma unroll
+      for (int e = 0; e < E::kVec; e += 2)
+        r[e / 2] = make_float2(heavy >> e & 1u ? 0.f : r[e / 2].x, heavy >> (e + 1) & 1u ? 0.f : r[e / 2].y);
+    }
+    if (w.without >= v * E::kVec && w.without < (v + 1) * E::kVec) {
+#pragma unroll
+      for (int e = 0; e < E::kVec; e += 2) {
+        if (v * E::kVec + e == w.without) r[e / 2].x = 0.f;
+        if (v * E::kVec + e + 1 == w.without) r[e / 2].y = 0.f;
+      }
+    }
+  }
+  static SA_DEV float sum_of(const float2 (&r)[E::kVec / 2]) {
+    float2 s = r[0];
+#pragma unroll
+    for (int e = 1; e < E::kVec / 2; ++e) s = fadd2(s, r[e]);
+    return s.x + s.y;
+  }
+  // f(x, y, index) for the heavy logits of the CTA's listed vectors, evenly over its threads.
+  template <class F>
+  SA_DEV void each_listed(const Weights& w, F f) const {
+    const int v_cta = static_cast<int>(rank_) * kWarps * run_;
+    for (int i = threadIdx.x; i < min(sh_.listed, kList); i += kThreads) {
+      const int v = v_cta + static_cast<int>(sh_.list[i] >> 8);
+      for (uint32_t bits = sh_.list[i] & 0xffu; bits != 0; bits &= bits - 1) {
+        const int index = v * E::kVec + __ffs(bits) - 1;
+        f(E::one(x_[index]), w.minus_q ? E::one(y_[index]) : 0.f, index, v);
+      }
+    }
+  }
+  // Enters a vector in the list of those with heavy logits; false if it is full.
+  SA_DEV bool enter(int v, uint32_t bits) {
+    const int at = atomicAdd(&sh_.listed, 1);
+    if (at >= kList) return false;
+    sh_.list[at] = static_cast<uint32_t>(v - static_cast<int>(rank_) * kWarps * run_) << 8 | bits;
+    return true;
   }
 
   // The ratio of the two rows' sums.
   SA_DEV void sum_ratio(Weights& w, const Scale& sc) {
-    const float unit_q = unit_for(w.q.sum);
-    int v0, v1;
-    my_run(v0, v1);
+    const float unit_q = unit_for(w.q.sum), d_least = least_difference(sc);
     u64 p = 0, q = 0;
-#pragma unroll kUnroll
-    for (int v = v0 + (threadIdx.x & 31); v < v1; v += 32) {
+    const auto add_heavy = [&](float x, float y) {
+      p += to_units(power_pair(exponent(x, w.p.top, sc)), w.unit);
+      q += to_units(power_pair(exponent(y, w.q.top, sc)), unit_q);
+    };
+#pragma unroll 2
+    for (int v = v0_ + (threadIdx.x & 31); v < v1_; v += 32) {
       float x[E::kVec], y[E::kVec];
-      load(x_, v, x);
-      load(y_, v, y);
+      const uint32_t heavy = load_both(v, w, x, y);
+      float2 sp = make_float2(0.f, 0.f), sq = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int e = 0; e < E::kVec; ++e) {
-        p += mass(x[e], w.p, w.heavy, w.unit, sc);
-        q += mass(y[e], w.q, w.heavy_q, unit_q, sc);
+      for (int e = 0; e < E::kVec; e += 2) {
+        float2 ep = light(x[e], x[e + 1], w.p.top, d_least, sc), eq = light(y[e], y[e + 1], w.q.top, d_least, sc);
+        if (heavy >> e & 3u) {
+          if (heavy >> e & 1u) ep.x = eq.x = 0.f;
+          if (heavy >> e & 2u) ep.y = eq.y = 0.f;
+        }
+        sp = fadd2(sp, ep);
+        sq = fadd2(sq, eq);
+      }
+      p += __float2uint_rn((sp.x + sp.y) * w.unit);
+      q += __float2uint_rn((sq.x + sq.y) * unit_q);
+      if (heavy != 0 && !enter(v, heavy)) {
+#pragma unroll
+        for (int e = 0; e < E::kVec; ++e)
+          if (heavy >> e & 1u) add_heavy(x[e], y[e]);
       }
     }
+    __syncthreads();
+    each_listed(w, [&](float x, float y, int, int) { add_heavy(x, y); });
     block_totals(p, q);
     u64 all_p = 0, all_q = 0;
     exchange(p, q, [&](u64 a, u64 b) { all_p += a, all_q += b; });
-    const double ratio = (static_cast<double>(all_p) / static_cast<double>(w.unit)) /
-                         (static_cast<double>(all_q) / static_cast<double>(unit_q));
-    w.ratio.hi = static_cast<float>(ratio);
-    w.ratio.lo = static_cast<float>(ratio - static_cast<double>(w.ratio.hi));
+    const Pair a = to_pair(all_p), b = to_pair(all_q);
+    const float hi = __fdiv_rn(a.hi, b.hi);
+    const float lo = __fdiv_rn(fmaf(-hi, b.hi, a.hi) + fmaf(-hi, b.lo, a.lo), b.hi);
+    const float scale = __fdiv_rn(unit_q, w.unit);  // a power of two
+    w.ratio = {hi * scale, lo * scale};
+    listed_ = true;
   }
   // Sums over the CTA, the same in all threads; the warps' own stay in sh_.warp_mass.
   SA_DEV void block_totals(u64& p, u64& q) {
@@ -569,28 +733,36 @@ class Sequence {
   // Draws the token of `row`; false (for all CTAs alike) if nothing has weight.
   SA_DEV bool draw(const Weights& w, const Scale& sc, int row, float u) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int v0, v1;
-    my_run(v0, v1);
-    const auto vector_weights = [&](int v, long long* m) {
+    const float d_least = least_difference(sc);
+    u64 own = 0;
+#pragma unroll 2
+    for (int v = v0_ + lane; v < v1_; v += 32) {
       float x[E::kVec], y[E::kVec];
-      load(x_, v, x);
-      if (w.minus_q) load(y_, v, y);
+      float2 r[E::kVec / 2];
+      const uint32_t heavy = load_both(v, w, x, y);
+      light_weights(v, heavy, x, y, w, d_least, sc, r);
+      own += __float2uint_rn(sum_of(r) * w.unit);
+      if (heavy != 0 && (listed_ ? sh_.listed > kList && !is_listed(v) : !enter(v, heavy))) {
 #pragma unroll
-      for (int e = 0; e < E::kVec; ++e) m[e] = weight(x[e], w.minus_q ? y[e] : 0.f, v * E::kVec + e, w, sc);
-    };
-    u64 own = 0, none = 0;
-#pragma unroll kUnroll
-    for (int v = v0 + lane; v < v1; v += 32) {
-      long long m[E::kVec];
-      vector_weights(v, m);
-#pragma unroll
-      for (int e = 0; e < E::kVec; ++e) own += m[e];
+        for (int e = 0; e < E::kVec; ++e)
+          if (heavy >> e & 1u) own += heavy_weight(x[e], w.minus_q ? y[e] : 0.f, v * E::kVec + e, w, sc);
+      }
     }
-    block_totals(own, none);
+    __syncthreads();
+    own = warp_sum(own);
+    if (lane == 0) sh_.warp_mass[warp] = own;
+    __syncthreads();
+    each_listed(w, [&](float x, float y, int index, int v) {
+      atomicAdd(&sh_.warp_mass[(v - static_cast<int>(rank_) * kWarps * run_) / run_],
+                static_cast<u64>(heavy_weight(x, y, index, w, sc)));
+    });
+    __syncthreads();
+    own = 0;
+    for (int i = 0; i < kWarps; ++i) own += sh_.warp_mass[i];
     u64 total = 0, before = 0;
-    unsigned r = 0;
+    unsigned rank = 0;
     exchange(own, 0, [&](u64 v, u64) {
-      if (r++ < rank_) before += v;
+      if (rank++ < rank_) before += v;
       total += v;
     });
     if (total == 0) return false;
@@ -599,36 +771,56 @@ class Sequence {
     if (target < before || target >= before + own) return true;  // another CTA has it
     for (int i = 0; i < warp; ++i) before += sh_.warp_mass[i];
     if (target < before || target >= before + sh_.warp_mass[warp]) return true;
-    for (int v = v0 + lane;; v += 32) {  // the warp that has it: some vector does
-      long long m[E::kVec];
+    for (int v = v0_ + lane;; v += 32) {  // the warp that has it: some vector does
+      float x[E::kVec], y[E::kVec];
+      float2 r[E::kVec / 2];
+      uint32_t heavy = 0;
       u64 mine = 0;
-      if (v < v1) {
-        vector_weights(v, m);
-#pragma unroll
-        for (int e = 0; e < E::kVec; ++e) mine += m[e];
+      if (v < v1_) {
+        heavy = load_both(v, w, x, y);
+        light_weights(v, heavy, x, y, w, d_least, sc, r);
+        mine = __float2uint_rn(sum_of(r) * w.unit);
+#pragma unroll 1
+        for (uint32_t bits = heavy; bits != 0; bits &= bits - 1) {
+          const int index = v * E::kVec + __ffs(bits) - 1;
+          mine += heavy_weight(E::one(x_[index]), w.minus_q ? E::one(y_[index]) : 0.f, index, w, sc);
+        }
       }
       u64 upto = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += y;
+        const u64 other = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += other;
       }
       u64 at = before + upto - mine;
       const bool here = target >= at && target < at + mine;
       if (here) {
-        int token = -1;
+        // the first whose own rounded mass passes it, or (rounding) the last with any
+        int token = -1, last = -1;
 #pragma unroll
         for (int e = 0; e < E::kVec; ++e) {
-          if (token < 0 && target < at + m[e]) token = v * E::kVec + e;
-          at += m[e];
+          const int index = v * E::kVec + e;
+          const float f = e & 1 ? r[e / 2].y : r[e / 2].x;
+          const u64 m = heavy >> e & 1u ? static_cast<u64>(heavy_weight(x[e], w.minus_q ? y[e] : 0.f, index, w, sc))
+                                        : __float2uint_rn(f * w.unit);
+          if (token < 0 && target < at + m) token = index;
+          if (m > 0 || f > 0.f) last = index;
+          at += m;
         }
+        if (token < 0) token = last;
         a_.tokens[row] = token;
         a_.logp[row] = log_share(E::one(x_[token]), w.p, sc);
       }
       before += __shfl_sync(0xffffffffu, upto, 31);
-      if (__any_sync(0xffffffffu, here) || v - lane >= v1) break;
+      if (__any_sync(0xffffffffu, here) || v - lane >= v1_) break;
     }
     return true;
+  }
+  SA_DEV bool is_listed(int v) const {
+    const uint32_t in_run = static_cast<uint32_t>(v - static_cast<int>(rank_) * kWarps * run_);
+    for (int i = 0; i < kList; ++i)
+      if (sh_.list[i] >> 8 == in_run) return true;
+    return false;
   }
 
   Shared& sh_;
@@ -637,6 +829,8 @@ class Sequence {
   int slices_;
   unsigned rank_, ctas_;
   int parity_ = 0;
+  int run_ = 0, v0_ = 0, v1_ = 0;  // vectors of a warp, and the warp's
+  bool listed_ = false;            // the vectors with heavy logits are in the list
   const T* x_ = nullptr;
   const T* y_ = nullptr;
 };
@@ -661,8 +855,8 @@ int slices_for(int vocab) {
 template <int kType>
 cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
   const int slices = slices_for<kType>(a.vocab);
-  if (a.rows > 0)
-    verify_rows_kernel<kType><<<static_cast<unsigned>(2LL * a.rows * slices), kStatThreads, 0, s>>>(a, slices);
+  const long long items = a.rows + (a.draft_logits != nullptr ? a.num_drafts : 0);
+  if (items > 0) verify_rows_kernel<kType><<<static_cast<unsigned>(items * slices), kStatThreads, 0, s>>>(a, slices);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   int ctas = 1;
@@ -684,7 +878,7 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
 
 size_t verify_workspace_bytes(int dtype, int rows, int vocab) {
   const int slices = dtype == 0 ? slices_for<0>(vocab) : slices_for<1>(vocab);
-  return static_cast<size_t>(rows) * 2 * slices * sizeof(Part);
+  return static_cast<size_t>(rows) * 2 * slices * sizeof(float4);
 }
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
