@@ -200,8 +200,7 @@ template <int kType>
 __global__ void __launch_bounds__(kStatThreads, 4) verify_rows_kernel(const VerifyArgs a, int slices) {
   typedef Elem<kType> E;
   typedef typename E::T T;
-  __shared__ float red[kStatWarps];
-  __shared__ int red_i[kStatWarps];
+  __shared__ float4 red[kStatWarps];
   __shared__ int seq_sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int item = blockIdx.x / slices, slice = blockIdx.x - item * slices;
@@ -261,14 +260,11 @@ __global__ void __launch_bounds__(kStatThreads, 4) verify_rows_kernel(const Veri
 #pragma unroll
   for (int i = 0; i < kStatVecs; ++i) top = fmaxf(top, E::largest(w[i]));
   top = warp_max(top);
-  if (lane == 0) red[warp] = top;
   __syncthreads();
   const int b = seq_sh;
   if (b >= a.num_seqs) return;  // a row of no entry
   const Scale sc(a.temperature[b]);
   if (!sc.valid || (draft && sc.greedy)) return;
-#pragma unroll
-  for (int i = 0; i < kStatWarps; ++i) top = fmaxf(top, red[i]);
   const float sum = warp_sum(sum_powers<kType>(w, top, sc.hi));
   int arg = 0x7fffffff;
   if (sc.greedy) {
@@ -282,14 +278,22 @@ __global__ void __launch_bounds__(kStatThreads, 4) verify_rows_kernel(const Veri
     }
     arg = warp_min(arg);
   }
-  __syncthreads();
-  if (lane == 0) red[warp] = sum, red_i[warp] = arg;
+  if (lane == 0) red[warp] = make_float4(top, sum, __int_as_float(arg), 0.f);
   __syncthreads();
   if (tid != 0) return;
-  float total = 0.f;
+  float4 all = red[0];
 #pragma unroll
-  for (int i = 0; i < kStatWarps; ++i) total += red[i], arg = min(arg, red_i[i]);
-  a.parts[static_cast<int64_t>(item) * slices + slice] = make_float4(top, total, __int_as_float(arg), 0.f);
+  for (int i = 1; i < kStatWarps; ++i) all.x = fmaxf(all.x, red[i].x);
+  all.y = 0.f;
+  arg = 0x7fffffff;
+#pragma unroll
+  for (int i = 0; i < kStatWarps; ++i) {
+    const float4 f = red[i];
+    all.y += f.y * ex2((f.x - all.x) * sc.hi);
+    if (f.x == all.x) arg = min(arg, __float_as_int(f.z));
+  }
+  all.z = __int_as_float(arg);
+  a.parts[static_cast<int64_t>(item) * slices + slice] = all;
 }
 
 // ---------------------------------------------------------------- exponentials
@@ -353,6 +357,7 @@ SA_DEV long long to_units(Pair e, float unit) { return __float2ll_rn(e.hi * unit
 
 // ---------------------------------------------------------------- a sequence
 constexpr int kThreads = 512;
+constexpr int kPerSm = 2;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kHeavyLog2 = 12;  // masses from 2^-12 of the whole on are heavy
@@ -769,14 +774,17 @@ class Sequence {
     // floor(total u), below total
     const u64 target = __umul64hi(total << 4, static_cast<u64>(u * 4294967296.f) << 28);
     if (target < before || target >= before + own) return true;  // another CTA has it
-    for (int i = 0; i < warp; ++i) before += sh_.warp_mass[i];
-    if (target < before || target >= before + sh_.warp_mass[warp]) return true;
-    for (int v = v0_ + lane;; v += 32) {  // the warp that has it: some vector does
+    // the warp's run that holds it, a vector to each thread
+    int holder = 0;
+    while (target >= before + sh_.warp_mass[holder]) before += sh_.warp_mass[holder++];
+    const int first = (static_cast<int>(rank_) * kWarps + holder) * run_;
+    const int last = min(first + run_, (a_.vocab + E::kVec - 1) / E::kVec);
+    for (int v = first + static_cast<int>(threadIdx.x);; v += kThreads) {  // some vector has it
       float x[E::kVec], y[E::kVec];
       float2 r[E::kVec / 2];
       uint32_t heavy = 0;
       u64 mine = 0;
-      if (v < v1_) {
+      if (v < last) {
         heavy = load_both(v, w, x, y);
         light_weights(v, heavy, x, y, w, d_least, sc, r);
         mine = __float2uint_rn(sum_of(r) * w.unit);
@@ -792,11 +800,17 @@ class Sequence {
         const u64 other = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += other;
       }
+      __syncthreads();  // the sums have been read
+      if (lane == 31) sh_.warp_mass_q[warp] = upto;
+      __syncthreads();
       u64 at = before + upto - mine;
-      const bool here = target >= at && target < at + mine;
-      if (here) {
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) at += sh_.warp_mass_q[i];
+        before += sh_.warp_mass_q[i];
+      }
+      if (target >= at && target < at + mine) {
         // the first whose own rounded mass passes it, or (rounding) the last with any
-        int token = -1, last = -1;
+        int token = -1, any = -1;
 #pragma unroll
         for (int e = 0; e < E::kVec; ++e) {
           const int index = v * E::kVec + e;
@@ -804,15 +818,14 @@ class Sequence {
           const u64 m = heavy >> e & 1u ? static_cast<u64>(heavy_weight(x[e], w.minus_q ? y[e] : 0.f, index, w, sc))
                                         : __float2uint_rn(f * w.unit);
           if (token < 0 && target < at + m) token = index;
-          if (m > 0 || f > 0.f) last = index;
+          if (m > 0 || f > 0.f) any = index;
           at += m;
         }
-        if (token < 0) token = last;
+        if (token < 0) token = any;
         a_.tokens[row] = token;
         a_.logp[row] = log_share(E::one(x_[token]), w.p, sc);
       }
-      before += __shfl_sync(0xffffffffu, upto, 31);
-      if (__any_sync(0xffffffffu, here) || v - lane >= v1_) break;
+      if (target < before || v - static_cast<int>(threadIdx.x) + kThreads >= last) break;
     }
     return true;
   }
@@ -836,7 +849,7 @@ class Sequence {
 };
 
 template <int kType>
-__global__ void __launch_bounds__(kThreads) verify_draw_kernel(const __grid_constant__ VerifyArgs a, int slices) {
+__global__ void __launch_bounds__(kThreads, kPerSm) verify_draw_kernel(const __grid_constant__ VerifyArgs a, int slices) {
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks();
@@ -859,8 +872,9 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
   if (items > 0) verify_rows_kernel<kType><<<static_cast<unsigned>(items * slices), kStatThreads, 0, s>>>(a, slices);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  // Enough CTAs for a sequence to be quick, not so many that the batch comes in several turns.
   int ctas = 1;
-  while (ctas < kMaxCluster && ctas * 8192 < a.vocab) ctas *= 2;
+  while (ctas < kMaxCluster && ctas * 8192 < a.vocab && 2LL * ctas * a.num_seqs <= device_sms() * kPerSm) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * ctas);
   cfg.blockDim = dim3(kThreads);
