@@ -97,13 +97,8 @@ SA_DEV float lg2(float x) {
 
 SA_DEV float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
 SA_DEV float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
-// v without its infinities and NaNs (0 in their place).
-SA_DEV uint32_t finite_bf16x2(uint32_t v) {
-  uint32_t r = v;
-  if ((v & 0x7f80u) == 0x7f80u) r &= 0xffff0000u;
-  if ((v & 0x7f800000u) == 0x7f800000u) r &= 0xffffu;
-  return r;
-}
+// Bits 15 and 31 are set where a half has an exponent of ones (an infinity or a NaN).
+SA_DEV uint32_t ones_exponent(uint32_t v) { return (v & 0x7fff7fffu) + 0x00800080u; }
 
 // A sequence of the call: its slot, length, and rows row0 .. row0 + n - 1 of q;
 // `rows` of a pair (query heads times rows of q) are computed.
@@ -430,6 +425,10 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
       }
     }
   }
+  // What a masked key holds must not reach a row that does not see it, and 0
+  // times an infinity or a NaN would: they are taken out of the product, and
+  // added to the rows that do see them.
+  bool odd = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     uint32_t a[4][4];
@@ -438,40 +437,25 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
       ldsm_x4_t(keys + kTurnHalf + (16 * u + row_v) * 128 + (((2 * i + chunk_v) ^ (lane & 7)) << 4), a[i][0], a[i][1],
                 a[i][2], a[i][3]);
     if (kMasked) {
-      // What a masked key holds must not reach a row that does not see it, and
-      // 0 times an infinity or a NaN would: they are taken out of the product
-      // and added to the rows that do see them.
-      const bool there = turn.loaded >> u & 1;
-      uint32_t odd = 0u;
+      if (!(turn.loaded >> u & 1)) {  // nothing to add
+#pragma unroll
+        for (int nt = 0; nt < HT; ++nt) {
+          // its keys count 0, or NaN for the rows that would see them
+          if (kSkip && kFirst + nt >= tiles) continue;
+          pf[u][nt][0] = pf[u][nt][1] = 0u;
+        }
+      }
+      uint32_t ones = 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          if (!there) a[i][m] = 0u;
-          odd |= (a[i][m] & 0x7fff7fffu) + 0x00800080u;  // an exponent of ones carries into the sign's place
-        }
-      if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0u)) {
+        for (int m = 0; m < 4; ++m) ones |= ones_exponent(a[i][m]);
+      if (__any_sync(0xffffffffu, (ones & 0x80008000u) != 0u)) {
+        odd = true;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int m = 0; m < 4; ++m) a[i][m] = finite_bf16x2(a[i][m]);
-#pragma unroll 1
-        for (int key = 0; key < 16; ++key) {
-          const uint32_t row = keys + kTurnHalf + (16 * u + key) * 128;
-          const int at = turn.key0 + 16 * u + key;
-#pragma unroll
-          for (int d = 0; d < 8; ++d) {  // dims 8 d + g: [d / 2][2 (d % 2) + e]
-            uint32_t two;
-            asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(two) : "r"(row + ((d ^ (key & 7)) << 4) + 2 * g));
-            const float v = bf16_lo(two);
-            if (!((two & 0x7f80u) == 0x7f80u)) continue;
-#pragma unroll
-            for (int nt = 0; nt < HT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (seen_bits(pos(kFirst + nt, e), at, window, prefix) & 1u) r.o[kFirst + nt][d >> 1][2 * (d & 1) + e] += v;
-          }
-        }
+          for (int m = 0; m < 4; ++m) a[i][m] &= ~((ones_exponent(a[i][m]) >> 15 & 0x00010001u) * 0xffffu);
       }
     }
 #pragma unroll
@@ -481,6 +465,29 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
         if (kSkip && kFirst + nt >= tiles) continue;
         mma16816(r.o[kFirst + nt][i], a[i], pf[u][nt][0], pf[u][nt][1]);
       }
+  }
+  if (kMasked && odd) {
+#pragma unroll 1
+    for (int key = 0; key < kTurn; ++key) {
+      if (!(turn.loaded >> (key >> 4) & 1)) continue;  // its rows are NaN by their scores
+      uint32_t sees = 0;
+#pragma unroll
+      for (int nt = 0; nt < HT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          sees |= (seen_bits(pos(kFirst + nt, e), turn.key0, window, prefix) >> key & 1u) << (2 * nt + e);
+      const uint32_t row = keys + kTurnHalf + key * 128;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {  // dims 8 d + g: [d / 2][2 (d % 2) + e]
+        uint32_t two;
+        asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(two) : "r"(row + ((d ^ (key & 7)) << 4) + 2 * g));
+        const float v = (two & 0x7f80u) == 0x7f80u ? bf16_lo(two) : 0.f;
+#pragma unroll
+        for (int nt = 0; nt < HT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) r.o[kFirst + nt][d >> 1][2 * (d & 1) + e] += sees >> (2 * nt + e) & 1u ? v : 0.f;
+      }
+    }
   }
 }
 
@@ -802,234 +809,222 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
         r.sum_o[nt].y += __shfl_xor_sync(0xffffffffu, r.sum_o[nt].y, o);
       }
   };
-  const auto segment_of = [&](int b, int head, long long x, int t0) {
+  // Alone, a warp takes pairs gridDim.x * kWarps apart, and meets no other warp
+  // from here on.  Else every head's turns make one line, in which the turns of
+  // each sequence stand behind `pad` places for what beginning a pair costs a
+  // CTA.  All heads' lines are cut alike, into equal shares, and neighbouring
+  // CTAs take the same share of neighbouring heads, which lie side by side in
+  // memory.  (More heads than CTAs: a line is not cut, and a CTA takes several.)
+  const int ctas = static_cast<int>(gridDim.x), heads_at_once = min(heads, ctas);
+  const int group = static_cast<int>(blockIdx.x) / heads_at_once;
+  int b_first = 0, head_first = static_cast<int>(blockIdx.x) - group * heads_at_once, pad = 0;
+  long long x_first = 0, x_begin = 0, x_end = 0;  // places in the line: of the first pair, and of the share
+  long long pair = static_cast<long long>(warp) * ctas + blockIdx.x;
+  Shares shares(1, 1);
+  if (alone) {
+    if (pair >= static_cast<long long>(p.num_seqs) * heads) return;
+    b_first = static_cast<int>(pair / heads);
+    head_first = static_cast<int>(pair - static_cast<long long>(b_first) * heads);
+  } else if constexpr (!kAlone) {
+    // a turn at least for every team, unless that leaves pairs without a worker of their own
+    const long long want = max((turns_all + kTeams - 1) / kTeams, static_cast<long long>(p.num_seqs));
+    const int n_workers = heads > ctas ? 1 : static_cast<int>(min(static_cast<long long>(ctas / heads_at_once), want));
+    pad = turns_all >= 4LL * kPairCost * n_workers ? kPairCost : 0;
+    shares = Shares(turns_all + static_cast<long long>(p.num_seqs) * pad, n_workers);
+    if (group >= n_workers) return;
+    x_begin = shares.start(group);
+    x_end = shares.start(group + 1);
+    int lo = 0, hi = (p.num_seqs - 1) / kUptoStep;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (upto[mid] + static_cast<long long>(mid) * kUptoStep * pad <= x_begin)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    b_first = lo * kUptoStep;
+    x_first = upto[lo] + static_cast<long long>(b_first) * pad;
+#pragma unroll 1
+    for (int i = 1; i < kUptoStep && b_first + 1 < p.num_seqs; ++i) {
+      const long long next = x_first + max(visible_span(p, sequence(p, b_first)).count(), 1) + pad;
+      if (next > x_begin) break;
+      x_first = next;
+      ++b_first;
+    }
+  }
+  // The worker's part of a pair that begins at x of the line.
+  const auto segment_at = [&](int b, int head, long long x) {
     Segment s;
     s.x = x;
     s.b = b;
     s.head = head;
-    s.t0 = t0;
     s.seq = sequence(p, b);
     s.span = visible_span(p, s.seq);
     s.turns = s.t1 = max(s.span.count(), 1);
+    s.t0 = 0;
+    if (!alone) {
+      s.t0 = static_cast<int>(max(x_begin - x - pad, 0LL));
+      s.t1 = static_cast<int>(min(static_cast<long long>(s.turns), x_end - x - pad));
+    }
     return s;
   };
 
-  if constexpr (kMayAlone) {
-    if (alone) {  // a warp meets no other one from here on
-      const long long pairs = static_cast<long long>(p.num_seqs) * heads;
-      const long long step = static_cast<long long>(gridDim.x) * kWarps;
-      long long pair = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
-      if (pair >= pairs) return;
-      const auto pair_at = [&](long long i) {
-        const int b = static_cast<int>(i / heads);
-        return segment_of(b, static_cast<int>(i - static_cast<long long>(b) * heads), 0, 0);
-      };
-      Segment seg = pair_at(pair);
-      stream.begin(seg);
-      while (true) {
-        process(seg);
-        const Segment done = seg;
-        pair += step;
-        if (pair < pairs) {  // on its way while this one is finished
-          seg = pair_at(pair);
-          stream.begin(seg);
-        }
-        finish_tiles<NT>(p, done.seq, done.head, done.seq.rows, r);
-        if (pair >= pairs) return;
-      }
-    }
-  }
-  if constexpr (!kAlone) {
-    // Every head's turns make one line, in which the turns of each sequence
-    // stand behind `pad` places for what beginning a pair costs a CTA.  All
-    // heads' lines are cut alike, into equal shares, and neighbouring CTAs take
-    // the same share of neighbouring heads, which lie side by side in memory.
-    // (More heads than CTAs: a line is not cut, and a CTA takes several.)
-    const int ctas = static_cast<int>(gridDim.x), lanes_of_heads = min(heads, ctas);
-    const int group = static_cast<int>(blockIdx.x) / lanes_of_heads, head0 = static_cast<int>(blockIdx.x) - group * lanes_of_heads;
-    // a turn at least for every team, unless that leaves pairs without a worker of their own
-    const long long want = max((turns_all + kTeams - 1) / kTeams, static_cast<long long>(p.num_seqs));
-    const int n_workers = heads > ctas ? 1 : static_cast<int>(min(static_cast<long long>(ctas / lanes_of_heads), want));
-    const int pad = turns_all >= 4LL * kPairCost * n_workers ? kPairCost : 0;
-    const Shares shares(turns_all + static_cast<long long>(p.num_seqs) * pad, n_workers);
-    if (group >= n_workers) return;
-    const long long x_begin = shares.start(group), x_end = shares.start(group + 1);
-    int b_first;  // the sequence that holds the share's first place
-    long long x_first;
-    {
-      int lo = 0, hi = (p.num_seqs - 1) / kUptoStep;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (upto[mid] + static_cast<long long>(mid) * kUptoStep * pad <= x_begin)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      b_first = lo * kUptoStep;
-      x_first = upto[lo] + static_cast<long long>(b_first) * pad;
-      for (int i = 1; i < kUptoStep && b_first + 1 < p.num_seqs; ++i) {
-        const long long next = x_first + max(visible_span(p, sequence(p, b_first)).count(), 1) + pad;
-        if (next > x_begin) break;
-        x_first = next;
-        ++b_first;
-      }
-    }
-    // The worker's part of a pair that begins at x of the line.
-    const auto segment_at = [&](int b, int head, long long x) {
-      Segment s = segment_of(b, head, x, static_cast<int>(max(x_begin - x - pad, 0LL)));
-      s.t1 = static_cast<int>(min(static_cast<long long>(s.turns), x_end - x - pad));
-      return s;
-    };
-    const int merge_row = min(tid / S::kPerRow, kRows), merge_dim = tid % S::kPerRow * kDims;  // kRows: none
-    int n_cuts = 0;
-    Segment seg = segment_at(b_first, head0, x_first);
-    stream.begin(seg);
-    while (true) {
-      if (S::kHalves > 1) {
-        // the pair's queries into shared memory, zeros behind the last row
-        const int rows = seg.seq.rows;
-        for (int u = tid; u < kRows * 8; u += kThreads) {
-          const int row = u >> 3, c = u & 7;
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          if (row < rows) {
-            const int i = p.row_of_seq(row), h = seg.head * p.group + row - i * p.group;
-            v = __ldg(reinterpret_cast<const uint4*>(p.q + ((static_cast<int64_t>(seg.seq.row0) + i) * p.hq + h) * kHeadDim) + c);
-          }
-          *reinterpret_cast<uint4*>(queries + swz(row, c)) = v;
-        }
-        __syncthreads();
-      }
-      process(seg);
-
-      // the next segment is on its way while this one is finished
-      const Segment done = seg;
+  const int merge_row = min(tid / S::kPerRow, kRows), merge_dim = tid % S::kPerRow * kDims;  // kRows: none
+  int n_cuts = 0;
+  Segment next = segment_at(b_first, head_first, x_first), done;
+  bool first = true, more = true;
+  while (true) {
+    if (more) stream.begin(next);  // on its way while the one before is finished
+    if (!first) {
       const int rows = done.seq.rows;
-      const long long x_next = done.x + done.turns + pad;
-      bool more = done.t1 == done.turns && done.b + 1 < p.num_seqs && x_next + pad < x_end;
-      if (more) {
-        seg = segment_at(done.b + 1, done.head, x_next);
-      } else if (done.head + ctas < heads) {  // more heads than CTAs
-        more = true;
-        seg = segment_at(b_first, done.head + ctas, x_first);
-      }
-      if (more) stream.begin(seg);
-
-      // A pair that is cut is published when the worker is through, with one
-      // fence and no copies in flight for it to wait for.
-      const bool whole = done.t0 == 0 && done.t1 == done.turns;
-      float* mine = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (done.x > x_begin ? 1 : 0)) * S::kPartFloats;
-      if (!whole) {
-        if (tid == 0) {
-          Cut c;
-          c.p0 = done.x;
-          c.c0 = shares.owner(done.x + pad);
-          c.c1 = shares.owner(done.x + pad + done.turns - 1);
-          c.b = done.b;
-          c.head = done.head;
-          cuts[n_cuts] = c;
+      if (kMayAlone && alone) {
+        finish_tiles<NT>(p, done.seq, done.head, rows, r);
+      } else if constexpr (!kAlone) {
+        // A pair that is cut is published when the worker is through, with one
+        // fence and no copies in flight for it to wait for.
+        const bool whole = done.t0 == 0 && done.t1 == done.turns;
+        float* mine = p.part + (2 * static_cast<int64_t>(blockIdx.x) + (done.x > x_begin ? 1 : 0)) * S::kPartFloats;
+        if (!whole) {
+          if (tid == 0) {
+            Cut c;
+            c.p0 = done.x;
+            c.c0 = shares.owner(done.x + pad);
+            c.c1 = shares.owner(done.x + pad + done.turns - 1);
+            c.b = done.b;
+            c.head = done.head;
+            cuts[n_cuts] = c;
+          }
+          ++n_cuts;
         }
-        ++n_cuts;
-      }
-
-      if constexpr (kSlots < kTeams) {
-        // the upper teams' results, lane for lane, to the lower ones
-        float* slot = acc_sh + ((team % kSlots) * kShare + share) * (NT * 16 * 32) + 4 * lane;
-        float4* stat = stat_sh + ((team % kSlots) * kShare + share) * (NT * 8);
-        if (team >= kSlots) {
+        if constexpr (kSlots < kTeams) {
+          // the upper teams' results, lane for lane, to the lower ones
+          float* slot = acc_sh + ((team % kSlots) * kShare + share) * (NT * 16 * 32) + 4 * lane;
+          float4* stat = stat_sh + ((team % kSlots) * kShare + share) * (NT * 8);
+          if (team >= kSlots) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<float4*>(slot + (nt * 4 + i) * 128) =
-                  make_float4(r.o[nt][i][0], r.o[nt][i][1], r.o[nt][i][2], r.o[nt][i][3]);
-            if (g == 0) {
-              stat[nt * 8 + 2 * t] = make_float4(r.ref[nt].x, r.sum[nt].x, r.sum_o[nt].x, 0.f);
-              stat[nt * 8 + 2 * t + 1] = make_float4(r.ref[nt].y, r.sum[nt].y, r.sum_o[nt].y, 0.f);
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(slot + (nt * 4 + i) * 128) =
+                    make_float4(r.o[nt][i][0], r.o[nt][i][1], r.o[nt][i][2], r.o[nt][i][3]);
+              if (g == 0) {
+                stat[nt * 8 + 2 * t] = make_float4(r.ref[nt].x, r.sum[nt].x, r.sum_o[nt].x, 0.f);
+                stat[nt * 8 + 2 * t + 1] = make_float4(r.ref[nt].y, r.sum[nt].y, r.sum_o[nt].y, 0.f);
+              }
             }
           }
+          __syncthreads();
+          if (team < kSlots) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float own[2], other[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float4 st = stat[nt * 8 + 2 * t + e];
+                float& ref = e ? r.ref[nt].y : r.ref[nt].x;
+                float& sum = e ? r.sum[nt].y : r.sum[nt].x;
+                float& sum_o = e ? r.sum_o[nt].y : r.sum_o[nt].x;
+                const float top = fmaxf(ref, st.x), unit = log2_ref(top, p.coef);
+                own[e] = weight_of(log2_ref(ref, p.coef), sum, unit);
+                other[e] = weight_of(log2_ref(st.x, p.coef), st.y, unit);
+                sum = own[e] * sum + other[e] * st.y;
+                sum_o = own[e] * sum_o + other[e] * st.z;
+                ref = top;
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 v = *reinterpret_cast<const float4*>(slot + (nt * 4 + i) * 128);
+                r.o[nt][i][0] = own[0] * r.o[nt][i][0] + other[0] * v.x;
+                r.o[nt][i][1] = own[1] * r.o[nt][i][1] + other[1] * v.y;
+                r.o[nt][i][2] = own[0] * r.o[nt][i][2] + other[0] * v.z;
+                r.o[nt][i][3] = own[1] * r.o[nt][i][3] + other[1] * v.w;
+              }
+            }
+          }
+          __syncthreads();
         }
-        __syncthreads();
         if (team < kSlots) {
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float own[2], other[2];
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float4 st = stat[nt * 8 + 2 * t + e];
-              float& ref = e ? r.ref[nt].y : r.ref[nt].x;
-              float& sum = e ? r.sum[nt].y : r.sum[nt].x;
-              float& sum_o = e ? r.sum_o[nt].y : r.sum_o[nt].x;
-              const float top = fmaxf(ref, st.x), unit = log2_ref(top, p.coef);
-              own[e] = weight_of(log2_ref(ref, p.coef), sum, unit);
-              other[e] = weight_of(log2_ref(st.x, p.coef), st.y, unit);
-              sum = own[e] * sum + other[e] * st.y;
-              sum_o = own[e] * sum_o + other[e] * st.z;
-              ref = top;
-            }
+              const int at = team * kRows + 8 * (nt * kShare + share) + 2 * t + e;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 v = *reinterpret_cast<const float4*>(slot + (nt * 4 + i) * 128);
-              r.o[nt][i][0] = own[0] * r.o[nt][i][0] + other[0] * v.x;
-              r.o[nt][i][1] = own[1] * r.o[nt][i][1] + other[1] * v.y;
-              r.o[nt][i][2] = own[0] * r.o[nt][i][2] + other[0] * v.z;
-              r.o[nt][i][3] = own[1] * r.o[nt][i][3] + other[1] * v.w;
+              for (int i = 0; i < 4; ++i) {
+                acc_sh[at * kRowPad + 16 * i + g] = r.o[nt][i][e];
+                acc_sh[at * kRowPad + 16 * i + g + 8] = r.o[nt][i][2 + e];
+              }
+              if (g == 0) {
+                stat_sh[at] = make_float4(log2_ref(e ? r.ref[nt].y : r.ref[nt].x, p.coef),
+                                          e ? r.sum[nt].y : r.sum[nt].x, e ? r.sum_o[nt].y : r.sum_o[nt].x, 0.f);
+              }
             }
-          }
         }
         __syncthreads();
-      }
-      if (team < kSlots) {
+        // thread: one row, kDims of its dims
+        Piece<kDims> f;
+        f.sum = f.sum_o = 0.f;
+        f.ref = -INFINITY;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int d = 0; d < kDims; ++d) f.acc[d] = 0.f;
+        const int row_sh = min(merge_row, kRows - 1);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int at = team * kRows + 8 * (nt * kShare + share) + 2 * t + e;
+        for (int w = 0; w < kSlots; ++w) f.ref = fmaxf(f.ref, stat_sh[w * kRows + row_sh].x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              acc_sh[at * kRowPad + 16 * i + g] = r.o[nt][i][e];
-              acc_sh[at * kRowPad + 16 * i + g + 8] = r.o[nt][i][2 + e];
-            }
-            if (g == 0) {
-              stat_sh[at] = make_float4(log2_ref(e ? r.ref[nt].y : r.ref[nt].x, p.coef), e ? r.sum[nt].y : r.sum[nt].x,
-                                        e ? r.sum_o[nt].y : r.sum_o[nt].x, 0.f);
-            }
+        for (int w = 0; w < kSlots; ++w) {
+          const float4 st = stat_sh[w * kRows + row_sh];
+          const float m = weight_of(st.x, st.y, f.ref);
+          f.sum += m * st.y;
+          f.sum_o += m * st.z;
+#pragma unroll
+          for (int d = 0; d < kDims; d += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(acc_sh + (w * kRows + row_sh) * kRowPad + merge_dim + d);
+            f.acc[d] += m * v.x;
+            f.acc[d + 1] += m * v.y;
+            f.acc[d + 2] += m * v.z;
+            f.acc[d + 3] += m * v.w;
           }
-      }
-      __syncthreads();
-      // thread: one row, kDims of its dims
-      Piece<kDims> f;
-      f.sum = f.sum_o = 0.f;
-      f.ref = -INFINITY;
-#pragma unroll
-      for (int d = 0; d < kDims; ++d) f.acc[d] = 0.f;
-      const int row_sh = min(merge_row, kRows - 1);
-#pragma unroll
-      for (int w = 0; w < kSlots; ++w) f.ref = fmaxf(f.ref, stat_sh[w * kRows + row_sh].x);
-#pragma unroll
-      for (int w = 0; w < kSlots; ++w) {
-        const float4 st = stat_sh[w * kRows + row_sh];
-        const float m = weight_of(st.x, st.y, f.ref);
-        f.sum += m * st.y;
-        f.sum_o += m * st.z;
-#pragma unroll
-        for (int d = 0; d < kDims; d += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(acc_sh + (w * kRows + row_sh) * kRowPad + merge_dim + d);
-          f.acc[d] += m * v.x;
-          f.acc[d + 1] += m * v.y;
-          f.acc[d + 2] += m * v.z;
-          f.acc[d + 3] += m * v.w;
         }
-      }
-      if (merge_row < rows) {
-        if (whole)
-          finish_row<kDims>(p, done.seq, done.head, merge_row, merge_dim, f);
-        else
-          put_piece<kRows, kDims>(mine, merge_row, merge_dim, f);
+        if (merge_row < rows) {
+          if (whole)
+            finish_row<kDims>(p, done.seq, done.head, merge_row, merge_dim, f);
+          else
+            put_piece<kRows, kDims>(mine, merge_row, merge_dim, f);
+        }
+        if (more) __syncthreads();  // the merge area is free again, and the queries
       }
       if (!more) break;
-      __syncthreads();  // the merge area is free again, and the queries
     }
+    done = next;
+    first = false;
+    if (S::kHalves > 1) {
+      // the pair's queries into shared memory, zeros behind the last row
+      for (int u = tid; u < kRows * 8; u += kThreads) {
+        const int row = u >> 3, c = u & 7;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (row < done.seq.rows) {
+          const int i = p.row_of_seq(row), h = done.head * p.group + row - i * p.group;
+          v = __ldg(reinterpret_cast<const uint4*>(p.q + ((static_cast<int64_t>(done.seq.row0) + i) * p.hq + h) * kHeadDim) + c);
+        }
+        *reinterpret_cast<uint4*>(queries + swz(row, c)) = v;
+      }
+      __syncthreads();
+    }
+    process(done);
+    if (alone) {
+      pair += static_cast<long long>(ctas) * kWarps;
+      more = pair < static_cast<long long>(p.num_seqs) * heads;
+      const int b = more ? static_cast<int>(pair / heads) : 0;
+      if (more) next = segment_at(b, static_cast<int>(pair - static_cast<long long>(b) * heads), 0);
+    } else {
+      const long long x = done.x + done.turns + pad;
+      const bool on = done.t1 == done.turns && done.b + 1 < p.num_seqs && x + pad < x_end;
+      more = on || done.head + ctas < heads;  // more heads than CTAs
+      if (more) next = segment_at(on ? done.b + 1 : b_first, on ? done.head : done.head + ctas, on ? x : x_first);
+    }
+  }
 
+  if constexpr (!kAlone) {
     if (n_cuts == 0) return;
     const auto arrive = [&](const Cut& c) {  // by one thread, after a barrier: is this worker the pair's last?
       int* counter = p.counters + static_cast<int64_t>(c.b) * heads + c.head;
@@ -1048,6 +1043,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
     __syncthreads();
     if (tid < n_cuts) last_sh[tid] = arrive(cuts[tid]);
     __syncthreads();
+#pragma unroll 1
     for (int i = 0; i < n_cuts; ++i) {
       if (!last_sh[i]) continue;
       const Cut c = cuts[i];

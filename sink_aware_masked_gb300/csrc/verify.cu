@@ -150,19 +150,26 @@ struct Rows {
 // ---------------------------------------------------------------- all rows
 constexpr int kStatThreads = 256;
 constexpr int kStatWarps = kStatThreads / 32;
-constexpr int kStatVecs = 8;  // 16-byte vectors a thread holds
+constexpr int kStatVecs = 8;       // 16-byte vectors that a thread has in flight
+constexpr int kStatMostVecs = 32;  // vectors of a thread, at most about (more slices where rows are few)
 
-template <int kType>
-__host__ __device__ constexpr int slice_logits() {
-  return kStatThreads * kStatVecs * Elem<kType>::kVec;
-}
+// A thread's running sum of 2^((x - top) scale).
+struct Running {
+  float top, sum;
+};
 
-// Sum of 2^((x - top) scale) over the vectors a thread holds.
+// Adds the vectors a thread holds.
 template <int kType>
-SA_DEV float sum_powers(const uint4 (&w)[kStatVecs], float top, float scale) {
+SA_DEV void add_powers(Running& r, const uint4 (&w)[kStatVecs], float scale) {
   typedef Elem<kType> E;
+  float top = r.top;
+#pragma unroll
+  for (int i = 0; i < kStatVecs; ++i) top = fmaxf(top, E::largest(w[i]));
+  const float by = (r.top - top) * scale;
+  r.sum *= ex2(by);
+  r.top = top;
   float2 sum = make_float2(0.f, 0.f);
-  const float2 by = make_float2(scale, scale);
+  const float2 s2 = make_float2(scale, scale);
   const float ref = top * scale;
   if (fabsf(ref) < 1048576.f) {
     // one fused x scale - ref, put right at the end for what ref was rounded by
@@ -173,11 +180,12 @@ SA_DEV float sum_powers(const uint4 (&w)[kStatVecs], float top, float scale) {
       E::unpack(w[i], f);
 #pragma unroll
       for (int e = 0; e < E::kVec; e += 2) {
-        const float2 t = ffma2(make_float2(f[e], f[e + 1]), by, minus);
+        const float2 t = ffma2(make_float2(f[e], f[e + 1]), s2, minus);
         sum = fadd2(sum, make_float2(ex2(t.x), ex2(t.y)));
       }
     }
-    return (sum.x + sum.y) * ex2(-fmaf(top, scale, -ref));
+    r.sum += (sum.x + sum.y) * ex2(-fmaf(top, scale, -ref));
+    return;
   }
   // where ref's rounding would swamp the exponent the difference comes first
   const float2 minus = make_float2(-top, -top);
@@ -187,17 +195,18 @@ SA_DEV float sum_powers(const uint4 (&w)[kStatVecs], float top, float scale) {
     E::unpack(w[i], f);
 #pragma unroll
     for (int e = 0; e < E::kVec; e += 2) {
-      const float2 t = fmul2(fadd2(make_float2(f[e], f[e + 1]), minus), by);
+      const float2 t = fmul2(fadd2(make_float2(f[e], f[e + 1]), minus), s2);
       sum = fadd2(sum, make_float2(ex2(t.x), ex2(t.y)));
     }
   }
-  return sum.x + sum.y;
+  r.sum += sum.x + sum.y;
 }
 
-// CTA: slice `slice` of target row or draft `index`.  The row is on its way
-// while the first warp finds the sequence that it belongs to.
+// CTA: slice `slice` (`turns` x kStatThreads vectors) of target row or draft
+// `index`.  The row is on its way while the first warp finds the sequence that
+// it belongs to.
 template <int kType>
-__global__ void __launch_bounds__(kStatThreads, 4) verify_rows_kernel(const VerifyArgs a, int slices) {
+__global__ void __launch_bounds__(kStatThreads, 3) verify_rows_kernel(const VerifyArgs a, int slices, int turns) {
   typedef Elem<kType> E;
   typedef typename E::T T;
   __shared__ float4 red[kStatWarps];
@@ -212,27 +221,33 @@ __global__ void __launch_bounds__(kStatThreads, 4) verify_rows_kernel(const Veri
   // 16-byte vectors as they are aligned in memory, what is outside the row -inf
   const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) / sizeof(T)) % E::kVec);
   const T* base = x - shift;
-  const int end = shift + a.vocab;
-  const int v0 = slice * kStatThreads * kStatVecs;
-  uint4 w[kStatVecs];
+  const int end = shift + a.vocab, whole0 = shift > 0, whole1 = end / E::kVec;  // vectors that are whole
+  const int v0 = slice * turns * kStatThreads, v1 = min(v0 + turns * kStatThreads, (end + E::kVec - 1) / E::kVec);
+  const auto load = [&](int v) {
+    union {
+      uint4 q;
+      T t[E::kVec];
+    } part;
+    if (v >= whole0 && v < min(whole1, v1)) return __ldg(reinterpret_cast<const uint4*>(base) + v);
 #pragma unroll
-  for (int i = 0; i < kStatVecs; ++i) {
-    const int v = v0 + i * kStatThreads + tid;
-    if (v * E::kVec >= shift && (v + 1) * E::kVec <= end) {
-      w[i] = __ldg(reinterpret_cast<const uint4*>(base) + v);
-    } else {
-      union {
-        uint4 q;
-        T t[E::kVec];
-      } part;
-#pragma unroll
-      for (int e = 0; e < E::kVec; ++e) {
-        const int at = v * E::kVec + e;
-        part.t[e] = at >= shift && at < end ? base[at] : E::lowest();
-      }
-      w[i] = part.q;
+    for (int e = 0; e < E::kVec; ++e) {
+      const int at = v * E::kVec + e;
+      part.t[e] = v < v1 && at >= shift && at < end ? base[at] : E::lowest();
     }
-  }
+    return part.q;
+  };
+  const auto load_some = [&](int v, uint4 (&w)[kStatVecs]) {
+    if (v - tid >= whole0 && v - tid + kStatVecs * kStatThreads <= min(whole1, v1)) {
+      const uint4* from = reinterpret_cast<const uint4*>(base) + v;
+#pragma unroll
+      for (int i = 0; i < kStatVecs; ++i) w[i] = __ldg(from + i * kStatThreads);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kStatVecs; ++i) w[i] = load(v + i * kStatThreads);
+    }
+  };
+  uint4 w[kStatVecs];
+  load_some(v0 + tid, w);
   if (warp == 0) {
     // the sequences that end at or before the row, or (one draft fewer than rows each) before the draft
     const int first = a.cu[0];
@@ -256,28 +271,34 @@ __global__ void __launch_bounds__(kStatThreads, 4) verify_rows_kernel(const Veri
     if (!draft && index < first) seqs = a.num_seqs;
     if (lane == 0) seq_sh = seqs;
   }
-  float top = kLowest;
-#pragma unroll
-  for (int i = 0; i < kStatVecs; ++i) top = fmaxf(top, E::largest(w[i]));
-  top = warp_max(top);
   __syncthreads();
   const int b = seq_sh;
   if (b >= a.num_seqs) return;  // a row of no entry
   const Scale sc(a.temperature[b]);
   if (!sc.valid || (draft && sc.greedy)) return;
-  const float sum = warp_sum(sum_powers<kType>(w, top, sc.hi));
+  Running r{kLowest, 0.f};
   int arg = 0x7fffffff;
-  if (sc.greedy) {
+  for (int v = v0 + tid;;) {
+    const float before = r.top;
+    add_powers<kType>(r, w, sc.hi);
+    if (sc.greedy && (r.top > before || arg == 0x7fffffff)) {  // the first of the largest so far
+      arg = 0x7fffffff;
 #pragma unroll
-    for (int i = kStatVecs - 1; i >= 0; --i) {
-      float f[E::kVec];
-      E::unpack(w[i], f);
+      for (int i = kStatVecs - 1; i >= 0; --i) {
+        float f[E::kVec];
+        E::unpack(w[i], f);
 #pragma unroll
-      for (int e = E::kVec - 1; e >= 0; --e)
-        if (f[e] == top) arg = (v0 + i * kStatThreads + tid) * E::kVec + e - shift;
+        for (int e = E::kVec - 1; e >= 0; --e)
+          if (f[e] == r.top) arg = (v + i * kStatThreads) * E::kVec + e - shift;
+      }
     }
-    arg = warp_min(arg);
+    v += kStatVecs * kStatThreads;
+    if (v - tid >= v1) break;
+    load_some(v, w);
   }
+  const float top = warp_max(r.top);
+  const float sum = warp_sum(r.sum * ex2((r.top - top) * sc.hi));
+  if (sc.greedy) arg = warp_min(r.top == top ? arg : 0x7fffffff);
   if (lane == 0) red[warp] = make_float4(top, sum, __int_as_float(arg), 0.f);
   __syncthreads();
   if (tid != 0) return;
@@ -371,11 +392,19 @@ struct RowStat {
   SA_DEV bool bad() const { return !(sum >= 0.f) || sum > 3e38f; }
 };
 
+// Of a run of tokens: what they weigh with the near ratio, and what that loses
+// for each unit that the ratio is more; the sums of both rows' masses.
+struct Sums {
+  u64 weight, p, q, slope;
+};
+
 struct Shared {
-  u64 exchange[2][kMaxCluster][2];
-  u64 warp_mass[kWarps], warp_mass_q[kWarps];
+  Sums exchange[2][kMaxCluster];
+  Sums warp[kWarps];
+  u64 weight[kWarps];  // the warps' runs' weights
   int count[kWarps];
-  int first, listed;
+  u64 scan[kWarps];
+  int first, listed, found, spare;
   uint32_t list[kList];  // vector in the CTA's run << 8 | its heavy logits, a bit each
 };
 
@@ -473,14 +502,14 @@ class Sequence {
       w.q = q;
       w.minus_q = true;
       w.heavy_q = heavy_from(q, sc);
+      w.near = __fdiv_rn(p.sum, q.sum);
+      w.ratio = {w.near, 0.f};
       y_ = static_cast<const T*>(a_.draft_logits) + static_cast<int64_t>(draft0 + j) * a_.draft_stride;
-      sum_ratio(w, sc);
     }
     if (!draw(w, sc, row, unit_of(a_.u[row0 + n - 1]))) {
-      // nothing is left of w: the target's own probabilities (and the list holds what was heavy in q too)
+      // nothing is left of w: the target's own probabilities
       w.minus_q = false;
       w.without = -1;
-      listed_ = false;
       __syncthreads();
       if (tid == 0) sh_.listed = 0;
       __syncthreads();
@@ -493,7 +522,8 @@ class Sequence {
     RowStat p, q;
     float unit;            // masses are e times unit
     float heavy, heavy_q;  // logits from which a mass is heavy
-    Pair ratio;            // of the sums: p - q is e_p - ratio e_q, but for a factor
+    float near;            // about the ratio of the sums: p - q is e_p - ratio e_q, but for a factor
+    Pair ratio;            // the same as exactly as the sums are known
     int without;           // the draft that is taken out, or -1
     bool minus_q;
   };
@@ -540,22 +570,18 @@ class Sequence {
     a_.logp[row] = logp;
   }
 
-  // Every CTA of the cluster gives two numbers and takes all of them in rank order.
+  // Every CTA of the cluster gives its sums and takes all of them in rank order.
   template <class F>
-  SA_DEV void exchange(u64 v, u64 w, F take) {
+  SA_DEV void exchange(const Sums& own, F take) {
     if (ctas_ == 1) {
-      take(v, w);
+      take(own);
       return;
     }
-    u64 (*buf)[2] = sh_.exchange[parity_];
+    Sums* buf = sh_.exchange[parity_];
     parity_ ^= 1;  // the other half may still be read by a slower CTA
-    if (threadIdx.x < ctas_) {
-      u64* to = cluster_.map_shared_rank(&buf[0][0], threadIdx.x) + 2 * rank_;
-      to[0] = v;
-      to[1] = w;
-    }
+    if (threadIdx.x < ctas_) cluster_.map_shared_rank(buf, threadIdx.x)[rank_] = own;
     cluster_.sync();
-    for (unsigned r = 0; r < ctas_; ++r) take(buf[r][0], buf[r][1]);
+    for (unsigned r = 0; r < ctas_; ++r) take(buf[r]);
   }
 
   // The vectors of a row (counted from its first logit) that the warp has, one run of them.
@@ -598,14 +624,16 @@ class Sequence {
   }
   static SA_DEV float least_difference(const Scale& sc) { return fmaxf(__fdiv_rn(-150.f, sc.hi), -3e38f); }
 
+  // e_p - ratio e_q in units, 0 at least.
+  static SA_DEV long long difference(Pair p, Pair q, Pair ratio, float unit) {
+    const float c = __fmul_rn(q.hi, ratio.hi), c_lo = fmaf(q.hi, ratio.hi, -c) + fmaf(q.hi, ratio.lo, q.lo * ratio.hi);
+    return max(to_units(p, unit) - to_units({c, c_lo}, unit), 0LL);
+  }
   // What a token weighs, in units, where its mass is heavy.
   SA_DEV long long heavy_weight(float x, float y, int index, const Weights& w, const Scale& sc) const {
     if (index == w.without) return 0;
     const Pair p = power_pair(exponent(x, w.p.top, sc));
-    if (!w.minus_q) return to_units(p, w.unit);
-    const Pair q = power_pair(exponent(y, w.q.top, sc));
-    const float c = __fmul_rn(q.hi, w.ratio.hi), c_lo = fmaf(q.hi, w.ratio.hi, -c) + fmaf(q.hi, w.ratio.lo, q.lo * w.ratio.hi);
-    return max(to_units(p, w.unit) - to_units({c, c_lo}, w.unit), 0LL);
+    return w.minus_q ? difference(p, power_pair(exponent(y, w.q.top, sc)), w.ratio, w.unit) : to_units(p, w.unit);
   }
   // A vector's logits, and which of them are heavy, a bit each.
   SA_DEV uint32_t load_both(int v, const Weights& w, float (&x)[E::kVec], float (&y)[E::kVec]) const {
@@ -629,23 +657,32 @@ class Sequence {
     for (int e = 2; e < E::kVec; e += 2) m = fmax3(m, x[e], x[e + 1]);
     return m;
   }
-  // What the logits of a vector weigh that are not heavy, before the unit.
+  // What the logits of a vector weigh that are not heavy, before the unit, with
+  // the ratio w.near + more.  kSums: also adds to the rows' masses and the slope.
+  template <bool kSums>
   SA_DEV void light_weights(int v, uint32_t heavy, const float (&x)[E::kVec], const float (&y)[E::kVec], const Weights& w,
-                            float d_least, const Scale& sc, float2 (&r)[E::kVec / 2]) const {
+                            float more, float d_least, const Scale& sc, float2 (&r)[E::kVec / 2], float2& p, float2& q,
+                            float2& slope) const {
+    const float2 near = make_float2(-w.near, -w.near), rest = make_float2(-more, -more);
 #pragma unroll
     for (int e = 0; e < E::kVec; e += 2) {
       float2 m = light(x[e], x[e + 1], w.p.top, d_least, sc);
       if (w.minus_q) {
-        const float2 q = light(y[e], y[e + 1], w.q.top, d_least, sc), n = make_float2(-q.x, -q.y);
-        m = ffma2(n, make_float2(w.ratio.lo, w.ratio.lo), ffma2(n, make_float2(w.ratio.hi, w.ratio.hi), m));
+        float2 n = light(y[e], y[e + 1], w.q.top, d_least, sc);
+        if (heavy >> e & 3u) {
+          if (heavy >> e & 1u) m.x = n.x = 0.f;
+          if (heavy >> e & 2u) m.y = n.y = 0.f;
+        }
+        if constexpr (kSums) p = fadd2(p, m), q = fadd2(q, n);
+        m = ffma2(n, near, m);
+        if constexpr (!kSums) m = ffma2(n, rest, m);
+        if constexpr (kSums) slope = fadd2(slope, make_float2(m.x > 0.f ? n.x : 0.f, m.y > 0.f ? n.y : 0.f));
         m = make_float2(fmaxf(m.x, 0.f), fmaxf(m.y, 0.f));
+      } else if (heavy >> e & 3u) {
+        if (heavy >> e & 1u) m.x = 0.f;
+        if (heavy >> e & 2u) m.y = 0.f;
       }
       r[e / 2] = m;
-    }
-    if (heavy != 0) {
-#pragma unroll
-      for (int e = 0; e < E::kVec; e += 2)
-        r[e / 2] = make_float2(heavy >> e & 1u ? 0.f : r[e / 2].x, heavy >> (e + 1) & 1u ? 0.f : r[e / 2].y);
     }
     if (w.without >= v * E::kVec && w.without < (v + 1) * E::kVec) {
 #pragma unroll
@@ -681,119 +718,132 @@ class Sequence {
     return true;
   }
 
-  // The ratio of the two rows' sums.
-  SA_DEV void sum_ratio(Weights& w, const Scale& sc) {
-    const float unit_q = unit_for(w.q.sum), d_least = least_difference(sc);
-    u64 p = 0, q = 0;
-    const auto add_heavy = [&](float x, float y) {
-      p += to_units(power_pair(exponent(x, w.p.top, sc)), w.unit);
-      q += to_units(power_pair(exponent(y, w.q.top, sc)), unit_q);
-    };
-#pragma unroll 2
-    for (int v = v0_ + (threadIdx.x & 31); v < v1_; v += 32) {
-      float x[E::kVec], y[E::kVec];
-      const uint32_t heavy = load_both(v, w, x, y);
-      float2 sp = make_float2(0.f, 0.f), sq = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int e = 0; e < E::kVec; e += 2) {
-        float2 ep = light(x[e], x[e + 1], w.p.top, d_least, sc), eq = light(y[e], y[e + 1], w.q.top, d_least, sc);
-        if (heavy >> e & 3u) {
-          if (heavy >> e & 1u) ep.x = eq.x = 0.f;
-          if (heavy >> e & 2u) ep.y = eq.y = 0.f;
-        }
-        sp = fadd2(sp, ep);
-        sq = fadd2(sq, eq);
-      }
-      p += __float2uint_rn((sp.x + sp.y) * w.unit);
-      q += __float2uint_rn((sq.x + sq.y) * unit_q);
-      if (heavy != 0 && !enter(v, heavy)) {
-#pragma unroll
-        for (int e = 0; e < E::kVec; ++e)
-          if (heavy >> e & 1u) add_heavy(x[e], y[e]);
-      }
-    }
-    __syncthreads();
-    each_listed(w, [&](float x, float y, int, int) { add_heavy(x, y); });
-    block_totals(p, q);
-    u64 all_p = 0, all_q = 0;
-    exchange(p, q, [&](u64 a, u64 b) { all_p += a, all_q += b; });
-    const Pair a = to_pair(all_p), b = to_pair(all_q);
-    const float hi = __fdiv_rn(a.hi, b.hi);
-    const float lo = __fdiv_rn(fmaf(-hi, b.hi, a.hi) + fmaf(-hi, b.lo, a.lo), b.hi);
-    const float scale = __fdiv_rn(unit_q, w.unit);  // a power of two
-    w.ratio = {hi * scale, lo * scale};
-    listed_ = true;
-  }
-  // Sums over the CTA, the same in all threads; the warps' own stay in sh_.warp_mass.
-  SA_DEV void block_totals(u64& p, u64& q) {
-    __syncthreads();
-    p = warp_sum(p);
-    q = warp_sum(q);
-    if ((threadIdx.x & 31) == 0) sh_.warp_mass[threadIdx.x >> 5] = p, sh_.warp_mass_q[threadIdx.x >> 5] = q;
-    __syncthreads();
-    p = q = 0;
-    for (int i = 0; i < kWarps; ++i) p += sh_.warp_mass[i], q += sh_.warp_mass_q[i];
-  }
-
   // Draws the token of `row`; false (for all CTAs alike) if nothing has weight.
-  SA_DEV bool draw(const Weights& w, const Scale& sc, int row, float u) {
+  // One pass over the run: weights with the ratio that the first launch's sums
+  // give, which is off by some 2^-22, and the rows' masses, which give the ratio
+  // as exactly as the draw needs it.  The weights change by the slope then (the
+  // few that get or lose their sign between are below the square of that).
+  SA_DEV bool draw(Weights& w, const Scale& sc, int row, float u) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float d_least = least_difference(sc);
-    u64 own = 0;
+    const float d_least = least_difference(sc), unit_q = w.minus_q ? unit_for(w.q.sum) : 0.f;
+    Sums own{0, 0, 0, 0};
+    const auto add_heavy = [&](Sums& to, float x, float y, int index) {
+      if (!w.minus_q) {
+        to.weight += heavy_weight(x, y, index, w, sc);
+        return;
+      }
+      const Pair p = power_pair(exponent(x, w.p.top, sc)), q = power_pair(exponent(y, w.q.top, sc));
+      const long long m = difference(p, q, {w.near, 0.f}, w.unit);
+      to.weight += m;
+      to.p += to_units(p, w.unit);
+      to.q += to_units(q, unit_q);
+      if (m > 0) to.slope += to_units(q, unit_q);
+    };
 #pragma unroll 2
     for (int v = v0_ + lane; v < v1_; v += 32) {
       float x[E::kVec], y[E::kVec];
-      float2 r[E::kVec / 2];
+      float2 r[E::kVec / 2], p = make_float2(0.f, 0.f), q = p, slope = p;
       const uint32_t heavy = load_both(v, w, x, y);
-      light_weights(v, heavy, x, y, w, d_least, sc, r);
-      own += __float2uint_rn(sum_of(r) * w.unit);
-      if (heavy != 0 && (listed_ ? sh_.listed > kList && !is_listed(v) : !enter(v, heavy))) {
+      light_weights<true>(v, heavy, x, y, w, 0.f, d_least, sc, r, p, q, slope);
+      own.weight += __float2uint_rn(sum_of(r) * w.unit);
+      if (w.minus_q) {
+        own.p += __float2uint_rn((p.x + p.y) * w.unit);
+        own.q += __float2uint_rn((q.x + q.y) * unit_q);
+        own.slope += __float2uint_rn((slope.x + slope.y) * unit_q);
+      }
+      if (heavy != 0 && !enter(v, heavy)) {
 #pragma unroll
         for (int e = 0; e < E::kVec; ++e)
-          if (heavy >> e & 1u) own += heavy_weight(x[e], w.minus_q ? y[e] : 0.f, v * E::kVec + e, w, sc);
+          if (heavy >> e & 1u) add_heavy(own, x[e], w.minus_q ? y[e] : 0.f, v * E::kVec + e);
       }
     }
-    __syncthreads();
-    own = warp_sum(own);
-    if (lane == 0) sh_.warp_mass[warp] = own;
+    own.weight = warp_sum(own.weight);
+    if (w.minus_q) {
+      own.p = warp_sum(own.p);
+      own.q = warp_sum(own.q);
+      own.slope = warp_sum(own.slope);
+    }
+    if (lane == 0) sh_.warp[warp] = own;
     __syncthreads();
     each_listed(w, [&](float x, float y, int index, int v) {
-      atomicAdd(&sh_.warp_mass[(v - static_cast<int>(rank_) * kWarps * run_) / run_],
-                static_cast<u64>(heavy_weight(x, y, index, w, sc)));
+      Sums one{0, 0, 0, 0};
+      add_heavy(one, x, y, index);
+      Sums& to = sh_.warp[(v - static_cast<int>(rank_) * kWarps * run_) / run_];
+      atomicAdd(&to.weight, one.weight);
+      if (w.minus_q) {
+        atomicAdd(&to.p, one.p);
+        atomicAdd(&to.q, one.q);
+        atomicAdd(&to.slope, one.slope);
+      }
     });
     __syncthreads();
-    own = 0;
-    for (int i = 0; i < kWarps; ++i) own += sh_.warp_mass[i];
-    u64 total = 0, before = 0;
-    unsigned rank = 0;
-    exchange(own, 0, [&](u64 v, u64) {
-      if (rank++ < rank_) before += v;
-      total += v;
-    });
+    Sums all{0, 0, 0, 0}, every{0, 0, 0, 0};
+    for (int i = 0; i < kWarps; ++i) add(all, sh_.warp[i]);
+    exchange(all, [&](const Sums& v) { add(every, v); });
+    float fall = 0.f;  // units of weight that a unit of slope costs
+    if (w.minus_q) {
+      const Pair a = to_pair(every.p), b = to_pair(every.q);
+      const float hi = __fdiv_rn(a.hi, b.hi);
+      const float lo = __fdiv_rn(fmaf(-hi, b.hi, a.hi) + fmaf(-hi, b.lo, a.lo), b.hi);
+      const float scale = __fdiv_rn(unit_q, w.unit);  // a power of two
+      w.ratio = {hi * scale, lo * scale};
+      fall = ((w.ratio.hi - w.near) + w.ratio.lo) * __fdiv_rn(w.unit, unit_q);
+    }
+    const auto weight_of = [&](const Sums& v) {
+      return static_cast<u64>(max(static_cast<long long>(v.weight) - __float2ll_rn(__ull2float_rn(v.slope) * fall), 0LL));
+    };
+    u64 total = 0, before = 0, mine_all = weight_of(all);
+    if (ctas_ == 1) {
+      total = mine_all;
+    } else {
+      const Sums* buf = sh_.exchange[parity_ ^ 1];
+      for (unsigned r = 0; r < ctas_; ++r) {
+        if (r < rank_) before += weight_of(buf[r]);
+        total += weight_of(buf[r]);
+      }
+    }
     if (total == 0) return false;
     // floor(total u), below total
     const u64 target = __umul64hi(total << 4, static_cast<u64>(u * 4294967296.f) << 28);
-    if (target < before || target >= before + own) return true;  // another CTA has it
-    // the warp's run that holds it, a vector to each thread
+    if (target < before || target >= before + mine_all) return true;  // another CTA has it
+    // the warp's run that holds it (or, the parts rounded one by one, the last with any)
     int holder = 0;
-    while (target >= before + sh_.warp_mass[holder]) before += sh_.warp_mass[holder++];
+    u64 start = before;
+    for (int i = 0; i < kWarps; ++i) {
+      const u64 m = weight_of(sh_.warp[i]);
+      if (m > 0) {
+        holder = i;
+        start = before;
+        if (target < before + m) break;
+      }
+      before += m;
+    }
+    before = start;
+    const float more = (w.ratio.hi - w.near) + w.ratio.lo;
     const int first = (static_cast<int>(rank_) * kWarps + holder) * run_;
     const int last = min(first + run_, (a_.vocab + E::kVec - 1) / E::kVec);
-    for (int v = first + static_cast<int>(threadIdx.x);; v += kThreads) {  // some vector has it
-      float x[E::kVec], y[E::kVec];
-      float2 r[E::kVec / 2];
-      uint32_t heavy = 0;
-      u64 mine = 0;
-      if (v < last) {
-        heavy = load_both(v, w, x, y);
-        light_weights(v, heavy, x, y, w, d_least, sc, r);
-        mine = __float2uint_rn(sum_of(r) * w.unit);
+    float x[E::kVec], y[E::kVec];
+    float2 r[E::kVec / 2], none = make_float2(0.f, 0.f);
+    uint32_t heavy = 0;
+    const auto vector_weight = [&](int v) {
+      heavy = load_both(v, w, x, y);
+      light_weights<false>(v, heavy, x, y, w, more, d_least, sc, r, none, none, none);
+      u64 m = __float2uint_rn(sum_of(r) * w.unit);
 #pragma unroll 1
-        for (uint32_t bits = heavy; bits != 0; bits &= bits - 1) {
-          const int index = v * E::kVec + __ffs(bits) - 1;
-          mine += heavy_weight(E::one(x_[index]), w.minus_q ? E::one(y_[index]) : 0.f, index, w, sc);
-        }
+      for (uint32_t bits = heavy; bits != 0; bits &= bits - 1) {
+        const int index = v * E::kVec + __ffs(bits) - 1;
+        m += heavy_weight(E::one(x_[index]), w.minus_q ? E::one(y_[index]) : 0.f, index, w, sc);
       }
+      return m;
+    };
+    const auto put_token = [&](int token) {
+      a_.tokens[row] = token;
+      a_.logp[row] = log_share(E::one(x_[token]), w.p, sc);
+    };
+    if (threadIdx.x == 0) sh_.found = 0, sh_.spare = -1;
+    for (int v0 = first; v0 < last && target >= before; v0 += kThreads) {  // a vector to each thread
+      const int v = v0 + static_cast<int>(threadIdx.x);
+      const u64 mine = v < last ? vector_weight(v) : 0;
       u64 upto = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -801,15 +851,15 @@ class Sequence {
         if (lane >= o) upto += other;
       }
       __syncthreads();  // the sums have been read
-      if (lane == 31) sh_.warp_mass_q[warp] = upto;
+      if (lane == 31) sh_.scan[warp] = upto;
       __syncthreads();
       u64 at = before + upto - mine;
       for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) at += sh_.warp_mass_q[i];
-        before += sh_.warp_mass_q[i];
+        if (i < warp) at += sh_.scan[i];
+        before += sh_.scan[i];
       }
       if (target >= at && target < at + mine) {
-        // the first whose own rounded mass passes it, or (rounding) the last with any
+        // the first whose own rounded weight passes it, or (rounding) the last with any
         int token = -1, any = -1;
 #pragma unroll
         for (int e = 0; e < E::kVec; ++e) {
@@ -821,19 +871,35 @@ class Sequence {
           if (m > 0 || f > 0.f) any = index;
           at += m;
         }
-        if (token < 0) token = any;
-        a_.tokens[row] = token;
-        a_.logp[row] = log_share(E::one(x_[token]), w.p, sc);
+        put_token(token < 0 ? any : token);
+        sh_.found = 1;
       }
-      if (target < before || v - static_cast<int>(threadIdx.x) + kThreads >= last) break;
     }
+    __syncthreads();
+    if (sh_.found) return true;
+    // The run's vectors come to a few units less than the run did with the near
+    // ratio: the last token of it that weighs something, or that p allows.
+    for (int v = first + static_cast<int>(threadIdx.x); v < last; v += kThreads) {
+      const u64 m = vector_weight(v);
+      int best = -1;
+#pragma unroll
+      for (int e = 0; e < E::kVec; ++e) {
+        const float f = e & 1 ? r[e / 2].y : r[e / 2].x;
+        const bool weighs = f > 0.f || (heavy >> e & 1u && m > 0);
+        if (x[e] > -INFINITY && v * E::kVec + e < a_.vocab && v * E::kVec + e != w.without)
+          best = max(best, (weighs ? 1 << 18 : 0) + v * E::kVec + e);
+      }
+      if (best >= 0) atomicMax(&sh_.spare, best);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && sh_.spare >= 0) put_token(sh_.spare & ((1 << 18) - 1));
     return true;
   }
-  SA_DEV bool is_listed(int v) const {
-    const uint32_t in_run = static_cast<uint32_t>(v - static_cast<int>(rank_) * kWarps * run_);
-    for (int i = 0; i < kList; ++i)
-      if (sh_.list[i] >> 8 == in_run) return true;
-    return false;
+  static SA_DEV void add(Sums& to, const Sums& v) {
+    to.weight += v.weight;
+    to.p += v.p;
+    to.q += v.q;
+    to.slope += v.slope;
   }
 
   Shared& sh_;
@@ -843,7 +909,6 @@ class Sequence {
   unsigned rank_, ctas_;
   int parity_ = 0;
   int run_ = 0, v0_ = 0, v1_ = 0;  // vectors of a warp, and the warp's
-  bool listed_ = false;            // the vectors with heavy logits are in the list
   const T* x_ = nullptr;
   const T* y_ = nullptr;
 };
@@ -860,21 +925,31 @@ __global__ void __launch_bounds__(kThreads, kPerSm) verify_draw_kernel(const __g
   if (ctas > 1) cluster.sync();  // no CTA leaves while another may still write to its shared memory
 }
 
-template <int kType>
-int slices_for(int vocab) {
-  return ceil_div(static_cast<long long>(vocab) + Elem<kType>::kVec - 1, slice_logits<kType>());
+// Vectors of a row however it is aligned, in turns of a CTA.
+int turns_for(int dtype, int vocab) {
+  const int vec = dtype == 0 ? Elem<0>::kVec : Elem<1>::kVec;
+  return ceil_div(ceil_div(static_cast<long long>(vocab) + vec - 1, vec), kStatThreads);
 }
+int most_slices(int dtype, int vocab) { return ceil_div(turns_for(dtype, vocab), kStatVecs); }
 
 template <int kType>
 cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
-  const int slices = slices_for<kType>(a.vocab);
   const long long items = a.rows + (a.draft_logits != nullptr ? a.num_drafts : 0);
-  if (items > 0) verify_rows_kernel<kType><<<static_cast<unsigned>(items * slices), kStatThreads, 0, s>>>(a, slices);
+  // A row in as few slices as keep the GPU busy (3 CTAs an SM, a few turns of them), each a whole number of turns that
+  // a thread has in flight, so that none is nearly empty.
+  const int all = turns_for(kType, a.vocab);
+  int slices = std::max(ceil_div(all, kStatMostVecs), 1);
+  if (items > 0)
+    slices = std::max(slices, static_cast<int>(std::min<long long>(most_slices(kType, a.vocab), 9LL * device_sms() / items)));
+  const int turns = ceil_div(ceil_div(all, slices), kStatVecs) * kStatVecs;
+  slices = ceil_div(all, turns);
+  if (items > 0)
+    verify_rows_kernel<kType><<<static_cast<unsigned>(items * slices), kStatThreads, 0, s>>>(a, slices, turns);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // Enough CTAs for a sequence to be quick, not so many that the batch comes in several turns.
   int ctas = 1;
-  while (ctas < kMaxCluster && ctas * 8192 < a.vocab && 2LL * ctas * a.num_seqs <= device_sms() * kPerSm) ctas *= 2;
+  while (ctas < kMaxCluster && ctas * 8192 < a.vocab && 2LL * ctas * a.num_seqs <= 2 * device_sms() * kPerSm) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * ctas);
   cfg.blockDim = dim3(kThreads);
@@ -891,8 +966,7 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t verify_workspace_bytes(int dtype, int rows, int vocab) {
-  const int slices = dtype == 0 ? slices_for<0>(vocab) : slices_for<1>(vocab);
-  return static_cast<size_t>(rows) * 2 * slices * sizeof(float4);
+  return static_cast<size_t>(rows) * 2 * most_slices(dtype, vocab) * sizeof(float4);
 }
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {
