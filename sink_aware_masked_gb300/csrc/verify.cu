@@ -9,11 +9,15 @@
 //   T = 0: a draft stands if it is the largest logit's first index, and that is the token.
 //
 // All rows are read once, which is what the call cannot do without: 2 or 4
-// bytes a logit and one exponential each.  A first launch does that, a CTA per
-// (row, slice of the vocabulary): the slice's maximum and the sum relative to
-// it, from registers.  A second launch gives each sequence to a cluster: it
-// tests the drafts and draws the last token from the one row (or pair of
-// rows) in which it stopped, read again, mostly from L2.
+// bytes a logit and one exponential each.  Three launches:
+//   rows     a CTA per (row, slice of the vocabulary): the slice's maximum and
+//            the sum relative to it
+//   weights  a CTA per (entry, part of the vocabulary): tests the entry's drafts
+//            (every part does, which costs less than a launch), and sums what
+//            the part weighs in the row where the entry stopped, run by run; the
+//            row, or pair of rows, is read again, in part from L2
+//   draw     a CTA per entry: the run that holds the place drawn, and the token
+//            in it
 //
 // Arithmetic.  Where the tests are concerned fp32 sums do: a test is decided
 // wrongly only where u q and p agree to some 2^-22.  The draw is another
@@ -29,7 +33,6 @@
 //     summed again in the same way from the two rows.
 // Integer sums are the same in every order.  FP64 is not used: its rate on this
 // GPU would cost more than all the rest.
-#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -39,8 +42,6 @@
 
 namespace sa {
 namespace {
-
-namespace cg = cooperative_groups;
 
 typedef unsigned long long u64;
 
@@ -139,12 +140,6 @@ struct Scale {
     hi = fminf(q, 1e38f);
     lo = q < 1e38f ? __fdiv_rn(fmaf(-q, temperature, kLog2e) + kLog2eLo, temperature) : 0.f;
   }
-};
-
-// A sequence's rows [row0, row0 + n) and drafts [draft0, ...): the drafts of
-// all sequences stand one after another, n - 1 of a sequence that has rows.
-struct Rows {
-  int row0, n, draft0;
 };
 
 // ---------------------------------------------------------------- all rows
@@ -356,7 +351,7 @@ SA_DEV float power(Pair t) {
 }
 // 2^t to some 2^-40 of itself, t in (-60, 0]: 2^(n + k/16) (1 + g + g^2/2 + ...), g = ln 2 times the rest of t,
 // |g| <= ln 2 / 32.
-SA_DEV Pair power_pair(Pair t) {
+__device__ __noinline__ Pair power_pair(Pair t) {
   const float m = rintf(t.hi * 16.f), rest = fmaf(m, -0.0625f, t.hi) + t.lo;  // the first difference is exact
   const float rest_lo = t.lo - (rest - fmaf(m, -0.0625f, t.hi));
   const int i = static_cast<int>(m), k = i & 15;
@@ -374,16 +369,16 @@ SA_DEV Pair to_pair(u64 m) {
   const float hi = __ull2float_rn(m);
   return {hi, __ll2float_rn(static_cast<long long>(m - static_cast<u64>(hi)))};
 }
-SA_DEV long long to_units(Pair e, float unit) { return __float2ll_rn(e.hi * unit) + __float2ll_rn(e.lo * unit); }
+__device__ __noinline__ long long to_units(Pair e, float unit) { return __float2ll_rn(e.hi * unit) + __float2ll_rn(e.lo * unit); }
 
-// ---------------------------------------------------------------- a sequence
-constexpr int kThreads = 512;
-constexpr int kPerSm = 2;
+// ---------------------------------------------------------------- an entry
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxParts = 16;
+constexpr int kWeightsPerSm = 3;  // CTAs of the second launch that an SM holds
 constexpr int kHeavyLog2 = 12;  // masses from 2^-12 of the whole on are heavy
 constexpr int kUnitLog2 = 40;   // masses in units of 2^-40 of (about) the whole
-constexpr int kList = 2048;     // vectors with heavy masses that a CTA keeps a list of
+constexpr int kList = 1024;     // vectors with heavy masses that a CTA keeps a list of
 
 struct RowStat {
   float top, sum;
@@ -394,74 +389,87 @@ struct RowStat {
 
 // Of a run of tokens: what they weigh with the near ratio, and what that loses
 // for each unit that the ratio is more; the sums of both rows' masses.
-struct Sums {
-  u64 weight, p, q, slope;
+struct alignas(16) Sums {
+  u64 weight, slope, p, q;
 };
 
-struct Shared {
-  Sums exchange[2][kMaxCluster];
-  Sums warp[kWarps];
-  u64 weight[kWarps];  // the warps' runs' weights
-  int count[kWarps];
-  u64 scan[kWarps];
-  int first, listed, found, spare;
-  uint32_t list[kList];  // vector in the CTA's run << 8 | its heavy logits, a bit each
+// Where an entry stopped and what its last token is drawn from; in the
+// workspace between the second launch and the third.
+struct alignas(16) Stop {
+  RowStat p, q;
+  int row, draft;  // row: -1 for an entry without rows; draft: the one that did not stand, or -1
+  int drawn;       // 0: the token is written already
+  int pad[3];
 };
 
+SA_DEV float unit_of(float u) { return fminf(fmaxf(u, 0.f), 0.99999994f); }
+// A power of two that brings the whole, `sum`, to 2^kUnitLog2 or just below.
+SA_DEV float unit_for(float sum) {
+  const int e = (__float_as_int(sum) >> 23) - 127 + 1;  // sum < 2^e, and at least 2^-1 (the largest counts 1)
+  return __int_as_float((127 + kUnitLog2 - e) << 23);
+}
+SA_DEV float log_share(float x, const RowStat& s, const Scale& sc) {
+  return __fdiv_rn(x - s.top, sc.temperature) - logf(s.sum);
+}
+
+// The rows of an entry, and where it stops.
 template <int kType>
-class Sequence {
+class Entry {
  public:
   typedef Elem<kType> E;
   typedef typename E::T T;
+  struct Shared {
+    int count[kWarps];
+    int first;
+  };
 
-  SA_DEV Sequence(Shared& sh, const VerifyArgs& a, int slices)
-      : sh_(sh), a_(a), cluster_(cg::this_cluster()), slices_(slices), rank_(cluster_.block_rank()),
-        ctas_(cluster_.num_blocks()) {}
+  SA_DEV Entry(Shared& sh, const VerifyArgs& a, int slices) : sh_(sh), a_(a), slices_(slices) {}
 
-  SA_DEV void run(int b) {
+  // Tests the drafts of entry b; `writes`: and writes what is decided by that.  The same in all threads.
+  SA_DEV Stop stop(int b, bool writes) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (ctas_ > 1) cluster_.barrier_arrive();
+    Stop s;
+    s.drawn = 0;
+    s.draft = -1;
     int full = 0;
     for (int j = tid; j < b; j += kThreads) full += a_.cu[j + 1] > a_.cu[j];
     full = warp_sum(full);
-    if (lane == 0) sh_.count[warp] = full;
     const int row0 = max(a_.cu[b], 0), n = min(a_.cu[b + 1], a_.rows) - row0;
-    if (tid == 0) sh_.first = max(n - 1, 0), sh_.listed = 0;
-    my_run();
-    if (ctas_ > 1) cluster_.barrier_wait();  // every CTA of the cluster runs: its shared memory may be written
+    if (lane == 0) sh_.count[warp] = full;
+    if (tid == 0) sh_.first = max(n - 1, 0);
     __syncthreads();
-    int draft0 = row0 - a_.cu[0];  // one draft fewer than rows in every sequence before that has rows
-    for (int w = 0; w < kWarps; ++w) draft0 -= sh_.count[w];
+    s.row = -1;
     if (n <= 0) {
-      if (rank_ == 0 && tid == 0) a_.accepted[b] = a_.rejected[b] = 0;
-      return;
+      if (writes && tid == 0) a_.accepted[b] = a_.rejected[b] = 0;
+      return s;
     }
+    int draft0 = row0 - a_.cu[0];  // one draft fewer than rows in every entry before that has rows
+    for (int w = 0; w < kWarps; ++w) draft0 -= sh_.count[w];
     const Scale sc(a_.temperature[b]);
     // the drafts, a warp each; what an earlier stop makes void is overwritten below
     for (int i = warp; i < n - 1; i += kWarps) {
       bool stands = false;
       if (sc.valid && draft0 + i < a_.num_drafts) {
         const int token = a_.drafts[draft0 + i];
+        const bool inside = token >= 0 && token < a_.vocab;
+        const float x = inside ? E::one(row_of(row0 + i)[token]) : -INFINITY;
+        const float y = inside && a_.draft_logits != nullptr ? E::one(draft_of(draft0 + i)[token]) : 0.f;
+        const float u = unit_of(a_.u[row0 + i]);
         const RowStat p = stat(row0 + i, sc);
-        if (!p.bad() && !p.none() && token >= 0 && token < a_.vocab) {
-          const float x = logit(row0 + i, token);
+        if (!p.bad() && !p.none() && inside) {
+          const Pair tp = exponent(x, p.top, sc);
           if (sc.greedy) {
             stands = token == p.arg;
+          } else if (a_.draft_logits == nullptr) {
+            stands = u * p.sum < power(tp);
           } else {
-            const float u = unit_of(a_.u[row0 + i]);
-            const Pair tp = exponent(x, p.top, sc);
-            if (a_.draft_logits == nullptr) {
-              stands = u * p.sum < power(tp);
-            } else {
-              // u q < p by their ratio, which stays in range where both are small
-              const RowStat s = stat(a_.rows + draft0 + i, sc);
-              const float y = draft_logit(draft0 + i, token);
-              const Pair tq = exponent(y, s.top, sc);
-              const float ratio = y == -INFINITY ? INFINITY : ex2((tp.hi - tq.hi) + (tp.lo - tq.lo)) * __fdiv_rn(s.sum, p.sum);
-              stands = !s.bad() && !s.none() && x > -INFINITY && u < ratio;
-            }
+            // u q < p by their ratio, which stays in range where both are small
+            const RowStat q = stat(a_.rows + draft0 + i, sc);
+            const Pair tq = exponent(y, q.top, sc);
+            const float ratio = y == -INFINITY ? INFINITY : ex2((tp.hi - tq.hi) + (tp.lo - tq.lo)) * __fdiv_rn(q.sum, p.sum);
+            stands = !q.bad() && !q.none() && x > -INFINITY && u < ratio;
           }
-          if (stands && rank_ == 0 && lane == 0) {
+          if (stands && writes && lane == 0) {
             a_.tokens[row0 + i] = token;
             a_.logp[row0 + i] = log_share(x, p, sc);
           }
@@ -470,8 +478,9 @@ class Sequence {
       if (!stands && lane == 0) atomicMin(&sh_.first, i);
     }
     __syncthreads();
-    const int j = sh_.first, row = row0 + j;
-    if (rank_ == 0) {
+    const int j = sh_.first;
+    s.row = row0 + j;
+    if (writes) {
       for (int i = j + 1 + tid; i < n; i += kThreads) {
         a_.tokens[row0 + i] = -1;
         a_.logp[row0 + i] = 0.f;
@@ -481,72 +490,47 @@ class Sequence {
         a_.rejected[b] = n - 1 - j;
       }
     }
+    const auto put = [&](int token, float logp) {
+      if (writes && tid == 0) {
+        a_.tokens[s.row] = token;
+        a_.logp[s.row] = logp;
+      }
+      return s;
+    };
     const bool refused = j < n - 1;
-    if (!sc.valid || (refused && draft0 + j >= a_.num_drafts)) return put(row, -1, NAN);
-    const RowStat p = stat(row, sc);
-    if (p.bad()) return put(row, -1, NAN);
-    if (p.none()) return put(row, -1, -INFINITY);
-    if (sc.greedy) return put(row, p.arg, log_share(p.top, p, sc));
-    Weights w;
-    w.p = p;
-    w.unit = unit_for(p.sum);
-    w.heavy = heavy_from(p, sc);
-    w.without = -1;
-    w.minus_q = false;
-    x_ = static_cast<const T*>(a_.logits) + static_cast<int64_t>(row) * a_.stride;
-    y_ = nullptr;
-    if (refused && a_.draft_logits == nullptr) w.without = a_.drafts[draft0 + j];
-    if (refused && a_.draft_logits != nullptr) {
-      const RowStat q = stat(a_.rows + draft0 + j, sc);
-      if (q.bad() || q.none()) return put(row, -1, NAN);
-      w.q = q;
-      w.minus_q = true;
-      w.heavy_q = heavy_from(q, sc);
-      w.near = __fdiv_rn(p.sum, q.sum);
-      w.ratio = {w.near, 0.f};
-      y_ = static_cast<const T*>(a_.draft_logits) + static_cast<int64_t>(draft0 + j) * a_.draft_stride;
-    }
-    if (!draw(w, sc, row, unit_of(a_.u[row0 + n - 1]))) {
-      // nothing is left of w: the target's own probabilities
-      w.minus_q = false;
-      w.without = -1;
-      __syncthreads();
-      if (tid == 0) sh_.listed = 0;
-      __syncthreads();
-      draw(w, sc, row, unit_of(a_.u[row0 + n - 1]));
-    }
+    if (!sc.valid || (refused && draft0 + j >= a_.num_drafts)) return put(-1, NAN);
+    if (refused) s.draft = draft0 + j;
+    s.p = stat(s.row, sc);
+    const bool minus_q = refused && a_.draft_logits != nullptr && !sc.greedy;
+    if (minus_q) s.q = stat(a_.rows + s.draft, sc);
+    if (s.p.bad()) return put(-1, NAN);
+    if (s.p.none()) return put(-1, -INFINITY);
+    if (sc.greedy) return put(s.p.arg, log_share(s.p.top, s.p, sc));
+    if (minus_q && (s.q.bad() || s.q.none())) return put(-1, NAN);
+    s.drawn = 1;
+    return s;
+  }
+  SA_DEV const T* row_of(int row) const { return static_cast<const T*>(a_.logits) + static_cast<int64_t>(row) * a_.stride; }
+  SA_DEV const T* draft_of(int draft) const {
+    return static_cast<const T*>(a_.draft_logits) + static_cast<int64_t>(draft) * a_.draft_stride;
   }
 
  private:
-  struct Weights {
-    RowStat p, q;
-    float unit;            // masses are e times unit
-    float heavy, heavy_q;  // logits from which a mass is heavy
-    float near;            // about the ratio of the sums: p - q is e_p - ratio e_q, but for a factor
-    Pair ratio;            // the same as exactly as the sums are known
-    int without;           // the draft that is taken out, or -1
-    bool minus_q;
-  };
-
-  static SA_DEV float heavy_from(const RowStat& s, const Scale& sc) {
-    float l;
-    asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(l) : "f"(s.sum));
-    return s.top + __fdiv_rn(l - kHeavyLog2, sc.hi);
-  }
-  static SA_DEV float unit_of(float u) { return fminf(fmaxf(u, 0.f), 0.99999994f); }
-  // A power of two that brings the whole, `sum`, to 2^kUnitLog2 or just below.
-  static SA_DEV float unit_for(float sum) {
-    const int e = (__float_as_int(sum) >> 23) - 127 + 1;  // sum < 2^e, and at least 2^-1 (the largest counts 1)
-    return __int_as_float((127 + kUnitLog2 - e) << 23);
-  }
-
   // Of target row `item`, or of draft item - rows; by a whole warp.
   SA_DEV RowStat stat(int item, const Scale& sc) const {
     const float4* parts = a_.parts + static_cast<int64_t>(item) * slices_;
+    const int lane = threadIdx.x & 31;
     RowStat r{kLowest, 0.f, 0x7fffffff};
-    for (int i = threadIdx.x & 31; i < slices_; i += 32) r.top = fmaxf(r.top, parts[i].x);
+    if (slices_ <= 32) {
+      const float4 f = lane < slices_ ? parts[lane] : make_float4(kLowest, 0.f, __int_as_float(0x7fffffff), 0.f);
+      r.top = warp_max(f.x);
+      r.sum = warp_sum(f.y * ex2((f.x - r.top) * sc.hi));
+      if (sc.greedy) r.arg = warp_min(f.x == r.top ? __float_as_int(f.z) : 0x7fffffff);
+      return r;
+    }
+    for (int i = lane; i < slices_; i += 32) r.top = fmaxf(r.top, parts[i].x);
     r.top = warp_max(r.top);
-    for (int i = threadIdx.x & 31; i < slices_; i += 32) {
+    for (int i = lane; i < slices_; i += 32) {
       const float4 f = parts[i];
       r.sum += f.y * ex2((f.x - r.top) * sc.hi);
       if (f.x == r.top) r.arg = min(r.arg, __float_as_int(f.z));
@@ -555,55 +539,187 @@ class Sequence {
     r.arg = warp_min(r.arg);
     return r;
   }
-  SA_DEV float logit(int row, int token) const {
-    return E::one(static_cast<const T*>(a_.logits)[static_cast<int64_t>(row) * a_.stride + token]);
+
+  Shared& sh_;
+  const VerifyArgs& a_;
+  int slices_;
+};
+
+// What the tokens of a row (x_), less those of a draft row (y_), weigh.
+template <int kType>
+class Weights {
+ public:
+  typedef Elem<kType> E;
+  typedef typename E::T T;
+  static constexpr int kVec = E::kVec;
+
+  // A vector's logits that are heavy in neither row (-inf in the others' place), and which those are, a bit each.
+  struct Vector {
+    float x[kVec], y[kVec];
+    uint32_t heavy;
+  };
+
+  SA_DEV Weights(const VerifyArgs& a, const Entry<kType>& entry, const Stop& s, const Scale& sc)
+      : vocab_(a.vocab), vectors_((a.vocab + kVec - 1) / kVec), sc_(sc), p_(s.p), q_(s.q) {
+    x_ = entry.row_of(s.row);
+    y_ = nullptr;
+    unit_ = unit_for(s.p.sum);
+    heavy_ = heavy_from(s.p);
+    d_least_ = fmaxf(__fdiv_rn(-150.f, sc.hi), -3e38f);
+    if (s.draft >= 0 && a.draft_logits != nullptr) {
+      y_ = entry.draft_of(s.draft);
+      unit_q_ = unit_for(s.q.sum);
+      heavy_q_ = heavy_from(s.q);
+      near_ = __fdiv_rn(s.p.sum, s.q.sum);
+    } else if (s.draft >= 0) {
+      without_ = a.drafts[s.draft];
+    }
   }
-  SA_DEV float draft_logit(int draft, int token) const {
-    return E::one(static_cast<const T*>(a_.draft_logits)[static_cast<int64_t>(draft) * a_.draft_stride + token]);
+  SA_DEV bool minus_q() const { return y_ != nullptr; }
+  SA_DEV bool plain() const { return y_ == nullptr && without_ < 0; }
+  SA_DEV void make_plain() {
+    y_ = nullptr;
+    without_ = -1;
   }
-  static SA_DEV float log_share(float x, const RowStat& s, const Scale& sc) {
-    return __fdiv_rn(x - s.top, sc.temperature) - logf(s.sum);
+  SA_DEV int vectors() const { return vectors_; }
+  SA_DEV float x_at(int index) const { return E::one(x_[index]); }
+
+  // The vectors of one warp's run among `runs`.
+  SA_DEV int run_length(int runs) const { return (vectors_ + runs - 1) / runs; }
+
+  // A vector as it comes from memory.
+  struct Raw {
+    uint4 x, y;
+  };
+  SA_DEV Raw fetch(int v) const {
+    Raw w;
+    w.x = raw(x_, v);
+    if (y_ != nullptr) w.y = raw(y_, v);
+    return w;
   }
-  SA_DEV void put(int row, int token, float logp) const {
-    if (rank_ != 0 || threadIdx.x != 0) return;
-    a_.tokens[row] = token;
-    a_.logp[row] = logp;
+  SA_DEV void unpack(const Raw& w, Vector& t) const {
+    bool any = E::largest(w.x) >= heavy_;
+    E::unpack(w.x, t.x);
+    if (y_ != nullptr) {
+      any |= E::largest(w.y) >= heavy_q_;
+      E::unpack(w.y, t.y);
+    }
+    t.heavy = 0;
+    if (any) {  // they leave the light path
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        if (t.x[e] >= heavy_ || (y_ != nullptr && t.y[e] >= heavy_q_)) {
+          t.heavy |= 1u << e;
+          t.x[e] = t.y[e] = -INFINITY;
+        }
+      }
+    }
   }
 
-  // Every CTA of the cluster gives its sums and takes all of them in rank order.
-  template <class F>
-  SA_DEV void exchange(const Sums& own, F take) {
-    if (ctas_ == 1) {
-      take(own);
+  // What the logits of vector v weigh that are not heavy, before the unit, with
+  // the near ratio (kSums: adding to the rows' masses and the slope) or with
+  // the exact one.
+  template <bool kSums>
+  SA_DEV void light_weights(int v, const Vector& t, float2 (&r)[kVec / 2], float2& p, float2& q, float2& slope) const {
+#pragma unroll
+    for (int e = 0; e < kVec; e += 2) {
+      float2 m = light(t.x[e], t.x[e + 1], p_.top);
+      if (y_ != nullptr) {
+        float2 n = light(t.y[e], t.y[e + 1], q_.top);
+        if constexpr (kSums) p = fadd2(p, m), q = fadd2(q, n);
+        m = ffma2(n, make_float2(-near_, -near_), m);
+        if constexpr (!kSums) m = ffma2(n, make_float2(-more_, -more_), m);
+        if constexpr (kSums) slope = fadd2(slope, make_float2(m.x > 0.f ? n.x : 0.f, m.y > 0.f ? n.y : 0.f));
+        m = make_float2(fmaxf(m.x, 0.f), fmaxf(m.y, 0.f));
+      }
+      r[e / 2] = m;
+    }
+    if (without_ >= v * kVec && without_ < (v + 1) * kVec) {
+#pragma unroll
+      for (int e = 0; e < kVec; e += 2) {
+        if (v * kVec + e == without_) r[e / 2].x = 0.f;
+        if (v * kVec + e + 1 == without_) r[e / 2].y = 0.f;
+      }
+    }
+  }
+  static SA_DEV float sum_of(const float2 (&r)[kVec / 2]) {
+    float2 s = r[0];
+#pragma unroll
+    for (int e = 1; e < kVec / 2; ++e) s = fadd2(s, r[e]);
+    return s.x + s.y;
+  }
+  SA_DEV u64 units(float f) const { return __float2uint_rn(f * unit_); }
+  SA_DEV u64 units_q(float f) const { return __float2uint_rn(f * unit_q_); }
+
+  // Adds a heavy token with the near ratio.
+  SA_DEV void add_heavy(Sums& to, int index) const {
+    const Pair p = power_pair(exponent(E::one(x_[index]), p_.top, sc_));
+    if (y_ == nullptr) {
+      if (index != without_) to.weight += to_units(p, unit_);
       return;
     }
-    Sums* buf = sh_.exchange[parity_];
-    parity_ ^= 1;  // the other half may still be read by a slower CTA
-    if (threadIdx.x < ctas_) cluster_.map_shared_rank(buf, threadIdx.x)[rank_] = own;
-    cluster_.sync();
-    for (unsigned r = 0; r < ctas_; ++r) take(buf[r]);
+    const Pair q = power_pair(exponent(E::one(y_[index]), q_.top, sc_));
+    const long long m = difference(p, q, near_, 0.f);
+    to.weight += m;
+    to.p += to_units(p, unit_);
+    to.q += to_units(q, unit_q_);
+    if (m > 0) to.slope += to_units(q, unit_q_);
+  }
+  // What a heavy token weighs with the exact ratio.
+  SA_DEV u64 heavy_weight(int index) const {
+    if (index == without_) return 0;
+    const Pair p = power_pair(exponent(E::one(x_[index]), p_.top, sc_));
+    if (y_ == nullptr) return to_units(p, unit_);
+    return difference(p, power_pair(exponent(E::one(y_[index]), q_.top, sc_)), ratio_.hi, ratio_.lo);
   }
 
-  // The vectors of a row (counted from its first logit) that the warp has, one run of them.
-  SA_DEV void my_run() {
-    const int vectors = (a_.vocab + E::kVec - 1) / E::kVec, parts = ctas_ * kWarps;
-    run_ = (vectors + parts - 1) / parts;
-    v0_ = min((static_cast<int>(rank_) * kWarps + static_cast<int>(threadIdx.x >> 5)) * run_, vectors);
-    v1_ = min(v0_ + run_, vectors);
+  // The ratio of the two rows' sums, from their masses.
+  SA_DEV void set_ratio(u64 all_p, u64 all_q) {
+    if (y_ == nullptr) return;
+    const Pair a = to_pair(all_p), b = to_pair(all_q);
+    const float hi = __fdiv_rn(a.hi, b.hi);
+    const float lo = __fdiv_rn(fmaf(-hi, b.hi, a.hi) + fmaf(-hi, b.lo, a.lo), b.hi);
+    const float scale = __fdiv_rn(unit_q_, unit_);  // a power of two
+    ratio_ = {hi * scale, lo * scale};
+    more_ = (ratio_.hi - near_) + ratio_.lo;
+    fall_ = more_ * __fdiv_rn(unit_, unit_q_);
   }
-  // Logits of vector v; -inf behind the row's end.
-  SA_DEV void load(const T* row, int v, float* f) const {
-    const int at = v * E::kVec;
-    if ((reinterpret_cast<uintptr_t>(row) & 15u) == 0 && at + E::kVec <= a_.vocab) {
-      E::unpack(__ldg(reinterpret_cast<const uint4*>(row) + v), f);
-    } else {
+  // What a run weighs with the exact ratio: the few tokens that get or lose their sign between near and exact ratio
+  // are below the square of the ratios' difference.
+  SA_DEV u64 exact(const Sums& v) const {
+    return max(static_cast<long long>(v.weight) - __float2ll_rn(__ull2float_rn(v.slope) * fall_), 0LL);
+  }
+  // What vector v weighs with the exact ratio; r: its light logits'.
+  SA_DEV u64 vector_weight(int v, Vector& t, float2 (&r)[kVec / 2]) const {
+    float2 none = make_float2(0.f, 0.f);
+    unpack(fetch(v), t);
+    light_weights<false>(v, t, r, none, none, none);
+    u64 m = units(sum_of(r));
+#pragma unroll 1
+    for (uint32_t bits = t.heavy; bits != 0; bits &= bits - 1) m += heavy_weight(v * kVec + __ffs(bits) - 1);
+    return m;
+  }
+
+ private:
+  SA_DEV float heavy_from(const RowStat& s) const {  // the logit from which a mass is heavy
+    float l;
+    asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(l) : "f"(s.sum));
+    return s.top + __fdiv_rn(l - kHeavyLog2, sc_.hi);
+  }
+  // Vector v of a row, counted from its first logit; -inf behind its end.
+  SA_DEV uint4 raw(const T* row, int v) const {
+    const int at = v * kVec;
+    if ((reinterpret_cast<uintptr_t>(row) & 15u) == 0 && at + kVec <= vocab_) return __ldg(reinterpret_cast<const uint4*>(row) + v);
+    union {
+      uint4 q;
+      T t[kVec];
+    } w;
 #pragma unroll
-      for (int e = 0; e < E::kVec; ++e) f[e] = at + e < a_.vocab ? E::one(row[at + e]) : -INFINITY;
-    }
+    for (int e = 0; e < kVec; ++e) w.t[e] = at + e < vocab_ ? row[at + e] : E::lowest();
+    return w.q;
   }
-
-  // 2^((x - top) scale) of two logits to some 2^-23 of itself, 0 far below; d_least is where that is.
-  static SA_DEV float2 light(float x, float y, float top, float d_least, const Scale& sc) {
+  // 2^((x - top) scale) of two logits to some 2^-23 of itself, 0 far below.
+  SA_DEV float2 light(float x, float y, float top) const {
     float2 d = fadd2(make_float2(x, y), make_float2(-top, -top));
     float2 d_lo = make_float2(0.f, 0.f);
     if constexpr (kType == 0) {
@@ -614,315 +730,247 @@ class Sequence {
       d_lo = fadd2(fadd2(make_float2(x, y), make_float2(-c.x, -c.y)), fadd2(make_float2(-top, -top), make_float2(-b.x, -b.y)));
       d_lo = make_float2(x > -INFINITY ? d_lo.x : 0.f, y > -INFINITY ? d_lo.y : 0.f);
     }
-    d = make_float2(fmaxf(d.x, d_least), fmaxf(d.y, d_least));
-    const float2 s2 = make_float2(sc.hi, sc.hi);
-    const float2 hi = fmul2(d, s2);
-    float2 lo = ffma2(d, make_float2(sc.lo, sc.lo), ffma2(d, s2, make_float2(-hi.x, -hi.y)));
-    if constexpr (kType == 0) lo = ffma2(d_lo, s2, lo);
+    d = make_float2(fmaxf(d.x, d_least_), fmaxf(d.y, d_least_));
+    const float2 hi = fmul2(d, make_float2(sc_.hi, sc_.hi));
+    // minus what hi was rounded by, and minus what the scale was
+    float2 lo = ffma2(d, make_float2(-sc_.lo, -sc_.lo), ffma2(d, make_float2(-sc_.hi, -sc_.hi), hi));
+    if constexpr (kType == 0) lo = ffma2(d_lo, make_float2(-sc_.hi, -sc_.hi), lo);
     const float2 e = make_float2(ex2(hi.x), ex2(hi.y));
-    return ffma2(e, fmul2(lo, make_float2(kLn2, kLn2)), e);
+    return ffma2(e, fmul2(lo, make_float2(-kLn2, -kLn2)), e);
   }
-  static SA_DEV float least_difference(const Scale& sc) { return fmaxf(__fdiv_rn(-150.f, sc.hi), -3e38f); }
-
   // e_p - ratio e_q in units, 0 at least.
-  static SA_DEV long long difference(Pair p, Pair q, Pair ratio, float unit) {
-    const float c = __fmul_rn(q.hi, ratio.hi), c_lo = fmaf(q.hi, ratio.hi, -c) + fmaf(q.hi, ratio.lo, q.lo * ratio.hi);
-    return max(to_units(p, unit) - to_units({c, c_lo}, unit), 0LL);
-  }
-  // What a token weighs, in units, where its mass is heavy.
-  SA_DEV long long heavy_weight(float x, float y, int index, const Weights& w, const Scale& sc) const {
-    if (index == w.without) return 0;
-    const Pair p = power_pair(exponent(x, w.p.top, sc));
-    return w.minus_q ? difference(p, power_pair(exponent(y, w.q.top, sc)), w.ratio, w.unit) : to_units(p, w.unit);
-  }
-  // A vector's logits, and which of them are heavy, a bit each.
-  SA_DEV uint32_t load_both(int v, const Weights& w, float (&x)[E::kVec], float (&y)[E::kVec]) const {
-    load(x_, v, x);
-    bool any = largest(x) >= w.heavy;
-    if (w.minus_q) {
-      load(y_, v, y);
-      any |= largest(y) >= w.heavy_q;
-    }
-    uint32_t bits = 0;
-    if (any) {
-#pragma unroll
-      for (int e = 0; e < E::kVec; ++e)
-        bits |= static_cast<uint32_t>(x[e] >= w.heavy || (w.minus_q && y[e] >= w.heavy_q)) << e;
-    }
-    return bits;
-  }
-  static SA_DEV float largest(const float (&x)[E::kVec]) {
-    float m = fmaxf(x[0], x[1]);
-#pragma unroll
-    for (int e = 2; e < E::kVec; e += 2) m = fmax3(m, x[e], x[e + 1]);
-    return m;
-  }
-  // What the logits of a vector weigh that are not heavy, before the unit, with
-  // the ratio w.near + more.  kSums: also adds to the rows' masses and the slope.
-  template <bool kSums>
-  SA_DEV void light_weights(int v, uint32_t heavy, const float (&x)[E::kVec], const float (&y)[E::kVec], const Weights& w,
-                            float more, float d_least, const Scale& sc, float2 (&r)[E::kVec / 2], float2& p, float2& q,
-                            float2& slope) const {
-    const float2 near = make_float2(-w.near, -w.near), rest = make_float2(-more, -more);
-#pragma unroll
-    for (int e = 0; e < E::kVec; e += 2) {
-      float2 m = light(x[e], x[e + 1], w.p.top, d_least, sc);
-      if (w.minus_q) {
-        float2 n = light(y[e], y[e + 1], w.q.top, d_least, sc);
-        if (heavy >> e & 3u) {
-          if (heavy >> e & 1u) m.x = n.x = 0.f;
-          if (heavy >> e & 2u) m.y = n.y = 0.f;
-        }
-        if constexpr (kSums) p = fadd2(p, m), q = fadd2(q, n);
-        m = ffma2(n, near, m);
-        if constexpr (!kSums) m = ffma2(n, rest, m);
-        if constexpr (kSums) slope = fadd2(slope, make_float2(m.x > 0.f ? n.x : 0.f, m.y > 0.f ? n.y : 0.f));
-        m = make_float2(fmaxf(m.x, 0.f), fmaxf(m.y, 0.f));
-      } else if (heavy >> e & 3u) {
-        if (heavy >> e & 1u) m.x = 0.f;
-        if (heavy >> e & 2u) m.y = 0.f;
-      }
-      r[e / 2] = m;
-    }
-    if (w.without >= v * E::kVec && w.without < (v + 1) * E::kVec) {
-#pragma unroll
-      for (int e = 0; e < E::kVec; e += 2) {
-        if (v * E::kVec + e == w.without) r[e / 2].x = 0.f;
-        if (v * E::kVec + e + 1 == w.without) r[e / 2].y = 0.f;
-      }
-    }
-  }
-  static SA_DEV float sum_of(const float2 (&r)[E::kVec / 2]) {
-    float2 s = r[0];
-#pragma unroll
-    for (int e = 1; e < E::kVec / 2; ++e) s = fadd2(s, r[e]);
-    return s.x + s.y;
-  }
-  // f(x, y, index) for the heavy logits of the CTA's listed vectors, evenly over its threads.
-  template <class F>
-  SA_DEV void each_listed(const Weights& w, F f) const {
-    const int v_cta = static_cast<int>(rank_) * kWarps * run_;
-    for (int i = threadIdx.x; i < min(sh_.listed, kList); i += kThreads) {
-      const int v = v_cta + static_cast<int>(sh_.list[i] >> 8);
-      for (uint32_t bits = sh_.list[i] & 0xffu; bits != 0; bits &= bits - 1) {
-        const int index = v * E::kVec + __ffs(bits) - 1;
-        f(E::one(x_[index]), w.minus_q ? E::one(y_[index]) : 0.f, index, v);
-      }
-    }
-  }
-  // Enters a vector in the list of those with heavy logits; false if it is full.
-  SA_DEV bool enter(int v, uint32_t bits) {
-    const int at = atomicAdd(&sh_.listed, 1);
-    if (at >= kList) return false;
-    sh_.list[at] = static_cast<uint32_t>(v - static_cast<int>(rank_) * kWarps * run_) << 8 | bits;
-    return true;
+  SA_DEV long long difference(Pair p, Pair q, float ratio, float ratio_lo) const {
+    const float c = __fmul_rn(q.hi, ratio), c_lo = fmaf(q.hi, ratio, -c) + fmaf(q.hi, ratio_lo, q.lo * ratio);
+    return max(to_units(p, unit_) - to_units({c, c_lo}, unit_), 0LL);
   }
 
-  // Draws the token of `row`; false (for all CTAs alike) if nothing has weight.
-  // One pass over the run: weights with the ratio that the first launch's sums
-  // give, which is off by some 2^-22, and the rows' masses, which give the ratio
-  // as exactly as the draw needs it.  The weights change by the slope then (the
-  // few that get or lose their sign between are below the square of that).
-  SA_DEV bool draw(Weights& w, const Scale& sc, int row, float u) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float d_least = least_difference(sc), unit_q = w.minus_q ? unit_for(w.q.sum) : 0.f;
-    Sums own{0, 0, 0, 0};
-    const auto add_heavy = [&](Sums& to, float x, float y, int index) {
-      if (!w.minus_q) {
-        to.weight += heavy_weight(x, y, index, w, sc);
-        return;
-      }
-      const Pair p = power_pair(exponent(x, w.p.top, sc)), q = power_pair(exponent(y, w.q.top, sc));
-      const long long m = difference(p, q, {w.near, 0.f}, w.unit);
-      to.weight += m;
-      to.p += to_units(p, w.unit);
-      to.q += to_units(q, unit_q);
-      if (m > 0) to.slope += to_units(q, unit_q);
-    };
-#pragma unroll 2
-    for (int v = v0_ + lane; v < v1_; v += 32) {
-      float x[E::kVec], y[E::kVec];
-      float2 r[E::kVec / 2], p = make_float2(0.f, 0.f), q = p, slope = p;
-      const uint32_t heavy = load_both(v, w, x, y);
-      light_weights<true>(v, heavy, x, y, w, 0.f, d_least, sc, r, p, q, slope);
-      own.weight += __float2uint_rn(sum_of(r) * w.unit);
-      if (w.minus_q) {
-        own.p += __float2uint_rn((p.x + p.y) * w.unit);
-        own.q += __float2uint_rn((q.x + q.y) * unit_q);
-        own.slope += __float2uint_rn((slope.x + slope.y) * unit_q);
-      }
-      if (heavy != 0 && !enter(v, heavy)) {
-#pragma unroll
-        for (int e = 0; e < E::kVec; ++e)
-          if (heavy >> e & 1u) add_heavy(own, x[e], w.minus_q ? y[e] : 0.f, v * E::kVec + e);
-      }
-    }
-    own.weight = warp_sum(own.weight);
-    if (w.minus_q) {
-      own.p = warp_sum(own.p);
-      own.q = warp_sum(own.q);
-      own.slope = warp_sum(own.slope);
-    }
-    if (lane == 0) sh_.warp[warp] = own;
-    __syncthreads();
-    each_listed(w, [&](float x, float y, int index, int v) {
-      Sums one{0, 0, 0, 0};
-      add_heavy(one, x, y, index);
-      Sums& to = sh_.warp[(v - static_cast<int>(rank_) * kWarps * run_) / run_];
-      atomicAdd(&to.weight, one.weight);
-      if (w.minus_q) {
-        atomicAdd(&to.p, one.p);
-        atomicAdd(&to.q, one.q);
-        atomicAdd(&to.slope, one.slope);
-      }
-    });
-    __syncthreads();
-    Sums all{0, 0, 0, 0}, every{0, 0, 0, 0};
-    for (int i = 0; i < kWarps; ++i) add(all, sh_.warp[i]);
-    exchange(all, [&](const Sums& v) { add(every, v); });
-    float fall = 0.f;  // units of weight that a unit of slope costs
-    if (w.minus_q) {
-      const Pair a = to_pair(every.p), b = to_pair(every.q);
-      const float hi = __fdiv_rn(a.hi, b.hi);
-      const float lo = __fdiv_rn(fmaf(-hi, b.hi, a.hi) + fmaf(-hi, b.lo, a.lo), b.hi);
-      const float scale = __fdiv_rn(unit_q, w.unit);  // a power of two
-      w.ratio = {hi * scale, lo * scale};
-      fall = ((w.ratio.hi - w.near) + w.ratio.lo) * __fdiv_rn(w.unit, unit_q);
-    }
-    const auto weight_of = [&](const Sums& v) {
-      return static_cast<u64>(max(static_cast<long long>(v.weight) - __float2ll_rn(__ull2float_rn(v.slope) * fall), 0LL));
-    };
-    u64 total = 0, before = 0, mine_all = weight_of(all);
-    if (ctas_ == 1) {
-      total = mine_all;
-    } else {
-      const Sums* buf = sh_.exchange[parity_ ^ 1];
-      for (unsigned r = 0; r < ctas_; ++r) {
-        if (r < rank_) before += weight_of(buf[r]);
-        total += weight_of(buf[r]);
-      }
-    }
-    if (total == 0) return false;
-    // floor(total u), below total
-    const u64 target = __umul64hi(total << 4, static_cast<u64>(u * 4294967296.f) << 28);
-    if (target < before || target >= before + mine_all) return true;  // another CTA has it
-    // the warp's run that holds it (or, the parts rounded one by one, the last with any)
-    int holder = 0;
-    u64 start = before;
-    for (int i = 0; i < kWarps; ++i) {
-      const u64 m = weight_of(sh_.warp[i]);
-      if (m > 0) {
-        holder = i;
-        start = before;
-        if (target < before + m) break;
-      }
-      before += m;
-    }
-    before = start;
-    const float more = (w.ratio.hi - w.near) + w.ratio.lo;
-    const int first = (static_cast<int>(rank_) * kWarps + holder) * run_;
-    const int last = min(first + run_, (a_.vocab + E::kVec - 1) / E::kVec);
-    float x[E::kVec], y[E::kVec];
-    float2 r[E::kVec / 2], none = make_float2(0.f, 0.f);
-    uint32_t heavy = 0;
-    const auto vector_weight = [&](int v) {
-      heavy = load_both(v, w, x, y);
-      light_weights<false>(v, heavy, x, y, w, more, d_least, sc, r, none, none, none);
-      u64 m = __float2uint_rn(sum_of(r) * w.unit);
-#pragma unroll 1
-      for (uint32_t bits = heavy; bits != 0; bits &= bits - 1) {
-        const int index = v * E::kVec + __ffs(bits) - 1;
-        m += heavy_weight(E::one(x_[index]), w.minus_q ? E::one(y_[index]) : 0.f, index, w, sc);
-      }
-      return m;
-    };
-    const auto put_token = [&](int token) {
-      a_.tokens[row] = token;
-      a_.logp[row] = log_share(E::one(x_[token]), w.p, sc);
-    };
-    if (threadIdx.x == 0) sh_.found = 0, sh_.spare = -1;
-    for (int v0 = first; v0 < last && target >= before; v0 += kThreads) {  // a vector to each thread
-      const int v = v0 + static_cast<int>(threadIdx.x);
-      const u64 mine = v < last ? vector_weight(v) : 0;
-      u64 upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 other = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += other;
-      }
-      __syncthreads();  // the sums have been read
-      if (lane == 31) sh_.scan[warp] = upto;
-      __syncthreads();
-      u64 at = before + upto - mine;
-      for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) at += sh_.scan[i];
-        before += sh_.scan[i];
-      }
-      if (target >= at && target < at + mine) {
-        // the first whose own rounded weight passes it, or (rounding) the last with any
-        int token = -1, any = -1;
-#pragma unroll
-        for (int e = 0; e < E::kVec; ++e) {
-          const int index = v * E::kVec + e;
-          const float f = e & 1 ? r[e / 2].y : r[e / 2].x;
-          const u64 m = heavy >> e & 1u ? static_cast<u64>(heavy_weight(x[e], w.minus_q ? y[e] : 0.f, index, w, sc))
-                                        : __float2uint_rn(f * w.unit);
-          if (token < 0 && target < at + m) token = index;
-          if (m > 0 || f > 0.f) any = index;
-          at += m;
-        }
-        put_token(token < 0 ? any : token);
-        sh_.found = 1;
-      }
-    }
-    __syncthreads();
-    if (sh_.found) return true;
-    // The run's vectors come to a few units less than the run did with the near
-    // ratio: the last token of it that weighs something, or that p allows.
-    for (int v = first + static_cast<int>(threadIdx.x); v < last; v += kThreads) {
-      const u64 m = vector_weight(v);
-      int best = -1;
-#pragma unroll
-      for (int e = 0; e < E::kVec; ++e) {
-        const float f = e & 1 ? r[e / 2].y : r[e / 2].x;
-        const bool weighs = f > 0.f || (heavy >> e & 1u && m > 0);
-        if (x[e] > -INFINITY && v * E::kVec + e < a_.vocab && v * E::kVec + e != w.without)
-          best = max(best, (weighs ? 1 << 18 : 0) + v * E::kVec + e);
-      }
-      if (best >= 0) atomicMax(&sh_.spare, best);
-    }
-    __syncthreads();
-    if (threadIdx.x == 0 && sh_.spare >= 0) put_token(sh_.spare & ((1 << 18) - 1));
-    return true;
-  }
-  static SA_DEV void add(Sums& to, const Sums& v) {
-    to.weight += v.weight;
-    to.p += v.p;
-    to.q += v.q;
-    to.slope += v.slope;
-  }
-
-  Shared& sh_;
-  const VerifyArgs& a_;
-  cg::cluster_group cluster_;
-  int slices_;
-  unsigned rank_, ctas_;
-  int parity_ = 0;
-  int run_ = 0, v0_ = 0, v1_ = 0;  // vectors of a warp, and the warp's
-  const T* x_ = nullptr;
-  const T* y_ = nullptr;
+  const T* x_;
+  const T* y_;
+  int vocab_, vectors_, without_ = -1;  // without: the draft that is taken out
+  Scale sc_;
+  RowStat p_, q_;
+  float unit_, unit_q_ = 0.f;       // masses are e times unit
+  float heavy_, heavy_q_ = 0.f;     // logits from which a mass is heavy
+  float d_least_;                   // a difference at which nothing is left
+  float near_ = 0.f;                // about the ratio of the sums: p - q is e_p - ratio e_q, but for a factor
+  float more_ = 0.f, fall_ = 0.f;   // what the exact ratio is more; units of weight that a unit of slope costs
+  Pair ratio_ = {0.f, 0.f};         // the exact ratio
 };
 
+// The parts of the workspace behind the slices' sums.
+struct Places {
+  int slices, parts;
+  bool by_row;  // an entry's place goes by its first row, not by its number: there are more entries than rows
+  Stop* stops;  // [min(rows, most entries)]
+  Sums* sums;   // [the same][parts][kWarps]
+  SA_DEV int of(const VerifyArgs& a, int b) const { return by_row ? a.cu[b] : b; }
+};
+
+// CTA: a part of entry b's vocabulary, cut into a run for each warp.
 template <int kType>
-__global__ void __launch_bounds__(kThreads, kPerSm) verify_draw_kernel(const __grid_constant__ VerifyArgs a, int slices) {
-  __shared__ Shared sh;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int ctas = cluster.num_blocks();
-  {
-    Sequence<kType> s(sh, a, slices);
-    s.run(blockIdx.x / ctas);
+__global__ void __launch_bounds__(kThreads, kWeightsPerSm) verify_weights_kernel(const __grid_constant__ VerifyArgs a, const Places w) {
+  constexpr int kVec = Elem<kType>::kVec;
+  __shared__ typename Entry<kType>::Shared entry_sh;
+  __shared__ Sums sums[kWarps];
+  __shared__ uint32_t list[kList];  // vector in the CTA's run << 8 | its heavy logits, a bit each
+  __shared__ int listed;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / w.parts, part = blockIdx.x - b * w.parts;
+  if (tid == 0) listed = 0;
+  cudaGridDependencySynchronize();
+  Entry<kType> entry(entry_sh, a, w.slices);
+  const Stop s = entry.stop(b, part == 0);
+  const int place = w.of(a, b);
+  if (part == 0 && tid == 0 && s.row >= 0) w.stops[place] = s;
+  if (!s.drawn) return;
+  const Weights<kType> weights(a, entry, s, Scale(a.temperature[b]));
+  const int run = weights.run_length(w.parts * kWarps), v_cta = part * kWarps * run;
+  const int v0 = min(v_cta + warp * run, weights.vectors()), v1 = min(v0 + run, weights.vectors());
+  Sums own{0, 0, 0, 0};
+  typename Weights<kType>::Raw next;
+  if (v0 + lane < v1) next = weights.fetch(v0 + lane);
+#pragma unroll 1
+  for (int v = v0 + lane; v < v1; v += 32) {
+    typename Weights<kType>::Vector t;
+    float2 r[kVec / 2], p = make_float2(0.f, 0.f), q = p, slope = p;
+    weights.unpack(next, t);
+    if (v + 32 < v1) next = weights.fetch(v + 32);
+    weights.template light_weights<true>(v, t, r, p, q, slope);
+    own.weight += weights.units(Weights<kType>::sum_of(r));
+    if (weights.minus_q()) {
+      own.p += weights.units(p.x + p.y);
+      own.q += weights.units_q(q.x + q.y);
+      own.slope += weights.units_q(slope.x + slope.y);
+    }
+    if (t.heavy != 0) {
+      const int at = atomicAdd(&listed, 1);
+      if (at < kList) {
+        list[at] = static_cast<uint32_t>(v - v_cta) << 8 | t.heavy;
+      } else {
+#pragma unroll 1
+        for (uint32_t bits = t.heavy; bits != 0; bits &= bits - 1) weights.add_heavy(own, v * kVec + __ffs(bits) - 1);
+      }
+    }
   }
-  if (ctas > 1) cluster.sync();  // no CTA leaves while another may still write to its shared memory
+  own.weight = warp_sum(own.weight);
+  if (weights.minus_q()) {
+    own.p = warp_sum(own.p);
+    own.q = warp_sum(own.q);
+    own.slope = warp_sum(own.slope);
+  }
+  if (lane == 0) sums[warp] = own;
+  __syncthreads();
+  // the heavy tokens, evenly over the threads; integer sums do not depend on the order
+  for (int i = tid; i < min(listed, kList); i += kThreads) {
+    const int in_cta = static_cast<int>(list[i] >> 8);
+    Sums some{0, 0, 0, 0};
+#pragma unroll 1
+    for (uint32_t bits = list[i] & 0xffu; bits != 0; bits &= bits - 1)
+      weights.add_heavy(some, (v_cta + in_cta) * kVec + __ffs(bits) - 1);
+    Sums& to = sums[in_cta / run];
+    atomicAdd(&to.weight, some.weight);
+    if (weights.minus_q()) {
+      atomicAdd(&to.slope, some.slope);
+      atomicAdd(&to.p, some.p);
+      atomicAdd(&to.q, some.q);
+    }
+  }
+  __syncthreads();
+  if (tid < kWarps) w.sums[(static_cast<int64_t>(place) * w.parts + part) * kWarps + tid] = sums[tid];
+}
+
+struct DrawShared {
+  u64 scan[2][kWarps];
+  int found, spare;
+};
+
+// Inclusive sum over the CTA's threads, and its total; the buffers alternate.
+SA_DEV u64 block_scan(DrawShared& sh, int turn, u64 x, u64& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 other = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += other;
+  }
+  u64* sums = sh.scan[turn & 1];
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  total = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) x += sums[w];
+    total += sums[w];
+  }
+  return x;
+}
+
+// CTA: draws entry b's last token.
+template <int kType>
+__global__ void __launch_bounds__(kThreads) verify_draw_kernel(const __grid_constant__ VerifyArgs a, const Places w) {
+  constexpr int kVec = Elem<kType>::kVec;
+  __shared__ typename Entry<kType>::Shared entry_sh;
+  __shared__ DrawShared sh;
+  __shared__ int holder_sh;
+  __shared__ u64 before_sh;
+  const int tid = threadIdx.x, b = blockIdx.x;
+  const int end = min(a.cu[b + 1], a.rows);
+  if (end <= max(a.cu[b], 0)) return;
+  const int place = w.of(a, b);
+  cudaGridDependencySynchronize();
+  const Stop s = w.stops[place];
+  if (!s.drawn) return;
+  const Entry<kType> entry(entry_sh, a, w.slices);
+  const Scale sc(a.temperature[b]);
+  Weights<kType> weights(a, entry, s, sc);
+  const float u = unit_of(a.u[end - 1]);
+  const auto target_of = [&](u64 total) {  // floor(total u), below total
+    return __umul64hi(total << 4, static_cast<u64>(u * 4294967296.f) << 28);
+  };
+  int turn = 0;
+  const int runs = w.parts * kWarps;  // <= kThreads
+  static_assert(kMaxParts * kWarps <= kThreads, "a run to each thread");
+  Sums mine{0, 0, 0, 0};
+  if (tid < runs) mine = w.sums[static_cast<int64_t>(place) * runs + tid];
+  if (weights.minus_q()) {
+    u64 p, q;
+    block_scan(sh, turn++, mine.p, p);
+    block_scan(sh, turn++, mine.q, q);
+    weights.set_ratio(p, q);
+  }
+  u64 total, target, before = 0;
+  int first = 0, last = weights.vectors();  // the vectors among which the token is
+  const u64 run_weight = weights.exact(mine), upto = block_scan(sh, turn++, run_weight, total);
+  if (tid == 0) sh.found = 0, sh.spare = -1;
+  if (total > 0) {
+    // the run that holds the place drawn
+    target = target_of(total);
+    if (target >= upto - run_weight && target < upto) holder_sh = tid, before_sh = upto - run_weight;
+    __syncthreads();
+    const int run = weights.run_length(runs);
+    first = min(holder_sh * run, last);
+    last = min(first + run, last);
+    before = before_sh;
+  } else {
+    // nothing is left of w: the target's own probabilities, over the whole row
+    weights.make_plain();
+    u64 sum = 0;
+    for (int v = tid; v < last; v += kThreads) {
+      typename Weights<kType>::Vector t;
+      float2 r[kVec / 2];
+      sum += weights.vector_weight(v, t, r);
+    }
+    block_scan(sh, turn++, sum, total);
+    target = target_of(total);
+  }
+  // A vector to each thread.  With the exact ratio they may come to a few units
+  // less than the run did: then (pass 1) the last token that weighs something
+  // is taken, or that p allows.
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int v0 = first; v0 < last; v0 += kThreads) {
+      const int v = v0 + tid;
+      typename Weights<kType>::Vector t;
+      float2 r[kVec / 2];
+      t.heavy = 0;
+      const u64 weight = v < last ? weights.vector_weight(v, t, r) : 0;
+      u64 all, at = 0;
+      if (pass == 0) {
+        at = before + block_scan(sh, turn++, weight, all) - weight;
+        before += all;
+      }
+      if (v < last && (pass == 1 || (target >= at && target < at + weight))) {
+        int token = -1, any = -1, allowed = -1;
+        float f[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) f[e] = e & 1 ? r[e / 2].y : r[e / 2].x;
+#pragma unroll 1
+        for (int e = 0; e < kVec && v * kVec + e < a.vocab; ++e) {
+          const int index = v * kVec + e;
+          const u64 m = t.heavy >> e & 1u ? weights.heavy_weight(index) : weights.units(f[0]);
+          if (token < 0 && target < at + m) token = index;
+          if (m > 0 || f[0] > 0.f) any = index;
+          if (weights.x_at(index) > -INFINITY) allowed = index;
+          at += m;
+#pragma unroll
+          for (int k = 0; k + 1 < kVec; ++k) f[k] = f[k + 1];
+        }
+        if (pass == 0) {
+          sh.spare = token < 0 ? any : token;
+          sh.found = 1;
+        } else {
+          atomicMax(&sh.spare, any >= 0 ? 1 << 18 | any : allowed);
+        }
+      }
+      if (pass == 0 && target < before) break;
+    }
+    __syncthreads();
+    if (sh.found) break;
+  }
+  if (tid == 0 && sh.spare >= 0) {
+    const int token = sh.spare & ((1 << 18) - 1);
+    a.tokens[s.row] = token;
+    a.logp[s.row] = log_share(weights.x_at(token), s.p, sc);
+  }
 }
 
 // Vectors of a row however it is aligned, in turns of a CTA.
@@ -945,28 +993,42 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
   slices = ceil_div(all, turns);
   if (items > 0)
     verify_rows_kernel<kType><<<static_cast<unsigned>(items * slices), kStatThreads, 0, s>>>(a, slices, turns);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  // Enough CTAs for a sequence to be quick, not so many that the batch comes in several turns.
-  int ctas = 1;
-  while (ctas < kMaxCluster && ctas * 8192 < a.vocab && 2LL * ctas * a.num_seqs <= 2 * device_sms() * kPerSm) ctas *= 2;
+  // An entry in parts of eight vectors a thread at least, four where there are few entries, and in no more than three
+  // turns of what the GPU holds at once (not all entries have anything to draw).
+  const int wave = kWeightsPerSm * device_sms();
+  int parts = 1;
+  while (parts < kMaxParts && 2LL * parts * a.num_seqs <= 3LL * wave &&
+         parts * kThreads * (4LL * parts * a.num_seqs <= wave ? 4 : 8) * Elem<kType>::kVec < a.vocab)
+    parts *= 2;
+  Places w;
+  w.slices = slices;
+  w.parts = parts;
+  uint8_t* behind = reinterpret_cast<uint8_t*>(a.parts) +
+                    static_cast<size_t>(a.rows) * 2 * most_slices(kType, a.vocab) * sizeof(float4);
+  w.by_row = a.num_seqs > a.rows;
+  w.stops = reinterpret_cast<Stop*>(behind);
+  w.sums = reinterpret_cast<Sums*>(behind + static_cast<size_t>(std::min(a.rows, kKv4MaxRequests)) * sizeof(Stop));
+  // Each waits for the one before on the device, so that its launch does not come on top.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * ctas);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * parts);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, verify_draw_kernel<kType>, a, slices);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, verify_weights_kernel<kType>, a, w);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs));
+  return cudaLaunchKernelEx(&cfg, verify_draw_kernel<kType>, a, w);
 }
 
 }  // namespace
 
 size_t verify_workspace_bytes(int dtype, int rows, int vocab) {
-  return static_cast<size_t>(rows) * 2 * most_slices(dtype, vocab) * sizeof(float4);
+  return static_cast<size_t>(rows) * 2 * most_slices(dtype, vocab) * sizeof(float4) +
+         static_cast<size_t>(std::min(rows, kKv4MaxRequests)) * (sizeof(Stop) + kMaxParts * kWarps * sizeof(Sums));
 }
 
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s) {

@@ -102,7 +102,7 @@ def test_decode_refuses(lib):
 def test_verify_refuses(lib):
     f = FAKE
     ws = lib.sinkattn_verify_workspace_size(0, 5, 10)
-    assert ws == 5 * 2 * 16
+    assert ws == 5 * (2 * 16 + 48 + 16 * 8 * 32)  # a slice of 16 bytes per row and draft row, what an entry stops with, its runs
 
     def call(x=f, xs=10, y=f, ys=10, dtype=0, rows=5, drafts=3, vocab=10, d=f, cu=f, n=2, u=f, t=f, tokens=f, logp=f, acc=f,
              rej=f, w=f, size=ws):
