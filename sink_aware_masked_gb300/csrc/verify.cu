@@ -145,7 +145,8 @@ struct Scale {
 // ---------------------------------------------------------------- all rows
 constexpr int kStatThreads = 256;
 constexpr int kStatWarps = kStatThreads / 32;
-constexpr int kStatVecs = 8;       // 16-byte vectors that a thread has in flight
+constexpr int kStatVecs = 4;       // 16-byte vectors that a thread works on, and as many that are on their way
+constexpr int kStatPerSm = 4;      // CTAs that an SM holds
 constexpr int kStatMostVecs = 32;  // vectors of a thread, at most about (more slices where rows are few)
 
 // A thread's running sum of 2^((x - top) scale).
@@ -201,7 +202,7 @@ SA_DEV void add_powers(Running& r, const uint4 (&w)[kStatVecs], float scale) {
 // `index`.  The row is on its way while the first warp finds the sequence that
 // it belongs to.
 template <int kType>
-__global__ void __launch_bounds__(kStatThreads, 3) verify_rows_kernel(const VerifyArgs a, int slices, int turns) {
+__global__ void __launch_bounds__(kStatThreads, kStatPerSm) verify_rows_kernel(const VerifyArgs a, int slices, int turns) {
   typedef Elem<kType> E;
   typedef typename E::T T;
   __shared__ float4 red[kStatWarps];
@@ -273,7 +274,10 @@ __global__ void __launch_bounds__(kStatThreads, 3) verify_rows_kernel(const Veri
   if (!sc.valid || (draft && sc.greedy)) return;
   Running r{kLowest, 0.f};
   int arg = 0x7fffffff;
-  for (int v = v0 + tid;;) {
+  for (int v = v0 + tid;; v += kStatVecs * kStatThreads) {
+    const bool more = v - tid + kStatVecs * kStatThreads < v1;
+    uint4 next[kStatVecs];
+    if (more) load_some(v + kStatVecs * kStatThreads, next);  // on their way meanwhile
     const float before = r.top;
     add_powers<kType>(r, w, sc.hi);
     if (sc.greedy && (r.top > before || arg == 0x7fffffff)) {  // the first of the largest so far
@@ -287,9 +291,9 @@ __global__ void __launch_bounds__(kStatThreads, 3) verify_rows_kernel(const Veri
           if (f[e] == r.top) arg = (v + i * kStatThreads) * E::kVec + e - shift;
       }
     }
-    v += kStatVecs * kStatThreads;
-    if (v - tid >= v1) break;
-    load_some(v, w);
+    if (!more) break;
+#pragma unroll
+    for (int i = 0; i < kStatVecs; ++i) w[i] = next[i];
   }
   const float top = warp_max(r.top);
   const float sum = warp_sum(r.sum * ex2((r.top - top) * sc.hi));
@@ -983,12 +987,12 @@ int most_slices(int dtype, int vocab) { return ceil_div(turns_for(dtype, vocab),
 template <int kType>
 cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
   const long long items = a.rows + (a.draft_logits != nullptr ? a.num_drafts : 0);
-  // A row in as few slices as keep the GPU busy (3 CTAs an SM, a few turns of them), each a whole number of turns that
+  // A row in as few slices as keep the GPU busy (what it holds at once, a few times), each a whole number of turns that
   // a thread has in flight, so that none is nearly empty.
   const int all = turns_for(kType, a.vocab);
   int slices = std::max(ceil_div(all, kStatMostVecs), 1);
   if (items > 0)
-    slices = std::max(slices, static_cast<int>(std::min<long long>(most_slices(kType, a.vocab), 9LL * device_sms() / items)));
+    slices = std::max(slices, static_cast<int>(std::min<long long>(most_slices(kType, a.vocab), 3LL * kStatPerSm * device_sms() / items)));
   const int turns = ceil_div(ceil_div(all, slices), kStatVecs) * kStatVecs;
   slices = ceil_div(all, turns);
   if (items > 0)
