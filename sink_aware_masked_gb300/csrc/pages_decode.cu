@@ -21,7 +21,7 @@
 // gives its value exactly; lse takes the fp32 sum of the unrounded ones.
 //
 // Work: the visible turns (32 tokens) of all (sequence, kv head) pairs in one
-// line, cut into equal shares, one per worker.  A worker is a CTA, whose warps
+// line, each as long as it costs, cut into equal shares, one per worker.  A worker is a CTA, whose warps
 // take a pair's turns in turn and merge in shared memory; or, where there are
 // many pairs with few turns each, a single warp, which takes whole pairs.  A
 // pair cut between CTAs leaves partial results in the workspace, and the last
@@ -32,6 +32,7 @@
 #include "tmap.h"
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 
@@ -48,8 +49,9 @@ constexpr int kPartPad = 4;                        // floats of statistics per r
 // Partial rows that the CTAs of one SM can leave in the workspace: two cut pairs each.
 constexpr int kPartRowsPerSm = 256;
 
-// What beginning a pair costs a CTA, in turns.
-constexpr int kPairCost = 6;
+// What a turn costs a CTA, in places of the line that is shared out, and a tile
+// of 8 rows on top; what beginning a pair costs.
+constexpr int kTurnCost = 7, kTileCost = 2, kPairCost = 60;
 // Turns of the longest pair up to which warps work alone, each on whole pairs.
 constexpr int kAloneTurns = 24;
 
@@ -123,10 +125,14 @@ SA_DEV Seq sequence(const PageDecK& p, int b) {
   return s;
 }
 
+// What a turn of a sequence costs.
+SA_DEV int turn_cost(const Seq& q) { return kTurnCost + kTileCost * ((q.rows + 7) / 8); }
+
 // The turns of a sequence that its last n positions can see: [0, pre) and [lo, end).
 struct Span {
   int pre, lo, end;
-  SA_DEV int count() const { return pre + end - lo; }
+  // at least 1: an empty sequence's rows are written too
+  SA_DEV int count() const { return max(pre + end - lo, 1); }
   SA_DEV int turn(int i) const { return i < pre ? i : i - pre + lo; }
 };
 
@@ -143,7 +149,7 @@ SA_DEV Span visible_span(const PageDecK& p, const Seq& q) {
 // The part of a pair that a worker takes: turns [t0, t1) of `turns`.
 struct Segment {
   long long x;  // where its pair begins in the line that is shared out
-  int b, head, t0, t1, turns;
+  int b, head, t0, t1, turns, cost;
   Seq seq;
   Span span;
 };
@@ -347,13 +353,13 @@ SA_DEV void move_reference(Rows<NT>& r, int nt, int e, float top, float coef, fl
 template <int NT, int kFirst, int HT, bool kMasked, class Pos>
 SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2], int tiles, float coef, float slack,
                       const Pos& pos, const Turn& turn, int window, int prefix) {
-  constexpr int U = kTurn / 16;
-  constexpr bool kSkip = NT > 2;  // tiles without rows are left out
+  constexpr int U = kTurn / 16, kEnd = kFirst + HT;
+  constexpr bool kSkip = NT > 1;  // tiles without rows are left out
   const int lane = threadIdx.x & 31, g = lane >> 2;
   // Rows of 128 bytes, 16-byte chunks XORed with the row's low three bits.
   const uint32_t row_k = (lane & 7) + (lane & 8), chunk_k = lane >> 4;
   const uint32_t row_v = (lane & 7) + (lane >> 4) * 8, chunk_v = lane >> 3 & 1;
-  // scores before the coefficient: s[u][nt][e] key g of block u, s[u][nt][2 + e] key g + 8, row 2 t + e
+  // scores before the coefficient: s[u][nt - kFirst][e] key g of block u, s[u][nt - kFirst][2 + e] key g + 8, row 2 t + e
   float s[U][HT][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -362,28 +368,28 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
       uint32_t a[4];
       ldsm_x4(keys + (16 * u + row_k) * 128 + (((2 * j + chunk_k) ^ (lane & 7)) << 4), a[0], a[1], a[2], a[3]);
 #pragma unroll
-      for (int nt = 0; nt < HT; ++nt) {
-        if (kSkip && kFirst + nt >= tiles) continue;
+      for (int nt = kFirst; nt < kEnd; ++nt) {
+        if (kSkip && nt >= tiles) continue;
         if (j == 0)
-          mma_first(s[u][nt], a, qf[nt][j][0], qf[nt][j][1]);
+          mma_first(s[u][nt - kFirst], a, qf[nt - kFirst][j][0], qf[nt - kFirst][j][1]);
         else
-          mma16816(s[u][nt], a, qf[nt][j][0], qf[nt][j][1]);
+          mma16816(s[u][nt - kFirst], a, qf[nt - kFirst][j][0], qf[nt - kFirst][j][1]);
       }
     }
   bool move = false;
   float top[HT][2];
 #pragma unroll
-  for (int nt = 0; nt < HT; ++nt) {
-    if (kSkip && kFirst + nt >= tiles) continue;
+  for (int nt = kFirst; nt < kEnd; ++nt) {
+    if (kSkip && nt >= tiles) continue;
     if (kMasked) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint32_t bits = seen_bits(pos(kFirst + nt, e), turn.key0, window, prefix) >> g;
+        const uint32_t bits = seen_bits(pos(nt, e), turn.key0, window, prefix) >> (g);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float& x = s[u][nt][2 * h + e];
+            float& x = s[u][nt - kFirst][2 * h + e];
             if (!(turn.loaded >> u & 1)) x = __int_as_float(0x7fffffff);  // its page is not in the pool
             if (!(bits >> (16 * u + 8 * h) & 1u)) x = -INFINITY;
           }
@@ -391,37 +397,38 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      top[nt][e] = fmaxf(fmax3(s[0][nt][e], s[0][nt][2 + e], s[1][nt][e]), s[1][nt][2 + e]);
-      const float ref = e ? r.ref[kFirst + nt].y : r.ref[kFirst + nt].x;
-      move |= top[nt][e] > ref + slack || (ref == kUnseen && top[nt][e] > kUnseen);
+      top[nt - kFirst][e] = fmaxf(s[0][nt - kFirst][e], s[0][nt - kFirst][2 + e]);
+#pragma unroll
+      for (int u = 1; u < U; ++u) top[nt - kFirst][e] = fmax3(top[nt - kFirst][e], s[u][nt - kFirst][e], s[u][nt - kFirst][2 + e]);
+      const float ref = e ? r.ref[nt].y : r.ref[nt].x;
+      move |= top[nt - kFirst][e] > ref + slack || (ref == kUnseen && top[nt - kFirst][e] > kUnseen);
     }
   }
   if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
-    for (int nt = 0; nt < HT; ++nt) {
-      if (kSkip && kFirst + nt >= tiles) continue;
-      move_reference(r, kFirst + nt, 0, top[nt][0], coef, slack);
-      move_reference(r, kFirst + nt, 1, top[nt][1], coef, slack);
+    for (int nt = kFirst; nt < kEnd; ++nt) {
+      if (kSkip && nt >= tiles) continue;
+      move_reference(r, nt, 0, top[nt - kFirst][0], coef, slack);
+      move_reference(r, nt, 1, top[nt - kFirst][1], coef, slack);
     }
   }
   uint32_t pf[U][HT][2];
 #pragma unroll
-  for (int nt = 0; nt < HT; ++nt) {
-    if (kSkip && kFirst + nt >= tiles) continue;
-    const int n = kFirst + nt;
-    const float2 minus = make_float2(-r.ref[n].x, -r.ref[n].y), c2 = make_float2(coef, coef);
+  for (int nt = kFirst; nt < kEnd; ++nt) {
+    if (kSkip && nt >= tiles) continue;
+    const float2 minus = make_float2(-r.ref[nt].x, -r.ref[nt].y), c2 = make_float2(coef, coef);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         // subtracted first: the largest of huge scores has to give exactly 2^-8
-        const float2 d = fadd2(make_float2(s[u][nt][2 * h], s[u][nt][2 * h + 1]), minus);
+        const float2 d = fadd2(make_float2(s[u][nt - kFirst][2 * h], s[u][nt - kFirst][2 * h + 1]), minus);
         const float2 x = ffma2(d, c2, make_float2(-kSlack, -kSlack));
         const float2 p = make_float2(ex2(x.x), ex2(x.y));
-        r.sum[n] = fadd2(r.sum[n], p);
+        r.sum[nt] = fadd2(r.sum[nt], p);
         const uint32_t two = pack_bf16(p.x, p.y);
-        r.sum_o[n] = fadd2(r.sum_o[n], make_float2(bf16_lo(two), bf16_hi(two)));
-        pf[u][nt][h] = transpose8(two);
+        r.sum_o[nt] = fadd2(r.sum_o[nt], make_float2(bf16_lo(two), bf16_hi(two)));
+        pf[u][nt - kFirst][h] = transpose8(two);
       }
     }
   }
@@ -439,10 +446,10 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
     if (kMasked) {
       if (!(turn.loaded >> u & 1)) {  // nothing to add
 #pragma unroll
-        for (int nt = 0; nt < HT; ++nt) {
+        for (int nt = kFirst; nt < kEnd; ++nt) {
           // its keys count 0, or NaN for the rows that would see them
-          if (kSkip && kFirst + nt >= tiles) continue;
-          pf[u][nt][0] = pf[u][nt][1] = 0u;
+          if (kSkip && nt >= tiles) continue;
+          pf[u][nt - kFirst][0] = pf[u][nt - kFirst][1] = 0u;
         }
       }
       uint32_t ones = 0u;
@@ -461,21 +468,21 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int nt = 0; nt < HT; ++nt) {
-        if (kSkip && kFirst + nt >= tiles) continue;
-        mma16816(r.o[kFirst + nt][i], a[i], pf[u][nt][0], pf[u][nt][1]);
+      for (int nt = kFirst; nt < kEnd; ++nt) {
+        if (kSkip && nt >= tiles) continue;
+        mma16816(r.o[nt][i], a[i], pf[u][nt - kFirst][0], pf[u][nt - kFirst][1]);
       }
   }
   if (kMasked && odd) {
 #pragma unroll 1
-    for (int key = 0; key < kTurn; ++key) {
+    for (int key = 0; key < 16 * U; ++key) {
       if (!(turn.loaded >> (key >> 4) & 1)) continue;  // its rows are NaN by their scores
       uint32_t sees = 0;
 #pragma unroll
-      for (int nt = 0; nt < HT; ++nt)
+      for (int nt = kFirst; nt < kEnd; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          sees |= (seen_bits(pos(kFirst + nt, e), turn.key0, window, prefix) >> key & 1u) << (2 * nt + e);
+          sees |= (seen_bits(pos(nt, e), turn.key0, window, prefix) >> (key) & 1u) << (2 * nt + e);
       const uint32_t row = keys + kTurnHalf + key * 128;
 #pragma unroll
       for (int d = 0; d < 8; ++d) {  // dims 8 d + g: [d / 2][2 (d % 2) + e]
@@ -483,9 +490,9 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
         asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(two) : "r"(row + ((d ^ (key & 7)) << 4) + 2 * g));
         const float v = (two & 0x7f80u) == 0x7f80u ? bf16_lo(two) : 0.f;
 #pragma unroll
-        for (int nt = 0; nt < HT; ++nt)
+        for (int nt = kFirst; nt < kEnd; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) r.o[kFirst + nt][d >> 1][2 * (d & 1) + e] += sees >> (2 * nt + e) & 1u ? v : 0.f;
+          for (int e = 0; e < 2; ++e) r.o[nt][d >> 1][2 * (d & 1) + e] += sees >> (2 * nt + e) & 1u ? v : 0.f;
       }
     }
   }
@@ -639,13 +646,13 @@ struct Cut {  // a pair that other workers have parts of
 
 constexpr int kUptoStep = 4;  // every fourth sequence's place in the line is kept
 
-// How a CTA is made up.  NT: tiles of 8 rows a warp has, taken in halves from
-// five on (the queries of a half come from shared memory then); kShare: warps
-// that share a ring and split the tiles; kTeams: rings of a CTA.
+// How a CTA is made up.  NT: tiles of 8 rows a warp has (above four it takes a
+// turn in two halves of them, and a half's queries from shared memory); kShare: warps that share a
+// ring and split the tiles; kTeams: rings of a CTA.
 template <int NT_, int kShare_, int kTeams_, int kStages_, int kPerSm_>
 struct Shape {
   static constexpr int NT = NT_, kShare = kShare_, kTeams = kTeams_, kStages = kStages_, kPerSm = kPerSm_;
-  static constexpr int kHalves = NT > 4 ? 2 : 1, HT = NT / kHalves;
+  static constexpr int HT = NT > 4 ? NT / 2 : NT;
   static constexpr int kWarps = kShare * kTeams, kThreads = kWarps * 32;
   static constexpr int kRows = 8 * NT * kShare;
   // Teams that merge by rows in shared memory; where there are twice as many, the others' results are added to
@@ -657,18 +664,18 @@ struct Shape {
   static constexpr int kPartFloats = kRows * (kHeadDim + kPartPad);
   static constexpr size_t kRing = static_cast<size_t>(kTeams) * kStages * kTurnBytes;
   static constexpr size_t kMerge = static_cast<size_t>(kSlots) * kRows * (kRowPad * 4 + 16);
-  static constexpr size_t kQueries = kHalves > 1 ? kRows * kHeadDim * 2 : 0;
+  static constexpr size_t kQueries = HT < NT ? kRows * kHeadDim * 2 : 0;
   static_assert(2 * kPerSm * kRows <= kPartRowsPerSm, "the workspace has no room for every CTA's cut pairs");
 };
 
 // The warp's query rows in registers: lane (g, t) has dims 16 j + 2 t, + 1 and
 // + 8, + 9 of row g of each tile (tile nt is number nt * step + first of the pair's).
-template <int HT>
+template <int NT>
 SA_DEV void load_queries(const PageDecK& p, const Seq& q, int head, int rows, int first, int step,
-                         uint32_t (&qf)[HT][4][2]) {
+                         uint32_t (&qf)[NT][4][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int nt = 0; nt < HT; ++nt) {
+  for (int nt = 0; nt < NT; ++nt) {
     const int row = 8 * (nt * step + first) + g;
 #pragma unroll
     for (int j = 0; j < 4; ++j) qf[nt][j][0] = qf[nt][j][1] = 0u;
@@ -702,7 +709,7 @@ SA_DEV void fetch_queries(uint32_t queries, int first, int step, uint32_t (&qf)[
 // kAlone: every warp takes whole pairs, by the host's word that all are short.
 template <class S, bool kAlone>
 __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const __grid_constant__ PageDecK p) {
-  constexpr int NT = S::NT, HT = S::HT, kShare = S::kShare, kTeams = S::kTeams, kStages = S::kStages;
+  constexpr int NT = S::NT, kShare = S::kShare, kTeams = S::kTeams, kStages = S::kStages;
   constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kRows = S::kRows, kSlots = S::kSlots, kDims = S::kDims;
   constexpr bool kMayAlone = kShare == 1 && NT <= 2;
   static_assert(!kAlone || kMayAlone, "a warp alone has the tiles of all rows");
@@ -717,6 +724,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
   __shared__ long long warp_sum[kWarps];
   __shared__ __align__(8) uint64_t bars[kTeams * 2 * kStages];
   __shared__ Cut cuts[2];
+  __shared__ Segment segments[2][kWarps];  // a warp's segment and its next one: registers are short while turns are taken
   __shared__ int last_sh[2], abort_flag;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int team = warp / kShare, share = warp % kShare;
@@ -733,16 +741,21 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
     tc::tma_prefetch_map(&p.tm_k);
     tc::tma_prefetch_map(&p.tm_v);
   }
-  // turns per sequence (an empty one counts as one: its rows are written too) and their running total
-  long long turns_all = 0;
+  // what the sequences' turns cost, and its running total
+  long long cost_all = 0;
   bool alone = kAlone;
   if (!kAlone) {
     int longest = 0;
     for (int base = 0; base < p.num_seqs; base += kThreads) {
       const int b = base + tid;
-      long long x = b < p.num_seqs ? max(visible_span(p, sequence(p, b)).count(), 1) : 0;
+      long long x = 0;
+      if (b < p.num_seqs) {
+        const Seq q = sequence(p, b);
+        const int count = visible_span(p, q).count();
+        longest = max(longest, count);
+        x = static_cast<long long>(count) * turn_cost(q);
+      }
       const long long mine = x;
-      longest = max(longest, static_cast<int>(x));
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -750,10 +763,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
       }
       if (lane == 31) warp_sum[warp] = x;
       __syncthreads();
-      long long before = turns_all;
+      long long before = cost_all;
       for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += warp_sum[w];
-        turns_all += warp_sum[w];
+        cost_all += warp_sum[w];
       }
       if (b < p.num_seqs && b % kUptoStep == 0) upto[b / kUptoStep] = before + x - mine;
       __syncthreads();
@@ -766,7 +779,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
   }
 
   const float slack = __fdividef(kSlack, p.coef);
-  const uint32_t q_sh = smem_u32(queries);
   Stream<kShare, kStages> stream(p, smem_u32(smem) + team * kStages * kTurnBytes, smem_u32(&bars[team * 2 * kStages]),
                                  tc::Abort{&abort_flag, p.status}, alone ? 0 : team, alone ? 1 : kTeams, share == 0);
   Rows<NT> r;
@@ -774,8 +786,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
   const auto process = [&](const Segment& seg) {
     const int rows = seg.seq.rows;
     const int tiles = min(max(((rows + 7) / 8 - share + kShare - 1) / kShare, 0), NT);
-    uint32_t qf[HT][4][2];
-    if (S::kHalves == 1) load_queries<HT>(p, seg.seq, seg.head, rows, share, kShare, qf);
+    uint32_t qf[S::HT][4][2];
+    if (S::HT == NT) load_queries<S::HT>(p, seg.seq, seg.head, rows, share, kShare, qf);
     const int first = seg.seq.len - seg.seq.n;
     const auto pos = [&](int nt, int e) {
       const int row = 8 * (nt * kShare + share) + 2 * t + e;
@@ -784,18 +796,17 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
     rows_clear(r);
     stream.run([&](uint32_t keys, const Turn& turn) {
       if (tiles == 0) return;
-      if constexpr (S::kHalves > 1) fetch_queries<HT>(q_sh, share, kShare, qf);
-      if (turn.masked)
-        turn_step<NT, 0, HT, true>(r, keys, qf, tiles, p.coef, slack, pos, turn, p.window, p.prefix);
-      else
-        turn_step<NT, 0, HT, false>(r, keys, qf, tiles, p.coef, slack, pos, turn, p.window, p.prefix);
-      if constexpr (S::kHalves > 1) {
-        if (tiles <= HT) return;
-        fetch_queries<HT>(q_sh, HT * kShare + share, kShare, qf);
+      const auto step = [&](auto first) {
+        constexpr int kFirst = decltype(first)::value;
+        if (S::HT < NT) fetch_queries<S::HT>(smem_u32(queries), kFirst * kShare + share, kShare, qf);
         if (turn.masked)
-          turn_step<NT, HT, HT, true>(r, keys, qf, tiles, p.coef, slack, pos, turn, p.window, p.prefix);
+          turn_step<NT, kFirst, S::HT, true>(r, keys, qf, tiles, p.coef, slack, pos, turn, p.window, p.prefix);
         else
-          turn_step<NT, HT, HT, false>(r, keys, qf, tiles, p.coef, slack, pos, turn, p.window, p.prefix);
+          turn_step<NT, kFirst, S::HT, false>(r, keys, qf, tiles, p.coef, slack, pos, turn, p.window, p.prefix);
+      };
+      step(std::integral_constant<int, 0>());
+      if constexpr (S::HT < NT) {
+        if (tiles > S::HT) step(std::integral_constant<int, S::HT>());
       }
     });
     // sums over the keys
@@ -826,11 +837,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
     b_first = static_cast<int>(pair / heads);
     head_first = static_cast<int>(pair - static_cast<long long>(b_first) * heads);
   } else if constexpr (!kAlone) {
-    // a turn at least for every team, unless that leaves pairs without a worker of their own
-    const long long want = max((turns_all + kTeams - 1) / kTeams, static_cast<long long>(p.num_seqs));
-    const int n_workers = heads > ctas ? 1 : static_cast<int>(min(static_cast<long long>(ctas / heads_at_once), want));
-    pad = turns_all >= 4LL * kPairCost * n_workers ? kPairCost : 0;
-    shares = Shares(turns_all + static_cast<long long>(p.num_seqs) * pad, n_workers);
+    // a turn at least for every team, unless that leaves pairs without a worker of their own; no less than the most
+    // that a turn costs, so that every share between a cut pair's first and last has a turn of it
+    constexpr int kMostCost = kTurnCost + kTileCost * NT * kShare;
+    const long long want = max(cost_all / (kTeams * (kTurnCost + kTileCost)), static_cast<long long>(p.num_seqs));
+    const int n_workers = heads > ctas ? 1 : static_cast<int>(max(min(min(static_cast<long long>(ctas / heads_at_once), want),
+                                                                      cost_all / kMostCost), 1LL));
+    pad = cost_all >= 4LL * kPairCost * n_workers ? kPairCost : 0;
+    shares = Shares(cost_all + static_cast<long long>(p.num_seqs) * pad, n_workers);
     if (group >= n_workers) return;
     x_begin = shares.start(group);
     x_end = shares.start(group + 1);
@@ -842,14 +856,17 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
       else
         hi = mid - 1;
     }
+    // the first pair that the share holds a turn of
     b_first = lo * kUptoStep;
     x_first = upto[lo] + static_cast<long long>(b_first) * pad;
 #pragma unroll 1
-    for (int i = 1; i < kUptoStep && b_first + 1 < p.num_seqs; ++i) {
-      const long long next = x_first + max(visible_span(p, sequence(p, b_first)).count(), 1) + pad;
-      if (next > x_begin) break;
-      x_first = next;
+    while (true) {
+      const Seq q = sequence(p, b_first);
+      const int count = visible_span(p, q).count(), cost = turn_cost(q);
+      if (x_first + pad + static_cast<long long>(count - 1) * cost >= x_begin) break;
+      x_first += pad + static_cast<long long>(count) * cost;
       ++b_first;
+      if (b_first >= p.num_seqs || x_first + pad >= x_end) return;  // it lies in one turn, or in what beginning a pair costs
     }
   }
   // The worker's part of a pair that begins at x of the line.
@@ -860,21 +877,28 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
     s.head = head;
     s.seq = sequence(p, b);
     s.span = visible_span(p, s.seq);
-    s.turns = s.t1 = max(s.span.count(), 1);
+    s.turns = s.t1 = s.span.count();
     s.t0 = 0;
-    if (!alone) {
-      s.t0 = static_cast<int>(max(x_begin - x - pad, 0LL));
-      s.t1 = static_cast<int>(min(static_cast<long long>(s.turns), x_end - x - pad));
+    s.cost = turn_cost(s.seq);
+    if (!alone) {  // turn t is the share's that holds place x + pad + t cost
+      s.t0 = static_cast<int>((max(x_begin - x - pad, 0LL) + s.cost - 1) / s.cost);
+      s.t1 = static_cast<int>(min(static_cast<long long>(s.turns), (x_end - x - pad + s.cost - 1) / s.cost));
     }
     return s;
   };
 
   const int merge_row = min(tid / S::kPerRow, kRows), merge_dim = tid % S::kPerRow * kDims;  // kRows: none
-  int n_cuts = 0;
-  Segment next = segment_at(b_first, head_first, x_first), done;
+  int n_cuts = 0, cur = 0;
+  // Lane 0's word for the warp's next segment.
+  const auto set_next = [&](const Segment& s) {
+    if (lane == 0) segments[cur ^ 1][warp] = s;
+    __syncwarp();
+  };
+  set_next(segment_at(b_first, head_first, x_first));
   bool first = true, more = true;
   while (true) {
-    if (more) stream.begin(next);  // on its way while the one before is finished
+    if (more) stream.begin(segments[cur ^ 1][warp]);  // on its way while the one before is finished
+    const Segment& done = segments[cur][warp];
     if (!first) {
       const int rows = done.seq.rows;
       if (kMayAlone && alone) {
@@ -889,7 +913,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
             Cut c;
             c.p0 = done.x;
             c.c0 = shares.owner(done.x + pad);
-            c.c1 = shares.owner(done.x + pad + done.turns - 1);
+            c.c1 = shares.owner(done.x + pad + static_cast<long long>(done.turns - 1) * done.cost);
             c.b = done.b;
             c.head = done.head;
             cuts[n_cuts] = c;
@@ -995,32 +1019,34 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
       }
       if (!more) break;
     }
-    done = next;
+    cur ^= 1;
     first = false;
-    if (S::kHalves > 1) {
+    if (S::HT < NT) {
       // the pair's queries into shared memory, zeros behind the last row
+      const Segment& now = segments[cur][warp];
       for (int u = tid; u < kRows * 8; u += kThreads) {
         const int row = u >> 3, c = u & 7;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (row < done.seq.rows) {
-          const int i = p.row_of_seq(row), h = done.head * p.group + row - i * p.group;
-          v = __ldg(reinterpret_cast<const uint4*>(p.q + ((static_cast<int64_t>(done.seq.row0) + i) * p.hq + h) * kHeadDim) + c);
+        if (row < now.seq.rows) {
+          const int i = p.row_of_seq(row), h = now.head * p.group + row - i * p.group;
+          v = __ldg(reinterpret_cast<const uint4*>(p.q + ((static_cast<int64_t>(now.seq.row0) + i) * p.hq + h) * kHeadDim) + c);
         }
         *reinterpret_cast<uint4*>(queries + swz(row, c)) = v;
       }
       __syncthreads();
     }
-    process(done);
+    process(segments[cur][warp]);
     if (alone) {
       pair += static_cast<long long>(ctas) * kWarps;
       more = pair < static_cast<long long>(p.num_seqs) * heads;
       const int b = more ? static_cast<int>(pair / heads) : 0;
-      if (more) next = segment_at(b, static_cast<int>(pair - static_cast<long long>(b) * heads), 0);
+      if (more) set_next(segment_at(b, static_cast<int>(pair - static_cast<long long>(b) * heads), 0));
     } else {
-      const long long x = done.x + done.turns + pad;
+      const Segment& done = segments[cur][warp];
+      const long long x = done.x + static_cast<long long>(done.turns) * done.cost + pad;
       const bool on = done.t1 == done.turns && done.b + 1 < p.num_seqs && x + pad < x_end;
       more = on || done.head + ctas < heads;  // more heads than CTAs
-      if (more) next = segment_at(on ? done.b + 1 : b_first, on ? done.head : done.head + ctas, on ? x : x_first);
+      if (more) set_next(segment_at(on ? done.b + 1 : b_first, on ? done.head : done.head + ctas, on ? x : x_first));
     }
   }
 
