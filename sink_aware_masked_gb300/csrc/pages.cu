@@ -72,17 +72,34 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPages c, 
     st.base[i] = pages_for(c, left[k]);
   }
   __syncthreads();
-  const auto entry = [&](int rank) -> int32_t* {  // the rank-th page given back, or handed out
-    const int i = request_of(sh, n, rank);
+  // where the rank-th page given back, or handed out, stands in the table; it is request i's
+  const auto entry_of = [&](int i, int rank) -> int32_t* {
     return c.block_table + static_cast<int64_t>(sh.slot[i]) * c.max_pages + st.base[i] + rank -
            (i > 0 ? sh.upto[i - 1] : 0);
   };
   const int back = scan_needs(sh, n);
-  for (int r = tid; r < back; r += kPlanThreads) {
-    int32_t* e = entry(r);
-    const int page = *e;
-    if (page >= 0 && page < c.num_pages && c.owner[page] == sh.slot[request_of(sh, n, r)]) c.owner[page] = -1;
-    *e = -1;
+  constexpr int kAtOnce = 4;  // pages whose table entries, and then owners, a thread waits for together
+  for (int r0 = tid; r0 < back; r0 += kAtOnce * kPlanThreads) {
+    int32_t* e[kAtOnce];
+    int page[kAtOnce], slot[kAtOnce], owner[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int r = r0 + k * kPlanThreads;
+      slot[k] = -1;
+      if (r >= back) continue;
+      const int i = request_of(sh, n, r);
+      slot[k] = sh.slot[i];
+      e[k] = entry_of(i, r);
+      page[k] = *e[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) owner[k] = slot[k] >= 0 && page[k] >= 0 && page[k] < c.num_pages ? c.owner[page[k]] : -1;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (slot[k] < 0) continue;
+      if (owner[k] == slot[k]) c.owner[page[k]] = -1;
+      *e[k] = -1;
+    }
   }
   __syncthreads();
   uint32_t needs = 0;
@@ -97,14 +114,15 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPages c, 
   __syncthreads();
   const int need = scan_needs(sh, n);
   const int found = hand_out<-1>(sh, c.owner, c.num_pages, need, [&](int rank, int page) {
-    *entry(rank) = page;
-    c.owner[page] = sh.slot[request_of(sh, n, rank)];
+    const int i = request_of(sh, n, rank);
+    *entry_of(i, rank) = page;
+    c.owner[page] = sh.slot[i];
   });
   __syncthreads();
   if (found < need) {  // the request in which the pages ran out, if it had begun
     const int i = request_of(sh, n, found);
     for (int r = (i > 0 ? sh.upto[i - 1] : 0) + tid; r < found; r += kPlanThreads) {
-      int32_t* e = entry(r);
+      int32_t* e = entry_of(i, r);
       c.owner[*e] = -1;
       *e = -1;
     }
@@ -145,17 +163,34 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const KvPages c, 
   }
 }
 
-// The rows' places from what the plan left: a served slot's length counts its new tokens.
+// The rows' places from what the plan left: a served slot's length counts its
+// new tokens.  Two warps look for the entries of the CTA's first and last row,
+// the threads between those.
 __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(const KvPages c, const KvPlanArgs a) {
-  const int first = blockIdx.x * (kMapThreads * kMapPer);
+  __shared__ int range[2];
+  const int first = blockIdx.x * (kMapThreads * kMapPer), tid = threadIdx.x, lane = tid & 31;
+  cudaGridDependencySynchronize();
   const int rows = a.cu[a.n];
+  if (tid < 64) {  // the number of entries that end at or before the row: 32 probes at a time
+    const int row = tid < 32 ? first : min(first + kMapThreads * kMapPer, a.total) - 1;
+    int lo = 0, hi = a.n;  // the answer lies in [lo, hi]
+    while (lo < hi) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const uint32_t done = __ballot_sync(0xffffffffu, at < hi && a.cu[min(at, a.n - 1) + 1] <= row);
+      const int k = __popc(done);  // probes 0 .. k - 1 end before it
+      if (k < 32) hi = min(hi, lo + k * step);
+      if (k > 0) lo += (k - 1) * step + 1;
+    }
+    if (lane == 0) range[tid >> 5] = lo;
+  }
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < kMapPer; ++k) {
-    const int row = first + k * kMapThreads + threadIdx.x;
+    const int row = first + k * kMapThreads + tid;
     if (row >= a.total) break;
     int slot = -1, pos = 0;
     if (row < rows) {
-      int lo = 0, hi = a.n - 1;  // the first with cu[i + 1] > row
+      int lo = range[0], hi = min(range[1], a.n - 1);  // the first with cu[i + 1] > row
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (a.cu[mid + 1] > row)
@@ -214,9 +249,19 @@ cudaError_t launch_kv_plan(const KvPages& c, const KvPlanArgs& a, cudaStream_t s
   cudaError_t e = opt_in(kv_plan_kernel, sizeof(StepShared));
   if (e != cudaSuccess) return e;
   kv_plan_kernel<<<1, kPlanThreads, sizeof(StepShared), s>>>(c, a);
-  if (a.total > kRowsInPlan)
-    kv_map_kernel<<<ceil_div(a.total, kMapThreads * kMapPer), kMapThreads, 0, s>>>(c, a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.total <= kRowsInPlan) return e;
+  // waits for the plan on the device, so that its launch does not come on top
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ceil_div(a.total, kMapThreads * kMapPer));
+  cfg.blockDim = dim3(kMapThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_map_kernel, c, a);
 }
 
 cudaError_t launch_kv_write(const KvPages& c, const KvWriteArgs& a, cudaStream_t s) {

@@ -1146,7 +1146,7 @@ cudaError_t launch_kv_decode(const KvPages& c, const KvDecodeArgs& a, int* statu
                                       : ceil_div(std::min<long long>(a.prefix, table), kTurn) +
                                             ceil_div(static_cast<long long>(a.window) + a.n, kTurn) + 1;
   const bool alone = most <= kAloneTurns && static_cast<long long>(a.num_seqs) * c.num_heads_kv >= device_sms();
-  if (rows <= 8) return alone ? launch_kernel<Shape<1, 1, 4, 2, 3>, true>(p, s) : launch_kernel<Shape<1, 1, 4, 3, 2>, false>(p, s);
+  if (rows <= 8) return alone ? launch_kernel<Shape<1, 1, 4, 2, 3>, true>(p, s) : launch_kernel<Shape<1, 1, 4, 2, 2>, false>(p, s);
   if (rows <= 16) return alone ? launch_kernel<Shape<2, 1, 4, 2, 3>, true>(p, s) : launch_kernel<Shape<2, 1, 4, 2, 2>, false>(p, s);
   if (rows <= 32) return launch_kernel<Shape<4, 1, 4, 2, 2>, false>(p, s);
   if (rows <= 48) return launch_kernel<Shape<6, 1, 8, 2, 1>, false>(p, s);

@@ -94,6 +94,8 @@ def kv_plan(pages: KVPages, slots, new_tokens, total: int, *, drop=None, live=No
     batch).  A slot that drops all it has is freed.
     """
     dev, i32, total = pages.device, torch.int32, int(total)
+    if total < 0:
+        raise ValueError(f"total must not be negative ({total})")
     n = _vector("slots", slots, i32, dev)
     sp, np_ = _tensor("slots", slots, i32, (n,), dev), _tensor("new_tokens", new_tokens, i32, (n,), dev)
     dp = None if drop is None else _tensor("drop", drop, i32, (n,), dev)
