@@ -469,7 +469,8 @@ sinkattn_status sinkattn_kv_decode_fwd(const sinkattn_kv_pages* pages, const int
  * Rows outside every entry's are left as they were; an entry without rows has
  * accepted = rejected = 0.
  * Logits of -inf are never drawn; so a choice of tokens (a grammar, a top-k) is
- * made by -inf in both rows.  A draft outside [0, vocab) does not stand.  An
+ * made by -inf in both rows.  p and q below 2^-1074 of their largest count as
+ * 0.  A draft outside [0, vocab) does not stand.  An
  * entry ends with token -1 at a row of nothing but -inf (logp -inf), and at a
  * row with a NaN or +inf logit, a draft row of such kind or of nothing but -inf,
  * or a temperature that is NaN, negative or above 1e36 (logp NaN).  u outside

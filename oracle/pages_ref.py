@@ -127,7 +127,7 @@ def verify(x, y, drafts, u, temperature):
                 elif inside:
                     q[d] = 1.0
                 stands = inside and clamp(u[i]) * q[d] < p[0][d]
-                if inside:
+                if inside and p[0][d] > 0:  # (what the target never gives never stands)
                     border = min(border, abs(clamp(u[i]) * q[d] - p[0][d]))
             if stands:
                 tokens[i], logp[i] = d, p[1][d]

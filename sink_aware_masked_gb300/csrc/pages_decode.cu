@@ -78,10 +78,17 @@ struct PageDecK {
 
 // D = A B, A 16 x 16 (keys), B 16 x 8.
 SA_DEV void mma_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// D += A B; nothing keeps the compiler from moving it among the loads.
+SA_DEV void mma_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // 8x8 16-bit transpose across the warp.
@@ -361,21 +368,30 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
   const uint32_t row_v = (lane & 7) + (lane >> 4) * 8, chunk_v = lane >> 3 & 1;
   // scores before the coefficient: s[u][nt - kFirst][e] key g of block u, s[u][nt - kFirst][2 + e] key g + 8, row 2 t + e
   float s[U][HT][4];
+  constexpr int kAhead = NT <= 2 ? 4 : 1;  // chunks of 16 dims that are loaded before their products
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j0 = 0; j0 < 4; j0 += kAhead) {
+    uint32_t ka[U][kAhead][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      uint32_t a[4];
-      ldsm_x4(keys + (16 * u + row_k) * 128 + (((2 * j + chunk_k) ^ (lane & 7)) << 4), a[0], a[1], a[2], a[3]);
+    for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        ldsm_x4(keys + (16 * u + row_k) * 128 + (((2 * (j0 + j) + chunk_k) ^ (lane & 7)) << 4), ka[u][j][0], ka[u][j][1],
+                ka[u][j][2], ka[u][j][3]);
+#pragma unroll
+    for (int i = 0; i < kAhead * U; ++i) {
+      const int j = j0 + i / U, u = i % U;
+      const uint32_t(&a)[4] = ka[u][j - j0];
 #pragma unroll
       for (int nt = kFirst; nt < kEnd; ++nt) {
         if (kSkip && nt >= tiles) continue;
         if (j == 0)
           mma_first(s[u][nt - kFirst], a, qf[nt - kFirst][j][0], qf[nt - kFirst][j][1]);
         else
-          mma16816(s[u][nt - kFirst], a, qf[nt - kFirst][j][0], qf[nt - kFirst][j][1]);
+          mma_add(s[u][nt - kFirst], a, qf[nt - kFirst][j][0], qf[nt - kFirst][j][1]);
       }
     }
+  }
   bool move = false;
   float top[HT][2];
 #pragma unroll
@@ -470,7 +486,7 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
 #pragma unroll
       for (int nt = kFirst; nt < kEnd; ++nt) {
         if (kSkip && nt >= tiles) continue;
-        mma16816(r.o[nt][i], a[i], pf[u][nt - kFirst][0], pf[u][nt - kFirst][1]);
+        mma_add(r.o[nt][i], a[i], pf[u][nt - kFirst][0], pf[u][nt - kFirst][1]);
       }
   }
   if (kMasked && odd) {

@@ -348,6 +348,10 @@ SA_DEV Pair exponent(float x, float top, const Scale& s) {
   const float hi = __fmul_rn(d, s.hi);
   return {hi, __fmaf_rn(d, s.hi, -hi) + __fmaf_rn(d, s.lo, d_lo * s.hi)};
 }
+// An exponent at which nothing is left (fp64's least): a token masked in both
+// rows, by whatever value, does not stand.
+constexpr float kNothing = -1074.f;
+
 // 2^t to some 2^-23 of itself; 0 below fp32's normal numbers.
 SA_DEV float power(Pair t) {
   const float e = ex2(t.hi);
@@ -467,11 +471,11 @@ class Entry {
           } else if (a_.draft_logits == nullptr) {
             stands = u * p.sum < power(tp);
           } else {
-            // u q < p by their ratio, which stays in range where both are small
+            // u q < p by their ratio, which stays in range where both are small, if either is anything
             const RowStat q = stat(a_.rows + draft0 + i, sc);
             const Pair tq = exponent(y, q.top, sc);
-            const float ratio = y == -INFINITY ? INFINITY : ex2((tp.hi - tq.hi) + (tp.lo - tq.lo)) * __fdiv_rn(q.sum, p.sum);
-            stands = !q.bad() && !q.none() && x > -INFINITY && u < ratio;
+            const float ratio = ex2((tp.hi - tq.hi) + (tp.lo - tq.lo)) * __fdiv_rn(q.sum, p.sum);
+            stands = !q.bad() && !q.none() && tp.hi > kNothing && (!(tq.hi > kNothing) || u < ratio);
           }
           if (stands && writes && lane == 0) {
             a_.tokens[row0 + i] = token;
@@ -732,7 +736,7 @@ class Weights {
       const float2 b = fadd2(d, make_float2(-x, -y));
       const float2 c = fadd2(d, make_float2(-b.x, -b.y));
       d_lo = fadd2(fadd2(make_float2(x, y), make_float2(-c.x, -c.y)), fadd2(make_float2(-top, -top), make_float2(-b.x, -b.y)));
-      d_lo = make_float2(x > -INFINITY ? d_lo.x : 0.f, y > -INFINITY ? d_lo.y : 0.f);
+      d_lo = make_float2(d.x > d_least_ ? d_lo.x : 0.f, d.y > d_least_ ? d_lo.y : 0.f);
     }
     d = make_float2(fmaxf(d.x, d_least_), fmaxf(d.y, d_least_));
     const float2 hi = fmul2(d, make_float2(sc_.hi, sc_.hi));
@@ -876,10 +880,10 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const __grid_cons
   __shared__ int holder_sh;
   __shared__ u64 before_sh;
   const int tid = threadIdx.x, b = blockIdx.x;
+  cudaGridDependencySynchronize();  // by all: this launch is not over before the others are
   const int end = min(a.cu[b + 1], a.rows);
   if (end <= max(a.cu[b], 0)) return;
   const int place = w.of(a, b);
-  cudaGridDependencySynchronize();
   const Stop s = w.stops[place];
   if (!s.drawn) return;
   const Entry<kType> entry(entry_sh, a, w.slices);

@@ -365,9 +365,9 @@ def verify_tokens(logits, drafts, u, cu_rows, *, draft_logits=None, temperature=
         raise ValueError("cu_rows has shape [0], expected one offset more than there are entries")
     xp, xs = None, V
     if draft_logits is not None:
-        if draft_logits.dtype is not logits.dtype:
+        draft_kind, xs = _logit_rows("draft_logits", draft_logits)
+        if draft_kind != kind:
             raise TypeError(f"draft_logits has dtype {draft_logits.dtype}, expected {logits.dtype}")
-        _, xs = _logit_rows("draft_logits", draft_logits)
         if draft_logits.shape != (D, V) or draft_logits.device != dev:
             raise ValueError(f"draft_logits has shape {list(draft_logits.shape)} on {draft_logits.device}, "
                              f"expected {[D, V]} on {dev}")

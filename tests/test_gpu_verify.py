@@ -176,6 +176,34 @@ def test_masked_rows_and_what_is_not_valid():
     check(x[24:33], drafts[16:22], u[24:33], counts[8:11], y[16:22], temp[8:11])
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("level", [0.0, 3e4])
+def test_masks_of_the_lowest_finite_value(dtype, level):
+    """Masked by the type's lowest value instead of -inf, in one row or both, drafts among the masked tokens."""
+    rng = np.random.RandomState(10)
+    counts = [3] * 8
+    low = torch.finfo(dtype).min
+    x, drafts, y, u = case(rng, counts, 3001, dtype)
+    x, y = (x.float() + level).to(dtype), (y.float() + level).to(dtype)
+    x[:9, 40:], y[4:10, 60:] = low, low
+    drafts[[0, 1, 8, 9]] = [2000, 39, 2500, 3000]  # masked in p; allowed in it; masked in q alone: they stand
+    tokens, logp, acc, rej = run(x, drafts, u, counts, y)
+    assert acc[0] == 0 and tokens[0] < 40 and acc[4] == 2
+    check(x, drafts, u, counts, y)
+    check(x, drafts, u, counts)
+
+
+def test_extreme_temperatures():
+    rng = np.random.RandomState(11)
+    temp = [2e-38, 1e-30, 1e-6, 1e4, 1e30, 1e36]  # (1e-38 is subnormal, and counts as 0)
+    counts = [3] * 6
+    for V in (900, 20000):
+        x, drafts, y, u = case(rng, counts, V, torch.float32)
+        x[:, 5], y[:, 5] = torch.finfo(torch.float32).min, -float("inf")
+        check(x, drafts, u, counts, y, temp)
+        check(x, drafts, u, counts, None, temp)
+
+
 def test_random_numbers_at_their_ends():
     rng = np.random.RandomState(6)
     x, drafts, y, u = case(rng, [2] * 6, 4001, torch.float32)
