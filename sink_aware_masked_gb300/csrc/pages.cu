@@ -16,7 +16,10 @@ using namespace handout;
 // ---------------------------------------------------------------- plan
 // left = max(len - drop, 0), then len = left + new: pages beyond left go back
 // first, all of them, then the requests are served.  One CTA, and for long
-// calls a second launch that writes the rows' places on all SMs.
+// calls a second launch that writes the rows' places on all SMs.  What bounds it
+// is the chain of scans, searches and dependent loads (GB300: 1 slot 5.0 us with
+// its launch, 256 slots with 1 to 5 rows each 9.8, 512 slots of which 64 are
+// refilled with 220 k rows 18.0, of these 5 for the rows' places).
 constexpr int kRowsInPlan = 4096;  // rows whose places the plan's own CTA writes
 constexpr int kMapThreads = 256;
 constexpr int kMapPer = 4;  // rows per thread of the second launch
@@ -207,7 +210,8 @@ __global__ void __launch_bounds__(kMapThreads) kv_map_kernel(const KvPages c, co
 
 // ---------------------------------------------------------------- write
 // A copy: `lanes` lanes take a row (the power of two that covers its 16-byte
-// units, 32 at most), several rows in flight each.
+// units, 32 at most), several rows in flight each.  70001 tokens x 8 heads out
+// of wider rows 44.3 us, 97 % of the copy rate.
 constexpr int kWriteThreads = 256;
 constexpr int kWriteRows = 4;
 

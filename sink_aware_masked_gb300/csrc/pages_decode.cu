@@ -25,8 +25,13 @@
 // take a pair's turns in turn and merge in shared memory; or, where there are
 // many pairs with few turns each, a single warp, which takes whole pairs.  A
 // pair cut between CTAs leaves partial results in the workspace, and the last
-// CTA of the pair to arrive merges them in order.  Above 32 rows two or four
+// CTA of the pair to arrive merges them in order.  Above 48 rows two or four
 // warps share a ring and split the rows.
+//
+// Measured (GB300): 32 x 8192 keys, 64/8 heads, 88.2 us (537 MB: 91 % of the
+// copy rate); 8 x 32768 keys x 1 to 5 rows 121 us (514 MB, 63 %: dependent
+// instructions, 8 warps an SM at 255 registers); 200 windowed sequences 17.9 us
+// (3000 instructions of one pair per warp); one sequence of 37 keys 6.1 us.
 #include "shares.cuh"
 #include "tc.cuh"
 #include "tmap.h"
@@ -50,9 +55,13 @@ constexpr int kPartPad = 4;                        // floats of statistics per r
 constexpr int kPartRowsPerSm = 256;
 
 // What a turn costs a CTA, in places of the line that is shared out, and a tile
-// of 8 rows on top; what beginning a pair costs.
+// of 8 rows on top; what beginning a pair costs.  (8 x 32768 keys x 1 to 5 rows:
+// 123.5 us with 7 and 2, 134 with 7 and 1, 133 with 4 and 2, 141 with 2 and 2,
+// 152 without the tiles; the pairs' cost shows little between 20 and 60.)
 constexpr int kTurnCost = 7, kTileCost = 2, kPairCost = 60;
-// Turns of the longest pair up to which warps work alone, each on whole pairs.
+// Turns of the longest pair up to which warps work alone, each on whole pairs
+// (200 sequences of 6 visible turns: 17.9 us; the 4-bit cache's decode, of the
+// same build, takes 10.6 this way and 40.9 by CTAs and shares).
 constexpr int kAloneTurns = 24;
 
 struct PageDecK {
@@ -1162,6 +1171,10 @@ cudaError_t launch_kv_decode(const KvPages& c, const KvDecodeArgs& a, int* statu
                                       : ceil_div(std::min<long long>(a.prefix, table), kTurn) +
                                             ceil_div(static_cast<long long>(a.window) + a.n, kTurn) + 1;
   const bool alone = most <= kAloneTurns && static_cast<long long>(a.num_seqs) * c.num_heads_kv >= device_sms();
+  // One tile of rows: two turns in flight for each of 8 warps an SM (32 x 8192 keys 88.5 us; three turns 92.3, two for
+  // 12 warps 91.1, four for 4 warps 92.5).  Up to 48 rows a warp has them all, in halves above 32 (8 x 32768 keys x 1 to
+  // 5 rows 121 us; thirds 126, three tiles by each of two warps 180, two turns ahead for 6 warps 154).  Alone: 12 warps an
+  // SM (17.9 us; 8 warps 25.4).
   if (rows <= 8) return alone ? launch_kernel<Shape<1, 1, 4, 2, 3>, true>(p, s) : launch_kernel<Shape<1, 1, 4, 2, 2>, false>(p, s);
   if (rows <= 16) return alone ? launch_kernel<Shape<2, 1, 4, 2, 3>, true>(p, s) : launch_kernel<Shape<2, 1, 4, 2, 2>, false>(p, s);
   if (rows <= 32) return launch_kernel<Shape<4, 1, 4, 2, 2>, false>(p, s);

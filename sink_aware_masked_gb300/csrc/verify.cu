@@ -19,6 +19,13 @@
 //   draw     a CTA per entry: the run that holds the place drawn, and the token
 //            in it
 //
+// Measured (GB300): 128 entries of 0 to 4 drafts over 201088 bf16 logits 105 us
+// (255 MB, 38 us at the copy rate): rows 44, weights 48 (300 instructions per 32
+// vectors of both rows, and entries that have nothing to draw beside others that
+// have), draw 10.  48 entries of up to 7 looked-up drafts over 100003 fp16 33 us,
+// one entry with 3 drafts over 50257 fp32 18 us: the chains of loads of three
+// launches, which wait for one another on the device.
+//
 // Arithmetic.  Where the tests are concerned fp32 sums do: a test is decided
 // wrongly only where u q and p agree to some 2^-22.  The draw is another
 // matter: among 200 k cumulated masses one border or another lies within 2^-24
