@@ -9,21 +9,22 @@
 //   T = 0: a draft stands if it is the largest logit's first index, and that is the token.
 //
 // All rows are read once, which is what the call cannot do without: 2 or 4
-// bytes a logit and one exponential each.  Three launches:
+// bytes a logit and one exponential each.  Three launches, four for large calls:
 //   rows     a CTA per (row, slice of the vocabulary): the slice's maximum and
 //            the sum relative to it
-//   weights  a CTA per (entry, part of the vocabulary): tests the entry's drafts
-//            (every part does, which costs less than a launch), and sums what
-//            the part weighs in the row where the entry stopped, run by run; the
-//            row, or pair of rows, is read again, in part from L2
+//   stop     a CTA per entry: tests its drafts (in small calls the next launch
+//            does, every part alike, which costs less)
+//   weights  a CTA per (entry, part of the vocabulary): sums what the part weighs
+//            in the row where the entry stopped, run by run; the row, or pair of
+//            rows, is read again, in part from L2
 //   draw     a CTA per entry: the run that holds the place drawn, and the token
 //            in it
 //
-// Measured (GB300): 128 entries of 0 to 4 drafts over 201088 bf16 logits 105 us
-// (255 MB, 38 us at the copy rate): rows 44, weights 48 (300 instructions per 32
-// vectors of both rows, and entries that have nothing to draw beside others that
-// have), draw 10.  48 entries of up to 7 looked-up drafts over 100003 fp16 33 us,
-// one entry with 3 drafts over 50257 fp32 18 us: the chains of loads of three
+// Measured (GB300): 128 entries of 0 to 4 drafts over 201088 bf16 logits 94 us
+// (255 MB, 38 us at the copy rate): rows 43, tests 4, weights 38 (300
+// instructions per 32 vectors of both rows, and entries that have nothing to draw
+// beside others that have), draw 9.  48 entries of up to 7 looked-up drafts over 100003 fp16 33 us,
+// one entry with 3 drafts over 50257 fp32 18 us: the chains of loads of the
 // launches, which wait for one another on the device.
 //
 // Arithmetic.  Where the tests are concerned fp32 sums do: a test is decided
@@ -390,7 +391,7 @@ __device__ __noinline__ long long to_units(Pair e, float unit) { return __float2
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxParts = 16;
-constexpr int kWeightsPerSm = 3;  // CTAs of the second launch that an SM holds
+constexpr int kWeightsPerSm = 4;  // CTAs of the weights' launch that an SM holds, one fewer where it tests the drafts too
 constexpr int kHeavyLog2 = 12;  // masses from 2^-12 of the whole on are heavy
 constexpr int kUnitLog2 = 40;   // masses in units of 2^-40 of (about) the whole
 constexpr int kList = 1024;     // vectors with heavy masses that a CTA keeps a list of
@@ -426,6 +427,16 @@ SA_DEV float unit_for(float sum) {
 SA_DEV float log_share(float x, const RowStat& s, const Scale& sc) {
   return __fdiv_rn(x - s.top, sc.temperature) - logf(s.sum);
 }
+
+template <class T>
+SA_DEV const T* row_of(const VerifyArgs& a, int row) {
+  return static_cast<const T*>(a.logits) + static_cast<int64_t>(row) * a.stride;
+}
+template <class T>
+SA_DEV const T* draft_of(const VerifyArgs& a, int draft) {
+  return static_cast<const T*>(a.draft_logits) + static_cast<int64_t>(draft) * a.draft_stride;
+}
+SA_DEV bool has_rows(const VerifyArgs& a, int b) { return min(a.cu[b + 1], a.rows) > max(a.cu[b], 0); }
 
 // The rows of an entry, and where it stops.
 template <int kType>
@@ -467,8 +478,8 @@ class Entry {
       if (sc.valid && draft0 + i < a_.num_drafts) {
         const int token = a_.drafts[draft0 + i];
         const bool inside = token >= 0 && token < a_.vocab;
-        const float x = inside ? E::one(row_of(row0 + i)[token]) : -INFINITY;
-        const float y = inside && a_.draft_logits != nullptr ? E::one(draft_of(draft0 + i)[token]) : 0.f;
+        const float x = inside ? E::one(row_of<T>(a_, row0 + i)[token]) : -INFINITY;
+        const float y = inside && a_.draft_logits != nullptr ? E::one(draft_of<T>(a_, draft0 + i)[token]) : 0.f;
         const float u = unit_of(a_.u[row0 + i]);
         const RowStat p = stat(row0 + i, sc);
         if (!p.bad() && !p.none() && inside) {
@@ -525,11 +536,6 @@ class Entry {
     s.drawn = 1;
     return s;
   }
-  SA_DEV const T* row_of(int row) const { return static_cast<const T*>(a_.logits) + static_cast<int64_t>(row) * a_.stride; }
-  SA_DEV const T* draft_of(int draft) const {
-    return static_cast<const T*>(a_.draft_logits) + static_cast<int64_t>(draft) * a_.draft_stride;
-  }
-
  private:
   // Of target row `item`, or of draft item - rows; by a whole warp.
   SA_DEV RowStat stat(int item, const Scale& sc) const {
@@ -574,15 +580,15 @@ class Weights {
     uint32_t heavy;
   };
 
-  SA_DEV Weights(const VerifyArgs& a, const Entry<kType>& entry, const Stop& s, const Scale& sc)
+  SA_DEV Weights(const VerifyArgs& a, const Stop& s, const Scale& sc)
       : vocab_(a.vocab), vectors_((a.vocab + kVec - 1) / kVec), sc_(sc), p_(s.p), q_(s.q) {
-    x_ = entry.row_of(s.row);
+    x_ = row_of<T>(a, s.row);
     y_ = nullptr;
     unit_ = unit_for(s.p.sum);
     heavy_ = heavy_from(s.p);
     d_least_ = fmaxf(__fdiv_rn(-150.f, sc.hi), -3e38f);
     if (s.draft >= 0 && a.draft_logits != nullptr) {
-      y_ = entry.draft_of(s.draft);
+      y_ = draft_of<T>(a, s.draft);
       unit_q_ = unit_for(s.q.sum);
       heavy_q_ = heavy_from(s.q);
       near_ = __fdiv_rn(s.p.sum, s.q.sum);
@@ -781,24 +787,41 @@ struct Places {
   SA_DEV int of(const VerifyArgs& a, int b) const { return by_row ? a.cu[b] : b; }
 };
 
-// CTA: a part of entry b's vocabulary, cut into a run for each warp.
+// CTA: tests entry b's drafts.
 template <int kType>
-__global__ void __launch_bounds__(kThreads, kWeightsPerSm) verify_weights_kernel(const __grid_constant__ VerifyArgs a, const Places w) {
+__global__ void __launch_bounds__(kThreads) verify_stop_kernel(const __grid_constant__ VerifyArgs a, const Places w) {
+  __shared__ typename Entry<kType>::Shared sh;
+  const int b = blockIdx.x;
+  cudaGridDependencySynchronize();
+  const Stop s = Entry<kType>(sh, a, w.slices).stop(b, true);
+  if (threadIdx.x == 0 && s.row >= 0) w.stops[w.of(a, b)] = s;
+}
+
+// CTA: a part of entry b's vocabulary, cut into a run for each warp.  kTests:
+// tests the entry's drafts itself, all parts alike.
+template <int kType, bool kTests>
+__global__ void __launch_bounds__(kThreads, kTests ? kWeightsPerSm - 1 : kWeightsPerSm) verify_weights_kernel(const __grid_constant__ VerifyArgs a, const Places w) {
   constexpr int kVec = Elem<kType>::kVec;
-  __shared__ typename Entry<kType>::Shared entry_sh;
   __shared__ Sums sums[kWarps];
   __shared__ uint32_t list[kList];  // vector in the CTA's run << 8 | its heavy logits, a bit each
   __shared__ int listed;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / w.parts, part = blockIdx.x - b * w.parts;
   if (tid == 0) listed = 0;
-  cudaGridDependencySynchronize();
-  Entry<kType> entry(entry_sh, a, w.slices);
-  const Stop s = entry.stop(b, part == 0);
+  __syncthreads();
+  cudaGridDependencySynchronize();  // by all: this launch is not over before the others are
   const int place = w.of(a, b);
-  if (part == 0 && tid == 0 && s.row >= 0) w.stops[place] = s;
+  Stop s;
+  if constexpr (kTests) {
+    __shared__ typename Entry<kType>::Shared entry_sh;
+    s = Entry<kType>(entry_sh, a, w.slices).stop(b, part == 0);
+    if (part == 0 && tid == 0 && s.row >= 0) w.stops[place] = s;
+  } else {
+    if (!has_rows(a, b)) return;
+    s = w.stops[place];
+  }
   if (!s.drawn) return;
-  const Weights<kType> weights(a, entry, s, Scale(a.temperature[b]));
+  const Weights<kType> weights(a, s, Scale(a.temperature[b]));
   const int run = weights.run_length(w.parts * kWarps), v_cta = part * kWarps * run;
   const int v0 = min(v_cta + warp * run, weights.vectors()), v1 = min(v0 + run, weights.vectors());
   Sums own{0, 0, 0, 0};
@@ -882,21 +905,18 @@ SA_DEV u64 block_scan(DrawShared& sh, int turn, u64 x, u64& total) {
 template <int kType>
 __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const __grid_constant__ VerifyArgs a, const Places w) {
   constexpr int kVec = Elem<kType>::kVec;
-  __shared__ typename Entry<kType>::Shared entry_sh;
   __shared__ DrawShared sh;
   __shared__ int holder_sh;
   __shared__ u64 before_sh;
   const int tid = threadIdx.x, b = blockIdx.x;
   cudaGridDependencySynchronize();  // by all: this launch is not over before the others are
-  const int end = min(a.cu[b + 1], a.rows);
-  if (end <= max(a.cu[b], 0)) return;
+  if (!has_rows(a, b)) return;
   const int place = w.of(a, b);
   const Stop s = w.stops[place];
   if (!s.drawn) return;
-  const Entry<kType> entry(entry_sh, a, w.slices);
   const Scale sc(a.temperature[b]);
-  Weights<kType> weights(a, entry, s, sc);
-  const float u = unit_of(a.u[end - 1]);
+  Weights<kType> weights(a, s, sc);
+  const float u = unit_of(a.u[min(a.cu[b + 1], a.rows) - 1]);
   const auto target_of = [&](u64 total) {  // floor(total u), below total
     return __umul64hi(total << 4, static_cast<u64>(u * 4294967296.f) << 28);
   };
@@ -1008,13 +1028,16 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
   slices = ceil_div(all, turns);
   if (items > 0)
     verify_rows_kernel<kType><<<static_cast<unsigned>(items * slices), kStatThreads, 0, s>>>(a, slices, turns);
-  // An entry in parts of eight vectors a thread at least, four where there are few entries, and in no more than three
-  // turns of what the GPU holds at once (not all entries have anything to draw).
+  // An entry in parts of eight vectors a thread at least, four where there are few entries, and in no more than five
+  // times what the GPU holds at once (not all entries have anything to draw; 128 x 201088 bf16 with 16 parts 94 us, with 8
+  // 103).  Parts that come in one turn test the drafts themselves (one entry 18.3 us, with a launch of its own for that
+  // 19.5), else all but the first turn would wait for the same tests again (128 x 201088: 105 us with 8 parts each).
   const int wave = kWeightsPerSm * device_sms();
   int parts = 1;
-  while (parts < kMaxParts && 2LL * parts * a.num_seqs <= 3LL * wave &&
+  while (parts < kMaxParts && 2LL * parts * a.num_seqs <= 5LL * wave &&
          parts * kThreads * (4LL * parts * a.num_seqs <= wave ? 4 : 8) * Elem<kType>::kVec < a.vocab)
     parts *= 2;
+  const bool tests_apart = static_cast<long long>(parts) * a.num_seqs > (kWeightsPerSm - 1) * device_sms();
   Places w;
   w.slices = slices;
   w.parts = parts;
@@ -1025,7 +1048,6 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
   w.sums = reinterpret_cast<Sums*>(behind + static_cast<size_t>(std::min(a.rows, kKv4MaxRequests)) * sizeof(Stop));
   // Each waits for the one before on the device, so that its launch does not come on top.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * parts);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute early[1];
@@ -1033,7 +1055,11 @@ cudaError_t launch_type(const VerifyArgs& a, cudaStream_t s) {
   early[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = early;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, verify_weights_kernel<kType>, a, w);
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs));
+  cudaError_t e = tests_apart ? cudaLaunchKernelEx(&cfg, verify_stop_kernel<kType>, a, w) : cudaSuccess;
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs) * parts);
+  e = cudaLaunchKernelEx(&cfg, tests_apart ? verify_weights_kernel<kType, false> : verify_weights_kernel<kType, true>, a, w);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(a.num_seqs));
   return cudaLaunchKernelEx(&cfg, verify_draw_kernel<kType>, a, w);
