@@ -211,6 +211,8 @@ CASES = [
     (16, 1, 1, [3000, 5, 77], [1, 1, 1], -1, 0),
     (64, 1, 64, [333], [2], 7, 130),
     (32, 2, 8, [9, 70], [8, 16], 5, 2),
+    (16, 1, 128, [300, 40], [1, 1], -1, 0),
+    (64, 1, 100, [131], [1], 64, 1),
 ]
 
 
@@ -256,6 +258,44 @@ def test_decode_cut_between_ctas(batch, length, page, heads, group, n):
     slots = list(range(batch))
     o, lse = sa.kv_decode_fwd(h, i32(slots), q, sink, q_per_seq=n)
     check_decode(c, slots, [n] * batch, hq, -1, 0, q, sink, o, lse)
+
+
+@pytest.mark.parametrize("longest", [3, 5000])
+def test_as_many_entries_as_a_call_takes(longest):
+    import sink_aware_masked_gb300 as sa
+
+    rng = np.random.RandomState(longest)
+    lens = [1 + b % 3 for b in range(4096)]
+    lens[1234] = longest
+    c = shuffled(rng, lens, 16, 1)
+    q, sink = bf16(rng, 4096, 4, 64).to(DEV), dev(rng.randn(4), torch.float32)
+    o, lse = sa.kv_decode_fwd(handle(c), i32(range(4096)), q, sink, q_per_seq=1)
+    check_decode(c, list(range(4096)), [1] * 4096, 4, -1, 0, q, sink, o, lse)
+
+
+def test_pools_beyond_32_bits():
+    """Pages whose bytes, and whose values, lie beyond 2^32: written, attended to, and no other place touched."""
+    import sink_aware_masked_gb300 as sa
+
+    page, heads, pages = 64, 8, 135000  # 8.6 M tokens: 8.8 GB of keys, 4.4 G values
+    rng = np.random.RandomState(12)
+    pool = [torch.empty((pages, page, heads, 64), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    at = [pages - 1, 5, pages - 3, 70000]
+    for t in pool:
+        t[[0, 4, 6, 69999, 70001, pages - 2]] = 3.0
+    table = i32([at])
+    h = sa.KVPages(*pool, table, i32([4 * page - 7]), torch.full((pages,), -1, dtype=torch.int32, device=DEV))
+    T = 4 * page - 7
+    places = np.array([at[i // page] * page + i % page for i in range(T)])
+    k, v = bf16(rng, T, heads, 64), bf16(rng, T, heads, 64)
+    sa.kv_write(h, i32(places), k.to(DEV), v.to(DEV))
+    q, sink = bf16(rng, 2, 16, 64).to(DEV), dev(rng.randn(16), torch.float32)
+    o, lse = sa.kv_decode_fwd(h, i32([0]), q, sink, q_per_seq=2)
+    f64 = lambda t: t.double().cpu().numpy()  # noqa: E731
+    want, want_l = oracle.decode_forward(f64(q), f64(k), f64(v), f64(sink), [0, T], 2)
+    assert np.abs(f64(o) - want).max() < 2.0 ** -5 and np.abs(f64(lse) - want_l).max() < 2.0 ** -14
+    for t in pool:
+        assert (t[[0, 4, 6, 69999, 70001, pages - 2]] == 3.0).all()
 
 
 def test_rows_outside_the_entries_are_left_alone():
