@@ -173,7 +173,8 @@ struct Segment {
 // A turn as a warp sees it.
 struct Turn {
   int key0;      // position of its first key
-  int loaded;    // tokens of it that are in the ring: its first 16, all 32 (a bit each)
+  int loaded;    // halves of it that are in the ring, a bit each
+  int missing;   // halves with tokens whose page is not in the pool
   bool masked;   // some (row, key) is not visible, or a half is not in the ring
 };
 
@@ -226,6 +227,7 @@ class Stream {
       const int r0 = __shfl_sync(0xffffffffu, cur0_, i & 31), r1 = __shfl_sync(0xffffffffu, cur1_, i & 31);
       t.key0 = seg_.span.turn(place(i)) * kTurn;
       t.loaded = (r0 >= 0) | (r1 >= 0) << 1;
+      t.missing = ~t.loaded & (t.key0 + 16 < seg_.seq.len ? 3 : 1);
       const int key1 = t.key0 + kTurn - 1;
       // seen by all rows: the earliest position causally, the last one's window
       t.masked = t.loaded != 3 || key1 > seg_.seq.len - seg_.seq.n ||
@@ -334,11 +336,22 @@ SA_DEV void rows_clear(Rows<NT>& r) {
   }
 }
 
-// The keys of a turn that row position `at` sees (-1: none), as bits.
-SA_DEV uint32_t seen_bits(int at, int key0, int window, int prefix) {
-  uint32_t bits = bits_below(at - key0 + 1);
-  if (window >= 0) bits &= ~bits_below(at - window - key0) | bits_below(prefix - key0);
-  return bits;
+// Bits below n set, n >= 0.
+SA_DEV uint32_t low_bits(int n) {
+  uint32_t d;
+  asm("bmsk.clamp.b32 %0, 0, %1;\n" : "=r"(d) : "r"(n));
+  return d;
+}
+// The keys of a turn that row position `at` sees (-1: none), as bits; of the
+// prefix: low_bits(prefix - key0), all without a window.
+SA_DEV uint32_t seen_bits(int at, int key0, int window, uint32_t of_prefix) {
+  return low_bits(max(at - key0 + 1, 0)) & (~low_bits(max(at - window - key0, 0)) | of_prefix);
+}
+// 0 or a NaN added to acc for each half: a NaN where v is an infinity or a NaN.
+SA_DEV uint32_t not_finite(uint32_t v, uint32_t acc) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;\n" : "=r"(d) : "r"(v), "r"(0u), "r"(acc));
+  return d;
 }
 
 // Moves a row's reference: all that was summed relative to the old one.
@@ -401,6 +414,7 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
       }
     }
   }
+  const uint32_t of_prefix = window < 0 ? 0xffffffffu : low_bits(max(prefix - turn.key0, 0));
   bool move = false;
   float top[HT][2];
 #pragma unroll
@@ -409,13 +423,13 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
     if (kMasked) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint32_t bits = seen_bits(pos(nt, e), turn.key0, window, prefix) >> (g);
+        const uint32_t bits = seen_bits(pos(nt, e), turn.key0, window, of_prefix) >> (g);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             float& x = s[u][nt - kFirst][2 * h + e];
-            if (!(turn.loaded >> u & 1)) x = __int_as_float(0x7fffffff);  // its page is not in the pool
+            if (turn.missing != 0 && (turn.missing >> u & 1)) x = __int_as_float(0x7fffffff);  // it reads as NaN
             if (!(bits >> (16 * u + 8 * h) & 1u)) x = -INFINITY;
           }
       }
@@ -477,12 +491,12 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
           pf[u][nt - kFirst][0] = pf[u][nt - kFirst][1] = 0u;
         }
       }
-      uint32_t ones = 0u;
+      uint32_t nan = 0u;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) ones |= ones_exponent(a[i][m]);
-      if (__any_sync(0xffffffffu, (ones & 0x80008000u) != 0u)) {
+        for (int m = 0; m < 4; ++m) nan = not_finite(a[i][m], nan);
+      if (__any_sync(0xffffffffu, (nan & 0x7fff7fffu) != 0u)) {
         odd = true;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -507,7 +521,7 @@ SA_DEV void turn_step(Rows<NT>& r, uint32_t keys, const uint32_t (&qf)[HT][4][2]
       for (int nt = kFirst; nt < kEnd; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
-          sees |= (seen_bits(pos(nt, e), turn.key0, window, prefix) >> (key) & 1u) << (2 * nt + e);
+          sees |= (seen_bits(pos(nt, e), turn.key0, window, of_prefix) >> (key) & 1u) << (2 * nt + e);
       const uint32_t row = keys + kTurnHalf + key * 128;
 #pragma unroll
       for (int d = 0; d < 8; ++d) {  // dims 8 d + g: [d / 2][2 (d % 2) + e]
@@ -855,12 +869,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
   const int group = static_cast<int>(blockIdx.x) / heads_at_once;
   int b_first = 0, head_first = static_cast<int>(blockIdx.x) - group * heads_at_once, pad = 0;
   long long x_first = 0, x_begin = 0, x_end = 0;  // places in the line: of the first pair, and of the share
-  long long pair = static_cast<long long>(warp) * ctas + blockIdx.x;
+  int pair = warp * ctas + static_cast<int>(blockIdx.x);  // pairs: 4096 entries of 256 heads at most
   Shares shares(1, 1);
   if (alone) {
-    if (pair >= static_cast<long long>(p.num_seqs) * heads) return;
-    b_first = static_cast<int>(pair / heads);
-    head_first = static_cast<int>(pair - static_cast<long long>(b_first) * heads);
+    if (pair >= p.num_seqs * heads) return;
+    b_first = pair / heads;
+    head_first = pair - b_first * heads;
   } else if constexpr (!kAlone) {
     // a turn at least for every team, unless that leaves pairs without a worker of their own; no less than the most
     // that a turn costs, so that every share between a cut pair's first and last has a turn of it
@@ -1062,10 +1076,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
     }
     process(segments[cur][warp]);
     if (alone) {
-      pair += static_cast<long long>(ctas) * kWarps;
-      more = pair < static_cast<long long>(p.num_seqs) * heads;
-      const int b = more ? static_cast<int>(pair / heads) : 0;
-      if (more) set_next(segment_at(b, static_cast<int>(pair - static_cast<long long>(b) * heads), 0));
+      pair += ctas * kWarps;
+      more = pair < p.num_seqs * heads;
+      const int b = pair / heads;
+      if (more) set_next(segment_at(b, pair - b * heads, 0));
     } else {
       const Segment& done = segments[cur][warp];
       const long long x = done.x + static_cast<long long>(done.turns) * done.cost + pad;
