@@ -79,6 +79,7 @@ struct PageDecK {
   int* status;
   int num_pages, page_log2, num_slots, max_pages, num_heads_kv;
   int num_seqs, total_rows, n, hq, group, window, prefix;
+  int row_groups;        // of a pair, where warps are alone: a warp has every row_groups-th tile
   uint32_t group_magic;  // ceil(2^16 / group)
   float coef;            // scale * log2 e
   // row / group, exact while row * group <= 2^16 (rows and groups are up to 128)
@@ -165,7 +166,7 @@ SA_DEV Span visible_span(const PageDecK& p, const Seq& q) {
 // The part of a pair that a worker takes: turns [t0, t1) of `turns`.
 struct Segment {
   long long x;  // where its pair begins in the line that is shared out
-  int b, head, t0, t1, turns, cost;
+  int b, head, row_group, t0, t1, turns, cost;
   Seq seq;
   Span span;
 };
@@ -587,22 +588,24 @@ SA_DEV void finish_row(const PageDecK& p, const Seq& q, int head, int row, int d
   if (d0 == 0) p.lse[static_cast<int64_t>(h_q) * p.total_rows + at] = w.lse;
 }
 
-// Writes the rows of a warp that had all keys of a pair: 8x8 transposes bring a row's dims together.
+// Writes the rows of a warp that had all keys of a pair, tiles first, first + step, ...: 8x8 transposes bring a row's
+// dims together.
 template <int NT>
-SA_DEV void finish_tiles(const PageDecK& p, const Seq& q, int head, int rows, const Rows<NT>& r) {
+SA_DEV void finish_tiles(const PageDecK& p, const Seq& q, int head, int rows, int first, int step, const Rows<NT>& r) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    if (8 * nt >= rows) break;
+    const int row0 = 8 * (nt * step + first);
+    if (row0 >= rows) break;
     Finish w[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int row = 8 * nt + 2 * t + e, i = p.row_of_seq(row), h_q = head * p.group + row - i * p.group;
+      const int row = row0 + 2 * t + e, i = p.row_of_seq(row), h_q = head * p.group + row - i * p.group;
       w[e] = finish_of(log2_ref(e ? r.ref[nt].y : r.ref[nt].x, p.coef), e ? r.sum[nt].y : r.sum[nt].x, e ? r.sum_o[nt].y : r.sum_o[nt].x,
                        row < rows ? __ldg(p.sink + h_q) : 0.f);
       if (g == 0 && row < rows) p.lse[static_cast<int64_t>(h_q) * p.total_rows + q.row0 + i] = w[e].lse;
     }
-    const int row = 8 * nt + g, i = p.row_of_seq(row), h_q = head * p.group + row - i * p.group;
+    const int row = row0 + g, i = p.row_of_seq(row), h_q = head * p.group + row - i * p.group;
     uint32_t* o = reinterpret_cast<uint32_t*>(p.o + ((static_cast<int64_t>(q.row0) + i) * p.hq + h_q) * kHeadDim);
 #pragma unroll
     for (int c = 0; c < 8; ++c) {  // dims 8 c + g of rows 2 t, 2 t + 1 -> dims 8 c + 2 t, + 1 of row g
@@ -749,9 +752,10 @@ SA_DEV void fetch_queries(uint32_t queries, int first, int step, uint32_t (&qf)[
 template <class S, bool kAlone>
 __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const __grid_constant__ PageDecK p) {
   constexpr int NT = S::NT, kShare = S::kShare, kTeams = S::kTeams, kStages = S::kStages;
+  constexpr int kQueryBytes = S::kRows * kHeadDim * 2;
   constexpr int kThreads = S::kThreads, kWarps = S::kWarps, kRows = S::kRows, kSlots = S::kSlots, kDims = S::kDims;
-  constexpr bool kMayAlone = kShare == 1 && NT <= 2;
-  static_assert(!kAlone || kMayAlone, "a warp alone has the tiles of all rows");
+  constexpr bool kMayAlone = kAlone || (kShare == 1 && NT <= 2);
+  static_assert(!kAlone || kShare == 1, "a warp alone shares its ring with no other");
   extern __shared__ uint8_t smem_raw[];
   // the rings (boxes are swizzled by their address: 1024-byte aligned), queries [rows][64], merge area
   // [slots][rows][kRowPad] and statistics [slots][rows][4], then the places of the sequences in the line
@@ -824,12 +828,14 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
   // All turns of a segment that are the warp's, summed up in r.
   const auto process = [&](const Segment& seg) {
     const int rows = seg.seq.rows;
-    const int tiles = min(max(((rows + 7) / 8 - share + kShare - 1) / kShare, 0), NT);
+    // tiles nt step + first of the pair's are the warp's
+    const int first_tile = kAlone ? seg.row_group : share, step_tile = kAlone ? p.row_groups : kShare;
+    const int tiles = min(max(((rows + 7) / 8 - first_tile + step_tile - 1) / step_tile, 0), NT);
     uint32_t qf[S::HT][4][2];
-    if (S::HT == NT) load_queries<S::HT>(p, seg.seq, seg.head, rows, share, kShare, qf);
+    if (S::HT == NT) load_queries<S::HT>(p, seg.seq, seg.head, rows, first_tile, step_tile, qf);
     const int first = seg.seq.len - seg.seq.n;
     const auto pos = [&](int nt, int e) {
-      const int row = 8 * (nt * kShare + share) + 2 * t + e;
+      const int row = 8 * (nt * step_tile + first_tile) + 2 * t + e;
       return row < rows ? first + p.row_of_seq(row) : -1;
     };
     rows_clear(r);
@@ -837,7 +843,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
       if (tiles == 0) return;
       const auto step = [&](auto first) {
         constexpr int kFirst = decltype(first)::value;
-        if (S::HT < NT) fetch_queries<S::HT>(smem_u32(queries), kFirst * kShare + share, kShare, qf);
+        if (S::HT < NT)
+          fetch_queries<S::HT>(smem_u32(queries) + (kAlone ? warp * kQueryBytes : 0), kFirst * kShare + share, kShare, qf);
         if (turn.masked)
           turn_step<NT, kFirst, S::HT, true>(r, keys, qf, tiles, p.coef, slack, pos, turn, p.window, p.prefix);
         else
@@ -869,12 +876,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
   const int group = static_cast<int>(blockIdx.x) / heads_at_once;
   int b_first = 0, head_first = static_cast<int>(blockIdx.x) - group * heads_at_once, pad = 0;
   long long x_first = 0, x_begin = 0, x_end = 0;  // places in the line: of the first pair, and of the share
-  int pair = warp * ctas + static_cast<int>(blockIdx.x);  // pairs: 4096 entries of 256 heads at most
+  int pair = warp * ctas + static_cast<int>(blockIdx.x);  // of 4096 entries with 256 heads and 3 groups of rows at most
+  const int per_seq = heads * (kAlone ? p.row_groups : 1);
   Shares shares(1, 1);
   if (alone) {
-    if (pair >= p.num_seqs * heads) return;
-    b_first = pair / heads;
-    head_first = pair - b_first * heads;
+    if (pair >= p.num_seqs * per_seq) return;
+    b_first = pair / per_seq;
+    head_first = pair - b_first * per_seq;
   } else if constexpr (!kAlone) {
     // a turn at least for every team, unless that leaves pairs without a worker of their own; no less than the most
     // that a turn costs, so that every share between a cut pair's first and last has a turn of it
@@ -908,12 +916,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
       if (b_first >= p.num_seqs || x_first + pad >= x_end) return;  // it lies in one turn, or in what beginning a pair costs
     }
   }
-  // The worker's part of a pair that begins at x of the line.
+  // The worker's part of a pair that begins at x of the line (alone: of head / row_groups, and that group of rows).
   const auto segment_at = [&](int b, int head, long long x) {
     Segment s;
     s.x = x;
     s.b = b;
-    s.head = head;
+    s.head = kAlone ? head / p.row_groups : head;
+    s.row_group = kAlone ? head - s.head * p.row_groups : 0;
     s.seq = sequence(p, b);
     s.span = visible_span(p, s.seq);
     s.turns = s.t1 = s.span.count();
@@ -941,7 +950,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
     if (!first) {
       const int rows = done.seq.rows;
       if (kMayAlone && alone) {
-        finish_tiles<NT>(p, done.seq, done.head, rows, r);
+        finish_tiles<NT>(p, done.seq, done.head, rows, kAlone ? done.row_group : 0, kAlone ? p.row_groups : 1, r);
       } else if constexpr (!kAlone) {
         // A pair that is cut is published when the worker is through, with one
         // fence and no copies in flight for it to wait for.
@@ -1061,25 +1070,30 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
     cur ^= 1;
     first = false;
     if (S::HT < NT) {
-      // the pair's queries into shared memory, zeros behind the last row
+      // the pair's queries into shared memory, zeros behind the last row (alone: the warp's tiles)
       const Segment& now = segments[cur][warp];
-      for (int u = tid; u < kRows * 8; u += kThreads) {
-        const int row = u >> 3, c = u & 7;
+      uint8_t* to = queries + (kAlone ? warp * kQueryBytes : 0);
+      for (int u = kAlone ? lane : tid; u < kRows * 8; u += kAlone ? 32 : kThreads) {
+        const int at = u >> 3, c = u & 7;
+        const int row = kAlone ? 8 * ((at >> 3) * p.row_groups + now.row_group) + (at & 7) : at;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (row < now.seq.rows) {
           const int i = p.row_of_seq(row), h = now.head * p.group + row - i * p.group;
           v = __ldg(reinterpret_cast<const uint4*>(p.q + ((static_cast<int64_t>(now.seq.row0) + i) * p.hq + h) * kHeadDim) + c);
         }
-        *reinterpret_cast<uint4*>(queries + swz(row, c)) = v;
+        *reinterpret_cast<uint4*>(to + swz(at, c)) = v;
       }
-      __syncthreads();
+      if (kAlone)
+        __syncwarp();
+      else
+        __syncthreads();
     }
     process(segments[cur][warp]);
     if (alone) {
       pair += ctas * kWarps;
-      more = pair < p.num_seqs * heads;
-      const int b = pair / heads;
-      if (more) set_next(segment_at(b, pair - b * heads, 0));
+      more = pair < p.num_seqs * per_seq;
+      const int b = pair / per_seq;
+      if (more) set_next(segment_at(b, pair - b * per_seq, 0));
     } else {
       const Segment& done = segments[cur][warp];
       const long long x = done.x + static_cast<long long>(done.turns) * done.cost + pad;
@@ -1122,7 +1136,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kPerSm) kv_decode_kernel(const
 
 template <class S, bool kAlone>
 cudaError_t launch_kernel(const PageDecK& p, cudaStream_t s) {
-  constexpr size_t kFixed = 1024 + S::kRing + (kAlone ? 0 : S::kQueries + S::kMerge);
+  constexpr size_t kFixed = 1024 + S::kRing + (kAlone ? S::kWarps * S::kQueries : S::kQueries + S::kMerge);
   static_assert(kFixed + kKv4MaxRequests / kUptoStep * sizeof(long long) <= 227 * 1024, "shared memory");
   const auto kernel = kv_decode_kernel<S, kAlone>;
   const auto bytes = [](int seqs) { return kFixed + (kAlone ? 0 : ceil_div(seqs, kUptoStep) * sizeof(long long)); };
@@ -1188,9 +1202,18 @@ cudaError_t launch_kv_decode(const KvPages& c, const KvDecodeArgs& a, int* statu
   // One tile of rows: two turns in flight for each of 8 warps an SM (32 x 8192 keys 88.5 us; three turns 92.3, two for
   // 12 warps 91.1, four for 4 warps 92.5).  Up to 48 rows a warp has them all, in halves above 32 (8 x 32768 keys x 1 to
   // 5 rows 121 us; thirds 126, three tiles by each of two warps 180, two turns ahead for 6 warps 154).  Alone: 12 warps an
-  // SM (17.9 us; 8 warps 25.4).
-  if (rows <= 8) return alone ? launch_kernel<Shape<1, 1, 4, 2, 3>, true>(p, s) : launch_kernel<Shape<1, 1, 4, 2, 2>, false>(p, s);
-  if (rows <= 16) return alone ? launch_kernel<Shape<2, 1, 4, 2, 3>, true>(p, s) : launch_kernel<Shape<2, 1, 4, 2, 2>, false>(p, s);
+  // SM (200 windowed sequences 17.9 us; 8 warps 25.4), 8 above 16 rows (with 4 rows each 39.8 us, by shares 64.9), and
+  // above 48 rows groups of them go to a warp each (with 8 rows, 40 a kv head, 84.9 us, by shares 150).
+  p.row_groups = 1;
+  if (alone) {
+    if (rows <= 8) return launch_kernel<Shape<1, 1, 4, 2, 3>, true>(p, s);
+    if (rows <= 16) return launch_kernel<Shape<2, 1, 4, 2, 3>, true>(p, s);
+    if (rows <= 32) return launch_kernel<Shape<4, 1, 4, 2, 2>, true>(p, s);
+    p.row_groups = ceil_div(rows, 48);
+    return launch_kernel<Shape<6, 1, 8, 2, 1>, true>(p, s);
+  }
+  if (rows <= 8) return launch_kernel<Shape<1, 1, 4, 2, 2>, false>(p, s);
+  if (rows <= 16) return launch_kernel<Shape<2, 1, 4, 2, 2>, false>(p, s);
   if (rows <= 32) return launch_kernel<Shape<4, 1, 4, 2, 2>, false>(p, s);
   if (rows <= 48) return launch_kernel<Shape<6, 1, 8, 2, 1>, false>(p, s);
   if (rows <= 64) return launch_kernel<Shape<4, 2, 4, 3, 1>, false>(p, s);

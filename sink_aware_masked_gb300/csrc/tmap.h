@@ -31,8 +31,7 @@ inline EncodeTiledFn encode_fn() {
 }
 
 // Returns false when the driver entry point is missing or the encode fails.
-inline bool make_rows_map(CUtensorMap* m, const void* base, long long tokens, int heads, int box_rows,
-                          CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
+inline bool make_rows_map(CUtensorMap* m, const void* base, long long tokens, int heads, int box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(heads) * 64, static_cast<cuuint64_t>(tokens)};
@@ -40,7 +39,7 @@ inline bool make_rows_map(CUtensorMap* m, const void* base, long long tokens, in
   cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
   cuuint32_t es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

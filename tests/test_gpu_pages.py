@@ -260,6 +260,27 @@ def test_decode_cut_between_ctas(batch, length, page, heads, group, n):
     check_decode(c, slots, [n] * batch, hq, -1, 0, q, sink, o, lse)
 
 
+@pytest.mark.parametrize("n,group", [(1, 5), (2, 8), (4, 8), (5, 8), (7, 8), (8, 16), (3, 40), (1, 50)])
+@pytest.mark.parametrize("window,prefix,hi", [(40, 3, 500), (0, 0, 90), (-1, 0, 150)])
+def test_many_short_pairs(n, group, window, prefix, hi):
+    """Warps that take whole pairs, alone: every count of rows, some entries without any, some longer than their slots."""
+    import sink_aware_masked_gb300 as sa
+
+    rng = np.random.RandomState(n + group)
+    lens = [int(x) for x in rng.randint(0, hi, 90)]
+    c = shuffled(rng, lens, 16, 2)
+    h, hq = handle(c), 2 * group
+    counts = [int(x) for x in rng.randint(0, n + 1, 90)]
+    counts[7] = n
+    R = sum(counts)
+    q, sink = bf16(rng, R, hq, 64).to(DEV), dev(rng.randn(hq), torch.float32)
+    cu = i32(np.concatenate(([0], np.cumsum(counts))))
+    slots = [int(x) for x in rng.permutation(90)]
+    slots[3] = -1
+    o, lse = sa.kv_decode_fwd(h, i32(slots), q, sink, q_per_seq=n, cu_rows=cu, window=window, prefix=prefix)
+    check_decode(c, slots, counts, hq, window, prefix, q, sink, o, lse)
+
+
 @pytest.mark.parametrize("longest", [3, 5000])
 def test_as_many_entries_as_a_call_takes(longest):
     import sink_aware_masked_gb300 as sa
