@@ -436,7 +436,8 @@ sinkattn_status sinkattn_kv_write(const sinkattn_kv_pages* pages, const int32_t*
  * Rows outside every entry's, and rows of an entry beyond q_per_seq, are left
  * as they were.  What a row does not see does not reach it, whatever it holds;
  * scores are fp32: a row that sees one beyond fp32's range in log2 units may
- * read as NaN; outputs below 2^-126 may be 0.  (num_heads_q / num_heads_kv) * q_per_seq <= 128.  The
+ * read as NaN; the weighted values are summed in fp32 (weights up to 1); outputs
+ * below 2^-126 may be 0.  (num_heads_q / num_heads_kv) * q_per_seq <= 128.  The
  * workspace (sinkattn_kv_decode_workspace_size bytes, 16-byte aligned, its size
  * depends on the device's SM count) is zero-filled once; every call leaves it
  * usable for later calls of any shape with as many kv heads or fewer, not for
@@ -467,7 +468,9 @@ sinkattn_status sinkattn_kv_decode_fwd(const sinkattn_kv_pages* pages, const int
  * logp [rows] their log p (what sinkattn_grpo_loss takes as logp_old), 0 behind
  * them.  accepted, rejected [num_seqs]: drafts that stand and that do not.
  * Rows outside every entry's are left as they were; an entry without rows has
- * accepted = rejected = 0.
+ * accepted = rejected = 0.  Where u q(d) and p(d) agree to 2^-20 of themselves, or
+ * a place drawn lies within 2^-24 of the whole of p from a border, either side
+ * may be given: the same for the same call, not for a row in another batch.
  * Logits of -inf are never drawn; so a choice of tokens (a grammar, a top-k) is
  * made by -inf in both rows.  p and q below 2^-1074 of their largest count as
  * 0.  A draft outside [0, vocab) does not stand.  An
