@@ -365,9 +365,12 @@ SA_DEV float power(Pair t) {
   const float e = ex2(t.hi);
   return t.hi > -126.f ? fmaf(e, t.lo * kLn2, e) : 0.f;
 }
-// 2^t to some 2^-40 of itself, t in (-60, 0]: 2^(n + k/16) (1 + g + g^2/2 + ...), g = ln 2 times the rest of t,
-// |g| <= ln 2 / 32.
+// 2^t to some 2^-40 of itself, t <= 0: 2^(n + k/16) (1 + g + g^2/2 + ...), g = ln 2 times the rest of t, |g| <= ln 2 / 32.
+// 0 from t = -60 down, where no unit of 2^-40 is left (a ratio of two sums brings back 2^18 at most), and where t is -inf
+// or, behind it, a NaN: a token that is heavy in one row may be anything in the other, and the scale holds for t > -127
+// alone.
 __device__ __noinline__ Pair power_pair(Pair t) {
+  if (!(t.hi > -60.f)) return {0.f, 0.f};
   const float m = rintf(t.hi * 16.f), rest = fmaf(m, -0.0625f, t.hi) + t.lo;  // the first difference is exact
   const float rest_lo = t.lo - (rest - fmaf(m, -0.0625f, t.hi));
   const int i = static_cast<int>(m), k = i & 15;
@@ -385,6 +388,7 @@ SA_DEV Pair to_pair(u64 m) {
   const float hi = __ull2float_rn(m);
   return {hi, __ll2float_rn(static_cast<long long>(m - static_cast<u64>(hi)))};
 }
+// Of a mass below 2^20 of its row's largest: the product stays below 2^61.
 __device__ __noinline__ long long to_units(Pair e, float unit) { return __float2ll_rn(e.hi * unit) + __float2ll_rn(e.lo * unit); }
 
 // ---------------------------------------------------------------- an entry

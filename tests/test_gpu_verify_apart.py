@@ -1,0 +1,100 @@
+"""Verification of drafts whose model and target disagree: CUDA path vs the float64 oracle (needs a GB300).
+
+A token that one row makes likely can have any logit in the other row: a mask
+of whatever finite value, or one far below the other row's favourite at a low
+temperature.  Every entry here ends at a refused draft, so that its last token
+is drawn from max(p - q, 0); tolerances are those of the verification's other
+tests (a place drawn is compared to 2^-24 of the target's whole).
+"""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_verify import DEV, built, check  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+TEMPERATURES = [0.05, 0.1, 0.2, 0.3, 0.6, 0.7, 0.8, 0.9, 1.0, 1.2]
+
+
+def softmax(x, temps):
+    return torch.softmax(x.double().cpu() / torch.tensor(np.float32(temps), dtype=torch.float64)[:, None], -1)
+
+
+def refused(x, y, temps, rng):
+    """One draft an entry (rows 2 b and 2 b + 1 of x, row b of y), the one that q likes best beyond p: none stands."""
+    p, q = softmax(x[::2], temps), softmax(y, temps)
+    drafts = (q - p).argmax(-1)
+    at = torch.arange(len(temps))
+    assert (q[at, drafts] > 1.01 * p[at, drafts]).all()  # u is 0.999 or more
+    u = np.stack((0.999 + 0.0009 * rng.rand(len(temps)), rng.rand(len(temps))), -1).reshape(-1)
+    assert check(x, drafts.numpy(), u, [2] * len(temps), y, temps) == len(temps)
+
+
+@pytest.mark.parametrize("vocab", [4, 37, 4099, 50257])
+@pytest.mark.parametrize("dtype,mask", [(t, m) for t in (torch.float32, torch.bfloat16, torch.float16)
+                                        for m in (-100.0, -200.0, -1e4, -65504.0, -1e9)
+                                        if t is not torch.float16 or m >= -65504.0])
+@pytest.mark.parametrize("side", ["target", "draft", "both"])
+def test_finite_masks_of_one_row(side, dtype, mask, vocab):
+    """The other row's favourite is masked, and a third of the tokens with it; "both": each row masks its own."""
+    rng = np.random.RandomState(vocab + int(-mask) % 97)
+    temps = [t for t in TEMPERATURES for _ in range(4 if vocab < 1000 else 1)]
+    B = len(temps)
+    x, y = (torch.from_numpy(rng.randn(n, vocab) * 2).to(dtype).to(DEV) for n in (2 * B, B))
+    for b in range(B):
+        best = int((x[2 * b] if side == "draft" else y[b]).argmax())
+        masked = torch.from_numpy(rng.rand(vocab) < 0.3).to(DEV)
+        masked[best] = True
+        masked[(best + 1) % vocab] = False
+        if side == "both":
+            x[2 * b, (best + 1) % vocab] = 9.0
+            y[b, best], y[b, (best + 1) % vocab] = 9.0, mask
+        if side == "draft":
+            x[2 * b, best] = 9.0
+            y[b, masked] = mask
+        else:
+            x[2 * b, masked] = mask
+    refused(x, y, temps, rng)
+
+
+def test_masks_drawn_over_a_grid():
+    """Small rows, a grid of the random numbers: a token masked in the target is never drawn, one masked in the draft is."""
+    rows = [((-1e9, 2, 1, 0), (3, 0.5, 1, 1.5)), ((-1e4, 2, 1, 0), (3, 0.5, 1, 1.5)), ((-100, 2, 1, 0), (3, 0.5, 1, 1.5)),
+            ((3, 2, 1, 0), (-1e9, 2, 1, 0)), ((3, 2, 1, 0), (-1e4, 2, 1, 0)), ((3, 2, 1, 0), (-100, 2, 1, 0))]
+    for x, y in rows:
+        for T in TEMPERATURES:
+            N = 64
+            xs, ys = (torch.tensor([r], device=DEV).expand(n, 4).float().contiguous() for r, n in ((x, 2 * N), (y, N)))
+            drafts = np.full(N, 0 if x[0] < 0 else 1)  # q likes it more than p does
+            u = np.stack((np.full(N, 0.9999), (np.arange(N) + 0.37) / N), -1).reshape(-1)
+            assert check(xs, drafts, u, [2] * N, ys, [T] * N) == N
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", [0.05, 0.1, 0.7, 1.0])
+@pytest.mark.parametrize("vocab", [5, 3001])
+def test_favourites_that_the_other_row_has_far_below(vocab, T, dtype):
+    """Each row's favourite lies 0.1 to 800 log2 units below the other's: in the target, in the draft row, in both."""
+    rng = np.random.RandomState(vocab)
+    gaps = np.linspace(0.1, 800, 240) * T * np.log(2)
+    B = len(gaps)
+    x, y = (torch.from_numpy(rng.randn(n, vocab) * 0.5).to(dtype).to(DEV) for n in (2 * B, B))
+    for b, gap in enumerate(gaps):
+        side = b % 3
+        x[2 * b, 2], y[b, 2] = 3.0, 3.0  # a token that both like
+        x[2 * b, 0], y[b, 1] = 4.0, 4.0
+        x[2 * b, 1] = 3.0 - gap if side != 1 else 2.5
+        y[b, 0] = 3.0 - gap if side != 0 else 2.5
+    refused(x, y, [T] * B, rng)
+
+
+def test_rows_that_have_nothing_in_common():
+    """Half of the vocabulary masked in one row, the other half in the other, by values of every size."""
+    rng = np.random.RandomState(1)
+    temps = TEMPERATURES * 6
+    B, V = len(temps), 2500
+    x, y = (torch.from_numpy(rng.randn(n, V)).float().to(DEV) for n in (2 * B, B))
+    for b in range(B):
+        low = -float(10.0 ** (1.5 + 8 * rng.rand()))
+        x[2 * b, :V // 2], y[b, V // 2:] = low, low * 1.5
+    refused(x, y, temps, rng)
