@@ -368,8 +368,10 @@ sinkattn_status sinkattn_sample_tokens(const void* logits, int32_t dtype, int32_
  *   sinkattn_kv_plan        where the new tokens of every slot go
  *   sinkattn_kv_write       their keys and values
  *   sinkattn_kv_decode_fwd  attention of all of them
- *   sinkattn_verify_tokens  which drafts stand; those that do not are the next
- *                           plan's `drop`
+ *   sinkattn_verify_live_tokens
+ *                           which drafts stand, of the entries that the plan
+ *                           served (its `live`); those that do not are the
+ *                           next plan's `drop`
  * All state is on the device and every call is asynchronous, so a step can be
  * captured into a CUDA graph and replayed while the sequences grow (make the
  * first call of each kind on a device outside any capture).
@@ -488,6 +490,19 @@ sinkattn_status sinkattn_verify_tokens(const void* logits, int64_t row_stride, c
                                        const float* u, const float* temperature, int32_t* tokens, float* logp,
                                        int32_t* accepted, int32_t* rejected, void* workspace, size_t workspace_bytes,
                                        void* stream);
+/* The same of a plan's entries: one with live[b] < 0 (int32 [num_seqs], as
+ * sinkattn_kv_plan leaves it; NULL: all are served) has none of its rows in the
+ * pages, so nothing of it is read, stands or is refused: tokens -1, logp 0,
+ * accepted = rejected = 0, and the next plan drops nothing of what its slot
+ * holds.  Its rows and drafts are counted in cu_rows and in the drafts like any
+ * other's.  (sinkattn_verify_tokens would refuse drafts that were never
+ * written: its `rejected` must not reach a plan for such an entry.) */
+sinkattn_status sinkattn_verify_live_tokens(const void* logits, int64_t row_stride, const void* draft_logits,
+                                            int64_t draft_stride, int32_t dtype, int32_t rows, int32_t num_drafts,
+                                            int32_t vocab, const int32_t* drafts, const int32_t* cu_rows,
+                                            const int32_t* live, int32_t num_seqs, const float* u,
+                                            const float* temperature, int32_t* tokens, float* logp, int32_t* accepted,
+                                            int32_t* rejected, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Packed-sequence front end (multi-turn trajectories of different lengths,
  * SinkFlex-RL section 3).  seqlens: device int32 [num_seqs];

@@ -118,6 +118,8 @@ SIGNATURES = {
     "sinkattn_verify_workspace_size": (_sz, [_i32, _i32, _i32]),
     "sinkattn_verify_tokens": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp,
                                               _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "sinkattn_verify_live_tokens": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i32, _vp,
+                                                   _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "sinkattn_varlen_plan": (ctypes.c_int, [_vp, _i32, _vp, _vp]),
     "sinkattn_pack": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp]),
     "sinkattn_unpack": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp]),

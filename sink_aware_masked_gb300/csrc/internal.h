@@ -270,6 +270,7 @@ struct VerifyArgs {
   long long stride, draft_stride;  // elements
   const int32_t* drafts;     // [num_drafts]
   const int32_t* cu;         // [num_seqs + 1]
+  const int32_t* live;       // [num_seqs], below 0: not served; or nullptr
   const float* u;            // [rows]
   const float* temperature;  // [num_seqs]
   int32_t* tokens;           // [rows]

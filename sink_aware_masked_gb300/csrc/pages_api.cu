@@ -124,6 +124,17 @@ sinkattn_status sinkattn_verify_tokens(const void* logits, int64_t row_stride, c
                                        const float* u, const float* temperature, int32_t* tokens, float* logp,
                                        int32_t* accepted, int32_t* rejected, void* workspace, size_t workspace_bytes,
                                        void* stream) {
+  return sinkattn_verify_live_tokens(logits, row_stride, draft_logits, draft_stride, dtype, rows, num_drafts, vocab,
+                                     drafts, cu_rows, nullptr, num_seqs, u, temperature, tokens, logp, accepted, rejected,
+                                     workspace, workspace_bytes, stream);
+}
+
+sinkattn_status sinkattn_verify_live_tokens(const void* logits, int64_t row_stride, const void* draft_logits,
+                                            int64_t draft_stride, int32_t dtype, int32_t rows, int32_t num_drafts,
+                                            int32_t vocab, const int32_t* drafts, const int32_t* cu_rows,
+                                            const int32_t* live, int32_t num_seqs, const float* u,
+                                            const float* temperature, int32_t* tokens, float* logp, int32_t* accepted,
+                                            int32_t* rejected, void* workspace, size_t workspace_bytes, void* stream) {
   if (dtype < 0 || dtype > 2 || rows < 0 || num_drafts < 0 || num_drafts > rows || vocab < 1 || row_stride < vocab ||
       (draft_logits != nullptr && draft_stride < vocab))
     return SINKATTN_ERR_INVALID_ARG;
@@ -134,7 +145,7 @@ sinkattn_status sinkattn_verify_tokens(const void* logits, int64_t row_stride, c
     return st;
   if (num_seqs == 0) return SINKATTN_OK;
   if (!cu_rows) return SINKATTN_ERR_INVALID_ARG;
-  if (!aligned4(cu_rows)) return SINKATTN_ERR_ALIGNMENT;
+  if (!aligned4(cu_rows) || !aligned4(live)) return SINKATTN_ERR_ALIGNMENT;
   if ((rows > 0 && (!logits || !u || !tokens || !logp)) || (num_drafts > 0 && !drafts)) return SINKATTN_ERR_INVALID_ARG;
   const uintptr_t size = dtype == 0 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(logits) % size != 0 || reinterpret_cast<uintptr_t>(draft_logits) % size != 0 ||
@@ -144,7 +155,7 @@ sinkattn_status sinkattn_verify_tokens(const void* logits, int64_t row_stride, c
   if (rows > 0 && (workspace == nullptr || !aligned16(workspace)))
     return workspace ? SINKATTN_ERR_ALIGNMENT : SINKATTN_ERR_INVALID_ARG;
   const sa::VerifyArgs a{logits, draft_logits, dtype, rows, num_drafts, vocab, num_seqs, row_stride, draft_stride,
-                         drafts, cu_rows, u, temperature, tokens, logp, accepted, rejected,
+                         drafts, cu_rows, live, u, temperature, tokens, logp, accepted, rejected,
                          static_cast<float4*>(workspace)};
   return from_cuda(sa::launch_verify(a, static_cast<cudaStream_t>(stream)));
 }

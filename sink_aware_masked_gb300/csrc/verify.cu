@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kStatThreads, kStatPerSm) verify_rows_kernel(c
   }
   __syncthreads();
   const int b = seq_sh;
-  if (b >= a.num_seqs) return;  // a row of no entry
+  if (b >= a.num_seqs || (a.live != nullptr && a.live[b] < 0)) return;  // a row of no entry, or of one that was not served
   const Scale sc(a.temperature[b]);
   if (!sc.valid || (draft && sc.greedy)) return;
   Running r{kLowest, 0.f};
@@ -418,7 +418,7 @@ struct alignas(16) Sums {
 struct alignas(16) Stop {
   RowStat p, q;
   int row, draft;  // row: -1 for an entry without rows; draft: the one that did not stand, or -1
-  int drawn;       // 0: the token is written already
+  int drawn;       // 0: the token is written already, or there is none
   int pad[3];
 };
 
@@ -471,6 +471,17 @@ class Entry {
     s.row = -1;
     if (n <= 0) {
       if (writes && tid == 0) a_.accepted[b] = a_.rejected[b] = 0;
+      return s;
+    }
+    if (a_.live != nullptr && a_.live[b] < 0) {  // its logits are of nothing: none of its drafts stands, and none is refused
+      s.row = row0;
+      if (writes) {
+        for (int i = tid; i < n; i += kThreads) {
+          a_.tokens[row0 + i] = -1;
+          a_.logp[row0 + i] = 0.f;
+        }
+        if (tid == 0) a_.accepted[b] = a_.rejected[b] = 0;
+      }
       return s;
     }
     int draft0 = row0 - a_.cu[0];  // one draft fewer than rows in every entry before that has rows

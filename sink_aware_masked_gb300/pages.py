@@ -13,7 +13,11 @@ behind it::
     kv_write(pages, slot_map, k, v)                      # k, v [total, Hkv, 64] bf16
     o, lse = kv_decode_fwd(pages, live, q, sink, q_per_seq=most, cu_rows=cu, workspace=ws)
     ...
-    tokens, logp, accepted, rejected = verify_tokens(logits, drafts, u, cu, draft_logits=...)
+    tokens, logp, accepted, rejected = verify_tokens(logits, drafts, u, cu, draft_logits=..., live=live)
+
+A request that found no page (live -1) has its rows in cu all the same, but not
+in the pages; with ``live`` the verification rejects nothing of it, and the slot
+keeps what it holds until a later plan serves it.
 """
 from __future__ import annotations
 

@@ -339,7 +339,7 @@ def verify_workspace(logits) -> torch.Tensor:
     return torch.empty(max(size, 16), dtype=torch.uint8, device=logits.device)
 
 
-def verify_tokens(logits, drafts, u, cu_rows, *, draft_logits=None, temperature=None, tokens=None, logp=None,
+def verify_tokens(logits, drafts, u, cu_rows, *, draft_logits=None, temperature=None, live=None, tokens=None, logp=None,
                   accepted=None, rejected=None, workspace=None):
     """Which drafted tokens stand, and the token that follows them: returns (tokens, logp, accepted, rejected).
 
@@ -350,7 +350,9 @@ def verify_tokens(logits, drafts, u, cu_rows, *, draft_logits=None, temperature=
     (the same type), or without (drafts that were looked up).  u fp32 [R] random
     numbers in [0, 1): a row's for its draft, an entry's last one for the token
     that is drawn.  temperature fp32 [B] (default 1; 0: the largest logit), for
-    both.  tokens int32 [R]: the drafts that stand, the token drawn, -1 behind
+    both.  live int32 [B] (from ``kv_plan``): an entry below 0 was not served, and
+    nothing of it stands or is rejected (tokens -1, logp 0, accepted = rejected
+    = 0), so that ``rejected`` can be the next plan's ``drop``.  tokens int32 [R]: the drafts that stand, the token drawn, -1 behind
     it; logp fp32 [R] their log-probabilities under the target (grpo_loss's
     logp_old), 0 behind them; accepted and rejected int32 [B].  An invalid row
     ends its entry with token -1 and logp NaN, one without an allowed token
@@ -376,6 +378,7 @@ def verify_tokens(logits, drafts, u, cu_rows, *, draft_logits=None, temperature=
     cp = _tensor("cu_rows", cu_rows, i32, (B + 1,), dev)
     temperature = torch.ones(B, dtype=f32, device=dev) if temperature is None else temperature
     tp = _tensor("temperature", temperature, f32, (B,), dev)
+    vp = None if live is None else _tensor("live", live, i32, (B,), dev)
     logp, lp = _output("logp", logp, u, f32, (R,), dev)
     tokens = torch.empty(R, dtype=i32, device=dev) if tokens is None else tokens
     accepted = torch.empty(B, dtype=i32, device=dev) if accepted is None else accepted
@@ -385,6 +388,6 @@ def verify_tokens(logits, drafts, u, cu_rows, *, draft_logits=None, temperature=
     if workspace is None:
         workspace = verify_workspace(logits)
     wn = _vector("workspace", workspace, torch.uint8, dev)
-    _call("sinkattn_verify_tokens", dev, logits.data_ptr(), stride, xp, xs, kind, R, D, V, dp, cp, B, up, tp, to, lp, ap,
-          rp, _tensor("workspace", workspace, torch.uint8, (wn,), dev), wn)
+    _call("sinkattn_verify_live_tokens", dev, logits.data_ptr(), stride, xp, xs, kind, R, D, V, dp, cp, vp, B, up, tp, to,
+          lp, ap, rp, _tensor("workspace", workspace, torch.uint8, (wn,), dev), wn)
     return tokens, logp, accepted, rejected
