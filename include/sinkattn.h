@@ -385,7 +385,8 @@ sinkattn_status sinkattn_sample_tokens(const void* logits, int32_t dtype, int32_
  * out: write and decode read the table and the lengths only.
  *
  * Rows of several sequences stand one after another: those of entry b are
- * cu[b] .. cu[b + 1] - 1 (int32 on the device, nondecreasing).  Entries of
+ * cu[b] .. cu[b + 1] - 1 (int32 on the device, nondecreasing; what lies
+ * outside the call's rows is not there).  Entries of
  * `slots` outside [0, num_slots) are idle: they read as an empty sequence.  A
  * page number outside [0, num_pages), or a position beyond the table, is never
  * accessed: tokens there are not written and read as NaN.  Limits: page_size

@@ -490,7 +490,7 @@ class Entry {
     // the drafts, a warp each; what an earlier stop makes void is overwritten below
     for (int i = warp; i < n - 1; i += kWarps) {
       bool stands = false;
-      if (sc.valid && draft0 + i < a_.num_drafts) {
+      if (sc.valid && has_draft(draft0 + i)) {
         const int token = a_.drafts[draft0 + i];
         const bool inside = token >= 0 && token < a_.vocab;
         const float x = inside ? E::one(row_of<T>(a_, row0 + i)[token]) : -INFINITY;
@@ -539,7 +539,7 @@ class Entry {
       return s;
     };
     const bool refused = j < n - 1;
-    if (!sc.valid || (refused && draft0 + j >= a_.num_drafts)) return put(-1, NAN);
+    if (!sc.valid || (refused && !has_draft(draft0 + j))) return put(-1, NAN);
     if (refused) s.draft = draft0 + j;
     s.p = stat(s.row, sc);
     const bool minus_q = refused && a_.draft_logits != nullptr && !sc.greedy;
@@ -552,6 +552,7 @@ class Entry {
     return s;
   }
  private:
+  SA_DEV bool has_draft(int i) const { return i >= 0 && i < a_.num_drafts; }
   // Of target row `item`, or of draft item - rows; by a whole warp.
   SA_DEV RowStat stat(int item, const Scale& sc) const {
     const float4* parts = a_.parts + static_cast<int64_t>(item) * slices_;
@@ -799,7 +800,7 @@ struct Places {
   bool by_row;  // an entry's place goes by its first row, not by its number: there are more entries than rows
   Stop* stops;  // [min(rows, most entries)]
   Sums* sums;   // [the same][parts][kWarps]
-  SA_DEV int of(const VerifyArgs& a, int b) const { return by_row ? a.cu[b] : b; }
+  SA_DEV int of(const VerifyArgs& a, int b) const { return by_row ? max(a.cu[b], 0) : b; }  // (of an entry that has rows)
 };
 
 // CTA: tests entry b's drafts.

@@ -98,3 +98,30 @@ def test_rows_that_have_nothing_in_common():
         low = -float(10.0 ** (1.5 + 8 * rng.rand()))
         x[2 * b, :V // 2], y[b, V // 2:] = low, low * 1.5
     refused(x, y, temps, rng)
+
+
+@pytest.mark.parametrize("entries", [3, 30, 900])
+@pytest.mark.parametrize("proposal", [True, False])
+def test_offsets_outside_the_rows(entries, proposal):
+    """Offsets that begin below 0 and end behind the rows, also with more entries than rows: the rows that are there count,
+    and nothing is written around the workspace."""
+    import sink_aware_masked_gb300 as sa
+
+    rng = np.random.RandomState(entries)
+    R, V = 12, 300
+    x = torch.from_numpy(rng.randn(R, V)).float().to(DEV)
+    drafts = torch.from_numpy(rng.randint(0, V, R)).int().to(DEV)
+    y = torch.from_numpy(rng.randn(R, V)).float().to(DEV) if proposal else None
+    u = torch.from_numpy(rng.rand(R)).float().to(DEV)
+    # rows -3 .. 1 (of which 0 and 1 are there, behind three drafts of rows that are not), empty entries, 2 .. 6, 7 .. 19
+    cu = [-3] + [2] * (entries - 2) + [7, 20]
+    want = sa.verify_tokens(x, drafts[3:], u, torch.tensor([0, 2, 7, 12], dtype=torch.int32, device=DEV),
+                            draft_logits=None if y is None else y[3:])
+    size = sa.verify_workspace(x).numel()
+    room = torch.full((size + (2 << 16),), 91, dtype=torch.uint8, device=DEV)
+    got = sa.verify_tokens(x, drafts, u, torch.tensor(cu, dtype=torch.int32, device=DEV), draft_logits=y,
+                           workspace=room[1 << 16:-(1 << 16)])
+    assert (room[:1 << 16] == 91).all() and (room[-(1 << 16):] == 91).all()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for a, b in zip(got[2:], want[2:]):
+        assert a[[0, -2, -1]].tolist() == b.tolist() and (a[1:-2] == 0).all()
