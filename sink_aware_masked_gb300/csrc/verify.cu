@@ -349,21 +349,28 @@ struct Pair {
   float hi, lo;
 };
 
+// a - b, and what it was rounded by.
+SA_DEV Pair minus(float a, float b) {
+  const float d = __fadd_rn(a, -b), c = __fadd_rn(d, -a);
+  return {d, __fadd_rn(__fadd_rn(a, -__fadd_rn(d, -c)), -__fadd_rn(b, c))};
+}
 // t = (x - top) scale in two parts.
 SA_DEV Pair exponent(float x, float top, const Scale& s) {
-  const float d = __fadd_rn(x, -top), b = __fadd_rn(d, -x);
-  const float d_lo = __fadd_rn(__fadd_rn(x, -__fadd_rn(d, -b)), -__fadd_rn(top, b));  // what d was rounded by
-  const float hi = __fmul_rn(d, s.hi);
-  return {hi, __fmaf_rn(d, s.hi, -hi) + __fmaf_rn(d, s.lo, d_lo * s.hi)};
+  const Pair d = minus(x, top);
+  const float hi = __fmul_rn(d.hi, s.hi);
+  return {hi, __fmaf_rn(d.hi, s.hi, -hi) + __fmaf_rn(d.hi, s.lo, d.lo * s.hi)};
 }
 // An exponent at which nothing is left (fp64's least): a token masked in both
 // rows, by whatever value, does not stand.
 constexpr float kNothing = -1074.f;
 
-// 2^t to some 2^-23 of itself; 0 below fp32's normal numbers.
-SA_DEV float power(Pair t) {
-  const float e = ex2(t.hi);
-  return t.hi > -126.f ? fmaf(e, t.lo * kLn2, e) : 0.f;
+// Whether u a < 2^t b, for sums a and b (1 to 2^18), u of 0 or from 2^-126 on, and any t that is not nothing: small
+// powers are brought up, large ones cut off (2^64 b is more than any u a), so that neither leaves fp32's range where it
+// decides.
+SA_DEV bool less(float u, float a, Pair t, float b) {
+  const bool small = t.hi < -64.f;
+  const float e = ex2(small ? t.hi + 64.f : fminf(t.hi, 64.f));
+  return u == 0.f || u * (small ? 18446744073709551616.f : 1.f) * a < fmaf(e, t.lo * kLn2, e) * b;
 }
 // 2^t to some 2^-40 of itself, t <= 0: 2^(n + k/16) (1 + g + g^2/2 + ...), g = ln 2 times the rest of t, |g| <= ln 2 / 32.
 // 0 from t = -60 down, where no unit of 2^-40 is left (a ratio of two sums brings back 2^18 at most), and where t is -inf
@@ -502,13 +509,14 @@ class Entry {
           if (sc.greedy) {
             stands = token == p.arg;
           } else if (a_.draft_logits == nullptr) {
-            stands = u * p.sum < power(tp);
+            stands = tp.hi > kNothing && less(u, p.sum, tp, 1.f);
           } else {
-            // u q < p by their ratio, which stays in range where both are small, if either is anything
+            // u q < p by their ratio, if either is anything
             const RowStat q = stat(a_.rows + draft0 + i, sc);
             const Pair tq = exponent(y, q.top, sc);
-            const float ratio = ex2((tp.hi - tq.hi) + (tp.lo - tq.lo)) * __fdiv_rn(q.sum, p.sum);
-            stands = !q.bad() && !q.none() && tp.hi > kNothing && (!(tq.hi > kNothing) || u < ratio);
+            Pair t = minus(tp.hi, tq.hi);
+            t.lo += tp.lo - tq.lo;
+            stands = !q.bad() && !q.none() && tp.hi > kNothing && (!(tq.hi > kNothing) || less(u, p.sum, t, q.sum));
           }
           if (stands && writes && lane == 0) {
             a_.tokens[row0 + i] = token;

@@ -10,7 +10,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_verify import DEV, built, check  # noqa: F401
+from tests.test_gpu_verify import DEV, built, check, run  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 TEMPERATURES = [0.05, 0.1, 0.2, 0.3, 0.6, 0.7, 0.8, 0.9, 1.0, 1.2]
@@ -125,3 +125,40 @@ def test_offsets_outside_the_rows(entries, proposal):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     for a, b in zip(got[2:], want[2:]):
         assert a[[0, -2, -1]].tolist() == b.tolist() and (a[1:-2] == 0).all()
+
+
+@pytest.mark.parametrize("T", [0.05, 1.0, 2.5])
+@pytest.mark.parametrize("proposal", [True, False])
+def test_probabilities_and_random_numbers_near_zero(proposal, T):
+    """p(d) and q(d) from 1 to 2^-1150 of their largest, u from 0 and 2^-126 on: a draft stands if log u + log q < log p.
+    Random numbers lie 2^-19 of themselves and more from the border (either side may be given up to 2^-20); what lies
+    below 2^-1074 of the largest counts as 0."""
+    rng = np.random.RandomState(int(T * 20) + proposal)
+    B, V = 4000, 4
+    T = float(np.float32(T))
+    x, y = torch.zeros((2 * B, V)), torch.zeros((B, V))
+    for t in (x[::2], y):
+        t[:, 1:3] = -torch.from_numpy(rng.rand(B, 2)).float() * T
+        t[:, 3] = -torch.from_numpy(1150 * rng.rand(B) ** rng.randint(1, 4, B) * np.log(2) * T).float()
+
+    def log2_of(t):  # (log2 of token 3's share, whether it counts as more than 0); no power below 2^-1022 is taken
+        z = t.double().numpy() / T / np.log(2)
+        z -= z.max(-1, keepdims=True)
+        return z[:, 3] - np.log2((2.0 ** np.maximum(z, -1000)).sum(-1)), z[:, 3] > -1074
+
+    (lp, p_is), (lq, q_is) = log2_of(x[::2]), log2_of(y) if proposal else (np.zeros(B), np.ones(B, dtype=bool))
+    away = rng.choice([-1, 1], B) * 2.0 ** rng.uniform(-19, 2, B)  # from the border, relative to it
+    border = lp - lq + np.log2(np.maximum(1 + away, 2.0 ** -30))
+    lu = np.where((border < 0) & (border >= -126) & (rng.rand(B) < 0.8), border, rng.uniform(-126, 0, B))
+    u = np.float32(np.where(rng.rand(B) < 0.2, 0.0, 2.0 ** np.maximum(lu, -126.0)))
+    with np.errstate(divide="ignore"):
+        lu = np.log2(u.astype(np.float64))
+    far = np.abs(2.0 ** np.clip(lu + lq - lp, -30, 30) - 1) > 2.0 ** -19.5  # (rounding u may have brought one nearer)
+    far &= (u < 0.9999999) & (np.abs(x[::2, 3].double().numpy() / T / np.log(2) + 1074) > 0.01)
+    far &= np.abs(y[:, 3].double().numpy() / T / np.log(2) + 1074) > 0.01
+    stands = p_is & (~q_is | (lu + lq < lp))
+    assert far.sum() > 0.95 * B and 0.2 * B < stands.sum() < 0.8 * B
+    assert (stands & (u == 0) & (lp < -126)).sum() > 20 and (~stands & (u == 0)).sum() > 5
+    all_u = np.stack((u, rng.rand(B).astype(np.float32)), -1).reshape(-1)
+    accepted = run(x.to(DEV), np.full(B, 3), all_u, [2] * B, y.to(DEV) if proposal else None, [T] * B)[2]
+    assert np.array_equal(accepted[far], stands[far].astype(np.int32)), np.flatnonzero(far & (accepted != stands))[:9]
