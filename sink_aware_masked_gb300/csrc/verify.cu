@@ -36,7 +36,7 @@
 //     of up to 20 otherwise), which leaves the hardware exponential's error,
 //     some 2^-23 of the mass;
 //   - masses from 2^-12 of the whole on, of which there are few, are listed and
-//     take an exponential of two fp32 parts (off by some 2^-40);
+//     take an exponential of two fp32 parts (off by 2^-40 of itself);
 //   - max(p - q, 0) needs the ratio of the two sums as exactly: they are
 //     summed again in the same way from the two rows.
 // Integer sums are the same in every order.  FP64 is not used: its rate on this
@@ -372,7 +372,8 @@ SA_DEV bool less(float u, float a, Pair t, float b) {
   const float e = ex2(small ? t.hi + 64.f : fminf(t.hi, 64.f));
   return u == 0.f || u * (small ? 18446744073709551616.f : 1.f) * a < fmaf(e, t.lo * kLn2, e) * b;
 }
-// 2^t to some 2^-40 of itself, t <= 0: 2^(n + k/16) (1 + g + g^2/2 + ...), g = ln 2 times the rest of t, |g| <= ln 2 / 32.
+// 2^t, t <= 0, off by 2^-40.4 of itself at most and 2^-43 on average where a mass is heavy (t > -12; the same steps against
+// exact values): 2^(n + k/16) (1 + g + g^2/2 + ...), g = ln 2 times the rest of t, |g| <= ln 2 / 32.
 // 0 from t = -60 down, where no unit of 2^-40 is left (a ratio of two sums brings back 2^18 at most), and where t is -inf
 // or, behind it, a NaN: a token that is heavy in one row may be anything in the other, and the scale holds for t > -127
 // alone.
@@ -383,11 +384,15 @@ __device__ __noinline__ Pair power_pair(Pair t) {
   const int i = static_cast<int>(m), k = i & 15;
   constexpr float kLn2Lo = static_cast<float>(0.693147180559945309 - static_cast<double>(kLn2));
   const float g = __fmul_rn(rest, kLn2), g_lo = fmaf(rest, kLn2, -g) + fmaf(rest, kLn2Lo, rest_lo * kLn2);
-  const float more = fmaf(g * g, fmaf(g, fmaf(g, fmaf(g, 1.f / 120, 1.f / 24), 1.f / 6), 0.5f), g_lo);  // e^g - 1 - g
+  // e^g - 1 in two parts: g and its square, whose parts matter (one fp32 for all but g would be off by 2^-34), then
+  // g^3 (1/6 + g/24 + g^2/120)
+  const float half = 0.5f * g, b = __fmul_rn(half, g), b_lo = fmaf(half, g, -b);
+  const float cube = fmaf(g * b, fmaf(g, fmaf(g, 1.f / 60, 1.f / 12), 1.f / 3), b_lo + fmaf(g_lo, g, g_lo));
+  const float e = __fadd_rn(g, b), e_lo = (b - (e - g)) + cube;  // |g| > |b|
   const float hi = kPowers.hi[k], lo = kPowers.lo[k];
-  const float a = __fmul_rn(hi, g), a_lo = fmaf(hi, g, -a);
+  const float a = __fmul_rn(hi, e), a_lo = fmaf(hi, e, -a);
   const float sum = __fadd_rn(hi, a), sum_lo = a - (sum - hi);  // |hi| > |a|
-  const float rest2 = sum_lo + (a_lo + fmaf(hi, more, fmaf(lo, g, lo)));
+  const float rest2 = sum_lo + (a_lo + fmaf(hi, e_lo, fmaf(lo, e, lo)));
   const float scale = __int_as_float((127 + (i >> 4)) << 23);
   return {sum * scale, rest2 * scale};
 }
