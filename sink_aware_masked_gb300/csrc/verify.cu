@@ -626,7 +626,6 @@ class Weights {
     }
   }
   SA_DEV bool minus_q() const { return y_ != nullptr; }
-  SA_DEV bool plain() const { return y_ == nullptr && without_ < 0; }
   SA_DEV void make_plain() {
     y_ = nullptr;
     without_ = -1;
