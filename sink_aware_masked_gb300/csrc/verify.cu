@@ -410,6 +410,12 @@ constexpr int kMaxParts = 16;
 constexpr int kWeightsPerSm = 4;  // CTAs of the weights' launch that an SM holds, one fewer where it tests the drafts too
 constexpr int kHeavyLog2 = 12;  // masses from 2^-12 of the whole on are heavy
 constexpr int kUnitLog2 = 40;   // masses in units of 2^-40 of (about) the whole
+// Units of max(p - q, 0) up to which the draw weighs the row's tokens again.  With the near ratio, off by 2^-23, the tokens
+// on which p and q agree to that get or lose their sign: 2^-23 of the whole at most, which is nothing beside most of w, but
+// all of it where w comes to no more (of 20 million entries, a third with u next to 1 so that rows alike are refused at all,
+// 304 got a token whose border lay up to 2.3 x 2^-24 of the whole away, or one of p where nothing was left; all had less
+// than 2^-20 of the whole in w, and with this limit none is off by more than 0.12 x 2^-24).  From 2^-16 on it is 2^-7 of w.
+constexpr u64 kEnough = 1ull << (kUnitLog2 - 16);
 constexpr int kList = 1024;     // vectors with heavy masses that a CTA keeps a list of
 
 struct RowStat {
@@ -618,9 +624,10 @@ class Weights {
     d_least_ = fmaxf(__fdiv_rn(-150.f, sc.hi), -3e38f);
     if (s.draft >= 0 && a.draft_logits != nullptr) {
       y_ = draft_of<T>(a, s.draft);
-      unit_q_ = unit_for(s.q.sum);
-      heavy_q_ = heavy_from(s.q);
       near_ = __fdiv_rn(s.p.sum, s.q.sum);
+      // (equal rows' sums can fall on either side of a power of two; in one unit what they leave is 0)
+      unit_q_ = fabsf(near_ - 1.f) < 0.001f ? unit_ : unit_for(s.q.sum);
+      heavy_q_ = heavy_from(s.q);
     } else if (s.draft >= 0) {
       without_ = a.drafts[s.draft];
     }
@@ -733,8 +740,8 @@ class Weights {
     more_ = (ratio_.hi - near_) + ratio_.lo;
     fall_ = more_ * __fdiv_rn(unit_, unit_q_);
   }
-  // What a run weighs with the exact ratio: the few tokens that get or lose their sign between near and exact ratio
-  // are below the square of the ratios' difference.
+  // What a run weighs with the exact ratio, but for tokens that get or lose their sign between near and exact ratio: each
+  // weighs less than the ratios' difference times itself.
   SA_DEV u64 exact(const Sums& v) const {
     return max(static_cast<long long>(v.weight) - __float2ll_rn(__ull2float_rn(v.slope) * fall_), 0LL);
   }
@@ -963,7 +970,7 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const __grid_cons
   int first = 0, last = weights.vectors();  // the vectors among which the token is
   const u64 run_weight = weights.exact(mine), upto = block_scan(sh, turn++, run_weight, total);
   if (tid == 0) sh.found = 0, sh.spare = -1;
-  if (total > 0) {
+  if (total >= (weights.minus_q() ? kEnough : 1)) {
     // the run that holds the place drawn
     target = target_of(total);
     if (target >= upto - run_weight && target < upto) holder_sh = tid, before_sh = upto - run_weight;
@@ -973,15 +980,20 @@ __global__ void __launch_bounds__(kThreads) verify_draw_kernel(const __grid_cons
     last = min(first + run, last);
     before = before_sh;
   } else {
-    // nothing is left of w: the target's own probabilities, over the whole row
-    weights.make_plain();
-    u64 sum = 0;
-    for (int v = tid; v < last; v += kThreads) {
-      typename Weights<kType>::Vector t;
-      float2 r[kVec / 2];
-      sum += weights.vector_weight(v, t, r);
+    // Little is left of w, next to what the runs' weights are off by: the whole row again, with the exact ratio.  Where
+    // that leaves nothing, the target's own probabilities.
+#pragma unroll 1
+    for (int again = 0; again < 2; ++again) {
+      if (again == 1 || !weights.minus_q()) weights.make_plain();
+      u64 sum = 0;
+      for (int v = tid; v < last; v += kThreads) {
+        typename Weights<kType>::Vector t;
+        float2 r[kVec / 2];
+        sum += weights.vector_weight(v, t, r);
+      }
+      block_scan(sh, turn++, sum, total);
+      if (total > 0) break;
     }
-    block_scan(sh, turn++, sum, total);
     target = target_of(total);
   }
   // A vector to each thread.  With the exact ratio they may come to a few units

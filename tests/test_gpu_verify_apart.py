@@ -10,6 +10,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle.pages_ref as ref
 from tests.test_gpu_verify import DEV, built, check, run  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -162,3 +163,60 @@ def test_probabilities_and_random_numbers_near_zero(proposal, T):
     all_u = np.stack((u, rng.rand(B).astype(np.float32)), -1).reshape(-1)
     accepted = run(x.to(DEV), np.full(B, 3), all_u, [2] * B, y.to(DEV) if proposal else None, [T] * B)[2]
     assert np.array_equal(accepted[far], stands[far].astype(np.int32)), np.flatnonzero(far & (accepted != stands))[:9]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [3, 300, 20011])
+def test_rows_that_agree_but_for_one_token(vocab, dtype):
+    """q gives one token 2^-13 to 2^-33 more than p does, and that is the draft: what is left, as much, is shared among all
+    others, whose p and q agree to that.  Equal tokens have equal exponentials in both rows, so what is left of each is
+    off by its units of 2^-40 (up to 3 a token: its mass in p, its mass in q, its own rounding)."""
+    rng = np.random.RandomState(vocab)
+    B = 200 if vocab < 1000 else 40
+    x = torch.from_numpy(rng.randn(2 * B, vocab) * 1.5).to(dtype)
+    x[::2, 1], x[::2, 0] = 4.0, -30.0
+    less = torch.softmax(x[::2].double(), -1)[:, 1]
+    # p of token 0 from 2^-12 to 2^-32, less than half of what q gives it
+    x[::2, 0] = (4.0 - np.log(2) * torch.linspace(12, 32, B) - less.log()).to(dtype)
+    y = x[::2].clone()
+    y[:, 0] = (y[:, 0].float() + 0.75).to(dtype)
+    u = np.stack((0.99 + 0.009 * rng.rand(B), rng.rand(B)), -1).reshape(-1).astype(np.float32)
+    tokens, logp, accepted, rejected = run(x.to(DEV), np.zeros(B, dtype=int), u, [2] * B, y.to(DEV))
+    assert (accepted == 0).all() and (rejected == 1).all() and (tokens[1::2] == -1).all()
+    tol, small = 2.0 ** -40 * (3 * vocab + 64), 0
+    for b in range(B):
+        _, _, acc, w, _ = ref.verify(x[2 * b:2 * b + 2].double().numpy(), y[b:b + 1].double().numpy(), [0],
+                                     u[2 * b:2 * b + 2].astype(np.float64), 1.0)
+        cum, t = np.cumsum(w), int(tokens[2 * b])
+        place = float(u[2 * b + 1]) * cum[-1]
+        small += cum[-1] < 2.0 ** -23
+        assert acc == 0 and t > 0 and cum[t - 1] - tol <= place <= cum[t] + tol, (b, t, cum[-1], place - cum[t])
+    assert small > B // 5
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T", [0.05, 0.3, 1.0])
+def test_rows_that_nearly_agree(T, dtype):
+    """q beside p by 10^-9 to 10^-4 of itself or not at all, u next to 1, the draft that q likes best beyond p: where it
+    falls, the token is drawn from the little that p leaves, or from p where that is nothing, to 2^-24 of the whole."""
+    rng = np.random.RandomState(3)
+    B, T, refusals = 600, float(np.float32(T)), 0
+    at = torch.arange(B, device=DEV)
+    for turn in range(80):
+        V = int(2 ** rng.uniform(1, 11))
+        x = (torch.from_numpy(rng.randn(2 * B, V)).to(DEV) * [0.3, 1, 3, 8][turn % 4]).to(dtype)
+        y = (x[::2].float() + torch.from_numpy(rng.randn(B, V)).float().to(DEV) * 10 ** rng.uniform(-9, -4)).to(dtype)
+        p, q = (torch.softmax(t.double() / T, -1) for t in (x[::2], y))
+        drafts = (q - p).argmax(-1)
+        u = np.stack((np.full(B, 1 - 2.0 ** -24), rng.rand(B)), -1).reshape(-1).astype(np.float32)
+        tokens, _, accepted, _ = (torch.from_numpy(t).to(DEV) for t in run(x, drafts.tolist(), u, [2] * B, y, [T] * B))
+        w, t = (p - q).clamp(min=0), tokens[::2].long()
+        # Equal rows leave nothing.  Rows that differ leave something, be it less than 2^-24 of the whole, where every
+        # border of w lies within that of every place and any token may be given.
+        cum = torch.where((x[::2] == y).all(-1, keepdim=True), p, w).cumsum(-1)
+        place = torch.from_numpy(u[1::2]).double().to(DEV) * cum[:, -1]
+        before = torch.where(t > 0, cum[at, (t - 1).clamp(min=0)], torch.zeros_like(place))
+        good = (t >= 0) & (before - 2.0 ** -24 <= place) & (place <= cum[at, t.clamp(min=0)] + 2.0 ** -24)
+        assert good[accepted == 0].all(), (turn, V, int((~good & (accepted == 0)).sum()))
+        refusals += int((accepted == 0).sum())
+    assert refusals > 5000
