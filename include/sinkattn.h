@@ -439,8 +439,9 @@ sinkattn_status sinkattn_kv_write(const sinkattn_kv_pages* pages, const int32_t*
  * Rows outside every entry's, and rows of an entry beyond q_per_seq, are left
  * as they were.  What a row does not see does not reach it, whatever it holds;
  * scores are fp32: a row that sees one beyond fp32's range in log2 units may
- * read as NaN; the weighted values are summed in fp32 (weights up to 1); outputs
- * below 2^-126 may be 0.  (num_heads_q / num_heads_kv) * q_per_seq <= 128.  The
+ * read as NaN; the weighted values are summed in fp32 (weights up to 1); an
+ * infinite value whose weight is below 2^-126 may read as NaN; outputs below
+ * 2^-126 may be 0.  (num_heads_q / num_heads_kv) * q_per_seq <= 128.  The
  * workspace (sinkattn_kv_decode_workspace_size bytes, 16-byte aligned, its size
  * depends on the device's SM count) is zero-filled once; every call leaves it
  * usable for later calls of any shape with as many kv heads or fewer, not for

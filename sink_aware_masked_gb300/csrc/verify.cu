@@ -18,13 +18,13 @@
 //            in the row where the entry stopped, run by run; the row, or pair of
 //            rows, is read again, in part from L2
 //   draw     a CTA per entry: the run that holds the place drawn, and the token
-//            in it
+//            in it (the whole row where p and q nearly agree)
 //
-// Measured (GB300): 128 entries of 0 to 4 drafts over 201088 bf16 logits 94 us
-// (255 MB, 38 us at the copy rate): rows 43, tests 4, weights 38 (300
+// Measured (GB300): 128 entries of 0 to 4 drafts over 201088 bf16 logits 95 us
+// (255 MB, 38 us at the copy rate): rows 42, tests 6, weights 39 (300
 // instructions per 32 vectors of both rows, and entries that have nothing to draw
-// beside others that have), draw 9.  48 entries of up to 7 looked-up drafts over 100003 fp16 33 us,
-// one entry with 3 drafts over 50257 fp32 18 us: the chains of loads of the
+// beside others that have), draw 8.  48 entries of up to 7 looked-up drafts over 100003 fp16 34 us,
+// one entry with 3 drafts over 50257 fp32 17.5 us: the chains of loads of the
 // launches, which wait for one another on the device.
 //
 // Arithmetic.  Where the tests are concerned fp32 sums do: a test is decided
@@ -38,7 +38,9 @@
 //   - masses from 2^-12 of the whole on, of which there are few, are listed and
 //     take an exponential of two fp32 parts (off by 2^-40 of itself);
 //   - max(p - q, 0) needs the ratio of the two sums as exactly: they are
-//     summed again in the same way from the two rows.
+//     summed again in the same way from the two rows; weights are taken with the
+//     fp32 sums' ratio and corrected by what that is off, and where little is
+//     left of them the draw takes them again with the exact one.
 // Integer sums are the same in every order.  FP64 is not used: its rate on this
 // GPU would cost more than all the rest.
 #include <cuda_fp16.h>
