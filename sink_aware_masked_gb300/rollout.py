@@ -339,8 +339,8 @@ def verify_workspace(logits) -> torch.Tensor:
     return torch.empty(max(size, 16), dtype=torch.uint8, device=logits.device)
 
 
-def verify_tokens(logits, drafts, u, cu_rows, *, draft_logits=None, temperature=None, live=None, tokens=None, logp=None,
-                  accepted=None, rejected=None, workspace=None):
+def verify_tokens(logits, drafts, u, cu_rows, *, draft_logits=None, temperature=None, live=None, tokens=None,
+                  logp=None, accepted=None, rejected=None, workspace=None):
     """Which drafted tokens stand, and the token that follows them: returns (tokens, logp, accepted, rejected).
 
     logits [R, V] fp32, bf16 or fp16, rows contiguous (any row stride): the
@@ -352,11 +352,11 @@ def verify_tokens(logits, drafts, u, cu_rows, *, draft_logits=None, temperature=
     that is drawn.  temperature fp32 [B] (default 1; 0: the largest logit), for
     both.  live int32 [B] (from ``kv_plan``): an entry below 0 was not served, and
     nothing of it stands or is rejected (tokens -1, logp 0, accepted = rejected
-    = 0), so that ``rejected`` can be the next plan's ``drop``.  tokens int32 [R]: the drafts that stand, the token drawn, -1 behind
-    it; logp fp32 [R] their log-probabilities under the target (grpo_loss's
-    logp_old), 0 behind them; accepted and rejected int32 [B].  An invalid row
-    ends its entry with token -1 and logp NaN, one without an allowed token
-    with -1 and -inf.
+    = 0), so that ``rejected`` can be the next plan's ``drop``.  tokens int32
+    [R]: the drafts that stand, the token drawn, -1 behind it; logp fp32 [R]
+    their log-probabilities under the target (grpo_loss's logp_old), 0 behind
+    them; accepted and rejected int32 [B].  An invalid row ends its entry with
+    token -1 and logp NaN, one without an allowed token with -1 and -inf.
     """
     kind, stride = _logit_rows("logits", logits)
     R, V = logits.shape
@@ -388,6 +388,6 @@ def verify_tokens(logits, drafts, u, cu_rows, *, draft_logits=None, temperature=
     if workspace is None:
         workspace = verify_workspace(logits)
     wn = _vector("workspace", workspace, torch.uint8, dev)
-    _call("sinkattn_verify_live_tokens", dev, logits.data_ptr(), stride, xp, xs, kind, R, D, V, dp, cp, vp, B, up, tp, to,
-          lp, ap, rp, _tensor("workspace", workspace, torch.uint8, (wn,), dev), wn)
+    _call("sinkattn_verify_live_tokens", dev, logits.data_ptr(), stride, xp, xs, kind, R, D, V, dp, cp, vp, B, up, tp,
+          to, lp, ap, rp, _tensor("workspace", workspace, torch.uint8, (wn,), dev), wn)
     return tokens, logp, accepted, rejected
